@@ -36,7 +36,10 @@ extern "C" {
 #endif
 
 /* 3: adds the per-head (fm_attn_*_heads) and multi-interval (fm_attn_*_multi)
- * entry points; the earlier ones are unchanged. */
+ * entry points; the earlier ones are unchanged. Entry points added since
+ * without touching an earlier one keep the number: norm and rotation
+ * (fm_qk_*, fm_rope_freqs), the paged cache (fm_cache_*) and the attention
+ * over it (fm_attn_paged). */
 #define FM_ABI_VERSION 3
 
 typedef enum fm_status {
@@ -406,6 +409,159 @@ fm_status fm_balance_chunks(const int64_t* w, int32_t n_chunks, int32_t P, int32
  * skipped: rank r needs chunk c's K / V rows, and only those. */
 fm_status fm_needed_chunks(const uint8_t* tile_class, int32_t B, int32_t nQ, int32_t nK, const int32_t* owner,
                            int32_t n_chunks, int32_t P, int32_t blocks_per_chunk, uint8_t* need);
+
+/* ---------------------------------------------------------------------------
+ * Norm and rotation of queries and keys: one pass from a projection's output
+ * to the attention calls' inputs (layout change included), and its backward.
+ *
+ * For every token and head, x the d elements of its row:
+ *   with weights w:  n = x * w / sqrt(mean(x^2) + eps);  without: n = x
+ *   pair i < rot / 2 of n, theta = pos * inv_freq[i]:
+ *     (a, b) -> rot_scale * (a cos theta - b sin theta, a sin theta + b cos theta)
+ *   pairs are elements (i, i + rot / 2), or (2i, 2i + 1) when interleaved != 0;
+ *   elements from rot on pass through. v rows are copied.
+ * Computed in fp32 (theta exact modulo a turn for any int32 position), each
+ * output rounded to bf16 once.
+ *
+ * Tensors are bf16 views (B, H, N, d) of any element strides sb, sh, sn that are
+ * multiples of 8, the d elements of a row contiguous, addresses 16-byte aligned:
+ * a projection's (B, N, heads, d) output and the attention calls' contiguous
+ * (B, H, N, d) are both such views. An output may be its own input (the same
+ * view); apart from that no tensors overlap. d is 64, 128 or 256; rot a multiple
+ * of 16, 0 <= rot <= d (0: no rotation; pos and inv_freq are then not read). pos: int32, entry b * pos_sb + n
+ * (pos_sb 0: one row for every batch entry); inv_freq: rot / 2 finite fp32
+ * values. q_weight / k_weight: d values each, fp32 when w_f32 != 0 else bf16;
+ * NULL: that side is not normed. v and vo both NULL: no values.
+ *
+ * Backward: dqo, dko, dvo are the gradients of the outputs; dq, dk, dv and the
+ * weights' gradients (type of the weights) are written. q and k, the forward's
+ * inputs, are read where normed and may be NULL elsewhere. The weights' sums
+ * over all tokens and heads are fp32 in a fixed order: the same call gives the
+ * same bits. Workspace: fm_qk_norm_rope_bwd_workspace_bytes.
+ *
+ * fm_rope_freqs (HOST function, host pointers) fills inv_freq[rot / 2] and
+ * rot_scale: base^(-2i / rot), and for contexts longer than the trained ones
+ *   FM_ROPE_LINEAR  all divided by factor (positions interpolated)
+ *   FM_ROPE_NTK     base replaced by base * factor^(rot / (rot - 2))
+ *   FM_ROPE_YARN    between both: pairs that turn more than beta_fast times
+ *                   within orig_len positions keep their frequency, those that
+ *                   turn less than beta_slow times are divided by factor, a
+ *                   linear ramp over the pair index in between; rot_scale =
+ *                   0.1 ln(factor) + 1
+ * (rot_scale 1 otherwise). factor >= 1, base > 1; YARN: orig_len > 0 and
+ * beta_fast > beta_slow > 0.
+ * ------------------------------------------------------------------------- */
+typedef struct fm_view {
+  void* ptr;
+  int64_t sb, sh, sn;
+} fm_view;
+
+typedef struct fm_qk_problem {
+  int32_t B, N, H_q, H_kv, d;
+  int32_t rot, interleaved, w_f32;
+  float eps, rot_scale;
+  const int32_t* pos;
+  int64_t pos_sb;
+  const float* inv_freq;
+  const void* q_weight;
+  const void* k_weight;
+} fm_qk_problem;
+
+enum { FM_ROPE_PLAIN = 0, FM_ROPE_LINEAR = 1, FM_ROPE_NTK = 2, FM_ROPE_YARN = 3 };
+
+fm_status fm_rope_freqs(int32_t rot, double base, int32_t kind, double factor, int64_t orig_len, double beta_fast,
+                        double beta_slow, float* inv_freq, float* rot_scale);
+fm_status fm_qk_norm_rope(const fm_qk_problem* p, const fm_view* q, const fm_view* k, const fm_view* v,
+                          const fm_view* qo, const fm_view* ko, const fm_view* vo, void* stream);
+size_t fm_qk_norm_rope_bwd_workspace_bytes(const fm_qk_problem* p);
+fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const fm_view* dko, const fm_view* dvo,
+                              const fm_view* q, const fm_view* k, const fm_view* dq, const fm_view* dk,
+                              const fm_view* dv, void* dq_weight, void* dk_weight, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged cache of keys and values.
+ *
+ * k, v: (n_pages, H_kv, page_size, d), contiguous, bf16 or (k_exp, v_exp not
+ * NULL) e4m3 with one scale a row: exponent bytes (n_pages, H_kv, page_size),
+ * value = stored * 2^(exponent - 127). page_size is 16, 32, 64 or 128, d 64, 128
+ * or 256. Addresses 16-byte aligned.
+ *
+ * A batch of R sequences: q_off (R + 1), the first new token of each in the
+ * call's T packed tokens, ascending from 0; kv_len (R), its keys in the cache,
+ * the new tokens' own included; page_table (R, width): entry i of row r is the
+ * page of its keys [i * page_size, (i + 1) * page_size). New token a of n has
+ * position kv_len - n + a. Entries past a sequence's last page are not read.
+ * All device int32. Tokens from q_off[R] on belong to no sequence: their rows are
+ * neither read nor written. Values that no such batch has (a page outside
+ * [0, n_pages), a length outside [0, width * page_size], offsets that descend or
+ * pass T) set FM_DEVERR_RANGE; their rows are then left out or read as zeros,
+ * nothing outside the tensors is touched.
+ *
+ * fm_cache_write puts the new tokens' rows k, v (element strides st a token, sh
+ * a head, multiples of 8) in their places, rounded to e4m3 with the smallest
+ * exponent >= 1 whose scale puts the row's largest magnitude at 448 or below; a
+ * row that holds a NaN or an infinity gets exponent 255 and reads as NaN. A new
+ * token without a page (kv_len < n included) sets FM_DEVERR_RANGE. A page that
+ * receives tokens may be in one place of the table only; pages that are only
+ * read may be shared.
+ *
+ * fm_cache_read copies keys and values back, as bf16: kv_off (R + 1) ascending
+ * from 0, sequence r's keys 0 .. kv_off[r + 1] - kv_off[r] - 1 become rows
+ * [kv_off[r], kv_off[r + 1]) of k, v, contiguous (H_kv, n_rows, d): the packed
+ * documents that fm_attn_fwd takes. Rows from kv_off[R] on are left as they were.
+ * ------------------------------------------------------------------------- */
+typedef struct fm_rows {
+  void* ptr;
+  int64_t st, sh;
+} fm_rows;
+
+typedef struct fm_kv_cache {
+  void* k;
+  void* v;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  int32_t n_pages, H_kv, page_size, d;
+} fm_kv_cache;
+
+typedef struct fm_paged_batch {
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int32_t R, width;
+} fm_paged_batch;
+
+fm_status fm_cache_write(const fm_kv_cache* cache, const fm_paged_batch* batch, int32_t T, const fm_rows* k,
+                         const fm_rows* v, void* stream);
+fm_status fm_cache_read(const fm_kv_cache* cache, const int32_t* kv_off, const int32_t* page_table, int32_t R,
+                        int32_t width, int32_t n_rows, void* k, void* v, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of new tokens over the paged cache (their own keys and values
+ * written first, fm_cache_write): chunks of prompts, single tokens, or any mix.
+ *
+ * O = softmax(scale q.k) V and LSE = log sum exp(scale q.k) (natural log) over
+ * the keys a token sees. Position p sees key j < kv_len iff
+ *   causal == 0, or j <= p and (window == 0, or j > p - window, or j < sinks)
+ * (causal with window and sinks: the sliding window with attention sinks of the
+ * column-wise mask LTS_j = j + window for j >= sinks, LTE_j = N; causal == 0:
+ * cross attention to states of another length). window >= 0, sinks >= 0, both 0
+ * when causal == 0. A token that sees no key gets O = 0, LSE = -inf. What lies in
+ * the cache at keys that no token of the batch sees does not matter, NaN included;
+ * a NaN or infinity among a visible key's values may reach every token of its
+ * sequence in the call.
+ *
+ * q, o: bf16 rows (T, H_q, d) of element strides st, sh (multiples of 8,
+ * 16-byte aligned); lse: (T, H_q) fp32, contiguous. GQA as fm_attn_fwd. e4m3
+ * caches give what the cache read back in bf16 gives. scale > 0. The joining
+ * order of a sequence's parts is fixed by the lengths: the same call gives the
+ * same bits. Workspace: fm_attn_paged_workspace_bytes (on the current device),
+ * rewritten by every call: calls that may overlap need one each.
+ * ------------------------------------------------------------------------- */
+size_t fm_attn_paged_workspace_bytes(const fm_kv_cache* cache, const fm_paged_batch* batch, int32_t T, int32_t H_q);
+fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, int32_t T, int32_t H_q,
+                        const fm_rows* q, float scale, int32_t causal, int32_t window, int32_t sinks,
+                        const fm_rows* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Device error word. Synchronizes `stream`, returns the accumulated FM_DEVERR_*

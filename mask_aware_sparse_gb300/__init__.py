@@ -15,7 +15,12 @@ Functions carry the names of the C entry points:
   fm_from_fms_fme, fm_merge_parts, fm_sum_parts, fm_chunk_loads,
   fm_balance_chunks, fm_needed_chunks (host code: the chunk balancer and the
   K / V exchange plan for context parallelism);
-plus fm_classify_tiles_heads (fm_classify_tiles over the B * H_q rows of
+  fm_rope_freqs, fm_qk_norm_rope, fm_qk_norm_rope_bwd (per-head norm and rotation of
+  queries and keys), fm_cache_write, fm_cache_read, fm_attn_paged (the paged key /
+  value cache and the attention of new tokens over it);
+plus KVCache, PagedBatch and fm_cache_new (a cache and a batch, checked once and
+kept by a serving program), QKNormRope (the norm and rotation of a
+flashmask_attention call), fm_classify_tiles_heads (fm_classify_tiles over the B * H_q rows of
 per-head vectors), fm_attn_multi_interval and fm_attn_per_head (the library
 calls of a multi-interval / per-head forward and backward in sequence) and
 flashmask_attention (autograd wrapper: the classification, forward and
@@ -54,6 +59,33 @@ class fm_balance_report(ctypes.Structure):
                 ("triple_moves", ctypes.c_int32), ("budget_exhausted", ctypes.c_int32)]
 
 
+class fm_view(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("sb", ctypes.c_int64), ("sh", ctypes.c_int64), ("sn", ctypes.c_int64)]
+
+
+class fm_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("st", ctypes.c_int64), ("sh", ctypes.c_int64)]
+
+
+class fm_qk_problem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("w_f32", ctypes.c_int32), ("eps", ctypes.c_float), ("rot_scale", ctypes.c_float),
+                ("pos", ctypes.c_void_p), ("pos_sb", ctypes.c_int64), ("inv_freq", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class fm_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class fm_paged_batch(ctypes.Structure):
+    _fields_ = [("q_off", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("R", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
 class FMError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} (status {status})")
@@ -63,7 +95,21 @@ class FMError(RuntimeError):
 _lib = None
 
 _P = ctypes.c_void_p
+_VIEW, _ROWS = ctypes.POINTER(fm_view), ctypes.POINTER(fm_rows)
+_CACHE, _BATCH = ctypes.POINTER(fm_kv_cache), ctypes.POINTER(fm_paged_batch)
 _SIGS = {
+    "fm_rope_freqs": (ctypes.c_int, [ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_int64,
+                                     ctypes.c_double, ctypes.c_double, _P, ctypes.POINTER(ctypes.c_float)]),
+    "fm_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(fm_qk_problem)] + [_VIEW] * 6 + [_P]),
+    "fm_qk_norm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(fm_qk_problem)]),
+    "fm_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(fm_qk_problem)] + [_VIEW] * 8 + [_P] * 3
+                            + [ctypes.c_size_t, _P]),
+    "fm_cache_write": (ctypes.c_int, [_CACHE, _BATCH, ctypes.c_int32, _ROWS, _ROWS, _P]),
+    "fm_cache_read": (ctypes.c_int, [_CACHE, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P]),
+    "fm_attn_paged_workspace_bytes": (ctypes.c_size_t, [_CACHE, _BATCH, ctypes.c_int32, ctypes.c_int32]),
+    "fm_attn_paged": (ctypes.c_int, [_CACHE, _BATCH, ctypes.c_int32, ctypes.c_int32, _ROWS, ctypes.c_float,
+                                     ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _ROWS, _P, _P, ctypes.c_size_t,
+                                     _P]),
     "fm_abi_version": (ctypes.c_int32, []),
     "fm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fm_attn_tiling": (ctypes.c_int, [ctypes.POINTER(fm_tiling)]),
@@ -715,6 +761,340 @@ def fm_balance_chunks(w, P: int, kappa: int, phases: int = 3, node_budget: int =
     return owner, {name: int(getattr(rep, name)) for name, _ in fm_balance_report._fields_}
 
 
+# ------------------------------------------------ norm, rotation, paged cache
+def _enqueue(name, dev, stream, *args):
+    """Call a library function whose last argument is the stream: the given one,
+    or the current stream of the tensors' device, with that device current."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _enqueue(name, dev, stream, *args)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    st = getattr(lib(), name)(*args, s.cuda_stream)
+    if st != FM_OK:
+        raise FMError(st, name)
+
+
+def _strides(t, name, dims):
+    """Element strides of all dimensions of t but the last, for a kernel that
+    reads rows in 16-byte pieces (0 for a dimension of size 1)."""
+    _need(isinstance(t, torch.Tensor) and t.dim() == dims, f"{name} must be a torch tensor of {dims} dimensions")
+    _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
+    shape, st = t.shape, t.stride()
+    _need(st[-1] == 1 or shape[-1] == 1, f"{name}: the elements of a row must be contiguous")
+    st = [x if n > 1 else 0 for x, n in zip(st, shape[:-1])]
+    ok = t.data_ptr() & 15 == 0
+    for x in st:
+        ok = ok and x & 7 == 0
+    _need(ok, f"{name}: rows must start on 16-byte boundaries (strides {tuple(t.stride())})")
+    return st
+
+
+def _view(t, name, shape=None):
+    sb, sh, sn = _strides(t, name, 4)
+    if shape is not None:
+        _need(t.shape == torch.Size(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return fm_view(t.data_ptr(), sb, sh, sn)
+
+
+def _rows(t, name, shape=None):
+    st, sh = _strides(t, name, 3)
+    if shape is not None:
+        _need(t.shape == torch.Size(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return fm_rows(t.data_ptr(), st, sh)
+
+
+def _no_overlap(name, t):
+    """Outputs: no two elements in one place."""
+    for n, s in zip(t.shape, t.stride()):
+        _need(n <= 1 or s != 0, f"{name}: an output cannot be a broadcast view")
+
+
+_ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def fm_rope_freqs(rot: int, *, base: float = 10000.0, kind: str = "plain", factor: float = 1.0, orig_len: int = 0,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(inv_freq fp32 (rot / 2,), rot_scale): a rotation's inverse frequencies and
+    the factor of its cos and sin. kind: "plain", or for contexts `factor` times
+    longer than the trained ones "linear", "ntk" or "yarn" (orig_len: the trained length)."""
+    _need(kind in _ROPE_KINDS, f"kind must be one of {sorted(_ROPE_KINDS)}, got {kind!r}")
+    f = np.empty(max(1, int(rot) // 2), dtype=np.float32)
+    sc = ctypes.c_float()
+    _check(lib().fm_rope_freqs(int(rot), float(base), _ROPE_KINDS[kind], float(factor), int(orig_len),
+                               float(beta_fast), float(beta_slow), f.ctypes.data, ctypes.byref(sc)), "fm_rope_freqs")
+    return torch.from_numpy(f).to("cpu" if device is None else device), sc.value
+
+
+def _qk_args(q, k, v, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps):
+    """The problem of a norm-and-rotation call, its shapes, dtypes and devices checked."""
+    _need(isinstance(q, torch.Tensor) and q.dim() == 4, "q must be a (B, H_q, N, d) tensor")
+    _need(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be a (B, H_kv, N, d) tensor")
+    B, Hq, N, d = q.shape
+    Hkv = k.shape[1]
+    _need(k.shape == torch.Size((B, Hkv, N, d)), f"k has shape {tuple(k.shape)}, expected (B={B}, H_kv, N={N}, d={d})")
+    p = fm_qk_problem(B, N, Hq, Hkv, d, 0, 1 if interleaved else 0, 0, eps, rot_scale)
+    if inv_freq is not None:
+        _need(isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1, "inv_freq must be a (rot / 2,) tensor")
+        _like(inv_freq, "inv_freq", inv_freq.shape, torch.float32)
+        _need(isinstance(positions, torch.Tensor), "positions must be a (N,) or (B, N) int32 tensor")
+        _need(positions.shape in (torch.Size((N,)), torch.Size((B, N))),
+              f"positions has shape {tuple(positions.shape)}, expected (N={N},) or (B={B}, N={N})")
+        _like(positions, "positions", positions.shape, torch.int32)
+        p.rot, p.pos, p.inv_freq = 2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr()
+        p.pos_sb = N if positions.dim() == 2 else 0
+    wt = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        _need(isinstance(w, torch.Tensor) and w.dtype in (torch.float32, torch.bfloat16),
+              f"{name} must be a float32 or bfloat16 tensor")
+        _like(w, name, (d,), w.dtype)
+        _need(wt in (None, w.dtype), "q_weight and k_weight must have one dtype")
+        wt = w.dtype
+        p.w_f32 = 1 if wt == torch.float32 else 0
+        setattr(p, name, w.data_ptr())
+    return p
+
+
+def fm_qk_norm_rope(q, k, v=None, *, positions=None, inv_freq=None, interleaved: bool = False, rot_scale: float = 1.0,
+                    q_weight=None, k_weight=None, eps: float = 1e-6, out=None, stream=None):
+    """Per-head norm and rotation of queries and keys in one pass: q (B, H_q, N, d),
+    k, v (B, H_kv, N, d) bf16 views of any strides (rows contiguous), e.g. of a
+    fused projection's output, to (q', k') or (q', k', v') contiguous (B, H, N, d),
+    or into the tensors `out` (views of any strides; an input itself is allowed).
+    positions: int32 (N,) or (B, N); inv_freq: fp32 (rot / 2,), None: no rotation;
+    q_weight / k_weight: (d,), None: no norm."""
+    p = _qk_args(q, k, v, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps)
+    ins = (q, k) if v is None else (q, k, v)
+    if out is None:
+        out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in ins)
+    _need(len(out) == len(ins), "out must hold one tensor per input")
+    names = ("q", "k", "v")
+    iv = [_view(t, n, k.shape if n == "v" else None) for t, n in zip(ins, names)]
+    ov = [_view(t, "output " + n, s.shape) for t, n, s in zip(out, names, ins)]
+    for t, n in zip(out, names):
+        _no_overlap("output " + n, t)
+    _same_cuda(q=q, k=k, v=v, positions=None if inv_freq is None else positions, inv_freq=inv_freq,
+               q_weight=q_weight, k_weight=k_weight, **{f"output {i}": t for i, t in enumerate(out)})
+    if v is None:
+        iv.append(None)
+        ov.append(None)
+    _enqueue("fm_qk_norm_rope", q.device, stream, p, *iv, *ov)
+    return tuple(out)
+
+
+def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, interleaved: bool = False,
+                        rot_scale: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6, out=None,
+                        stream=None):
+    """Backward of fm_qk_norm_rope: the gradients dqo, dko, dvo (or None) of its
+    outputs and its inputs q, k give (dq, dk, dv, dq_weight, dk_weight); None
+    where there is no such input. dq, dk, dv are (B, H, N, d) views of contiguous
+    (B, N, H, d) tensors (a projection's own layout), or the views `out` (dq, dk[, dv])."""
+    p = _qk_args(q, k, dvo, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps)
+    gs = (dqo, dko) if dvo is None else (dqo, dko, dvo)
+    shapes = (q.shape, k.shape, k.shape)
+    if out is None:
+        out = tuple(torch.empty((s[0], s[2], s[1], s[3]), dtype=torch.bfloat16, device=q.device).transpose(1, 2)
+                    for s in shapes[:len(gs)])
+    _need(len(out) == len(gs), "out must hold one tensor per gradient")
+    names = ("dq", "dk", "dv")
+    gv = [_view(t, n + "o", s) for t, n, s in zip(gs, names, shapes)]
+    ov = [_view(t, "output " + n, s) for t, n, s in zip(out, names, shapes)]
+    for t, n in zip(out, names):
+        _no_overlap("output " + n, t)
+    qv, kv = _view(q, "q"), _view(k, "k")
+    _same_cuda(dqo=dqo, dko=dko, dvo=dvo, q=q, k=k, positions=None if inv_freq is None else positions,
+               inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight,
+               **{f"output {i}": t for i, t in enumerate(out)})
+    if dvo is None:
+        gv.append(None)
+        ov.append(None)
+    dwq = None if q_weight is None else torch.empty_like(q_weight)
+    dwk = None if k_weight is None else torch.empty_like(k_weight)
+    ws, wsb = None, 0
+    if dwq is not None or dwk is not None:
+        with torch.cuda.device(q.device):
+            wsb = lib().fm_qk_norm_rope_bwd_workspace_bytes(p)
+        ws = torch.empty(max(1, wsb), dtype=torch.uint8, device=q.device)
+    _enqueue("fm_qk_norm_rope_bwd", q.device, stream, p, *gv, qv, kv, *ov, _ptr(dwq), _ptr(dwk), _ptr(ws), wsb)
+    return out[0], out[1], (out[2] if dvo is not None else None), dwq, dwk
+
+
+class KVCache:
+    """The paged cache: k, v (n_pages, H_kv, page_size, d) bf16, or float8_e4m3fn with
+    exponent bytes k_exp, v_exp (n_pages, H_kv, page_size) uint8 (value = stored *
+    2^(exponent - 127)). Checked once; holds the tensors it was given."""
+
+    __slots__ = ("k", "v", "k_exp", "v_exp", "device", "c")
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        _need(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be (n_pages, H_kv, page_size, d)")
+        _need((k_exp is None) == (v_exp is None), "k_exp and v_exp go together")
+        dt = torch.bfloat16 if k_exp is None else torch.float8_e4m3fn
+        _like(k, "k", k.shape, dt)
+        _like(v, "v", k.shape, dt)
+        if k_exp is not None:
+            _like(k_exp, "k_exp", k.shape[:3], torch.uint8)
+            _like(v_exp, "v_exp", k.shape[:3], torch.uint8)
+        n, h, page, d = k.shape
+        _need(n > 0 and h > 0, "a cache needs pages and heads")
+        _need(page in (16, 32, 64, 128), f"page_size must be 16, 32, 64 or 128, got {page}")
+        _need(d in (64, 128, 256), f"d must be 64, 128 or 256, got {d}")
+        for name, t in (("k", k), ("v", v), ("k_exp", k_exp), ("v_exp", v_exp)):
+            _need(t is None or t.data_ptr() & 15 == 0, f"{name} must start on a 16-byte boundary")
+        _same_cuda(k=k, v=v, k_exp=k_exp, v_exp=v_exp)
+        self.k, self.v, self.k_exp, self.v_exp, self.device = k, v, k_exp, v_exp, k.device
+        self.c = fm_kv_cache(k.data_ptr(), v.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(),
+                             0 if v_exp is None else v_exp.data_ptr(), n, h, page, d)
+
+
+def fm_cache_new(n_pages: int, H_kv: int, page_size: int, d: int, *, dtype=torch.bfloat16, device="cuda") -> KVCache:
+    """A cache of n_pages pages, its contents undefined. dtype: torch.bfloat16 or torch.float8_e4m3fn."""
+    _need(dtype in (torch.bfloat16, torch.float8_e4m3fn), f"dtype must be bfloat16 or float8_e4m3fn, got {dtype}")
+    shape = (n_pages, H_kv, page_size, d)
+    kv = [torch.empty(shape, dtype=dtype, device=device) for _ in range(2)]
+    ex = [None, None]
+    if dtype == torch.float8_e4m3fn:
+        ex = [torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)]
+    return KVCache(*kv, *ex)
+
+
+class PagedBatch:
+    """A batch of R sequences over a cache, int32 CUDA tensors: q_off (R + 1,) first new
+    token of each among a call's packed tokens, kv_len (R,) keys of each (new ones
+    included), page_table (R, width) page of each page_size keys. Checked once; the
+    tensors' values may change between calls (their addresses may not)."""
+
+    __slots__ = ("q_off", "kv_len", "page_table", "device", "c")
+
+    def __init__(self, q_off, kv_len, page_table):
+        _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, "page_table must be (R, width)")
+        R, width = page_table.shape
+        _need(R > 0 and width > 0, "a batch needs sequences and pages")
+        _like(page_table, "page_table", (R, width), torch.int32)
+        _like(q_off, "q_off", (R + 1,), torch.int32)
+        _like(kv_len, "kv_len", (R,), torch.int32)
+        _same_cuda(q_off=q_off, kv_len=kv_len, page_table=page_table)
+        self.q_off, self.kv_len, self.page_table, self.device = q_off, kv_len, page_table, q_off.device
+        self.c = fm_paged_batch(q_off.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), R, width)
+
+
+def _serve_args(cache, batch, **ts):
+    _need(isinstance(cache, KVCache), "cache must be a KVCache")
+    dev = cache.device
+    if batch is not None:
+        _need(isinstance(batch, PagedBatch), "batch must be a PagedBatch")
+        _need(batch.device == dev, f"the batch is on {batch.device}, the cache on {dev}")
+    for name, t in ts.items():
+        _need(t is None or t.device == dev, f"{name} is on {t.device if t is not None else None}, the cache on {dev}")
+    return dev
+
+
+def fm_cache_write(k, v, cache: KVCache, batch: PagedBatch, stream=None):
+    """Put the rows of T new tokens, k and v (T, H_kv, d) bf16 views, in their places
+    in the cache (rounded to e4m3 with a scale a row where the cache is e4m3)."""
+    _need(isinstance(k, torch.Tensor) and k.dim() == 3, "k must be a (T, H_kv, d) tensor")
+    _need(isinstance(cache, KVCache), "cache must be a KVCache")
+    shape = (k.shape[0], cache.c.H_kv, cache.c.d)
+    kr, vr = _rows(k, "k", shape), _rows(v, "v", shape)
+    dev = _serve_args(cache, batch, k=k, v=v)
+    _enqueue("fm_cache_write", dev, stream, cache.c, batch.c, shape[0], kr, vr)
+
+
+def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=None, stream=None):
+    """Keys and values as packed bf16 rows (1, H_kv, n_rows, d): sequence r's keys from 0
+    on become rows [kv_off[r], kv_off[r + 1]). kv_off (R + 1,) and page_table (R, width)
+    int32. Rows that no sequence has are left as they were (undefined in new tensors)."""
+    dev = _serve_args(cache, None)
+    _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2 and page_table.numel() > 0,
+          "page_table must be (R, width)")
+    R, width = page_table.shape
+    _like(page_table, "page_table", (R, width), torch.int32)
+    _like(kv_off, "kv_off", (R + 1,), torch.int32)
+    shape = (1, cache.c.H_kv, int(n_rows), cache.c.d)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    _like(k, "k", shape, torch.bfloat16)
+    _like(v, "v", shape, torch.bfloat16)
+    _same_cuda(cache=cache.k, kv_off=kv_off, page_table=page_table, k=k, v=v)
+    _enqueue("fm_cache_read", dev, stream, cache.c, kv_off.data_ptr(), page_table.data_ptr(), R, width, shape[2],
+             k.data_ptr(), v.data_ptr())
+    return k, v
+
+
+def fm_attn_paged_workspace_bytes(cache: KVCache, batch: PagedBatch, T: int, H_q: int) -> int:
+    """Bytes of workspace an fm_attn_paged call of these shapes needs."""
+    dev = _serve_args(cache, batch)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return lib().fm_attn_paged_workspace_bytes(cache.c, batch.c, T, H_q)
+    return lib().fm_attn_paged_workspace_bytes(cache.c, batch.c, T, H_q)
+
+
+def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal: bool = True, window: int = 0,
+                  sinks: int = 0, o=None, lse=None, ws=None, stream=None):
+    """Attention of T new tokens q (T, H_q, d) over the paged cache, their own keys and
+    values written before (fm_cache_write): (O bf16 (T, H_q, d), LSE fp32 (T, H_q)).
+    Position p sees key j < kv_len iff j <= p (when causal) and, with a window,
+    j > p - window or j < sinks. Rows of tokens past q_off[R] are left as they
+    were (undefined in new tensors). ws: a uint8 workspace of
+    fm_attn_paged_workspace_bytes, one for each call that may run at once."""
+    _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a (T, H_q, d) tensor")
+    dev = _serve_args(cache, batch, q=q, o=o, lse=lse, ws=ws)
+    T, Hq, d = q.shape
+    _need(d == cache.c.d, f"q has d={d}, the cache d={cache.c.d}")
+    _need(Hq > 0 and Hq % cache.c.H_kv == 0, f"H_q={Hq} must be a multiple of H_kv={cache.c.H_kv}")
+    qr = _rows(q, "q")
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        orow = fm_rows(o.data_ptr(), Hq * d, d)
+    else:
+        orow = _rows(o, "o", q.shape)
+        _no_overlap("o", o)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _like(lse, "lse", (T, Hq), torch.float32)
+    wsb = fm_attn_paged_workspace_bytes(cache, batch, T, Hq)
+    if ws is None:
+        ws = torch.empty(max(16, wsb), dtype=torch.uint8, device=dev)
+    else:
+        _need(isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.dtype == torch.uint8 and ws.numel() >= wsb,
+              f"ws must be a contiguous uint8 tensor of at least {wsb} bytes")
+    _enqueue("fm_attn_paged", dev, stream, cache.c, batch.c, T, Hq, qr, scale, 1 if causal else 0, window, sinks,
+             orow, lse.data_ptr(), ws.data_ptr(), wsb)
+    return o, lse
+
+
+@dataclass
+class QKNormRope:
+    """Norm and rotation of a flashmask_attention call's queries and keys
+    (the arguments of fm_qk_norm_rope). Gradients reach q_weight and k_weight."""
+    positions: torch.Tensor | None = None
+    inv_freq: torch.Tensor | None = None
+    interleaved: bool = False
+    rot_scale: float = 1.0
+    q_weight: torch.Tensor | None = None
+    k_weight: torch.Tensor | None = None
+    eps: float = 1e-6
+
+
+class _QKNormRopeFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, wq, wk, positions, inv_freq, interleaved, rot_scale, eps):
+        how = dict(interleaved=interleaved, rot_scale=rot_scale, eps=eps)
+        ctx.save_for_backward(q, k, wq, wk, positions, inv_freq)
+        ctx.how = how
+        return fm_qk_norm_rope(q, k, v, positions=positions, inv_freq=inv_freq, q_weight=wq, k_weight=wk, **how)
+
+    @staticmethod
+    def backward(ctx, dqo, dko, dvo):
+        q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
+        grads = fm_qk_norm_rope_bwd(dqo.contiguous(), dko.contiguous(), dvo.contiguous(), q, k, positions=positions,
+                                    inv_freq=inv_freq, q_weight=wq, k_weight=wk, **ctx.how)
+        return (*grads, None, None, None, None, None)
+
+
 class _FlashMaskFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, lts, lte, uts, ute, scale, causal):
@@ -733,7 +1113,15 @@ class _FlashMaskFn(torch.autograd.Function):
         return dq, dk, dv, None, None, None, None, None, None
 
 
-def flashmask_attention(q, k, v, lts, lte, uts, ute, *, causal: bool, scale: float | None = None):
-    """Masked SDPA with the FlashMask column-wise mask; differentiable in q, k, v."""
+def flashmask_attention(q, k, v, lts, lte, uts, ute, *, causal: bool, scale: float | None = None,
+                        qk: QKNormRope | None = None):
+    """Masked SDPA with the FlashMask column-wise mask; differentiable in q, k, v.
+
+    qk: norm and rotate the queries and keys first (fm_qk_norm_rope, in one pass
+    that also lays q, k, v out): q, k, v may then be strided views, e.g. of a fused
+    projection's output, and gradients reach the norms' weights too."""
     scale = q.shape[-1] ** -0.5 if scale is None else scale
+    if qk is not None:
+        q, k, v = _QKNormRopeFn.apply(q, k, v, qk.q_weight, qk.k_weight, qk.positions, qk.inv_freq,
+                                      bool(qk.interleaved), float(qk.rot_scale), float(qk.eps))
     return _FlashMaskFn.apply(q, k, v, lts, lte, uts, ute, float(scale), bool(causal))

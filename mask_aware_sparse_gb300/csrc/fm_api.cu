@@ -95,6 +95,21 @@ bool make_tmap_bhnd_w32(void* out, const void* base, int64_t BH, int64_t N, int6
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_pages(void* out, const void* base, const fm_kv_cache& c, int box_rows, int row_bytes) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const int es = c.k_exp ? 1 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages * c.H_kv};
+  cuuint64_t strides[2] = {(cuuint64_t)c.d * es, (cuuint64_t)c.page_size * c.d * es};
+  cuuint32_t box[3] = {(cuuint32_t)(row_bytes / es), (cuuint32_t)box_rows, 1};
+  cuuint32_t st[3] = {1, 1, 1};
+  CUresult r = fn(static_cast<CUtensorMap*>(out), es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  3, const_cast<void*>(base), dims, strides, box, st, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static std::mutex mu;
   static int cached[64] = {0};

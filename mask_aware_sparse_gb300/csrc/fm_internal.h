@@ -108,6 +108,32 @@ bool make_tmap_f32_bhnd(void* out_tmap /* CUtensorMap* */, const void* base, int
 // columns of a store (rows >= N are not written).
 bool make_tmap_bhnd_w32(void* out_tmap /* CUtensorMap* */, const void* base, int64_t BH, int64_t N, int64_t d);
 
+// 3-D map over a cache's pages (k or v): (n_pages * H_kv, page_size, d), box
+// {row_bytes, box_rows, 1}, swizzle of row_bytes (64 or 128); e4m3 where the
+// cache has exponents.
+bool make_tmap_pages(void* out_tmap /* CUtensorMap* */, const void* base, const fm_kv_cache& c, int box_rows,
+                     int row_bytes);
+
+// Norm and rotation of queries and keys (fm_rope.cu).
+cudaError_t launch_qk_fwd(const fm_qk_problem& P, const fm_view* q, const fm_view* k, const fm_view* v,
+                          const fm_view* qo, const fm_view* ko, const fm_view* vo, cudaStream_t s);
+size_t qk_bwd_ws_bytes(const fm_qk_problem& P);
+cudaError_t launch_qk_bwd(const fm_qk_problem& P, const fm_view* dqo, const fm_view* dko, const fm_view* dvo,
+                          const fm_view* q, const fm_view* k, const fm_view* dq, const fm_view* dk, const fm_view* dv,
+                          void* dwq, void* dwk, void* ws, cudaStream_t s);
+
+// The paged cache, written and read back (fm_cache.cu).
+cudaError_t launch_cache_write(const fm_kv_cache& c, const fm_paged_batch& b, int T, const fm_rows& k,
+                               const fm_rows& v, cudaStream_t s, int* err);
+cudaError_t launch_cache_read(const fm_kv_cache& c, const int32_t* kv_off, const int32_t* table, int R, int width,
+                              int n_rows, void* k, void* v, cudaStream_t s, int* err);
+
+// Attention over the paged cache (fm_paged.cu).
+size_t paged_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_q);
+cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_q, const fm_rows& q,
+                         const fm_rows& o, float* lse, float scale, int causal, int window, int sinks, void* ws,
+                         cudaStream_t st, int* err);
+
 constexpr int kTile = 128;  // attention tile (block_m = block_n)
 
 // Key / value rows of a problem (N_kv = 0 stands for N_kv = N).

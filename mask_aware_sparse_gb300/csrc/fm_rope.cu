@@ -1,0 +1,434 @@
+// fm_rope.cu — per-head norm and position rotation of queries and keys, one
+// pass from a projection's output to the attention kernels' inputs, and its
+// backward pass.
+//
+// Mathematics, per token and head (x: d elements, w: the norm's weights):
+//   r = 1 / sqrt(mean(x^2) + eps),  n = x r w          (n = x without weights)
+//   theta_i = pos f_i,  c_i = s cos theta_i,  s_i = s sin theta_i
+//   (a, b) -> (a c_i - b s_i, a s_i + b c_i)            for pair i < rot / 2
+// with pairs (i, i + rot/2) (half layout) or (2i, 2i + 1) (interleaved); the
+// elements from rot on pass through. Backward, with g the rotation's transpose
+// applied to dy:  dw = sum g x r,  dx = r g w - x r^3 / d sum(g w x).
+// Sums, norms and the rotation are fp32; each output is rounded to bf16 once.
+//
+// What bounds it: memory, one read and one write of every element (backward:
+// dy and x read, dx written). The layout therefore needs no exchange between
+// threads but the norm's sum: d / 16 threads own a head's row, each holding the
+// two 8-element chunks whose elements pair up, so one 16-byte load per chunk,
+// the rotation in registers, one 16-byte store per chunk.
+//
+// Angles: f_i / 2 pi is turned once per block into a 64-bit fraction of a turn;
+// pos times it, modulo 2^64, is the exact fraction of theta (error below
+// |pos| 2^-65 turns, against |pos| 2^-24 for an fp32 product), which
+// sincospif takes. A block computes the angles of its tokens once, in shared
+// memory, for all heads.
+#include <cmath>
+#include <cuda_bf16.h>
+#include "fm_internal.h"
+
+namespace fm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kAll = 0xffffffffu;
+
+struct View {
+  char* p;
+  int64_t sb, sh, sn;  // element strides
+};
+
+struct QkParams {
+  int B, N, H_q, H_kv, rot;
+  int w_f32;
+  float eps, rot_scale;
+  const int32_t* pos;
+  int64_t pos_sb;
+  const float* inv_freq;
+  const void* wq;
+  const void* wk;
+  View q, k, v;     // forward: inputs; backward: gradients of the outputs
+  View xq, xk;      // backward: the forward's inputs (read where normed)
+  View qo, ko, vo;  // forward: outputs; backward: gradients of the inputs
+  int has_v;
+  float* part;  // backward: per-block partial weight gradients, (grid, 2, d)
+};
+
+__device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Where thread c of a row finds its two chunks. Rotated threads of the half
+// layout hold [8c, 8c + 8) and the same of the second half; all others 16
+// consecutive elements. Either way a rotated thread's eight pairs have the
+// frequencies 8c .. 8c + 7.
+template <int D, bool INTER>
+struct Chunks {
+  static constexpr int TG = D / 16;  // threads per row
+  int oa, ob;
+  bool turned;
+  __device__ Chunks(int c, int rot) {
+    turned = 16 * c < rot;
+    oa = (!INTER && turned) ? 8 * c : 16 * c;
+    ob = (!INTER && turned) ? rot / 2 + 8 * c : 16 * c + 8;
+  }
+};
+
+// (a, b) of the eight pairs rotated by +theta (DIR = 1) or -theta (DIR = -1)
+template <bool INTER, int DIR>
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&co)[8], const float (&si)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& x = INTER ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
+    float& y = INTER ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
+    const float s = DIR > 0 ? si[i] : -si[i];
+    const float nx = x * co[i] - y * s, ny = x * s + y * co[i];
+    x = nx;
+    y = ny;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int m = D / 32; m > 0; m >>= 1) v += __shfl_xor_sync(kAll, v, m);
+  return v;
+}
+
+__device__ __forceinline__ float weight_at(const void* w, int f32, int i) {
+  return f32 ? static_cast<const float*>(w)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
+}
+
+// The block's frequencies as fractions of a turn (in units of 2^-64).
+__device__ __forceinline__ void load_fractions(const QkParams& p, unsigned long long* frac) {
+  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
+    double t = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    t -= floor(t);
+    frac[i] = (t < 1.0) ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;  // t < 1: below 2^64
+  }
+}
+
+// cos and sin (times rot_scale) of the block's TB tokens from tok0 on. Slot
+// (pair of frequencies j of thread c): cs[t][j * rot/16 + c] = {cos, sin, cos,
+// sin}, so that the 16-byte reads of neighbouring threads are neighbours.
+__device__ __forceinline__ void load_angles(const QkParams& p, const unsigned long long* frac, float4* cs, int TB,
+                                            int64_t tok0, int64_t total) {
+  const int half = p.rot / 2, RT = p.rot / 16;
+  float2* out = reinterpret_cast<float2*>(cs);
+  for (int i = threadIdx.x; i < TB * half; i += kThreads) {
+    const int t = i / half, f = i - t * half;
+    const int64_t tok = tok0 + t;
+    if (tok >= total) break;
+    const int64_t b = tok / p.N;
+    const int pos = p.pos[b * p.pos_sb + (tok - b * p.N)];
+    const unsigned long long turns = (unsigned long long)(long long)pos * frac[f];
+    float s, c;
+    sincospif((float)(long long)turns * 1.0842021724855044e-19f /* 2^-63 */, &s, &c);
+    const int thr = f >> 3, k = f & 7;
+    out[(t * half) + ((k >> 1) * RT + thr) * 2 + (k & 1)] = make_float2(c * p.rot_scale, s * p.rot_scale);
+  }
+}
+
+__device__ __forceinline__ uint4* at(const View& v, int64_t b, int h, int64_t n, int off) {
+  return reinterpret_cast<uint4*>(v.p + 2 * (b * v.sb + h * v.sh + n * v.sn + off));
+}
+
+// TB tokens per block and step, kWarps / TB warps on each. BWD: the backward.
+template <int D, bool INTER, bool BWD>
+__global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p, const int TB) {
+  using C = Chunks<D, INTER>;
+  constexpr int TG = C::TG, HPW = 32 / TG;  // threads per row, rows per warp
+  __shared__ __align__(16) float4 cs[kWarps * D / 4];  // TB <= kWarps tokens, rot <= D
+  __shared__ unsigned long long frac[D / 2];
+  __shared__ float red[BWD ? kWarps * D : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = lane % TG, hl = lane / TG;
+  const C ch(c, p.rot);
+  const int wpt = kWarps / TB;
+  const int tw = warp / wpt, w0 = warp - tw * wpt;  // this warp's token of the step, its place among the token's warps
+  const int64_t total = (int64_t)p.B * p.N;
+  const int RT = p.rot / 16;
+  float acc[2][BWD ? 16 : 1];  // weight gradients of this thread's 16 columns (q, k)
+  if constexpr (BWD) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
+  }
+  load_fractions(p, frac);
+  __syncthreads();
+  for (int64_t tok0 = (int64_t)blockIdx.x * TB; tok0 < total; tok0 += (int64_t)gridDim.x * TB) {
+    load_angles(p, frac, cs, TB, tok0, total);
+    __syncthreads();
+    const int64_t tok = tok0 + tw;
+    if (tok < total) {
+      const int64_t b = tok / p.N, n = tok - b * p.N;
+      float co[8], si[8];
+      if (ch.turned) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 t = cs[tw * (p.rot / 4) + j * RT + c];
+          co[2 * j] = t.x;
+          si[2 * j] = t.y;
+          co[2 * j + 1] = t.z;
+          si[2 * j + 1] = t.w;
+        }
+      }
+#pragma unroll
+      for (int kind = 0; kind < 3; ++kind) {  // q, k, v
+        if (kind == 2 && !p.has_v) break;
+        const View& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+        const View& out = kind == 0 ? p.qo : kind == 1 ? p.ko : p.vo;
+        const View& src = kind == 0 ? p.xq : p.xk;
+        const int H = kind == 0 ? p.H_q : p.H_kv;
+        const void* wp = kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr;
+        float wa[8], wb[8];
+        if (wp) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            wa[i] = weight_at(wp, p.w_f32, ch.oa + i);
+            wb[i] = weight_at(wp, p.w_f32, ch.ob + i);
+          }
+        }
+        // the next rows' loads are in flight while these are computed (a row is
+        // read and written by the same threads, so in and out may be one tensor)
+        uint4 ra = {}, rb = {}, xa = {}, xb = {};
+        auto fetch = [&](int g) {
+          const int h = g * HPW + hl;
+          if (h < H) {
+            ra = *at(in, b, h, n, ch.oa);
+            rb = *at(in, b, h, n, ch.ob);
+            if (BWD && wp) {
+              xa = *at(src, b, h, n, ch.oa);
+              xb = *at(src, b, h, n, ch.ob);
+            }
+          }
+        };
+        const int groups = (H + HPW - 1) / HPW;
+        fetch(w0);
+        for (int g = w0; g < groups; g += wpt) {
+          const int h = g * HPW + hl;
+          const bool live = h < H;
+          if (kind == 2) {
+            const uint4 ca = ra, cb = rb;
+            if (g + wpt < groups) fetch(g + wpt);
+            if (live) {
+              *at(out, b, h, n, ch.oa) = ca;
+              *at(out, b, h, n, ch.ob) = cb;
+            }
+            continue;
+          }
+          float fa[8], fb[8];
+          unpack8(ra, fa);
+          unpack8(rb, fb);
+          if constexpr (!BWD) {
+            if (g + wpt < groups) fetch(g + wpt);
+            if (wp) {
+              float ss = 0.f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) ss += fa[i] * fa[i] + fb[i] * fb[i];
+              const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                fa[i] = fa[i] * r * wa[i];
+                fb[i] = fb[i] * r * wb[i];
+              }
+            }
+            if (ch.turned) turn<INTER, 1>(fa, fb, co, si);
+          } else {
+            float va[8], vb[8];
+            if (wp) {
+              unpack8(xa, va);
+              unpack8(xb, vb);
+            }
+            if (g + wpt < groups) fetch(g + wpt);
+            if (ch.turned) turn<INTER, -1>(fa, fb, co, si);
+            if (wp) {
+              float ss = 0.f, sg = 0.f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                ss += va[i] * va[i] + vb[i] * vb[i];
+                sg += fa[i] * wa[i] * va[i] + fb[i] * wb[i] * vb[i];
+              }
+              const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
+              const float t = row_sum<D>(sg) * (1.f / D) * r * r * r;
+              if (live) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  acc[kind & 1][i] += fa[i] * va[i] * r;
+                  acc[kind & 1][8 + i] += fb[i] * vb[i] * r;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                fa[i] = r * fa[i] * wa[i] - va[i] * t;
+                fb[i] = r * fb[i] * wb[i] - vb[i] * t;
+              }
+            }
+          }
+          if (live) {
+            *at(out, b, h, n, ch.oa) = pack8(fa);
+            *at(out, b, h, n, ch.ob) = pack8(fb);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if constexpr (BWD) {
+    // one fixed order: lanes of a warp, then warps, then (next kernel) blocks
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      if (!(kind ? p.wk : p.wq)) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float v = acc[kind][i];
+#pragma unroll
+        for (int m = TG; m < 32; m <<= 1) v += __shfl_xor_sync(kAll, v, m);
+        if (hl == 0) red[warp * D + (i < 8 ? ch.oa + i : ch.ob + i - 8)] = v;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < D; i += kThreads) {
+        float v = 0.f;
+        for (int w = 0; w < kWarps; ++w) v += red[w * D + i];
+        p.part[((int64_t)blockIdx.x * 2 + kind) * D + i] = v;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Weight gradients: the blocks' partial sums, 32 columns a block, in one order.
+__global__ void __launch_bounds__(1024) qk_weights_kernel(const float* part, int blocks, int D, void* dwq, void* dwk,
+                                                          int f32) {
+  __shared__ float red[32][33];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+  const int kind = col / D, i = col - kind * D;
+  void* dst = kind ? dwk : dwq;
+  float v = 0.f;
+  if (dst)
+    for (int r = y; r < blocks; r += 32) v += part[((int64_t)r * 2 + kind) * D + i];
+  red[y][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (y == 0 && dst) {
+    v = 0.f;
+    for (int r = 0; r < 32; ++r) v += red[r][threadIdx.x];
+    if (f32)
+      static_cast<float*>(dst)[i] = v;
+    else
+      static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
+  }
+}
+
+View view_of(const fm_view* v) {
+  if (!v) return View{nullptr, 0, 0, 0};
+  return View{static_cast<char*>(v->ptr), v->sb, v->sh, v->sn};
+}
+
+// Tokens per block and step: one warp per token once every SM has work (the
+// angles are then read once per token), more warps per token before that.
+int tokens_per_step(int64_t total) {
+  int tb = 1;
+  while (tb < kWarps && total >= 2ll * tb * 4 * sm_count()) tb *= 2;
+  return tb;
+}
+// The forward keeps eight blocks an SM busy; the backward has a partial row per
+// block, so its grid is what an SM holds at once.
+int grid_blocks(int64_t total, int tb, int per_sm) {
+  const int64_t steps = (total + tb - 1) / tb;
+  const int64_t most = (int64_t)sm_count() * per_sm;
+  return (int)(steps < most ? steps : most);
+}
+constexpr int kBwdPerSm = 3;
+
+template <bool BWD>
+cudaError_t launch_qk(const fm_qk_problem& P, const QkParams& p, int grid, int tb, cudaStream_t s) {
+  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p, tb); };
+  if (P.d == 64)
+    P.interleaved ? go(qk_kernel<64, true, BWD>) : go(qk_kernel<64, false, BWD>);
+  else if (P.d == 128)
+    P.interleaved ? go(qk_kernel<128, true, BWD>) : go(qk_kernel<128, false, BWD>);
+  else
+    P.interleaved ? go(qk_kernel<256, true, BWD>) : go(qk_kernel<256, false, BWD>);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+QkParams params_of(const fm_qk_problem& P) {
+  QkParams p = {};
+  p.B = P.B;
+  p.N = P.N;
+  p.H_q = P.H_q;
+  p.H_kv = P.H_kv;
+  p.rot = P.rot;
+  p.w_f32 = P.w_f32;
+  p.eps = P.eps;
+  p.rot_scale = P.rot_scale;
+  p.pos = P.pos;
+  p.pos_sb = P.pos_sb;
+  p.inv_freq = P.inv_freq;
+  p.wq = P.q_weight;
+  p.wk = P.k_weight;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_qk_fwd(const fm_qk_problem& P, const fm_view* q, const fm_view* k, const fm_view* v,
+                          const fm_view* qo, const fm_view* ko, const fm_view* vo, cudaStream_t s) {
+  QkParams p = params_of(P);
+  p.q = view_of(q);
+  p.k = view_of(k);
+  p.v = view_of(v);
+  p.qo = view_of(qo);
+  p.ko = view_of(ko);
+  p.vo = view_of(vo);
+  p.has_v = v != nullptr;
+  const int64_t total = (int64_t)P.B * P.N;
+  const int tb = tokens_per_step(total);
+  return launch_qk<false>(P, p, grid_blocks(total, tb, 8), tb, s);
+}
+
+size_t qk_bwd_ws_bytes(const fm_qk_problem& P) {
+  const int64_t total = (int64_t)P.B * P.N;
+  return (size_t)grid_blocks(total, tokens_per_step(total), kBwdPerSm) * 2 * P.d * sizeof(float);
+}
+
+cudaError_t launch_qk_bwd(const fm_qk_problem& P, const fm_view* dqo, const fm_view* dko, const fm_view* dvo,
+                          const fm_view* q, const fm_view* k, const fm_view* dq, const fm_view* dk, const fm_view* dv,
+                          void* dwq, void* dwk, void* ws, cudaStream_t s) {
+  QkParams p = params_of(P);
+  p.q = view_of(dqo);
+  p.k = view_of(dko);
+  p.v = view_of(dvo);
+  p.xq = view_of(q);
+  p.xk = view_of(k);
+  p.qo = view_of(dq);
+  p.ko = view_of(dk);
+  p.vo = view_of(dv);
+  p.has_v = dvo != nullptr;
+  p.part = static_cast<float*>(ws);
+  const int64_t total = (int64_t)P.B * P.N;
+  const int tb = tokens_per_step(total);
+  const int grid = grid_blocks(total, tb, kBwdPerSm);
+  cudaError_t e = launch_qk<true>(P, p, grid, tb, s);
+  if (e != cudaSuccess || (!P.q_weight && !P.k_weight)) return e;
+  qk_weights_kernel<<<2 * P.d / 32, 1024, 0, s>>>(p.part, grid, P.d, P.q_weight ? dwq : nullptr,
+                                                  P.k_weight ? dwk : nullptr, P.w_f32);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace fm

@@ -110,6 +110,21 @@ bool make_tmap_pages(void* out, const void* base, const fm_kv_cache& c, int box_
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_tokens(void* out, const fm_rows& q, int T, int H_kv, int G, int d, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  // a dimension of size 1 has any stride
+  const cuuint64_t sh = (cuuint64_t)(H_kv * G > 1 ? q.sh : d) * 2, st = (cuuint64_t)(T > 1 ? q.st : d) * 2;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)H_kv, (cuuint64_t)T};
+  cuuint64_t strides[3] = {sh, sh * G, st};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)box_tokens};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = fn(static_cast<CUtensorMap*>(out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, q.ptr, dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static std::mutex mu;
   static int cached[64] = {0};

@@ -114,6 +114,11 @@ bool make_tmap_bhnd_w32(void* out_tmap /* CUtensorMap* */, const void* base, int
 bool make_tmap_pages(void* out_tmap /* CUtensorMap* */, const void* base, const fm_kv_cache& c, int box_rows,
                      int row_bytes);
 
+// 4-D map over packed tokens' rows (T, H_kv, G, d) of any strides, box {64, G, 1,
+// box_tokens}, 128-byte swizzle: whole tokens of one KV head's group.
+bool make_tmap_tokens(void* out_tmap /* CUtensorMap* */, const fm_rows& q, int T, int H_kv, int G, int d,
+                      int box_tokens);
+
 // Norm and rotation of queries and keys (fm_rope.cu).
 cudaError_t launch_qk_fwd(const fm_qk_problem& P, const fm_view* q, const fm_view* k, const fm_view* v,
                           const fm_view* qo, const fm_view* ko, const fm_view* vo, cudaStream_t s);

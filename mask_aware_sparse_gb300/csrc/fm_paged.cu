@@ -234,19 +234,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -254,50 +244,6 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
-
-// Byte address of 16-byte chunk `chunk` of row `row` inside a swizzled box.
-template <int ROW>
-__device__ __forceinline__ uint32_t in_box(int row, int chunk) {
-  if constexpr (ROW == 128)
-    return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
-  else
-    return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
-}
-
-// e4m3 in the high bytes of two 16-bit lanes -> bf16 pair, times 2^-120
-__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) {
-  return ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
-}
-__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// The bf16 bits of 2^(e - 7) = 2^(e - 127) 2^120, up to e = 134; and of what is
-// left above that, 2^(e - 134). e = 255: NaN.
-__device__ __forceinline__ uint32_t factor_lo(uint32_t e) { return e == 255u ? 0x7fc0u : (min(e, 134u) + 120u) << 7; }
-__device__ __forceinline__ uint32_t factor_hi(uint32_t e) {
-  return (127u + (e > 134u && e < 255u ? e - 134u : 0u)) << 7;
-}
-
-// What the producer keeps of a page table: 32 entries from `base` on, one a lane.
-struct PageWindow {
-  const int32_t* row;
-  int base, held, width;
-  __device__ void reset(const int32_t* table, int r, int w) {
-    row = table + (int64_t)r * w;
-    width = w;
-    base = INT_MIN / 2;
-    held = -1;
-  }
-  // entries [i, i + n), n <= 32, may be asked next
-  __device__ void hold(int i, int n, int lane) {
-    if (i < base || i + n > base + 32) {
-      base = i;
-      held = (i + lane < width) ? row[i + lane] : -1;
-    }
-  }
-};
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
@@ -770,7 +716,20 @@ cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cach
   return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), kFewThreads, C::SMEM, st, tk, tv, p);
 }
 
-PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_q, int causal, int window, int sinks) {
+// Which kernel: chunk_kernel's tiles of 128 rows once the sequences have more
+// than 16 rows a KV head on average (few_kernel would read the keys again for
+// every 16), few_kernel otherwise, and where the other has no form: d = 256,
+// groups of more than 128 heads, queries that are broadcast (a TMA map has no
+// stride of zero).
+bool use_chunk(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_q, const fm_rows* q) {
+  const int G = H_q / c.H_kv;
+  if (c.d == 256 || G > 128) return false;
+  if (q && ((T > 1 && q->st <= 0) || (H_q > 1 && q->sh <= 0))) return false;
+  return (long long)T * G > 16ll * b.R;
+}
+
+PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_q, int causal, int window, int sinks,
+                    bool chunk) {
   PagedShape s = {};
   s.T = T;
   s.R = b.R;
@@ -785,9 +744,9 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   // positions stay below 2^30: larger windows and sinks hide nothing more
   s.window = std::min(window, 1 << 30);
   s.sinks = window > 0 ? std::min(sinks, 1 << 30) : 0;
-  s.step = kFewRows;
-  s.tile = kTileKeys;
-  s.ctas = sm_count() * (c.d == 256 ? 1 : 2);
+  s.step = chunk ? 2 * (128 / s.G) * s.G : kFewRows;
+  s.tile = chunk ? 128 : kTileKeys;
+  s.ctas = sm_count() * (chunk || c.d == 256 ? 1 : 2);
   s.max_units = ((long long)T * s.G + s.step - 1) / s.step + b.R;
   return s;
 }
@@ -795,15 +754,20 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
 }  // namespace
 
 size_t paged_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_q) {
-  const PagedShape s = shape_of(c, b, T, H_q, 1, 0, 0);
-  return paged_work(s, kFewRows, nullptr).bytes;
+  // of either kernel: which one runs goes by the queries' strides too
+  size_t bytes = paged_work(shape_of(c, b, T, H_q, 1, 0, 0, false), kFewRows, nullptr).bytes;
+  if (use_chunk(c, b, T, H_q, nullptr))
+    bytes = std::max(bytes, paged_work(shape_of(c, b, T, H_q, 1, 0, 0, true), kChunkRows, nullptr).bytes);
+  return bytes;
 }
 
 cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_q, const fm_rows& q,
                          const fm_rows& o, float* lse, float scale, int causal, int window, int sinks, void* ws,
                          cudaStream_t st, int* err) {
-  const PagedShape s = shape_of(c, b, T, H_q, causal, window, sinks);
-  const PagedWork w = paged_work(s, kFewRows, ws);
+  const bool chunk = use_chunk(c, b, T, H_q, &q);
+  const int rows = chunk ? kChunkRows : kFewRows;
+  const PagedShape s = shape_of(c, b, T, H_q, causal, window, sinks, chunk);
+  const PagedWork w = paged_work(s, rows, ws);
   const PagedOut out{static_cast<char*>(o.ptr), o.st, o.sh, lse, H_q};
   PlanParams pp{s, b.q_off, b.kv_len, w, err};
   plan_kernel<<<1, kPlanThreads, 0, st>>>(pp);
@@ -811,19 +775,21 @@ cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, i
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const bool f8 = c.k_exp != nullptr;
-  if (c.d == 64) {
+  if (chunk)
+    e = launch_paged_chunk(s, w, c, b, q, out, scale, st, err);
+  else if (c.d == 64)
     e = f8 ? launch_few<64, true>(s, w, c, b, q, out, scale, st, err)
            : launch_few<64, false>(s, w, c, b, q, out, scale, st, err);
-    return e != cudaSuccess ? e : launch_join<64>(s, w, out, kFewRows, st);
-  }
-  if (c.d == 128) {
+  else if (c.d == 128)
     e = f8 ? launch_few<128, true>(s, w, c, b, q, out, scale, st, err)
            : launch_few<128, false>(s, w, c, b, q, out, scale, st, err);
-    return e != cudaSuccess ? e : launch_join<128>(s, w, out, kFewRows, st);
-  }
-  e = f8 ? launch_few<256, true>(s, w, c, b, q, out, scale, st, err)
-         : launch_few<256, false>(s, w, c, b, q, out, scale, st, err);
-  return e != cudaSuccess ? e : launch_join<256>(s, w, out, kFewRows, st);
+  else
+    e = f8 ? launch_few<256, true>(s, w, c, b, q, out, scale, st, err)
+           : launch_few<256, false>(s, w, c, b, q, out, scale, st, err);
+  if (e != cudaSuccess) return e;
+  return c.d == 64    ? launch_join<64>(s, w, out, rows, st)
+         : c.d == 128 ? launch_join<128>(s, w, out, rows, st)
+                      : launch_join<256>(s, w, out, rows, st);
 }
 
 }  // namespace fm

@@ -11,8 +11,10 @@
 // the combining kernel joins the slots of such units in CTA order.
 #pragma once
 #include <atomic>
+#include <climits>
 #include <cstdint>
 #include "fm_internal.h"
+#include "sm100.cuh"
 
 namespace fm {
 
@@ -105,6 +107,60 @@ inline PagedWork paged_work(const PagedShape& s, int rows, void* ws) {
   return w;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// Byte address of 16-byte chunk `chunk` of row `row` inside a swizzled box.
+template <int ROW>
+__device__ __forceinline__ uint32_t in_box(int row, int chunk) {
+  if constexpr (ROW == 128)
+    return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+  else
+    return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
+// e4m3 in the high bytes of two 16-bit lanes -> bf16 pair, times 2^-120
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) {
+  return ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The bf16 bits of 2^(e - 7) = 2^(e - 127) 2^120, up to e = 134; and of what is
+// left above that, 2^(e - 134). e = 255: NaN.
+__device__ __forceinline__ uint32_t factor_lo(uint32_t e) { return e == 255u ? 0x7fc0u : (min(e, 134u) + 120u) << 7; }
+__device__ __forceinline__ uint32_t factor_hi(uint32_t e) {
+  return (127u + (e > 134u && e < 255u ? e - 134u : 0u)) << 7;
+}
+
+// What the producer keeps of a page table: 32 entries from `base` on, one a lane.
+struct PageWindow {
+  const int32_t* row;
+  int base, held, width;
+  __device__ void reset(const int32_t* table, int r, int w) {
+    row = table + (int64_t)r * w;
+    width = w;
+    base = INT_MIN / 2;
+    held = -1;
+  }
+  // entries [i, i + n), n <= 32, may be asked next
+  __device__ void hold(int i, int n, int lane) {
+    if (i < base || i + n > base + 32) {
+      base = i;
+      held = (i + lane < width) ? row[i + lane] : -1;
+    }
+  }
+};
+
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 
@@ -127,6 +183,10 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
   if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
   return e;
 }
+
+constexpr int kChunkRows = 256;  // rows of a chunk_kernel partial slot: two tiles
+cudaError_t launch_paged_chunk(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const fm_paged_batch& b,
+                               const fm_rows& q, const PagedOut& out, float scale, cudaStream_t st, int* err);
 
 // Launch with the programmatic dependency on the kernel before it: the new
 // grid's prologue runs while that kernel ends, and its grid_dependency_wait

@@ -29,7 +29,9 @@ backward calls in one differentiable op).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -762,51 +764,91 @@ def fm_balance_chunks(w, P: int, kappa: int, phases: int = 3, node_budget: int =
 
 
 # ------------------------------------------------ norm, rotation, paged cache
+# These calls are made many times a token, on tensors whose kernels take a few
+# microseconds, so their checks are plain comparisons (messages are built only
+# on failure) and their structures are packed bytes, passed by address.
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_pack_view, _pack_rows = struct.Struct("=Qqqq").pack, struct.Struct("=Qqq").pack  # fm_view, fm_rows
+_pack_qk = struct.Struct("=8i2fQqQQQ").pack  # fm_qk_problem
+_fast = {}
+
+
+def _fast_fn(name):
+    """A library function that takes every pointer as an address or packed bytes."""
+    f = _fast.get(name)
+    if f is None:
+        f = lib()[name]  # a function object of its own
+        res, args = _SIGS[name]
+        simple = (ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float)
+        f.restype, f.argtypes = res, [t if t in simple else _P for t in args]
+        _fast[name] = f
+    return f
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _enqueue(name, dev, stream, *args):
-    """Call a library function whose last argument is the stream: the given one,
-    or the current stream of the tensors' device, with that device current."""
-    if dev.index != torch.cuda.current_device():
+    """Call a library function whose last argument is the stream: the given one, or
+    the current stream of device `dev` (an index), with that device current."""
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors: the library computes on the GPU only")
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _enqueue(name, dev, stream, *args)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    st = getattr(lib(), name)(*args, s.cuda_stream)
+    if stream is not None:
+        s = stream.cuda_stream
+    else:
+        s = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    st = _fast_fn(name)(*args, s)
     if st != FM_OK:
         raise FMError(st, name)
 
 
-def _strides(t, name, dims):
-    """Element strides of all dimensions of t but the last, for a kernel that
-    reads rows in 16-byte pieces (0 for a dimension of size 1)."""
-    _need(isinstance(t, torch.Tensor) and t.dim() == dims, f"{name} must be a torch tensor of {dims} dimensions")
-    _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
-    shape, st = t.shape, t.stride()
-    _need(st[-1] == 1 or shape[-1] == 1, f"{name}: the elements of a row must be contiguous")
-    st = [x if n > 1 else 0 for x, n in zip(st, shape[:-1])]
-    ok = t.data_ptr() & 15 == 0
-    for x in st:
-        ok = ok and x & 7 == 0
-    _need(ok, f"{name}: rows must start on 16-byte boundaries (strides {tuple(t.stride())})")
-    return st
+def _tensor(t, name, dims):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a torch tensor of {dims} dimensions")
 
 
-def _view(t, name, shape=None):
-    sb, sh, sn = _strides(t, name, 4)
-    if shape is not None:
-        _need(t.shape == torch.Size(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return fm_view(t.data_ptr(), sb, sh, sn)
+def _expect(t, name, shape, dtype, dev):
+    """t is a contiguous tensor of this shape, dtype and device."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        _like(t, name, shape, dtype)  # raises, saying which
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the other tensors")
 
 
-def _rows(t, name, shape=None):
-    st, sh = _strides(t, name, 3)
-    if shape is not None:
-        _need(t.shape == torch.Size(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return fm_rows(t.data_ptr(), st, sh)
+def _bf16_rows(t, name, shape, dev):
+    """Address and element strides of a bf16 tensor whose rows (last dimension) are
+    read in 16-byte pieces; 0 for the stride of a dimension of size 1."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != _BF16:
+        _need(isinstance(t, torch.Tensor), f"{name} must be a torch tensor")
+        _need(t.shape == shape, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    at, st, bits = t.data_ptr(), list(t.stride()), 0
+    for i in range(len(st) - 1):
+        if shape[i] == 1:
+            st[i] = 0
+        bits |= st[i]
+    if at & 15 or bits & 7 or st[-1] != 1:
+        raise ValueError(f"{name}: rows must be contiguous and start on 16-byte boundaries (strides {t.stride()})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the other tensors")
+    return at, st
 
 
-def _no_overlap(name, t):
-    """Outputs: no two elements in one place."""
-    for n, s in zip(t.shape, t.stride()):
-        _need(n <= 1 or s != 0, f"{name}: an output cannot be a broadcast view")
+def _view(t, name, shape, dev, out=False):
+    at, (sb, sh, sn, _) = _bf16_rows(t, name, shape, dev)
+    if out and not ((sb or shape[0] <= 1) and (sh or shape[1] <= 1) and (sn or shape[2] <= 1)):
+        raise ValueError(f"{name}: an output cannot be a broadcast view")
+    return _pack_view(at, sb, sh, sn)
+
+
+def _rows(t, name, shape, dev, out=False):
+    at, (st, sh, _) = _bf16_rows(t, name, shape, dev)
+    if out and not ((st or shape[0] <= 1) and (sh or shape[1] <= 1)):
+        raise ValueError(f"{name}: an output cannot be a broadcast view")
+    return _pack_rows(at, st, sh)
 
 
 _ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -825,35 +867,34 @@ def fm_rope_freqs(rot: int, *, base: float = 10000.0, kind: str = "plain", facto
     return torch.from_numpy(f).to("cpu" if device is None else device), sc.value
 
 
-def _qk_args(q, k, v, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps):
-    """The problem of a norm-and-rotation call, its shapes, dtypes and devices checked."""
-    _need(isinstance(q, torch.Tensor) and q.dim() == 4, "q must be a (B, H_q, N, d) tensor")
-    _need(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be a (B, H_kv, N, d) tensor")
+def _qk_args(q, k, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps):
+    """The packed problem of a norm-and-rotation call, its shapes, dtypes and devices checked."""
+    _tensor(q, "q", 4)
+    _tensor(k, "k", 4)
     B, Hq, N, d = q.shape
-    Hkv = k.shape[1]
-    _need(k.shape == torch.Size((B, Hkv, N, d)), f"k has shape {tuple(k.shape)}, expected (B={B}, H_kv, N={N}, d={d})")
-    p = fm_qk_problem(B, N, Hq, Hkv, d, 0, 1 if interleaved else 0, 0, eps, rot_scale)
+    Hkv, dev = k.shape[1], q.get_device()
+    if k.shape != (B, Hkv, N, d):
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected (B={B}, H_kv, N={N}, d={d})")
+    rot = pos = sb = fr = f32 = 0
     if inv_freq is not None:
-        _need(isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1, "inv_freq must be a (rot / 2,) tensor")
-        _like(inv_freq, "inv_freq", inv_freq.shape, torch.float32)
-        _need(isinstance(positions, torch.Tensor), "positions must be a (N,) or (B, N) int32 tensor")
-        _need(positions.shape in (torch.Size((N,)), torch.Size((B, N))),
-              f"positions has shape {tuple(positions.shape)}, expected (N={N},) or (B={B}, N={N})")
-        _like(positions, "positions", positions.shape, torch.int32)
-        p.rot, p.pos, p.inv_freq = 2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr()
-        p.pos_sb = N if positions.dim() == 2 else 0
-    wt = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        _need(isinstance(w, torch.Tensor) and w.dtype in (torch.float32, torch.bfloat16),
-              f"{name} must be a float32 or bfloat16 tensor")
-        _like(w, name, (d,), w.dtype)
-        _need(wt in (None, w.dtype), "q_weight and k_weight must have one dtype")
-        wt = w.dtype
-        p.w_f32 = 1 if wt == torch.float32 else 0
-        setattr(p, name, w.data_ptr())
-    return p
+        _tensor(inv_freq, "inv_freq", 1)
+        _expect(inv_freq, "inv_freq", inv_freq.shape, _F32, dev)
+        if not isinstance(positions, torch.Tensor) or positions.shape not in ((N,), (B, N)):
+            raise ValueError(f"positions must be an int32 tensor of shape (N={N},) or (B={B}, N={N})")
+        _expect(positions, "positions", positions.shape, _I32, dev)
+        rot, pos, fr = 2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr()
+        sb = N if positions.dim() == 2 else 0
+    w = [0, 0]
+    for i, t in enumerate((q_weight, k_weight)):
+        if t is not None:
+            name = "k_weight" if i else "q_weight"
+            if not isinstance(t, torch.Tensor) or t.dtype not in (_F32, _BF16):
+                raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
+            _expect(t, name, (d,), t.dtype, dev)
+            w[i], f32 = t.data_ptr(), 1 if t.dtype == _F32 else 0
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    return _pack_qk(B, N, Hq, Hkv, d, rot, 1 if interleaved else 0, f32, eps, rot_scale, pos, sb, fr, *w), dev
 
 
 def fm_qk_norm_rope(q, k, v=None, *, positions=None, inv_freq=None, interleaved: bool = False, rot_scale: float = 1.0,
@@ -864,23 +905,29 @@ def fm_qk_norm_rope(q, k, v=None, *, positions=None, inv_freq=None, interleaved:
     or into the tensors `out` (views of any strides; an input itself is allowed).
     positions: int32 (N,) or (B, N); inv_freq: fp32 (rot / 2,), None: no rotation;
     q_weight / k_weight: (d,), None: no norm."""
-    p = _qk_args(q, k, v, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps)
-    ins = (q, k) if v is None else (q, k, v)
+    p, dev = _qk_args(q, k, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps)
+    qs, ks = q.shape, k.shape
+    qi, ki = _view(q, "q", qs, dev), _view(k, "k", ks, dev)
+    vi = None if v is None else _view(v, "v", ks, dev)
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor: the library computes on the GPU only")
     if out is None:
-        out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in ins)
-    _need(len(out) == len(ins), "out must hold one tensor per input")
-    names = ("q", "k", "v")
-    iv = [_view(t, n, k.shape if n == "v" else None) for t, n in zip(ins, names)]
-    ov = [_view(t, "output " + n, s.shape) for t, n, s in zip(out, names, ins)]
-    for t, n in zip(out, names):
-        _no_overlap("output " + n, t)
-    _same_cuda(q=q, k=k, v=v, positions=None if inv_freq is None else positions, inv_freq=inv_freq,
-               q_weight=q_weight, k_weight=k_weight, **{f"output {i}": t for i, t in enumerate(out)})
-    if v is None:
-        iv.append(None)
-        ov.append(None)
-    _enqueue("fm_qk_norm_rope", q.device, stream, p, *iv, *ov)
+        on = q.device
+        out = (torch.empty(qs, dtype=_BF16, device=on), torch.empty(ks, dtype=_BF16, device=on))
+        if v is not None:
+            out += (torch.empty(ks, dtype=_BF16, device=on),)
+    elif len(out) != (2 if v is None else 3):
+        raise ValueError("out must hold one tensor per input")
+    _enqueue("fm_qk_norm_rope", dev, stream, p, qi, ki, vi, _view(out[0], "output q", qs, dev, True),
+             _view(out[1], "output k", ks, dev, True), None if v is None else _view(out[2], "output v", ks, dev, True))
     return tuple(out)
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_bwd_bytes(dev, B, N, d):
+    """Workspace of a backward pass with normed sides (it goes by sizes alone)."""
+    with torch.cuda.device(dev):
+        return lib().fm_qk_norm_rope_bwd_workspace_bytes(fm_qk_problem(B, N, 1, 1, d, q_weight=16, k_weight=16))
 
 
 def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, interleaved: bool = False,
@@ -890,33 +937,29 @@ def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, i
     outputs and its inputs q, k give (dq, dk, dv, dq_weight, dk_weight); None
     where there is no such input. dq, dk, dv are (B, H, N, d) views of contiguous
     (B, N, H, d) tensors (a projection's own layout), or the views `out` (dq, dk[, dv])."""
-    p = _qk_args(q, k, dvo, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps)
-    gs = (dqo, dko) if dvo is None else (dqo, dko, dvo)
-    shapes = (q.shape, k.shape, k.shape)
+    p, dev = _qk_args(q, k, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps)
+    qs, ks = q.shape, k.shape
+    gq, gk = _view(dqo, "dqo", qs, dev), _view(dko, "dko", ks, dev)
+    gv = None if dvo is None else _view(dvo, "dvo", ks, dev)
+    qi, ki = _view(q, "q", qs, dev), _view(k, "k", ks, dev)
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor: the library computes on the GPU only")
+    on = q.device
     if out is None:
-        out = tuple(torch.empty((s[0], s[2], s[1], s[3]), dtype=torch.bfloat16, device=q.device).transpose(1, 2)
-                    for s in shapes[:len(gs)])
-    _need(len(out) == len(gs), "out must hold one tensor per gradient")
-    names = ("dq", "dk", "dv")
-    gv = [_view(t, n + "o", s) for t, n, s in zip(gs, names, shapes)]
-    ov = [_view(t, "output " + n, s) for t, n, s in zip(out, names, shapes)]
-    for t, n in zip(out, names):
-        _no_overlap("output " + n, t)
-    qv, kv = _view(q, "q"), _view(k, "k")
-    _same_cuda(dqo=dqo, dko=dko, dvo=dvo, q=q, k=k, positions=None if inv_freq is None else positions,
-               inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight,
-               **{f"output {i}": t for i, t in enumerate(out)})
-    if dvo is None:
-        gv.append(None)
-        ov.append(None)
+        out = tuple(torch.empty((s[0], s[2], s[1], s[3]), dtype=_BF16, device=on).transpose(1, 2)
+                    for s in ((qs, ks) if dvo is None else (qs, ks, ks)))
+    elif len(out) != (2 if dvo is None else 3):
+        raise ValueError("out must hold one tensor per gradient")
     dwq = None if q_weight is None else torch.empty_like(q_weight)
     dwk = None if k_weight is None else torch.empty_like(k_weight)
     ws, wsb = None, 0
     if dwq is not None or dwk is not None:
-        with torch.cuda.device(q.device):
-            wsb = lib().fm_qk_norm_rope_bwd_workspace_bytes(p)
-        ws = torch.empty(max(1, wsb), dtype=torch.uint8, device=q.device)
-    _enqueue("fm_qk_norm_rope_bwd", q.device, stream, p, *gv, qv, kv, *ov, _ptr(dwq), _ptr(dwk), _ptr(ws), wsb)
+        wsb = _qk_bwd_bytes(dev, qs[0], qs[2], qs[3])
+        ws = torch.empty(max(16, wsb), dtype=_U8, device=on)
+    _enqueue("fm_qk_norm_rope_bwd", dev, stream, p, gq, gk, gv, qi, ki, _view(out[0], "output dq", qs, dev, True),
+             _view(out[1], "output dk", ks, dev, True), None if dvo is None else _view(out[2], "output dv", ks, dev, True),
+             None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
+             None if ws is None else ws.data_ptr(), wsb)
     return out[0], out[1], (out[2] if dvo is not None else None), dwq, dwk
 
 
@@ -925,7 +968,7 @@ class KVCache:
     exponent bytes k_exp, v_exp (n_pages, H_kv, page_size) uint8 (value = stored *
     2^(exponent - 127)). Checked once; holds the tensors it was given."""
 
-    __slots__ = ("k", "v", "k_exp", "v_exp", "device", "c")
+    __slots__ = ("k", "v", "k_exp", "v_exp", "n_pages", "H_kv", "page_size", "d", "device", "index", "c", "at")
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
         _need(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be (n_pages, H_kv, page_size, d)")
@@ -943,9 +986,11 @@ class KVCache:
         for name, t in (("k", k), ("v", v), ("k_exp", k_exp), ("v_exp", v_exp)):
             _need(t is None or t.data_ptr() & 15 == 0, f"{name} must start on a 16-byte boundary")
         _same_cuda(k=k, v=v, k_exp=k_exp, v_exp=v_exp)
-        self.k, self.v, self.k_exp, self.v_exp, self.device = k, v, k_exp, v_exp, k.device
+        self.k, self.v, self.k_exp, self.v_exp, self.device, self.index = k, v, k_exp, v_exp, k.device, k.get_device()
+        self.n_pages, self.H_kv, self.page_size, self.d = n, h, page, d
         self.c = fm_kv_cache(k.data_ptr(), v.data_ptr(), 0 if k_exp is None else k_exp.data_ptr(),
                              0 if v_exp is None else v_exp.data_ptr(), n, h, page, d)
+        self.at = ctypes.addressof(self.c)
 
 
 def fm_cache_new(n_pages: int, H_kv: int, page_size: int, d: int, *, dtype=torch.bfloat16, device="cuda") -> KVCache:
@@ -965,7 +1010,7 @@ class PagedBatch:
     included), page_table (R, width) page of each page_size keys. Checked once; the
     tensors' values may change between calls (their addresses may not)."""
 
-    __slots__ = ("q_off", "kv_len", "page_table", "device", "c")
+    __slots__ = ("q_off", "kv_len", "page_table", "R", "width", "index", "c", "at")
 
     def __init__(self, q_off, kv_len, page_table):
         _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, "page_table must be (R, width)")
@@ -975,60 +1020,69 @@ class PagedBatch:
         _like(q_off, "q_off", (R + 1,), torch.int32)
         _like(kv_len, "kv_len", (R,), torch.int32)
         _same_cuda(q_off=q_off, kv_len=kv_len, page_table=page_table)
-        self.q_off, self.kv_len, self.page_table, self.device = q_off, kv_len, page_table, q_off.device
+        self.q_off, self.kv_len, self.page_table, self.index = q_off, kv_len, page_table, q_off.get_device()
+        self.R, self.width = R, width
         self.c = fm_paged_batch(q_off.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), R, width)
+        self.at = ctypes.addressof(self.c)
 
 
-def _serve_args(cache, batch, **ts):
-    _need(isinstance(cache, KVCache), "cache must be a KVCache")
-    dev = cache.device
-    if batch is not None:
-        _need(isinstance(batch, PagedBatch), "batch must be a PagedBatch")
-        _need(batch.device == dev, f"the batch is on {batch.device}, the cache on {dev}")
-    for name, t in ts.items():
-        _need(t is None or t.device == dev, f"{name} is on {t.device if t is not None else None}, the cache on {dev}")
-    return dev
+def _serve_args(cache, batch):
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    if not isinstance(batch, PagedBatch):
+        raise ValueError("batch must be a PagedBatch")
+    if batch.index != cache.index:
+        raise ValueError("the batch is on another device than the cache")
+    return cache.index
 
 
 def fm_cache_write(k, v, cache: KVCache, batch: PagedBatch, stream=None):
     """Put the rows of T new tokens, k and v (T, H_kv, d) bf16 views, in their places
     in the cache (rounded to e4m3 with a scale a row where the cache is e4m3)."""
-    _need(isinstance(k, torch.Tensor) and k.dim() == 3, "k must be a (T, H_kv, d) tensor")
-    _need(isinstance(cache, KVCache), "cache must be a KVCache")
-    shape = (k.shape[0], cache.c.H_kv, cache.c.d)
-    kr, vr = _rows(k, "k", shape), _rows(v, "v", shape)
-    dev = _serve_args(cache, batch, k=k, v=v)
-    _enqueue("fm_cache_write", dev, stream, cache.c, batch.c, shape[0], kr, vr)
+    dev = _serve_args(cache, batch)
+    _tensor(k, "k", 3)
+    shape = (k.shape[0], cache.H_kv, cache.d)
+    kr, vr = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
+    _enqueue("fm_cache_write", dev, stream, cache.at, batch.at, shape[0], kr, vr)
 
 
 def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=None, stream=None):
     """Keys and values as packed bf16 rows (1, H_kv, n_rows, d): sequence r's keys from 0
     on become rows [kv_off[r], kv_off[r + 1]). kv_off (R + 1,) and page_table (R, width)
     int32. Rows that no sequence has are left as they were (undefined in new tensors)."""
-    dev = _serve_args(cache, None)
-    _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2 and page_table.numel() > 0,
-          "page_table must be (R, width)")
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    dev = cache.index
+    _tensor(page_table, "page_table", 2)
     R, width = page_table.shape
-    _like(page_table, "page_table", (R, width), torch.int32)
-    _like(kv_off, "kv_off", (R + 1,), torch.int32)
-    shape = (1, cache.c.H_kv, int(n_rows), cache.c.d)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    _like(k, "k", shape, torch.bfloat16)
-    _like(v, "v", shape, torch.bfloat16)
-    _same_cuda(cache=cache.k, kv_off=kv_off, page_table=page_table, k=k, v=v)
-    _enqueue("fm_cache_read", dev, stream, cache.c, kv_off.data_ptr(), page_table.data_ptr(), R, width, shape[2],
+    _expect(page_table, "page_table", (R, width), _I32, dev)
+    _expect(kv_off, "kv_off", (R + 1,), _I32, dev)
+    shape = (1, cache.H_kv, int(n_rows), cache.d)
+    if k is None:
+        k = torch.empty(shape, dtype=_BF16, device=cache.device)
+    else:
+        _expect(k, "k", shape, _BF16, dev)
+    if v is None:
+        v = torch.empty(shape, dtype=_BF16, device=cache.device)
+    else:
+        _expect(v, "v", shape, _BF16, dev)
+    _enqueue("fm_cache_read", dev, stream, cache.at, kv_off.data_ptr(), page_table.data_ptr(), R, width, shape[2],
              k.data_ptr(), v.data_ptr())
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
+def _paged_bytes(dev, T, Hq, R, width, n_pages, H_kv, page, d, f8):
+    """Workspace of an attention call (it goes by sizes alone; the addresses only have to be set)."""
+    c = fm_kv_cache(16, 16, 16 if f8 else 0, 16 if f8 else 0, n_pages, H_kv, page, d)
+    with torch.cuda.device(dev):
+        return lib().fm_attn_paged_workspace_bytes(c, fm_paged_batch(16, 16, 16, R, width), T, Hq)
+
+
 def fm_attn_paged_workspace_bytes(cache: KVCache, batch: PagedBatch, T: int, H_q: int) -> int:
     """Bytes of workspace an fm_attn_paged call of these shapes needs."""
-    dev = _serve_args(cache, batch)
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return lib().fm_attn_paged_workspace_bytes(cache.c, batch.c, T, H_q)
-    return lib().fm_attn_paged_workspace_bytes(cache.c, batch.c, T, H_q)
+    return _paged_bytes(_serve_args(cache, batch), T, H_q, batch.R, batch.width, cache.n_pages, cache.H_kv,
+                        cache.page_size, cache.d, cache.k_exp is not None)
 
 
 def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal: bool = True, window: int = 0,
@@ -1039,29 +1093,30 @@ def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal:
     j > p - window or j < sinks. Rows of tokens past q_off[R] are left as they
     were (undefined in new tensors). ws: a uint8 workspace of
     fm_attn_paged_workspace_bytes, one for each call that may run at once."""
-    _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a (T, H_q, d) tensor")
-    dev = _serve_args(cache, batch, q=q, o=o, lse=lse, ws=ws)
-    T, Hq, d = q.shape
-    _need(d == cache.c.d, f"q has d={d}, the cache d={cache.c.d}")
-    _need(Hq > 0 and Hq % cache.c.H_kv == 0, f"H_q={Hq} must be a multiple of H_kv={cache.c.H_kv}")
-    qr = _rows(q, "q")
+    dev = _serve_args(cache, batch)
+    _tensor(q, "q", 3)
+    T, Hq, d = shape = q.shape
+    if d != cache.d:
+        raise ValueError(f"q has d={d}, the cache d={cache.d}")
+    if Hq <= 0 or Hq % cache.H_kv:
+        raise ValueError(f"H_q={Hq} must be a multiple of H_kv={cache.H_kv}")
+    qr = _rows(q, "q", shape, dev)
     if o is None:
-        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-        orow = fm_rows(o.data_ptr(), Hq * d, d)
+        o = torch.empty(shape, dtype=_BF16, device=cache.device)
+        orow = _pack_rows(o.data_ptr(), Hq * d, d)
     else:
-        orow = _rows(o, "o", q.shape)
-        _no_overlap("o", o)
+        orow = _rows(o, "o", shape, dev, True)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, Hq), dtype=_F32, device=cache.device)
     else:
-        _like(lse, "lse", (T, Hq), torch.float32)
+        _expect(lse, "lse", (T, Hq), _F32, dev)
     wsb = fm_attn_paged_workspace_bytes(cache, batch, T, Hq)
     if ws is None:
-        ws = torch.empty(max(16, wsb), dtype=torch.uint8, device=dev)
-    else:
-        _need(isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.dtype == torch.uint8 and ws.numel() >= wsb,
-              f"ws must be a contiguous uint8 tensor of at least {wsb} bytes")
-    _enqueue("fm_attn_paged", dev, stream, cache.c, batch.c, T, Hq, qr, scale, 1 if causal else 0, window, sinks,
+        ws = torch.empty(max(16, wsb), dtype=_U8, device=cache.device)
+    elif (not isinstance(ws, torch.Tensor) or not ws.is_contiguous() or ws.dtype != _U8 or ws.numel() < wsb
+          or ws.get_device() != dev):
+        raise ValueError(f"ws must be a contiguous uint8 tensor of at least {wsb} bytes on the cache's device")
+    _enqueue("fm_attn_paged", dev, stream, cache.at, batch.at, T, Hq, qr, scale, 1 if causal else 0, window, sinks,
              orow, lse.data_ptr(), ws.data_ptr(), wsb)
     return o, lse
 

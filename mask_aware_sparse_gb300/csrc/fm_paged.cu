@@ -20,13 +20,18 @@
 // left), so P's rounding adds nothing to O's own; the products are a small part
 // of the time either way.
 //
-// e4m3 caches: a row's values times its power-of-two scale are exact in bf16
-// (a multiply of the e4m3 bits, moved into bf16's exponent field, by 2^(e - 7),
-// which also normalises e4m3's subnormals), so the kernel computes exactly what
-// it would on the cache read back.
+// e4m3 caches: e4m3 is exact in fp16, one conversion for two values, so the
+// products run in fp16 on the stored values and the rows' power-of-two scales
+// stay outside: a key's on its score, a value's in its weight, 2^(score +
+// exponent - mo) with a running maximum mo of its own, so that the weight of
+// the largest summand is near 1 whatever the rows' scales are. One fp16 term
+// (2^-12 of a weight; weights below 2^-14 of the largest are off by 2^-25 of it
+// at most) is finer than bf16's 2^-9. Measured at 32 sequences of 4K to 16K keys, 32 / 8 heads, d = 128: 258 us
+// with the values widened to bf16 by integer operations (867 instructions for 16 keys).
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include "fm_internal.h"
@@ -234,6 +239,35 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four e4m3 values as two fp16 pairs (exact)
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+// 2^(e - 127), NaN for e = 255
+__device__ __forceinline__ float scale_of(uint32_t e) {
+  return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -360,7 +394,32 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
           }
       }
       const int plo = u.pos + u.g0 / G, phi = u.pos + (u.g0 + u.nrows - 1) / G;  // the unit's first and last position
+      float sc[2] = {sl2, sl2};  // per row: scores to log2 units
+      if constexpr (F8) {
+        // Q in fp16, each row times the power of two that puts its largest value at
+        // the top of fp16's range: values down to 2^-29 of it keep all their bits
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < C::KSTEPS; ++k)
+            top = __vmaxu2(top, __vmaxu2(qf[k][i] & 0x7fff7fffu, qf[k][2 + i] & 0x7fff7fffu));
+          top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 1));
+          top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 2));
+          const int E = (int)(max(top & 0xffffu, top >> 16) >> 7);
+          // 2^(142 - E), kept finite; a row of zeros, infinities or NaN stays as it is
+          const int up = (E == 0 || E == 255) ? 0 : min(142 - E, 126);
+          const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+          sc[i] = sl2 * __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+          for (int k = 0; k < C::KSTEPS; ++k)
+#pragma unroll
+            for (int x = i; x < 4; x += 2)
+              qf[k][x] = pack_f16x2(__uint_as_float(qf[k][x] << 16) * f, __uint_as_float(qf[k][x] & 0xffff0000u) * f);
+        }
+      }
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float mo[2] = {-INFINITY, -INFINITY};  // e4m3: the running maximum of score + exponent of the value's scale
       float o[D / 8][4];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -378,14 +437,6 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
           for (int n = 0; n < 2; ++n) {
             s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
             const int row = warp * 16 + 8 * n + g;
-            uint32_t fl = 0, fh = 0;
-            bool two = false;
-            if constexpr (F8) {
-              const uint32_t e = lds8(eb + 8 * n + g);
-              fl = factor_lo(e) * 0x10001u;
-              fh = factor_hi(e) * 0x10001u;
-              two = __any_sync(kAll, e > 134u && e < 255u);
-            }
 #pragma unroll
             for (int b = 0; b < C::BOXES; ++b)
 #pragma unroll
@@ -396,13 +447,9 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
                   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                   for (int x = 0; x < 4; ++x) {
-                    uint32_t b0 = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x1404)), fl);
-                    uint32_t b1 = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x3424)), fl);
-                    if (two) {
-                      b0 = mul_bf2(b0, fh);
-                      b1 = mul_bf2(b1, fh);
-                    }
-                    mma16816(s[n], qf[k + x], b0, b1);
+                    uint32_t b0, b1;
+                    e4m3_to_f16(w[x], b0, b1);
+                    mma16816_f16(s[n], qf[k + x], b0, b1);
                   }
                 } else {
                   mma16816(s[n], qf[k], v.x, v.y);
@@ -410,13 +457,32 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
                 }
               }
           }
+          float ve[2][2];  // e4m3: the exponents of the values' scales
+          if constexpr (F8) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint32_t ek = lds16(eb + 8 * n + 2 * t), ev = lds16(eb + kTileKeys + 8 * n + 2 * t);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float f = scale_of((ek >> (8 * x)) & 255u);
+                s[n][x] *= f * sc[0];
+                s[n][2 + x] *= f * sc[1];
+                const uint32_t e = (ev >> (8 * x)) & 255u;
+                ve[n][x] = e == 255u ? NAN : (float)((int)e - 127);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) s[n][x] *= sl2;
+          }
           // masked scores: a tile whose 16 keys all rows see is left as it is
-          uint32_t vz[2] = {0xffffffffu, 0xffffffffu};
           const bool part = key0 + 16 > u.hi || (p.s.causal && key0 + 15 > plo) ||
                             (p.s.window > 0 && key0 <= phi - p.s.window);
           if (part) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int key = key0 + 8 * n + 2 * t + (x & 1), ps = pos[x >> 1];
@@ -424,32 +490,38 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
                                  (p.s.window == 0 || key > ps - p.s.window || key < p.s.sinks);
                 s[n][x] = see ? s[n][x] : -INFINITY;
               }
-              // values of keys no row sees (past the sequence's end: anything may lie there) count as zero
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int key = key0 + 8 * n + 2 * t + x;
-                if (!(key < u.hi && (key >= u.lo || key < p.s.sinks))) vz[n] &= x ? 0x0000ffffu : 0xffff0000u;
-              }
-            }
           }
+          // a running maximum moves only when it is passed by more than 8 (weights stay below 2^8)
           float f[2];
           bool moved = false;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float x = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 2)) * sl2;
-            // m moves only when it is passed by more than 8 (P stays below 2^8)
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 2));
             f[i] = 1.f;
             if (x > m[i] + 8.f) {
-              f[i] = ex2_approx(m[i] - x);
+              const float y = ex2_approx(m[i] - x);
+              l[i] *= y;
               m[i] = x;
-              moved = true;
+              if (!F8) {
+                f[i] = y;
+                moved = true;
+              }
+            }
+            if constexpr (F8) {
+              float z = fmaxf(fmaxf(s[0][2 * i] + ve[0][0], s[0][2 * i + 1] + ve[0][1]),
+                              fmaxf(s[1][2 * i] + ve[1][0], s[1][2 * i + 1] + ve[1][1]));
+              z = fmaxf(z, __shfl_xor_sync(kAll, z, 1));
+              z = fmaxf(z, __shfl_xor_sync(kAll, z, 2));
+              if (z > mo[i] + 8.f) {
+                f[i] = ex2_approx(mo[i] - z);
+                mo[i] = z;
+                moved = true;
+              }
             }
           }
           if (__any_sync(kAll, moved)) {
-            l[0] *= f[0];
-            l[1] *= f[1];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
               o[i][0] *= f[0];
@@ -458,65 +530,74 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
               o[i][3] *= f[1];
             }
           }
+          // weights: bf16 in two terms (p and what its rounding left), fp16 in one
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float base = m[i] == -INFINITY ? 0.f : m[i];
-              const float a = ex2_approx(fmaf(s[n][2 * i], sl2, -base)), b = ex2_approx(fmaf(s[n][2 * i + 1], sl2, -base));
+              const float a = ex2_approx(s[n][2 * i] - base), b = ex2_approx(s[n][2 * i + 1] - base);
               l[i] += a + b;
-              const uint32_t h = pack_bf16x2(a, b);
-              hi[2 * n + i] = h;
-              lo[2 * n + i] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-            }
-          if constexpr (F8) {
-            uint32_t fl[2], fh[2];
-            bool two = false;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t ea = lds8(eb + kTileKeys + 8 * n + 2 * t), ez = lds8(eb + kTileKeys + 8 * n + 2 * t + 1);
-              fl[n] = factor_lo(ea) | factor_lo(ez) << 16;
-              fh[n] = factor_hi(ea) | factor_hi(ez) << 16;
-              two |= (ea > 134u && ea < 255u) || (ez > 134u && ez < 255u);
-            }
-            two = __any_sync(kAll, two);
-            const int r0 = warp * 16 + 2 * t;
-#pragma unroll
-            for (int cg = 0; cg < D / 32; ++cg) {
-              // four columns 32 cg + 4 g + i of keys 2t, 2t + 1, 2t + 8, 2t + 9
-              const int box = cg / (C::ROW / 32), ch = (cg % (C::ROW / 32)) * 2 + (g >> 2);
-              uint32_t w[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = lds32(vb + box * C::BOX + in_box<C::ROW>(r0 + (x & 1) + 8 * (x >> 1), ch) + 4 * (g & 3));
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t sel = 0x4000u + 0x1111u * i;
-                uint32_t b0 = mul_bf2(e4m3_bits(__byte_perm(w[0], w[1], sel)), fl[0]);
-                uint32_t b1 = mul_bf2(e4m3_bits(__byte_perm(w[2], w[3], sel)), fl[1]);
-                if (two) {
-                  b0 = mul_bf2(b0, fh[0]);
-                  b1 = mul_bf2(b1, fh[1]);
-                }
-                b0 &= vz[0];
-                b1 &= vz[1];
-                mma16816(o[4 * cg + i], hi, b0, b1);
-                mma16816(o[4 * cg + i], lo, b0, b1);
+              if constexpr (F8) {
+                const float bo = mo[i] == -INFINITY ? 0.f : mo[i];
+                // a masked score stays masked whatever its key's exponent byte holds
+                const float x = s[n][2 * i] == -INFINITY ? 0.f : ex2_approx(s[n][2 * i] + (ve[n][0] - bo));
+                const float y = s[n][2 * i + 1] == -INFINITY ? 0.f : ex2_approx(s[n][2 * i + 1] + (ve[n][1] - bo));
+                hi[2 * n + i] = pack_f16x2(x, y);
+              } else {
+                const uint32_t h = pack_bf16x2(a, b);
+                hi[2 * n + i] = h;
+                lo[2 * n + i] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
               }
             }
-          } else {
+          auto product = [&](auto masked) {
+            // values of keys no row sees (past the sequence's end: anything may lie there) count as zero
+            uint32_t vz[2] = {0xffffffffu, 0xffffffffu};
+            if constexpr (masked.value) {
 #pragma unroll
-            for (int c = 0; c < D / 8; c += 2) {
-              uint32_t r[4];
-              const int ch = c + (lane >> 4);
-              ldmatrix4_trans(vb + (ch >> 3) * C::BOX + in_box<128>(warp * 16 + (lane & 15), ch & 7), r);
-              mma16816(o[c], hi, r[0] & vz[0], r[1] & vz[1]);
-              mma16816(o[c], lo, r[0] & vz[0], r[1] & vz[1]);
-              mma16816(o[c + 1], hi, r[2] & vz[0], r[3] & vz[1]);
-              mma16816(o[c + 1], lo, r[2] & vz[0], r[3] & vz[1]);
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int key = key0 + 8 * n + 2 * t + x;
+                  if (!(key < u.hi && (key >= u.lo || key < p.s.sinks))) vz[n] &= x ? 0x0000ffffu : 0xffff0000u;
+                }
             }
-          }
+            if constexpr (F8) {
+              const int r0 = warp * 16 + 2 * t;
+#pragma unroll
+              for (int cg = 0; cg < D / 32; ++cg) {
+                // four columns 32 cg + 4 g + i of keys 2t, 2t + 1, 2t + 8, 2t + 9
+                const int box = cg / (C::ROW / 32), ch = (cg % (C::ROW / 32)) * 2 + (g >> 2);
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  w[x] = lds32(vb + box * C::BOX + in_box<C::ROW>(r0 + (x & 1) + 8 * (x >> 1), ch) + 4 * (g & 3));
+                uint32_t b0[4], b1[4];
+                e4m3_to_f16(__byte_perm(w[0], w[1], 0x5140), b0[0], b0[1]);
+                e4m3_to_f16(__byte_perm(w[0], w[1], 0x7362), b0[2], b0[3]);
+                e4m3_to_f16(__byte_perm(w[2], w[3], 0x5140), b1[0], b1[1]);
+                e4m3_to_f16(__byte_perm(w[2], w[3], 0x7362), b1[2], b1[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma16816_f16(o[4 * cg + i], hi, b0[i] & vz[0], b1[i] & vz[1]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 8; c += 2) {
+                uint32_t r[4];
+                const int ch = c + (lane >> 4);
+                ldmatrix4_trans(vb + (ch >> 3) * C::BOX + in_box<128>(warp * 16 + (lane & 15), ch & 7), r);
+                mma16816(o[c], hi, r[0] & vz[0], r[1] & vz[1]);
+                mma16816(o[c + 1], hi, r[2] & vz[0], r[3] & vz[1]);
+                mma16816(o[c], lo, r[0] & vz[0], r[1] & vz[1]);
+                mma16816(o[c + 1], lo, r[2] & vz[0], r[3] & vz[1]);
+              }
+            }
+          };
+          if (part)
+            product(std::true_type{});
+          else
+            product(std::false_type{});
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&empty[stage]);
@@ -525,6 +606,15 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
       // join the four warps' (m, l, O): a common maximum, then the sums in warp order
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        if constexpr (F8) {
+          // O in units of l's: 2^mo of its scores-and-exponents to 2^m of the scores
+          const float y = m[i] == -INFINITY ? 0.f : ex2_approx(mo[i] - m[i]);
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) {
+            o[x][2 * i] *= y;
+            o[x][2 * i + 1] *= y;
+          }
+        }
         l[i] += __shfl_xor_sync(kAll, l[i], 1);
         l[i] += __shfl_xor_sync(kAll, l[i], 2);
         if (t == 0) {

@@ -10,12 +10,17 @@
 // few_kernel, one unit = 16 query rows of a KV head (a token's query heads of
 // the group, then the next token's): bound by memory, each key and value byte
 // is read once for all query heads of its group and 16 rows cost few
-// operations, so the design is about loads in flight. A producer warp brings
-// tiles of 64 keys in by TMA, page by page, into a ring of 96 KB a CTA (two
-// CTAs an SM, 192 KB in flight an SM); four warps take 16 keys of a tile each,
-// so every byte in shared memory is read once, and keep their own running
-// (m, l, O) in registers (m16n8k16 products), joined at a segment's end. The
-// tensor-memory path has nothing to offer here: its smallest tile is 64 rows.
+// operations, so the design is about loads in flight. Each of a CTA's four warps
+// takes a quarter of the segment's key tiles (32 keys) and brings them in itself,
+// 16 bytes a lane and copy, into a ring of its own (keys and values as entries of
+// their own; 96 KB a CTA, two CTAs an SM), with its own running (m, l, O) in
+// registers (m16n8k16 products): every byte in shared memory is read once, and
+// no warp waits for another before a segment's end, where the four are joined.
+// Measured against TMA boxes issued by a producer warp (e4m3, pages of 64, loads
+// alone, nothing computed): boxes of 32 rows and the exponents' own bulk copies
+// reach 3.9 TB/s; the copies also cost the same for pages of any size, and fill
+// with zeros where a page ends. The tensor-memory path has nothing to offer
+// here: its smallest tile is 64 rows.
 // P goes into the second product as two bf16 terms (p and what its rounding
 // left), so P's rounding adds nothing to O's own; the products are a small part
 // of the time either way.
@@ -169,11 +174,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   const long long total = carry;
   if (tid == 0) p.w.sum[units] = total;
   __syncthreads();
-  // each CTA's range: [c total / ctas, (c + 1) total / ctas)
+  // the first `used` CTAs have ranges, [c total / used, (c + 1) total / used): all
+  // of them, or as many as get s.least tiles each
+  const long long used = max(1ll, min((long long)s.ctas, total / s.least));
   for (int c = tid; c < s.ctas; c += kPlanThreads) {
-    const long long f = total * c / s.ctas, g = total * (c + 1) / s.ctas;
-    PagedStart st = {0, 0, 0, (int)(g - f)};
-    if (st.count > 0) {
+    PagedStart st = {};
+    if (c < used && total > 0) {
+      const long long f = total * c / used;
+      st.count = (int)(total * (c + 1) / used - f);
       int lo = 0, hi = units - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -187,6 +195,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       st.u = lo;
       st.h = (int)(rem / nt);
       st.kt = (int)(rem - (long long)st.h * nt);
+      // the CTA of tile x is the last c with c total / used <= x
+      const long long f0 = f - st.kt;
+      st.first = (int)(((f0 + 1) * used - 1) / total);
+      st.last = (int)(((f0 + nt) * used - 1) / total);
     }
     p.w.starts[c] = st;
   }
@@ -194,30 +206,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 }
 
 // -------------------------------------------------------------- few query rows
-constexpr int kFewThreads = 160;  // four computing warps and the producer
+constexpr int kFewWarps = 4;
+constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRows = 16;
-constexpr int kTileKeys = 64;
+constexpr int kTileKeys = 32;
 
 template <int D, bool F8>
 struct FewCfg {
   static constexpr int ES = F8 ? 1 : 2;
-  static constexpr int ROW = D * ES < 128 ? D * ES : 128;  // bytes of a row inside a box
-  static constexpr int BOXES = D * ES / ROW;
+  static constexpr int RB = D * ES;                  // bytes of a row
+  static constexpr int ROW = RB < 128 ? RB : 128;    // of them in one swizzled box
+  static constexpr int BOXES = RB / ROW;
   static constexpr int BOX = kTileKeys * ROW;
-  static constexpr int TILE = BOXES * BOX;  // K or V of one stage
-  static constexpr int EXP = F8 ? 2 * kTileKeys : 0;
-  static constexpr int STAGE = 2 * TILE + 0;
-  static constexpr int STAGES = D == 256 ? (F8 ? 6 : 3) : D == 128 ? (F8 ? 6 : 3) : (F8 ? 8 : 6);
+  static constexpr int TILE = BOXES * BOX;           // one ring entry: a tile's keys, or its values
+  static constexpr int EXP = F8 ? kTileKeys : 0;
   static constexpr int PER_SM = D == 256 ? 1 : 2;
-  static constexpr int MERGE_OFF = STAGES * STAGE;
+  static constexpr int RING = D == 64 ? (F8 ? 8 : 6) : (F8 ? 6 : 3);  // entries of a warp's ring
+  static constexpr int ENTRIES = kFewWarps * RING;
+  static constexpr int MERGE_OFF = ENTRIES * TILE;
   static constexpr int EXP_OFF = MERGE_OFF + kFewRows * D * 4;
-  static constexpr int BAR_OFF = EXP_OFF + STAGES * EXP;
-  static constexpr int ML_OFF = BAR_OFF + 2 * STAGES * 8;
-  static constexpr int BYTES = ML_OFF + 4 * kFewRows * 2 * 4 + 16;
-  static constexpr int SMEM = BYTES + 1024;
+  static constexpr int ML_OFF = EXP_OFF + ENTRIES * EXP;
+  static constexpr int SMEM = ML_OFF + kFewWarps * kFewRows * 2 * 4 + 1024;
   static constexpr int KSTEPS = D / 16;
-  static constexpr int CHUNKS = ROW / 64;         // 16-byte chunks a thread reads of a box's row
-  static constexpr int SPC = F8 ? 4 : 2;          // k-steps of a chunk
+  static constexpr int CHUNKS = ROW / 64;  // 16-byte chunks a thread reads of a box's row
+  static constexpr int SPC = F8 ? 4 : 2;   // k-steps of a chunk
+  // loading: CPR lanes a row, RPI rows an instruction
+  static constexpr int CPR = RB / 16, RPI = 32 / CPR, LOADS = kTileKeys / RPI;
 };
 
 struct FewParams {
@@ -226,12 +240,23 @@ struct FewParams {
   const char* q;
   int64_t q_st, q_sh;
   PagedOut out;
-  const uint8_t* k_exp;
-  const uint8_t* v_exp;
+  const char* kv[2];
+  const uint8_t* exps[2];
   const int32_t* table;
   float scale_log2;
   int* err;
 };
+
+// 16 bytes from global to shared memory without a register between; zeros where !live
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -268,9 +293,9 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
 __device__ __forceinline__ float scale_of(uint32_t e) {
   return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -280,92 +305,83 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
-    few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel(const FewParams p) {
   using C = FewCfg<D, F8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  uint64_t* empty = full + C::STAGES;
   float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::ML_OFF + 4 * kFewRows * 2 * 4);
+  float* merge = reinterpret_cast<float*>(smem + C::MERGE_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  FM_DEBUG_BEGIN();
-  if (threadIdx.x == 0) {
-    *abort_flag = timeout_pending(p.err) ? 1 : 0;
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 4);
-    }
-    fence_mbar_init();
-  }
-  if (warp == 4 && lane == 0) {
-    tma_prefetch_desc(&tk);
-    tma_prefetch_desc(&tv);
-  }
-  __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
   const PagedStart st = p.w.starts[blockIdx.x];
-  const int G = p.s.G;
-  bool ok = *abort_flag == 0;
+  const int G = p.s.G, P = p.s.page;
   PagedWalk walk(p.w.units, st, p.s.H_kv);
-  uint32_t it = 0;  // tiles so far
+  const int g = lane >> 2, t = lane & 3;
+  const float sl2 = p.scale_log2;
+  const uint32_t ring = smem_u32(smem) + warp * C::RING * C::TILE;
+  const uint32_t ring_exp = smem_u32(smem + C::EXP_OFF) + warp * C::RING * C::EXP;
+  // this thread's place in a tile. Keys: row 8 n + g, chunk CHUNKS t; swizzled, so
+  // that chunk + c is an exclusive or of c
+  const uint32_t k_at = in_box<C::ROW>(g, C::CHUNKS * t);
+  // values, bf16: row lane % 16 of 16 keys, chunk lane / 16; e4m3: keys 2 t and
+  // 2 t + 1, 8 bytes from column 8 g on
+  const uint32_t v_at0 = F8 ? in_box<C::ROW>(2 * t, g >> 1) + 8 * (g & 1) : in_box<C::ROW>(lane & 15, lane >> 4);
+  const uint32_t v_at1 = F8 ? in_box<C::ROW>(2 * t + 1, g >> 1) + 8 * (g & 1) : 0u;
+  // loading: row lane / CPR of RPI rows, chunk lane % CPR
+  const int l_row = lane / C::CPR, l_chunk = lane % C::CPR;
+  const uint32_t l_at = (l_chunk * 16 / C::ROW) * C::BOX + in_box<C::ROW>(l_row, l_chunk % (C::ROW / 16));
+  PageWindow pages;
 
-  if (warp == 4) {
-    // ------------------------------------------------------------- producer
-    const int P = p.s.page, rows = min(P, kTileKeys), per = kTileKeys / rows;  // box rows, boxes along the keys
-    const int zmax = p.s.n_pages * p.s.H_kv;
-    PageWindow pages;
-    for (; walk.more() && ok; walk.next()) {
+  for (; walk.more(); walk.next()) {
       const PagedUnit& u = walk.u;
+      // the warp's tiles of the segment: [j0, j0 + nt), its entries 0 .. 2 nt - 1
+      // (keys and values in turn), RING of them in the ring or on their way
+      const int j0 = walk.n * warp / kFewWarps, nt = walk.n * (warp + 1) / kFewWarps - j0;
       pages.reset(p.table, u.r, p.s.width);
-      for (int j = 0; j < walk.n && ok; ++j, ++it) {
-        const int key0 = tile_of(u, walk.kt + j) * kTileKeys;
-        const int pg0 = key0 / P;
-        pages.hold(pg0, per, lane);
-        const int stage = it % C::STAGES;
-        ok = __all_sync(kAll, mbar_wait(&empty[stage], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, p.err));
-        if (!ok) break;
-        // boxes whose first key is held: the rest of the tile is never read
-        const int boxes = min(per, (u.kv_len - key0 + rows - 1) / rows);
-        if (lane == 0) mbar_arrive_expect_tx(&full[stage], boxes * rows * (2 * D * C::ES + (F8 ? 2 : 0)));
-        __syncwarp();
-        constexpr int OPS = 2 * C::BOXES + (F8 ? 2 : 0);  // copies of one page's part
-        for (int i0 = 0; i0 < boxes * OPS; i0 += 32) {
-          const int i = i0 + lane;
-          const int b = min(i / OPS, boxes - 1), op = i % OPS;
-          const int pg = __shfl_sync(kAll, pages.held, pg0 + b - pages.base);
-          if (i >= boxes * OPS) continue;
-          const bool good = pg >= 0 && pg < p.s.n_pages;
-          if (!good) record_error(p.err, FM_DEV_ERR_RANGE);
-          const int z = good ? pg * p.s.H_kv + walk.h : zmax;  // zmax: out of range, reads as zero
-          const int y = key0 - pg0 * P;
-          uint8_t* at = smem + stage * C::STAGE + b * rows * C::ROW;
-          if (op < 2 * C::BOXES) {
-            const int v = op >= C::BOXES, x = op - v * C::BOXES;
-            tma_load_3d(at + v * C::TILE + x * C::BOX, v ? &tv : &tk, &full[stage], x * (C::ROW / C::ES), y, z);
-          } else {
-            const int v = op - 2 * C::BOXES;
-            bulk_load(smem + C::EXP_OFF + stage * C::EXP + v * kTileKeys + b * rows,
-                      (v ? p.v_exp : p.k_exp) + (int64_t)(good ? z : walk.h) * P + y, rows, &full[stage]);
+      int64_t src_a = 0, src_b = 0;  // rows of the cache: the tile's first 16 (or all) keys, its last 16
+      bool bad_a = false, bad_b = false;
+      auto issue = [&](int e, int slot) {
+        if (e < 2 * nt) {
+          const int key0 = tile_of(u, walk.kt + j0 + (e >> 1)) * kTileKeys;
+          const int which = e & 1;
+          if (which == 0) {
+            const int pg0 = key0 / P, per = P < kTileKeys ? 2 : 1;
+            pages.hold(pg0, per, lane);
+            const int a = __shfl_sync(kAll, pages.held, pg0 - pages.base);
+            const int b = __shfl_sync(kAll, pages.held, pg0 + per - 1 - pages.base);
+            const bool two = per == 2 && key0 + 16 < u.kv_len;  // the second page holds keys
+            bad_a = a < 0 || a >= p.s.n_pages;
+            bad_b = per == 2 ? !two || b < 0 || b >= p.s.n_pages : bad_a;
+            if (bad_a || (two && bad_b)) record_error(p.err, FM_DEV_ERR_RANGE);
+            src_a = ((int64_t)(bad_a ? 0 : a) * p.s.H_kv + walk.h) * P + (key0 - pg0 * P);
+            src_b = per == 2 ? ((int64_t)(bad_b ? 0 : b) * p.s.H_kv + walk.h) * P : src_a + 16;
           }
+          // keys that no row of the unit sees (past the sequence's end: anything may lie there) become zeros
+          const bool edge = key0 + kTileKeys > u.hi || (p.s.window > 0 && key0 < u.lo) || bad_a || bad_b;
+          const char* base = p.kv[which] + l_chunk * 16;
+          const uint32_t dst = ring + slot * C::TILE + l_at;
+          const char* from_a = base + (src_a + l_row) * C::RB;
+          const char* from_b = base + (src_b + l_row) * C::RB;
+#pragma unroll
+          for (int i = 0; i < C::LOADS; ++i) {
+            const int r0 = i * C::RPI;
+            const char* from = r0 < 16 ? from_a + r0 * C::RB : from_b + (r0 - 16) * C::RB;
+            bool live = true;
+            if (edge) {
+              const int key = key0 + r0 + l_row;
+              live = key < u.hi && (key >= u.lo || key < p.s.sinks) && !(r0 < 16 ? bad_a : bad_b);
+            }
+            const uint32_t x = C::ROW == 128 ? (uint32_t)((r0 & 7) << 4) : (uint32_t)(((r0 >> 1) & 3) << 4);
+            copy16((dst ^ x) + r0 * C::ROW, from, live);
+          }
+          if (F8 && lane < 2)
+            copy16(ring_exp + slot * C::EXP + 16 * lane, p.exps[which] + (lane ? src_b : src_a), !(lane ? bad_b : bad_a));
         }
-      }
-    }
-    if (!ok) {
-      // leave with no copy in flight: every stage handed out has landed, or a second bound passed
-      volatile int none = 0;
-      for (uint32_t s = it > C::STAGES ? it - C::STAGES : 0; s < it; ++s)
-        mbar_wait(&full[s % C::STAGES], (s / C::STAGES) & 1u, &none, p.err);
-    }
-  } else {
-    // ------------------------------------------------------------ computing
-    const int g = lane >> 2, t = lane & 3;
-    float* merge = reinterpret_cast<float*>(smem + C::MERGE_OFF);
-    const float sl2 = p.scale_log2;
-    for (; walk.more(); walk.next()) {
-      const PagedUnit& u = walk.u;
+        copy_commit();
+      };
+#pragma unroll 1
+      for (int e = 0; e < C::RING; ++e) issue(e, e);
       // this thread's rows g and g + 8: their positions (-1: no such row), their Q
       int pos[2];
       uint32_t qf[C::KSTEPS][4];
@@ -384,7 +400,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
 #pragma unroll
             for (int x4 = 0; x4 < C::SPC / 2; ++x4) {
               uint4 v = make_uint4(0, 0, 0, 0);
-              if (live && ok && walk.n > 0) v = *reinterpret_cast<const uint4*>(src + 2 * (e0 + 8 * x4));
+              if (live && walk.n > 0) v = *reinterpret_cast<const uint4*>(src + 2 * (e0 + 8 * x4));
               const int k = (b * C::CHUNKS + c) * C::SPC + 2 * x4;
               qf[k][i] = v.x;
               qf[k][2 + i] = v.y;
@@ -424,24 +440,26 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-      for (int j = 0; j < walk.n; ++j, ++it) {
-        const int stage = it % C::STAGES;
-        if (ok) ok = __all_sync(kAll, mbar_wait(&full[stage], (it / C::STAGES) & 1u, abort_flag, p.err));
-        const int key0 = tile_of(u, walk.kt + j) * kTileKeys + warp * 16;
-        // keys of this warp that some row sees: below hi, and from lo on or sinks
-        if (ok && key0 < u.hi && (key0 + 16 > u.lo || key0 < p.s.sinks)) {
-          const uint32_t kb = smem_u32(smem + stage * C::STAGE), vb = kb + C::TILE;
-          const uint32_t eb = smem_u32(smem + C::EXP_OFF + stage * C::EXP) + warp * 16;
-          float s[2][4];
+      int slot = 0;  // of the next entry
+      for (int j = 0; j < nt; ++j) {
+        const int key0 = tile_of(u, walk.kt + j0 + j) * kTileKeys;
+        const int sk = slot, sv = slot + 1 == C::RING ? 0 : slot + 1;
+        slot = sv + 1 == C::RING ? 0 : sv + 1;
+        copy_wait<C::RING - 1>();
+        __syncwarp();
+        float s[4][4];
+        float ve[4][2];  // e4m3: the exponents of the values' scales
+        {
+          const uint32_t kb = ring + sk * C::TILE + k_at;
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-            const int row = warp * 16 + 8 * n + g;
+          for (int n = 0; n < 4; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-            for (int b = 0; b < C::BOXES; ++b)
+          for (int b = 0; b < C::BOXES; ++b)
 #pragma unroll
-              for (int c = 0; c < C::CHUNKS; ++c) {
-                const uint4 v = lds128(kb + b * C::BOX + in_box<C::ROW>(row, C::CHUNKS * t + c));
+            for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                const uint4 v = lds128((kb ^ (16 * c)) + b * C::BOX + n * 8 * C::ROW);
                 const int k = (b * C::CHUNKS + c) * C::SPC;
                 if constexpr (F8) {
                   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -456,33 +474,46 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
                   mma16816(s[n], qf[k + 1], v.z, v.w);
                 }
               }
-          }
-          float ve[2][2];  // e4m3: the exponents of the values' scales
           if constexpr (F8) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t ek = lds16(eb + 8 * n + 2 * t), ev = lds16(eb + kTileKeys + 8 * n + 2 * t);
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t ek = lds16(ring_exp + sk * C::EXP + 8 * n + 2 * t);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const float f = scale_of((ek >> (8 * x)) & 255u);
                 s[n][x] *= f * sc[0];
                 s[n][2 + x] *= f * sc[1];
-                const uint32_t e = (ev >> (8 * x)) & 255u;
-                ve[n][x] = e == 255u ? NAN : (float)((int)e - 127);
               }
             }
           } else {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
               for (int x = 0; x < 4; ++x) s[n][x] *= sl2;
           }
-          // masked scores: a tile whose 16 keys all rows see is left as it is
-          const bool part = key0 + 16 > u.hi || (p.s.causal && key0 + 15 > plo) ||
+        }
+        __syncwarp();
+        issue(2 * j + C::RING, sk);
+        copy_wait<C::RING - 1>();
+        __syncwarp();
+        {
+          if constexpr (F8) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t ev = lds16(ring_exp + sv * C::EXP + 8 * n + 2 * t);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t y = (ev >> (8 * x)) & 255u;
+                ve[n][x] = y == 255u ? NAN : (float)((int)y - 127);
+              }
+            }
+          }
+          // masked scores: a tile whose keys all rows see is left as it is
+          const bool part = key0 + kTileKeys > u.hi || (p.s.causal && key0 + kTileKeys - 1 > plo) ||
                             (p.s.window > 0 && key0 <= phi - p.s.window);
           if (part) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int key = key0 + 8 * n + 2 * t + (x & 1), ps = pos[x >> 1];
@@ -496,9 +527,16 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
           bool moved = false;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+            float x = -INFINITY, z = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              x = max3f(x, s[n][2 * i], s[n][2 * i + 1]);
+              if constexpr (F8) z = max3f(z, s[n][2 * i] + ve[n][0], s[n][2 * i + 1] + ve[n][1]);
+            }
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
+            if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 1));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 2));
+            if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 2));
             f[i] = 1.f;
             if (x > m[i] + 8.f) {
               const float y = ex2_approx(m[i] - x);
@@ -509,16 +547,10 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
                 moved = true;
               }
             }
-            if constexpr (F8) {
-              float z = fmaxf(fmaxf(s[0][2 * i] + ve[0][0], s[0][2 * i + 1] + ve[0][1]),
-                              fmaxf(s[1][2 * i] + ve[1][0], s[1][2 * i + 1] + ve[1][1]));
-              z = fmaxf(z, __shfl_xor_sync(kAll, z, 1));
-              z = fmaxf(z, __shfl_xor_sync(kAll, z, 2));
-              if (z > mo[i] + 8.f) {
-                f[i] = ex2_approx(mo[i] - z);
-                mo[i] = z;
-                moved = true;
-              }
+            if (F8 && z > mo[i] + 8.f) {
+              f[i] = ex2_approx(mo[i] - z);
+              mo[i] = z;
+              moved = true;
             }
           }
           if (__any_sync(kAll, moved)) {
@@ -531,9 +563,9 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
             }
           }
           // weights: bf16 in two terms (p and what its rounding left), fp16 in one
-          uint32_t hi[4], lo[4];
+          uint32_t hi[2][4], lo[2][4];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float base = m[i] == -INFINITY ? 0.f : m[i];
@@ -544,64 +576,55 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
                 // a masked score stays masked whatever its key's exponent byte holds
                 const float x = s[n][2 * i] == -INFINITY ? 0.f : ex2_approx(s[n][2 * i] + (ve[n][0] - bo));
                 const float y = s[n][2 * i + 1] == -INFINITY ? 0.f : ex2_approx(s[n][2 * i + 1] + (ve[n][1] - bo));
-                hi[2 * n + i] = pack_f16x2(x, y);
+                hi[n >> 1][2 * (n & 1) + i] = pack_f16x2(x, y);
               } else {
                 const uint32_t h = pack_bf16x2(a, b);
-                hi[2 * n + i] = h;
-                lo[2 * n + i] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+                hi[n >> 1][2 * (n & 1) + i] = h;
+                lo[n >> 1][2 * (n & 1) + i] =
+                    pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
               }
             }
-          auto product = [&](auto masked) {
-            // values of keys no row sees (past the sequence's end: anything may lie there) count as zero
-            uint32_t vz[2] = {0xffffffffu, 0xffffffffu};
-            if constexpr (masked.value) {
+          const uint32_t vb0 = ring + sv * C::TILE + v_at0, vb1 = ring + sv * C::TILE + v_at1;
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
+          for (int kk = 0; kk < 2; ++kk) {  // 16 keys each
+              const uint32_t at = 16 * kk * C::ROW;
+              if constexpr (F8) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const int key = key0 + 8 * n + 2 * t + x;
-                  if (!(key < u.hi && (key >= u.lo || key < p.s.sinks))) vz[n] &= x ? 0x0000ffffu : 0xffff0000u;
+                for (int cg = 0; cg < D / 64; ++cg) {
+                  // eight columns 64 cg + 8 g + i of keys 2t, 2t + 1, 2t + 8, 2t + 9
+                  const uint32_t box = (cg * 64 / C::ROW) * C::BOX + at, x64 = cg * 64 % C::ROW;
+                  const uint2 w0 = lds64((vb0 ^ x64) + box), w1 = lds64((vb1 ^ x64) + box);
+                  const uint2 w2 = lds64((vb0 ^ x64) + box + 8 * C::ROW), w3 = lds64((vb1 ^ x64) + box + 8 * C::ROW);
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t a0 = h ? w0.y : w0.x, a1 = h ? w1.y : w1.x, a2 = h ? w2.y : w2.x, a3 = h ? w3.y : w3.x;
+                    uint32_t b0[4], b1[4];
+                    e4m3_to_f16(__byte_perm(a0, a1, 0x5140), b0[0], b0[1]);
+                    e4m3_to_f16(__byte_perm(a0, a1, 0x7362), b0[2], b0[3]);
+                    e4m3_to_f16(__byte_perm(a2, a3, 0x5140), b1[0], b1[1]);
+                    e4m3_to_f16(__byte_perm(a2, a3, 0x7362), b1[2], b1[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      mma16816_f16(o[8 * cg + 4 * h + i], hi[kk], b0[i], b1[i]);
+                  }
                 }
-            }
-            if constexpr (F8) {
-              const int r0 = warp * 16 + 2 * t;
+              } else {
 #pragma unroll
-              for (int cg = 0; cg < D / 32; ++cg) {
-                // four columns 32 cg + 4 g + i of keys 2t, 2t + 1, 2t + 8, 2t + 9
-                const int box = cg / (C::ROW / 32), ch = (cg % (C::ROW / 32)) * 2 + (g >> 2);
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  w[x] = lds32(vb + box * C::BOX + in_box<C::ROW>(r0 + (x & 1) + 8 * (x >> 1), ch) + 4 * (g & 3));
-                uint32_t b0[4], b1[4];
-                e4m3_to_f16(__byte_perm(w[0], w[1], 0x5140), b0[0], b0[1]);
-                e4m3_to_f16(__byte_perm(w[0], w[1], 0x7362), b0[2], b0[3]);
-                e4m3_to_f16(__byte_perm(w[2], w[3], 0x5140), b1[0], b1[1]);
-                e4m3_to_f16(__byte_perm(w[2], w[3], 0x7362), b1[2], b1[3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mma16816_f16(o[4 * cg + i], hi, b0[i] & vz[0], b1[i] & vz[1]);
+                for (int c = 0; c < D / 8; c += 2) {
+                  uint32_t r[4];
+                  ldmatrix4_trans((vb0 ^ (16 * (c & 7))) + (c >> 3) * C::BOX + at, r);
+                  mma16816(o[c], hi[kk], r[0], r[1]);
+                  mma16816(o[c + 1], hi[kk], r[2], r[3]);
+                  mma16816(o[c], lo[kk], r[0], r[1]);
+                  mma16816(o[c + 1], lo[kk], r[2], r[3]);
+                }
               }
-            } else {
-#pragma unroll
-              for (int c = 0; c < D / 8; c += 2) {
-                uint32_t r[4];
-                const int ch = c + (lane >> 4);
-                ldmatrix4_trans(vb + (ch >> 3) * C::BOX + in_box<128>(warp * 16 + (lane & 15), ch & 7), r);
-                mma16816(o[c], hi, r[0] & vz[0], r[1] & vz[1]);
-                mma16816(o[c + 1], hi, r[2] & vz[0], r[3] & vz[1]);
-                mma16816(o[c], lo, r[0] & vz[0], r[1] & vz[1]);
-                mma16816(o[c + 1], lo, r[2] & vz[0], r[3] & vz[1]);
-              }
-            }
-          };
-          if (part)
-            product(std::true_type{});
-          else
-            product(std::false_type{});
+          }
         }
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&empty[stage]);
+        issue(2 * j + 1 + C::RING, sv);
       }
+      copy_wait<0>();
 
       // join the four warps' (m, l, O): a common maximum, then the sums in warp order
 #pragma unroll
@@ -622,15 +645,15 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
           ml[(warp * kFewRows + g + 8 * i) * 2 + 1] = l[i];
         }
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 32 * kFewWarps);
       float top[2], sum[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         top[i] = -INFINITY;
-        for (int w = 0; w < 4; ++w) top[i] = fmaxf(top[i], ml[(w * kFewRows + g + 8 * i) * 2]);
+        for (int w = 0; w < kFewWarps; ++w) top[i] = fmaxf(top[i], ml[(w * kFewRows + g + 8 * i) * 2]);
         sum[i] = 0.f;
         const float base = top[i] == -INFINITY ? 0.f : top[i];
-        for (int w = 0; w < 4; ++w)
+        for (int w = 0; w < kFewWarps; ++w)
           sum[i] += ex2_approx(ml[(w * kFewRows + g + 8 * i) * 2] - base) * ml[(w * kFewRows + g + 8 * i) * 2 + 1];
         const float f = ex2_approx(m[i] - base);
 #pragma unroll
@@ -639,7 +662,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
           o[x][2 * i + 1] *= f;
         }
       }
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kFewWarps; ++w) {
         if (warp == w) {
 #pragma unroll
           for (int x = 0; x < D / 8; ++x) {
@@ -651,12 +674,12 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
               o[x][2] += v.z;
               o[x][3] += v.w;
             }
-            if (w < 3) *at = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
+            if (w < kFewWarps - 1) *at = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
           }
         }
-        named_bar_sync(1, 128);
+        named_bar_sync(1, 32 * kFewWarps);
       }
-      if (warp == 3 && ok) {
+      if (warp == kFewWarps - 1) {
         const bool whole = walk.whole();
         float* part = p.w.part + p.w.part_floats * (2 * (size_t)blockIdx.x + walk.slot());
 #pragma unroll
@@ -669,16 +692,17 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
             const float inv = sum[i] > 0.f ? 1.f / sum[i] : (sum[i] == 0.f ? 0.f : sum[i]);
             char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
             if constexpr (F8) {
+              // columns 64 cg + 16 t + 8 y + (0 .. 7)
 #pragma unroll
-              for (int cg = 0; cg < D / 32; ++cg) {
-                uint32_t v[4];
+              for (int cg = 0; cg < D / 64; ++cg)
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < 2; ++y) {
+                  uint32_t v[4];
 #pragma unroll
-                  for (int z = 0; z < 2; ++z)
-                    v[2 * y + z] = pack_bf16x2(o[4 * cg + 2 * z][2 * i + y] * inv, o[4 * cg + 2 * z + 1][2 * i + y] * inv);
-                *reinterpret_cast<uint4*>(dst + 2 * (32 * cg + 8 * t)) = make_uint4(v[0], v[1], v[2], v[3]);
-              }
+                  for (int z = 0; z < 4; ++z)
+                    v[z] = pack_bf16x2(o[8 * cg + 2 * z][2 * i + y] * inv, o[8 * cg + 2 * z + 1][2 * i + y] * inv);
+                  *reinterpret_cast<uint4*>(dst + 2 * (64 * cg + 16 * t + 8 * y)) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
             } else {
 #pragma unroll
               for (int c = 0; c < D / 8; ++c)
@@ -691,12 +715,14 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
             float* dst = part + (size_t)row * D;
             if constexpr (F8) {
 #pragma unroll
-              for (int cg = 0; cg < D / 32; ++cg)
+              for (int cg = 0; cg < D / 64; ++cg)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                  *reinterpret_cast<float4*>(dst + 32 * cg + 8 * t + 4 * y) =
-                      make_float4(o[4 * cg][2 * i + y], o[4 * cg + 1][2 * i + y], o[4 * cg + 2][2 * i + y],
-                                  o[4 * cg + 3][2 * i + y]);
+#pragma unroll
+                  for (int z = 0; z < 2; ++z)
+                    *reinterpret_cast<float4*>(dst + 64 * cg + 16 * t + 8 * y + 4 * z) =
+                        make_float4(o[8 * cg + 4 * z][2 * i + y], o[8 * cg + 4 * z + 1][2 * i + y],
+                                    o[8 * cg + 4 * z + 2][2 * i + y], o[8 * cg + 4 * z + 3][2 * i + y]);
             } else {
 #pragma unroll
               for (int c = 0; c < D / 8; ++c)
@@ -710,9 +736,6 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM)
         }
       }
     }
-  }
-  __syncthreads();
-  FM_DEBUG_END(p.err);
 }
 
 // ------------------------------------------------------------------- joining
@@ -722,50 +745,59 @@ struct JoinParams {
   int ctas, G, rows;  // rows of a slot
 };
 
-// Block (c, y): if CTA c's range begins inside a unit that no earlier CTA's
-// range begins inside of, the unit's pieces are joined, 8 rows a block.
+// Block (c, y): where CTA c's range is the second one inside a unit and head,
+// their parts (CTA c - 1's last segment, then c .. last's first segments) are
+// joined, 8 rows a block, a row a warp. Parts are weighed 32 at a time (a lane
+// each), then read one after the other with their loads in flight together.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   grid_dependency_wait();
   const int c = blockIdx.x + 1;
   const PagedStart st = p.w.starts[c];
-  if (st.count <= 0 || st.kt == 0) return;
-  // the CTA before it that has work holds the piece before this one
-  int b = c - 1;
-  while (b > 0 && p.w.starts[b].count <= 0) --b;
-  const PagedStart before = p.w.starts[b];
-  if (before.u == st.u && before.h == st.h && before.kt > 0) return;
+  if (st.count <= 0 || st.kt == 0 || st.first != c - 1) return;
   const PagedUnit u = p.w.units[st.u];
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= u.nrows) return;
-  const float* first = p.w.part + p.w.part_floats * (2 * (size_t)b + 1);
   const size_t ml = (size_t)p.rows * D + 2 * row;
-  int end = c;  // one past the unit's last CTA
-  while (end < p.ctas) {
-    const PagedStart x = p.w.starts[end];
-    if (x.count > 0 && !(x.u == st.u && x.h == st.h)) break;
-    ++end;
-  }
-  auto slot = [&](int i) { return i < c ? first : p.w.part + p.w.part_floats * (2 * (size_t)i); };
+  const int parts = st.last - c + 2;
+  // part i: slot 1 of CTA c - 1 (i = 0), slot 0 of CTA c - 1 + i
+  auto part = [&](int i) { return p.w.part + p.w.part_floats * (2 * (size_t)(c - 1 + i) + (i == 0 ? 1 : 0)); };
   float top = -INFINITY;
-  for (int i = c - 1 + lane; i < end; i += 32)
-    if (i < c || p.w.starts[i].count > 0) top = fmaxf(top, slot(i)[ml]);
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, part(i)[ml]);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
   const float base = top == -INFINITY ? 0.f : top;
   float sum = 0.f, acc[D / 32];
 #pragma unroll
   for (int x = 0; x < D / 32; ++x) acc[x] = 0.f;
-  for (int i = c - 1; i < end; ++i) {
-    if (i >= c && p.w.starts[i].count <= 0) continue;
-    const float* s = slot(i);
-    const float f = ex2_approx(s[ml] - base);
-    sum += f * s[ml + 1];
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const int n = min(32, parts - i0);
+    float f = 0.f, l = 0.f;
+    if (lane < n) {
+      const float* s = part(i0 + lane);
+      f = ex2_approx(s[ml] - base);
+      l = f * s[ml + 1];
+    }
+    for (int i = 0; i < n; i += 8) {
+      float2 v[8][D / 64];
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) {
-      const float2 v = *reinterpret_cast<const float2*>(s + (size_t)row * D + 64 * x + 2 * lane);
-      acc[2 * x] += f * v.x;
-      acc[2 * x + 1] += f * v.y;
+      for (int k = 0; k < 8; ++k)
+        if (i + k < n) {
+          const float* s = part(i0 + i + k) + (size_t)row * D + 2 * lane;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) v[k][x] = *reinterpret_cast<const float2*>(s + 64 * x);
+        }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i + k < n) {
+          const float w = __shfl_sync(kAll, f, i + k);
+          sum += __shfl_sync(kAll, l, i + k);
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            acc[2 * x] += w * v[k][x].x;
+            acc[2 * x + 1] += w * v[k][x].y;
+          }
+        }
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
@@ -792,18 +824,15 @@ template <int D, bool F8>
 cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const fm_paged_batch& b,
                        const fm_rows& q, const PagedOut& out, float scale, cudaStream_t st, int* err) {
   using C = FewCfg<D, F8>;
-  static_assert(C::PER_SM * (C::SMEM + 1024) <= 233472, "few_kernel: shared memory of an SM");
+  static_assert(C::SMEM <= 232448 && C::PER_SM * (C::SMEM + 1024) <= 233472, "few_kernel: shared memory of an SM");
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(few_kernel<D, F8>), C::SMEM, ready);
   if (e != cudaSuccess) return e;
-  CUtensorMap tk, tv;
-  const int rows = std::min(s.page, kTileKeys);
-  if (!make_tmap_pages(&tk, c.k, c, rows, C::ROW) || !make_tmap_pages(&tv, c.v, c, rows, C::ROW))
-    return cudaErrorInvalidValue;
-  FewParams p{s, w, static_cast<const char*>(q.ptr), q.st, q.sh, out, c.k_exp, c.v_exp, b.page_table,
+  FewParams p{s, w, static_cast<const char*>(q.ptr), q.st, q.sh, out,
+              {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, b.page_table,
               scale * 1.4426950408889634f, err};
   count_launches(1);
-  return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), kFewThreads, C::SMEM, st, tk, tv, p);
+  return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), kFewThreads, C::SMEM, st, p);
 }
 
 // Which kernel: chunk_kernel's tiles of 128 rows once the sequences have more
@@ -836,6 +865,7 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   s.sinks = window > 0 ? std::min(sinks, 1 << 30) : 0;
   s.step = chunk ? 2 * (128 / s.G) * s.G : kFewRows;
   s.tile = chunk ? 128 : kTileKeys;
+  s.least = chunk ? 1 : kFewWarps;  // a tile for each computing warp, and fewer parts to join
   s.ctas = sm_count() * (chunk || c.d == 256 ? 1 : 2);
   s.max_units = ((long long)T * s.G + s.step - 1) / s.step + b.R;
   return s;

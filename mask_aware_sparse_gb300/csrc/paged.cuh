@@ -28,13 +28,15 @@ struct __align__(16) PagedUnit {
 
 struct __align__(16) PagedStart {
   int u, h, kt, count;  // a CTA's first unit, head and tile, and its number of tiles
+  int first, last;      // where kt > 0: the first and the last CTA with tiles of that unit and head
+  int pad[2];
 };
 
 struct PagedShape {
   int T, R, H_q, H_kv, G, d, width, page, n_pages;
   int causal, window, sinks;  // window 0: none
   int step, tile;  // query rows of a unit, keys of a tile
-  int ctas;
+  int ctas, least;  // CTAs launched; tiles a CTA gets before another one does
   long long max_units;
 };
 

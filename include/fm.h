@@ -484,7 +484,7 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  *
  * k, v: (n_pages, H_kv, page_size, d), contiguous, bf16 or (k_exp, v_exp not
  * NULL) e4m3 with one scale a row: exponent bytes (n_pages, H_kv, page_size),
- * value = stored * 2^(exponent - 127). page_size is 16, 32, 64 or 128, d 64, 128
+ * value = stored * 2^(exponent - 127), 1 to 254; 255 goes with a row of NaN. page_size is 16, 32, 64 or 128, d 64, 128
  * or 256. Addresses 16-byte aligned.
  *
  * A batch of R sequences: q_off (R + 1), the first new token of each in the

@@ -252,6 +252,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live)
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -289,10 +292,9 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
-// 2^(e - 127), NaN for e = 255
-__device__ __forceinline__ float scale_of(uint32_t e) {
-  return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
-}
+// 2^(e - 127), and e - 127 (bytes 1 .. 254: rows without a scale, 255, hold NaN already)
+__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
+__device__ __forceinline__ float exponent_of(uint32_t e) { return __uint_as_float(0x4b000000u | e) - 8388735.f; }
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -363,18 +365,25 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
           const uint32_t dst = ring + slot * C::TILE + l_at;
           const char* from_a = base + (src_a + l_row) * C::RB;
           const char* from_b = base + (src_b + l_row) * C::RB;
+          auto copies = [&](auto whole) {
 #pragma unroll
-          for (int i = 0; i < C::LOADS; ++i) {
-            const int r0 = i * C::RPI;
-            const char* from = r0 < 16 ? from_a + r0 * C::RB : from_b + (r0 - 16) * C::RB;
-            bool live = true;
-            if (edge) {
-              const int key = key0 + r0 + l_row;
-              live = key < u.hi && (key >= u.lo || key < p.s.sinks) && !(r0 < 16 ? bad_a : bad_b);
+            for (int i = 0; i < C::LOADS; ++i) {
+              const int r0 = i * C::RPI;
+              const char* from = r0 < 16 ? from_a + r0 * C::RB : from_b + (r0 - 16) * C::RB;
+              const uint32_t x = C::ROW == 128 ? (uint32_t)((r0 & 7) << 4) : (uint32_t)(((r0 >> 1) & 3) << 4);
+              if constexpr (whole.value) {
+                copy16((dst ^ x) + r0 * C::ROW, from);
+              } else {
+                const int key = key0 + r0 + l_row;
+                copy16((dst ^ x) + r0 * C::ROW, from,
+                       key < u.hi && (key >= u.lo || key < p.s.sinks) && !(r0 < 16 ? bad_a : bad_b));
+              }
             }
-            const uint32_t x = C::ROW == 128 ? (uint32_t)((r0 & 7) << 4) : (uint32_t)(((r0 >> 1) & 3) << 4);
-            copy16((dst ^ x) + r0 * C::ROW, from, live);
-          }
+          };
+          if (edge)
+            copies(std::false_type{});
+          else
+            copies(std::true_type{});
           if (F8 && lane < 2)
             copy16(ring_exp + slot * C::EXP + 16 * lane, p.exps[which] + (lane ? src_b : src_a), !(lane ? bad_b : bad_a));
         }
@@ -478,18 +487,12 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               const uint32_t ek = lds16(ring_exp + sk * C::EXP + 8 * n + 2 * t);
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const float f = scale_of((ek >> (8 * x)) & 255u);
-                s[n][x] *= f * sc[0];
-                s[n][2 + x] *= f * sc[1];
-              }
+              const float f0 = scale_of(ek & 255u), f1 = scale_of(ek >> 8);
+              s[n][0] *= f0;
+              s[n][1] *= f1;
+              s[n][2] *= f0;
+              s[n][3] *= f1;
             }
-          } else {
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) s[n][x] *= sl2;
           }
         }
         __syncwarp();
@@ -501,11 +504,8 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               const uint32_t ev = lds16(ring_exp + sv * C::EXP + 8 * n + 2 * t);
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t y = (ev >> (8 * x)) & 255u;
-                ve[n][x] = y == 255u ? NAN : (float)((int)y - 127);
-              }
+              ve[n][0] = exponent_of(ev & 255u);
+              ve[n][1] = exponent_of(ev >> 8);
             }
           }
           // masked scores: a tile whose keys all rows see is left as it is
@@ -521,6 +521,16 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
                                  (p.s.window == 0 || key > ps - p.s.window || key < p.s.sinks);
                 s[n][x] = see ? s[n][x] : -INFINITY;
               }
+            if constexpr (F8) {
+              // a key that no row sees: whatever its exponent byte holds
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int key = key0 + 8 * n + 2 * t + x;
+                  if (!(key < u.hi && (key >= u.lo || key < p.s.sinks))) ve[n][x] = 0.f;
+                }
+            }
           }
           // a running maximum moves only when it is passed by more than 8 (weights stay below 2^8)
           float f[2];
@@ -531,11 +541,12 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               x = max3f(x, s[n][2 * i], s[n][2 * i + 1]);
-              if constexpr (F8) z = max3f(z, s[n][2 * i] + ve[n][0], s[n][2 * i + 1] + ve[n][1]);
+              if constexpr (F8)
+                z = max3f(z, fmaf(s[n][2 * i], sc[i], ve[n][0]), fmaf(s[n][2 * i + 1], sc[i], ve[n][1]));
             }
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
             if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 1));
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 2));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 2)) * sc[i];
             if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 2));
             f[i] = 1.f;
             if (x > m[i] + 8.f) {
@@ -569,13 +580,13 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float base = m[i] == -INFINITY ? 0.f : m[i];
-              const float a = ex2_approx(s[n][2 * i] - base), b = ex2_approx(s[n][2 * i + 1] - base);
+              const float a = ex2_approx(fmaf(s[n][2 * i], sc[i], -base));
+              const float b = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], -base));
               l[i] += a + b;
               if constexpr (F8) {
                 const float bo = mo[i] == -INFINITY ? 0.f : mo[i];
-                // a masked score stays masked whatever its key's exponent byte holds
-                const float x = s[n][2 * i] == -INFINITY ? 0.f : ex2_approx(s[n][2 * i] + (ve[n][0] - bo));
-                const float y = s[n][2 * i + 1] == -INFINITY ? 0.f : ex2_approx(s[n][2 * i + 1] + (ve[n][1] - bo));
+                const float x = ex2_approx(fmaf(s[n][2 * i], sc[i], ve[n][0] - bo));
+                const float y = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], ve[n][1] - bo));
                 hi[n >> 1][2 * (n & 1) + i] = pack_f16x2(x, y);
               } else {
                 const uint32_t h = pack_bf16x2(a, b);

@@ -812,6 +812,9 @@ def _tensor(t, name, dims):
 
 def _expect(t, name, shape, dtype, dev):
     """t is a contiguous tensor of this shape, dtype and device."""
+    if (type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.get_device() == dev
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         _like(t, name, shape, dtype)  # raises, saying which
     if t.get_device() != dev:
@@ -838,13 +841,37 @@ def _bf16_rows(t, name, shape, dev):
 
 
 def _view(t, name, shape, dev, out=False):
+    """fm_view of a bf16 (B, H, N, d) tensor."""
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype is _BF16 and t.get_device() == dev:
+        at, (sb, sh, sn, one) = t.data_ptr(), t.stride()
+        if one == 1 and not (at & 15 or (sb | sh | sn) & 7) and (sb and sh and sn or not out):
+            return _pack_view(at, sb, sh, sn)  # nothing to look at more closely
     at, (sb, sh, sn, _) = _bf16_rows(t, name, shape, dev)
     if out and not ((sb or shape[0] <= 1) and (sh or shape[1] <= 1) and (sn or shape[2] <= 1)):
         raise ValueError(f"{name}: an output cannot be a broadcast view")
     return _pack_view(at, sb, sh, sn)
 
 
+def _new_view(shape, device):
+    """A new contiguous bf16 (B, H, N, d) tensor and its fm_view."""
+    t = torch.empty(shape, dtype=_BF16, device=device)
+    _, H, N, d = shape
+    return t, _pack_view(t.data_ptr(), H * N * d, N * d, d)
+
+
+def _new_token_view(shape, device):
+    """The same, laid out (B, N, H, d)."""
+    B, H, N, d = shape
+    t = torch.empty((B, N, H, d), dtype=_BF16, device=device)
+    return t.transpose(1, 2), _pack_view(t.data_ptr(), H * N * d, d, H * d)
+
+
 def _rows(t, name, shape, dev, out=False):
+    """fm_rows of a bf16 (T, H, d) tensor."""
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype is _BF16 and t.get_device() == dev:
+        at, (st, sh, one) = t.data_ptr(), t.stride()
+        if one == 1 and not (at & 15 or (st | sh) & 7) and (st and sh or not out):
+            return _pack_rows(at, st, sh)
     at, (st, sh, _) = _bf16_rows(t, name, shape, dev)
     if out and not ((st or shape[0] <= 1) and (sh or shape[1] <= 1)):
         raise ValueError(f"{name}: an output cannot be a broadcast view")
@@ -913,14 +940,19 @@ def fm_qk_norm_rope(q, k, v=None, *, positions=None, inv_freq=None, interleaved:
         raise ValueError("q must be a CUDA tensor: the library computes on the GPU only")
     if out is None:
         on = q.device
-        out = (torch.empty(qs, dtype=_BF16, device=on), torch.empty(ks, dtype=_BF16, device=on))
+        (qo, qv), (ko, kv) = _new_view(qs, on), _new_view(ks, on)
+        out, vv = (qo, ko), None
         if v is not None:
-            out += (torch.empty(ks, dtype=_BF16, device=on),)
-    elif len(out) != (2 if v is None else 3):
-        raise ValueError("out must hold one tensor per input")
-    _enqueue("fm_qk_norm_rope", dev, stream, p, qi, ki, vi, _view(out[0], "output q", qs, dev, True),
-             _view(out[1], "output k", ks, dev, True), None if v is None else _view(out[2], "output v", ks, dev, True))
-    return tuple(out)
+            vo, vv = _new_view(ks, on)
+            out = (qo, ko, vo)
+    else:
+        if len(out) != (2 if v is None else 3):
+            raise ValueError("out must hold one tensor per input")
+        qv, kv = _view(out[0], "output q", qs, dev, True), _view(out[1], "output k", ks, dev, True)
+        vv = None if v is None else _view(out[2], "output v", ks, dev, True)
+        out = tuple(out)
+    _enqueue("fm_qk_norm_rope", dev, stream, p, qi, ki, vi, qv, kv, vv)
+    return out
 
 
 @functools.lru_cache(maxsize=256)
@@ -945,22 +977,29 @@ def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, i
     if dev < 0:
         raise ValueError("q must be a CUDA tensor: the library computes on the GPU only")
     on = q.device
+    dv = vv = None
     if out is None:
-        out = tuple(torch.empty((s[0], s[2], s[1], s[3]), dtype=_BF16, device=on).transpose(1, 2)
-                    for s in ((qs, ks) if dvo is None else (qs, ks, ks)))
-    elif len(out) != (2 if dvo is None else 3):
-        raise ValueError("out must hold one tensor per gradient")
+        (dq, qv), (dk, kv) = _new_token_view(qs, on), _new_token_view(ks, on)
+        if dvo is not None:
+            dv, vv = _new_token_view(ks, on)
+    else:
+        if len(out) != (2 if dvo is None else 3):
+            raise ValueError("out must hold one tensor per gradient")
+        dq, dk = out[0], out[1]
+        qv, kv = _view(dq, "output dq", qs, dev, True), _view(dk, "output dk", ks, dev, True)
+        if dvo is not None:
+            dv = out[2]
+            vv = _view(dv, "output dv", ks, dev, True)
     dwq = None if q_weight is None else torch.empty_like(q_weight)
     dwk = None if k_weight is None else torch.empty_like(k_weight)
     ws, wsb = None, 0
     if dwq is not None or dwk is not None:
         wsb = _qk_bwd_bytes(dev, qs[0], qs[2], qs[3])
         ws = torch.empty(max(16, wsb), dtype=_U8, device=on)
-    _enqueue("fm_qk_norm_rope_bwd", dev, stream, p, gq, gk, gv, qi, ki, _view(out[0], "output dq", qs, dev, True),
-             _view(out[1], "output dk", ks, dev, True), None if dvo is None else _view(out[2], "output dv", ks, dev, True),
+    _enqueue("fm_qk_norm_rope_bwd", dev, stream, p, gq, gk, gv, qi, ki, qv, kv, vv,
              None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
              None if ws is None else ws.data_ptr(), wsb)
-    return out[0], out[1], (out[2] if dvo is not None else None), dwq, dwk
+    return dq, dk, dv, dwq, dwk
 
 
 class KVCache:

@@ -84,19 +84,12 @@ __device__ __forceinline__ V block_scan(V v, V* warp_sums) {  // inclusive
   return v;
 }
 
-// new tokens of sequence r: [s, e), kept inside [0, T] whatever q_off holds
-__device__ __forceinline__ void span_of(const PlanParams& p, int r, int& s, int& e, bool& bad) {
-  const int a = p.q_off[r], b = p.q_off[r + 1];
-  s = min(max(a, 0), p.s.T);
-  e = min(max(b, s), p.s.T);
-  bad = a != s || b != e;
-}
-
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   __shared__ long long sums[32];
   __shared__ long long carry;
   const PagedShape& s = p.s;
   const int tid = threadIdx.x;
+  grid_dependency_wait();
   grid_launch_dependents();
   bool bad = false;
   // units of each sequence
@@ -109,11 +102,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     const int r = r0 + tid;
     long long n = 0;
     if (r < s.R) {
-      int a, b;
-      bool x;
-      span_of(p, r, a, b, x);
-      bad |= x;
-      n = ((long long)(b - a) * s.G + s.step - 1) / s.step;
+      int a, k, L;
+      bad |= sequence_at(s, p.q_off, p.kv_len, r, a, k, L);
+      n = ((long long)k * s.G + s.step - 1) / s.step;
     }
     const long long in = block_scan(n, sums) + carry;
     if (r < s.R) p.w.first[r + 1] = (int)min(in, s.max_units);
@@ -139,29 +130,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         else
           hi = mid - 1;
       }
-      int a, b;
-      bool x;
-      span_of(p, lo, a, b, x);
-      const int n = b - a;
-      const int L0 = p.kv_len[lo];
-      const int L = min(max(L0, 0), s.width * s.page);
-      bad |= L0 != L;
-      const long long row0 = (long long)(u - p.w.first[lo]) * s.step;
-      PagedUnit q;
-      q.r = lo;
-      q.tok = a + (int)(row0 / s.G);
-      q.g0 = (int)(row0 % s.G);
-      q.nrows = (int)min((long long)s.step, (long long)n * s.G - row0);
-      q.pos = L - n + (int)(row0 / s.G);
-      q.kv_len = L;
-      const int last = q.pos + (q.g0 + q.nrows - 1) / s.G;
-      q.hi = s.causal ? min(max(last + 1, 0), L) : L;
-      q.lo = s.window > 0 ? max(0, q.pos - s.window + 1) : 0;
-      const int all = (q.hi + s.tile - 1) / s.tile;
-      q.ns = s.window > 0 ? min((s.sinks + s.tile - 1) / s.tile, all) : 0;
-      q.w0 = max(q.ns, min(q.lo / s.tile, all));
-      q.ntiles = q.ns + max(0, all - q.w0);
-      q.pad = 0;
+      int a, n, L;
+      sequence_at(s, p.q_off, p.kv_len, lo, a, n, L);
+      const PagedUnit q = unit_at(s, lo, a, n, L, u - p.w.first[lo]);
       p.w.units[u] = q;
       work = (long long)max(q.ntiles, 1) * s.H_kv;
     }
@@ -174,14 +145,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   const long long total = carry;
   if (tid == 0) p.w.sum[units] = total;
   __syncthreads();
-  // the first `used` CTAs have ranges, [c total / used, (c + 1) total / used): all
-  // of them, or as many as get s.least tiles each
-  const long long used = max(1ll, min((long long)s.ctas, total / s.least));
+  const long long used = used_ctas(s, total);
   for (int c = tid; c < s.ctas; c += kPlanThreads) {
     PagedStart st = {};
     if (c < used && total > 0) {
       const long long f = total * c / used;
-      st.count = (int)(total * (c + 1) / used - f);
       int lo = 0, hi = units - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -191,14 +159,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
           hi = mid - 1;
       }
       const long long rem = f - p.w.sum[lo];
-      const int nt = max(p.w.units[lo].ntiles, 1);
+      st.unit = p.w.units[lo];
+      const int nt = max(st.unit.ntiles, 1);
       st.u = lo;
       st.h = (int)(rem / nt);
       st.kt = (int)(rem - (long long)st.h * nt);
-      // the CTA of tile x is the last c with c total / used <= x
-      const long long f0 = f - st.kt;
-      st.first = (int)(((f0 + 1) * used - 1) / total);
-      st.last = (int)(((f0 + nt) * used - 1) / total);
+      st.count = (int)(total * (c + 1) / used - f);
+      sharers(st, f - st.kt, (long long)nt, total, used);
     }
     p.w.starts[c] = st;
   }
@@ -223,10 +190,10 @@ struct FewCfg {
   static constexpr int PER_SM = D == 256 ? 1 : 2;
   static constexpr int RING = D == 64 ? (F8 ? 8 : 6) : (F8 ? 6 : 3);  // entries of a warp's ring
   static constexpr int ENTRIES = kFewWarps * RING;
-  static constexpr int MERGE_OFF = ENTRIES * TILE;
-  static constexpr int EXP_OFF = MERGE_OFF + kFewRows * D * 4;
+  static constexpr int EXP_OFF = ENTRIES * TILE;
   static constexpr int ML_OFF = EXP_OFF + ENTRIES * EXP;
-  static constexpr int SMEM = ML_OFF + kFewWarps * kFewRows * 2 * 4 + 1024;
+  static constexpr int SMEM = ML_OFF + kFewWarps * kFewRows * 16 + 1024;
+  static_assert(RING * TILE >= kFewRows * (D + 8) * 4, "a warp's ring holds its O at a segment's end");
   static constexpr int KSTEPS = D / 16;
   static constexpr int CHUNKS = ROW / 64;  // 16-byte chunks a thread reads of a box's row
   static constexpr int SPC = F8 ? 4 : 2;   // k-steps of a chunk
@@ -242,6 +209,8 @@ struct FewParams {
   PagedOut out;
   const char* kv[2];
   const uint8_t* exps[2];
+  const int32_t* q_off;
+  const int32_t* kv_len;
   const int32_t* table;
   float scale_log2;
   int* err;
@@ -311,14 +280,21 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
   using C = FewCfg<D, F8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);
-  float* merge = reinterpret_cast<float*>(smem + C::MERGE_OFF);
+  float4* ml = reinterpret_cast<float4*>(smem + C::ML_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ PagedStart start;
+  __shared__ int4 seq[kLocalSeqs];
   grid_dependency_wait();
   grid_launch_dependents();
-  const PagedStart st = p.w.starts[blockIdx.x];
+  if (p.s.local) {
+    plan_locally(p.s, p.q_off, p.kv_len, seq, reinterpret_cast<unsigned*>(smem), &start, p.err);
+    if (threadIdx.x == 0 && !p.s.whole) p.w.starts[blockIdx.x] = start;  // for join_kernel
+  } else {
+    if (threadIdx.x == 0) start = p.w.starts[blockIdx.x];
+    __syncthreads();
+  }
   const int G = p.s.G, P = p.s.page;
-  PagedWalk walk(p.w.units, st, p.s.H_kv);
+  PagedWalk walk(p.s, p.w.units, seq, start);
   const int g = lane >> 2, t = lane & 3;
   const float sl2 = p.scale_log2;
   const uint32_t ring = smem_u32(smem) + warp * C::RING * C::TILE;
@@ -336,496 +312,468 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
   PageWindow pages;
 
   for (; walk.more(); walk.next()) {
-      const PagedUnit& u = walk.u;
-      // the warp's tiles of the segment: [j0, j0 + nt), its entries 0 .. 2 nt - 1
-      // (keys and values in turn), RING of them in the ring or on their way
-      const int j0 = walk.n * warp / kFewWarps, nt = walk.n * (warp + 1) / kFewWarps - j0;
-      pages.reset(p.table, u.r, p.s.width);
-      int64_t src_a = 0, src_b = 0;  // rows of the cache: the tile's first 16 (or all) keys, its last 16
-      bool bad_a = false, bad_b = false;
-      auto issue = [&](int e, int slot) {
-        if (e < 2 * nt) {
-          const int key0 = tile_of(u, walk.kt + j0 + (e >> 1)) * kTileKeys;
-          const int which = e & 1;
-          if (which == 0) {
-            const int pg0 = key0 / P, per = P < kTileKeys ? 2 : 1;
-            pages.hold(pg0, per, lane);
-            const int a = __shfl_sync(kAll, pages.held, pg0 - pages.base);
-            const int b = __shfl_sync(kAll, pages.held, pg0 + per - 1 - pages.base);
-            const bool two = per == 2 && key0 + 16 < u.kv_len;  // the second page holds keys
-            bad_a = a < 0 || a >= p.s.n_pages;
-            bad_b = per == 2 ? !two || b < 0 || b >= p.s.n_pages : bad_a;
-            if (bad_a || (two && bad_b)) record_error(p.err, FM_DEV_ERR_RANGE);
-            src_a = ((int64_t)(bad_a ? 0 : a) * p.s.H_kv + walk.h) * P + (key0 - pg0 * P);
-            src_b = per == 2 ? ((int64_t)(bad_b ? 0 : b) * p.s.H_kv + walk.h) * P : src_a + 16;
-          }
-          // keys that no row of the unit sees (past the sequence's end: anything may lie there) become zeros
-          const bool edge = key0 + kTileKeys > u.hi || (p.s.window > 0 && key0 < u.lo) || bad_a || bad_b;
-          const char* base = p.kv[which] + l_chunk * 16;
-          const uint32_t dst = ring + slot * C::TILE + l_at;
-          const char* from_a = base + (src_a + l_row) * C::RB;
-          const char* from_b = base + (src_b + l_row) * C::RB;
-          auto copies = [&](auto whole) {
-#pragma unroll
-            for (int i = 0; i < C::LOADS; ++i) {
-              const int r0 = i * C::RPI;
-              const char* from = r0 < 16 ? from_a + r0 * C::RB : from_b + (r0 - 16) * C::RB;
-              const uint32_t x = C::ROW == 128 ? (uint32_t)((r0 & 7) << 4) : (uint32_t)(((r0 >> 1) & 3) << 4);
-              if constexpr (whole.value) {
-                copy16((dst ^ x) + r0 * C::ROW, from);
-              } else {
-                const int key = key0 + r0 + l_row;
-                copy16((dst ^ x) + r0 * C::ROW, from,
-                       key < u.hi && (key >= u.lo || key < p.s.sinks) && !(r0 < 16 ? bad_a : bad_b));
-              }
-            }
-          };
-          if (edge)
-            copies(std::false_type{});
-          else
-            copies(std::true_type{});
-          if (F8 && lane < 2)
-            copy16(ring_exp + slot * C::EXP + 16 * lane, p.exps[which] + (lane ? src_b : src_a), !(lane ? bad_b : bad_a));
+    const PagedUnit& u = walk.u;
+    // the warp's tiles of the segment: [j0, j0 + nt), its entries 0 .. 2 nt - 1
+    // (keys and values in turn), RING of them in the ring or on their way
+    const int j0 = walk.n * warp / kFewWarps, nt = walk.n * (warp + 1) / kFewWarps - j0;
+    pages.reset(p.table, u.r, p.s.width);
+    int64_t src_a = 0, src_b = 0;  // rows of the cache: the tile's first 16 (or all) keys, its last 16
+    bool bad_a = false, bad_b = false;
+    auto issue = [&](int e, int slot) {
+      if (e < 2 * nt) {
+        const int key0 = tile_of(u, walk.kt + j0 + (e >> 1)) * kTileKeys;
+        const int which = e & 1;
+        if (which == 0) {
+          const int pg0 = key0 / P, per = P < kTileKeys ? 2 : 1;
+          pages.hold(pg0, per, lane);
+          const int a = __shfl_sync(kAll, pages.held, pg0 - pages.base);
+          const int b = __shfl_sync(kAll, pages.held, pg0 + per - 1 - pages.base);
+          const bool two = per == 2 && key0 + 16 < u.kv_len;  // the second page holds keys
+          bad_a = a < 0 || a >= p.s.n_pages;
+          bad_b = per == 2 ? !two || b < 0 || b >= p.s.n_pages : bad_a;
+          if (bad_a || (two && bad_b)) record_error(p.err, FM_DEV_ERR_RANGE);
+          src_a = ((int64_t)(bad_a ? 0 : a) * p.s.H_kv + walk.h) * P + (key0 - pg0 * P);
+          src_b = per == 2 ? ((int64_t)(bad_b ? 0 : b) * p.s.H_kv + walk.h) * P : src_a + 16;
         }
-        copy_commit();
-      };
+        // keys that no row of the unit sees (past the sequence's end: anything may lie there) become zeros
+        const bool edge = key0 + kTileKeys > u.hi || (p.s.window > 0 && key0 < u.lo) || bad_a || bad_b;
+        const char* base = p.kv[which] + l_chunk * 16;
+        const uint32_t dst = ring + slot * C::TILE + l_at;
+        const char* from_a = base + (src_a + l_row) * C::RB;
+        const char* from_b = base + (src_b + l_row) * C::RB;
+        auto copies = [&](auto whole) {
+#pragma unroll
+          for (int i = 0; i < C::LOADS; ++i) {
+            const int r0 = i * C::RPI;
+            const char* from = r0 < 16 ? from_a + r0 * C::RB : from_b + (r0 - 16) * C::RB;
+            const uint32_t x = C::ROW == 128 ? (uint32_t)((r0 & 7) << 4) : (uint32_t)(((r0 >> 1) & 3) << 4);
+            if constexpr (whole.value) {
+              copy16((dst ^ x) + r0 * C::ROW, from);
+            } else {
+              const int key = key0 + r0 + l_row;
+              copy16((dst ^ x) + r0 * C::ROW, from,
+                     key < u.hi && (key >= u.lo || key < p.s.sinks) && !(r0 < 16 ? bad_a : bad_b));
+            }
+          }
+        };
+        if (edge)
+          copies(std::false_type{});
+        else
+          copies(std::true_type{});
+        if (F8 && lane < 2)
+          copy16(ring_exp + slot * C::EXP + 16 * lane, p.exps[which] + (lane ? src_b : src_a), !(lane ? bad_b : bad_a));
+      }
+      copy_commit();
+    };
 #pragma unroll 1
-      for (int e = 0; e < C::RING; ++e) issue(e, e);
-      // this thread's rows g and g + 8: their positions (-1: no such row), their Q
-      int pos[2];
-      uint32_t qf[C::KSTEPS][4];
+    for (int e = 0; e < C::RING; ++e) issue(e, e);
+    // this thread's rows g and g + 8: their positions (-1: no such row), their Q
+    int pos[2];
+    uint32_t qf[C::KSTEPS][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = g + 8 * i, x = u.g0 + row;
+      const bool live = row < u.nrows;
+      pos[i] = live ? (p.s.causal ? u.pos + x / G : u.kv_len - 1) : -1;
+      const char* src = p.q + 2 * ((int64_t)(u.tok + x / G) * p.q_st + (int64_t)(walk.h * G + x % G) * p.q_sh);
+#pragma unroll
+      for (int b = 0; b < C::BOXES; ++b)
+#pragma unroll
+        for (int c = 0; c < C::CHUNKS; ++c) {
+          // the elements of the chunk that this thread reads of a key's row
+          const int e0 = (b * C::ROW + (C::CHUNKS * t + c) * 16) / C::ES;
+#pragma unroll
+          for (int x4 = 0; x4 < C::SPC / 2; ++x4) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (live && walk.n > 0) v = *reinterpret_cast<const uint4*>(src + 2 * (e0 + 8 * x4));
+            const int k = (b * C::CHUNKS + c) * C::SPC + 2 * x4;
+            qf[k][i] = v.x;
+            qf[k][2 + i] = v.y;
+            qf[k + 1][i] = v.z;
+            qf[k + 1][2 + i] = v.w;
+          }
+        }
+    }
+    const int plo = u.pos + u.g0 / G, phi = u.pos + (u.g0 + u.nrows - 1) / G;  // the unit's first and last position
+    float sc[2] = {sl2, sl2};  // per row: scores to log2 units
+    if constexpr (F8) {
+      // Q in fp16, each row times the power of two that puts its largest value at
+      // the top of fp16's range: values down to 2^-29 of it keep all their bits
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = g + 8 * i, x = u.g0 + row;
-        const bool live = row < u.nrows;
-        pos[i] = live ? (p.s.causal ? u.pos + x / G : u.kv_len - 1) : -1;
-        const char* src = p.q + 2 * ((int64_t)(u.tok + x / G) * p.q_st + (int64_t)(walk.h * G + x % G) * p.q_sh);
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < C::KSTEPS; ++k)
+          top = __vmaxu2(top, __vmaxu2(qf[k][i] & 0x7fff7fffu, qf[k][2 + i] & 0x7fff7fffu));
+        top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 2));
+        const int E = (int)(max(top & 0xffffu, top >> 16) >> 7);
+        // 2^(142 - E), kept finite; a row of zeros, infinities or NaN stays as it is
+        const int up = (E == 0 || E == 255) ? 0 : min(142 - E, 126);
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        sc[i] = sl2 * __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+        for (int k = 0; k < C::KSTEPS; ++k)
+#pragma unroll
+          for (int x = i; x < 4; x += 2)
+            qf[k][x] = pack_f16x2(__uint_as_float(qf[k][x] << 16) * f, __uint_as_float(qf[k][x] & 0xffff0000u) * f);
+      }
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float mo[2] = {-INFINITY, -INFINITY};  // e4m3: the running maximum of score + exponent of the value's scale
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    int slot = 0;  // of the next entry
+    for (int j = 0; j < nt; ++j) {
+      const int key0 = tile_of(u, walk.kt + j0 + j) * kTileKeys;
+      const int sk = slot, sv = slot + 1 == C::RING ? 0 : slot + 1;
+      slot = sv + 1 == C::RING ? 0 : sv + 1;
+      copy_wait<C::RING - 1>();
+      __syncwarp();
+      float s[4][4];
+      float ve[4][2];  // e4m3: the exponents of the values' scales
+      {
+        const uint32_t kb = ring + sk * C::TILE + k_at;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
         for (int b = 0; b < C::BOXES; ++b)
 #pragma unroll
-          for (int c = 0; c < C::CHUNKS; ++c) {
-            // the elements of the chunk that this thread reads of a key's row
-            const int e0 = (b * C::ROW + (C::CHUNKS * t + c) * 16) / C::ES;
+          for (int c = 0; c < C::CHUNKS; ++c)
 #pragma unroll
-            for (int x4 = 0; x4 < C::SPC / 2; ++x4) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (live && walk.n > 0) v = *reinterpret_cast<const uint4*>(src + 2 * (e0 + 8 * x4));
-              const int k = (b * C::CHUNKS + c) * C::SPC + 2 * x4;
-              qf[k][i] = v.x;
-              qf[k][2 + i] = v.y;
-              qf[k + 1][i] = v.z;
-              qf[k + 1][2 + i] = v.w;
+            for (int n = 0; n < 4; ++n) {
+              const uint4 v = lds128((kb ^ (16 * c)) + b * C::BOX + n * 8 * C::ROW);
+              const int k = (b * C::CHUNKS + c) * C::SPC;
+              if constexpr (F8) {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  uint32_t b0, b1;
+                  e4m3_to_f16(w[x], b0, b1);
+                  mma16816_f16(s[n], qf[k + x], b0, b1);
+                }
+              } else {
+                mma16816(s[n], qf[k], v.x, v.y);
+                mma16816(s[n], qf[k + 1], v.z, v.w);
+              }
             }
+        if constexpr (F8) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t ek = lds16(ring_exp + sk * C::EXP + 8 * n + 2 * t);
+            const float f0 = scale_of(ek & 255u), f1 = scale_of(ek >> 8);
+            s[n][0] *= f0;
+            s[n][1] *= f1;
+            s[n][2] *= f0;
+            s[n][3] *= f1;
           }
-      }
-      const int plo = u.pos + u.g0 / G, phi = u.pos + (u.g0 + u.nrows - 1) / G;  // the unit's first and last position
-      float sc[2] = {sl2, sl2};  // per row: scores to log2 units
-      if constexpr (F8) {
-        // Q in fp16, each row times the power of two that puts its largest value at
-        // the top of fp16's range: values down to 2^-29 of it keep all their bits
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int k = 0; k < C::KSTEPS; ++k)
-            top = __vmaxu2(top, __vmaxu2(qf[k][i] & 0x7fff7fffu, qf[k][2 + i] & 0x7fff7fffu));
-          top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 1));
-          top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 2));
-          const int E = (int)(max(top & 0xffffu, top >> 16) >> 7);
-          // 2^(142 - E), kept finite; a row of zeros, infinities or NaN stays as it is
-          const int up = (E == 0 || E == 255) ? 0 : min(142 - E, 126);
-          const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-          sc[i] = sl2 * __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll
-          for (int k = 0; k < C::KSTEPS; ++k)
-#pragma unroll
-            for (int x = i; x < 4; x += 2)
-              qf[k][x] = pack_f16x2(__uint_as_float(qf[k][x] << 16) * f, __uint_as_float(qf[k][x] & 0xffff0000u) * f);
         }
       }
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-      float mo[2] = {-INFINITY, -INFINITY};  // e4m3: the running maximum of score + exponent of the value's scale
-      float o[D / 8][4];
+      __syncwarp();
+      issue(2 * j + C::RING, sk);
+      copy_wait<C::RING - 1>();
+      __syncwarp();
+      {
+        if constexpr (F8) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-      int slot = 0;  // of the next entry
-      for (int j = 0; j < nt; ++j) {
-        const int key0 = tile_of(u, walk.kt + j0 + j) * kTileKeys;
-        const int sk = slot, sv = slot + 1 == C::RING ? 0 : slot + 1;
-        slot = sv + 1 == C::RING ? 0 : sv + 1;
-        copy_wait<C::RING - 1>();
-        __syncwarp();
-        float s[4][4];
-        float ve[4][2];  // e4m3: the exponents of the values' scales
-        {
-          const uint32_t kb = ring + sk * C::TILE + k_at;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-#pragma unroll
-          for (int b = 0; b < C::BOXES; ++b)
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
-#pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                const uint4 v = lds128((kb ^ (16 * c)) + b * C::BOX + n * 8 * C::ROW);
-                const int k = (b * C::CHUNKS + c) * C::SPC;
-                if constexpr (F8) {
-                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    uint32_t b0, b1;
-                    e4m3_to_f16(w[x], b0, b1);
-                    mma16816_f16(s[n], qf[k + x], b0, b1);
-                  }
-                } else {
-                  mma16816(s[n], qf[k], v.x, v.y);
-                  mma16816(s[n], qf[k + 1], v.z, v.w);
-                }
-              }
-          if constexpr (F8) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const uint32_t ek = lds16(ring_exp + sk * C::EXP + 8 * n + 2 * t);
-              const float f0 = scale_of(ek & 255u), f1 = scale_of(ek >> 8);
-              s[n][0] *= f0;
-              s[n][1] *= f1;
-              s[n][2] *= f0;
-              s[n][3] *= f1;
-            }
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t ev = lds16(ring_exp + sv * C::EXP + 8 * n + 2 * t);
+            ve[n][0] = exponent_of(ev & 255u);
+            ve[n][1] = exponent_of(ev >> 8);
           }
         }
-        __syncwarp();
-        issue(2 * j + C::RING, sk);
-        copy_wait<C::RING - 1>();
-        __syncwarp();
-        {
-          if constexpr (F8) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const uint32_t ev = lds16(ring_exp + sv * C::EXP + 8 * n + 2 * t);
-              ve[n][0] = exponent_of(ev & 255u);
-              ve[n][1] = exponent_of(ev >> 8);
-            }
-          }
-          // masked scores: a tile whose keys all rows see is left as it is
-          const bool part = key0 + kTileKeys > u.hi || (p.s.causal && key0 + kTileKeys - 1 > plo) ||
-                            (p.s.window > 0 && key0 <= phi - p.s.window);
-          if (part) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const int key = key0 + 8 * n + 2 * t + (x & 1), ps = pos[x >> 1];
-                const bool see = key <= ps && key < u.kv_len &&
-                                 (p.s.window == 0 || key > ps - p.s.window || key < p.s.sinks);
-                s[n][x] = see ? s[n][x] : -INFINITY;
-              }
-            if constexpr (F8) {
-              // a key that no row sees: whatever its exponent byte holds
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const int key = key0 + 8 * n + 2 * t + x;
-                  if (!(key < u.hi && (key >= u.lo || key < p.s.sinks))) ve[n][x] = 0.f;
-                }
-            }
-          }
-          // a running maximum moves only when it is passed by more than 8 (weights stay below 2^8)
-          float f[2];
-          bool moved = false;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float x = -INFINITY, z = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              x = max3f(x, s[n][2 * i], s[n][2 * i + 1]);
-              if constexpr (F8)
-                z = max3f(z, fmaf(s[n][2 * i], sc[i], ve[n][0]), fmaf(s[n][2 * i + 1], sc[i], ve[n][1]));
-            }
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
-            if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 1));
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 2)) * sc[i];
-            if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 2));
-            f[i] = 1.f;
-            if (x > m[i] + 8.f) {
-              const float y = ex2_approx(m[i] - x);
-              l[i] *= y;
-              m[i] = x;
-              if (!F8) {
-                f[i] = y;
-                moved = true;
-              }
-            }
-            if (F8 && z > mo[i] + 8.f) {
-              f[i] = ex2_approx(mo[i] - z);
-              mo[i] = z;
-              moved = true;
-            }
-          }
-          if (__any_sync(kAll, moved)) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[i][0] *= f[0];
-              o[i][1] *= f[0];
-              o[i][2] *= f[1];
-              o[i][3] *= f[1];
-            }
-          }
-          // weights: bf16 in two terms (p and what its rounding left), fp16 in one
-          uint32_t hi[2][4], lo[2][4];
+        // masked scores: a tile whose keys all rows see is left as it is
+        const bool part = key0 + kTileKeys > u.hi || (p.s.causal && key0 + kTileKeys - 1 > plo) ||
+                          (p.s.window > 0 && key0 <= phi - p.s.window);
+        if (part) {
 #pragma unroll
           for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float base = m[i] == -INFINITY ? 0.f : m[i];
-              const float a = ex2_approx(fmaf(s[n][2 * i], sc[i], -base));
-              const float b = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], -base));
-              l[i] += a + b;
-              if constexpr (F8) {
-                const float bo = mo[i] == -INFINITY ? 0.f : mo[i];
-                const float x = ex2_approx(fmaf(s[n][2 * i], sc[i], ve[n][0] - bo));
-                const float y = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], ve[n][1] - bo));
-                hi[n >> 1][2 * (n & 1) + i] = pack_f16x2(x, y);
-              } else {
-                const uint32_t h = pack_bf16x2(a, b);
-                hi[n >> 1][2 * (n & 1) + i] = h;
-                lo[n >> 1][2 * (n & 1) + i] =
-                    pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-              }
+            for (int x = 0; x < 4; ++x) {
+              const int key = key0 + 8 * n + 2 * t + (x & 1), ps = pos[x >> 1];
+              const bool see = key <= ps && key < u.kv_len &&
+                               (p.s.window == 0 || key > ps - p.s.window || key < p.s.sinks);
+              s[n][x] = see ? s[n][x] : -INFINITY;
             }
-          const uint32_t vb0 = ring + sv * C::TILE + v_at0, vb1 = ring + sv * C::TILE + v_at1;
+          if constexpr (F8) {
+            // a key that no row sees: whatever its exponent byte holds
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {  // 16 keys each
-              const uint32_t at = 16 * kk * C::ROW;
-              if constexpr (F8) {
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int cg = 0; cg < D / 64; ++cg) {
-                  // eight columns 64 cg + 8 g + i of keys 2t, 2t + 1, 2t + 8, 2t + 9
-                  const uint32_t box = (cg * 64 / C::ROW) * C::BOX + at, x64 = cg * 64 % C::ROW;
-                  const uint2 w0 = lds64((vb0 ^ x64) + box), w1 = lds64((vb1 ^ x64) + box);
-                  const uint2 w2 = lds64((vb0 ^ x64) + box + 8 * C::ROW), w3 = lds64((vb1 ^ x64) + box + 8 * C::ROW);
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t a0 = h ? w0.y : w0.x, a1 = h ? w1.y : w1.x, a2 = h ? w2.y : w2.x, a3 = h ? w3.y : w3.x;
-                    uint32_t b0[4], b1[4];
-                    e4m3_to_f16(__byte_perm(a0, a1, 0x5140), b0[0], b0[1]);
-                    e4m3_to_f16(__byte_perm(a0, a1, 0x7362), b0[2], b0[3]);
-                    e4m3_to_f16(__byte_perm(a2, a3, 0x5140), b1[0], b1[1]);
-                    e4m3_to_f16(__byte_perm(a2, a3, 0x7362), b1[2], b1[3]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                      mma16816_f16(o[8 * cg + 4 * h + i], hi[kk], b0[i], b1[i]);
-                  }
-                }
-              } else {
-#pragma unroll
-                for (int c = 0; c < D / 8; c += 2) {
-                  uint32_t r[4];
-                  ldmatrix4_trans((vb0 ^ (16 * (c & 7))) + (c >> 3) * C::BOX + at, r);
-                  mma16816(o[c], hi[kk], r[0], r[1]);
-                  mma16816(o[c + 1], hi[kk], r[2], r[3]);
-                  mma16816(o[c], lo[kk], r[0], r[1]);
-                  mma16816(o[c + 1], lo[kk], r[2], r[3]);
-                }
+              for (int x = 0; x < 2; ++x) {
+                const int key = key0 + 8 * n + 2 * t + x;
+                if (!(key < u.hi && (key >= u.lo || key < p.s.sinks))) ve[n][x] = 0.f;
               }
           }
         }
-        __syncwarp();
-        issue(2 * j + 1 + C::RING, sv);
-      }
-      copy_wait<0>();
-
-      // join the four warps' (m, l, O): a common maximum, then the sums in warp order
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if constexpr (F8) {
-          // O in units of l's: 2^mo of its scores-and-exponents to 2^m of the scores
-          const float y = m[i] == -INFINITY ? 0.f : ex2_approx(mo[i] - m[i]);
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x) {
-            o[x][2 * i] *= y;
-            o[x][2 * i + 1] *= y;
-          }
-        }
-        l[i] += __shfl_xor_sync(kAll, l[i], 1);
-        l[i] += __shfl_xor_sync(kAll, l[i], 2);
-        if (t == 0) {
-          ml[(warp * kFewRows + g + 8 * i) * 2] = m[i];
-          ml[(warp * kFewRows + g + 8 * i) * 2 + 1] = l[i];
-        }
-      }
-      named_bar_sync(1, 32 * kFewWarps);
-      float top[2], sum[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = -INFINITY;
-        for (int w = 0; w < kFewWarps; ++w) top[i] = fmaxf(top[i], ml[(w * kFewRows + g + 8 * i) * 2]);
-        sum[i] = 0.f;
-        const float base = top[i] == -INFINITY ? 0.f : top[i];
-        for (int w = 0; w < kFewWarps; ++w)
-          sum[i] += ex2_approx(ml[(w * kFewRows + g + 8 * i) * 2] - base) * ml[(w * kFewRows + g + 8 * i) * 2 + 1];
-        const float f = ex2_approx(m[i] - base);
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) {
-          o[x][2 * i] *= f;
-          o[x][2 * i + 1] *= f;
-        }
-      }
-      for (int w = 0; w < kFewWarps; ++w) {
-        if (warp == w) {
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x) {
-            float4* at = reinterpret_cast<float4*>(merge) + x * 32 + lane;
-            if (w > 0) {
-              const float4 v = *at;
-              o[x][0] += v.x;
-              o[x][1] += v.y;
-              o[x][2] += v.z;
-              o[x][3] += v.w;
-            }
-            if (w < kFewWarps - 1) *at = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
-          }
-        }
-        named_bar_sync(1, 32 * kFewWarps);
-      }
-      if (warp == kFewWarps - 1) {
-        const bool whole = walk.whole();
-        float* part = p.w.part + p.w.part_floats * (2 * (size_t)blockIdx.x + walk.slot());
+        // a running maximum moves only when it is passed by more than 8 (weights stay below 2^8)
+        float f[2];
+        bool moved = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int row = g + 8 * i, x = u.g0 + row;
-          if (row >= u.nrows) continue;
-          const int64_t tok = u.tok + x / G;
-          const int head = walk.h * G + x % G;
-          if (whole) {
-            const float inv = sum[i] > 0.f ? 1.f / sum[i] : (sum[i] == 0.f ? 0.f : sum[i]);
-            char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
+          float x = -INFINITY, z = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            x = max3f(x, s[n][2 * i], s[n][2 * i + 1]);
+            if constexpr (F8)
+              z = max3f(z, fmaf(s[n][2 * i], sc[i], ve[n][0]), fmaf(s[n][2 * i + 1], sc[i], ve[n][1]));
+          }
+          x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
+          if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 1));
+          x = fmaxf(x, __shfl_xor_sync(kAll, x, 2)) * sc[i];
+          if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 2));
+          f[i] = 1.f;
+          if (x > m[i] + 8.f) {
+            const float y = ex2_approx(m[i] - x);
+            l[i] *= y;
+            m[i] = x;
+            if (!F8) {
+              f[i] = y;
+              moved = true;
+            }
+          }
+          if (F8 && z > mo[i] + 8.f) {
+            f[i] = ex2_approx(mo[i] - z);
+            mo[i] = z;
+            moved = true;
+          }
+        }
+        if (__any_sync(kAll, moved)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= f[0];
+            o[i][1] *= f[0];
+            o[i][2] *= f[1];
+            o[i][3] *= f[1];
+          }
+        }
+        // weights: bf16 in two terms (p and what its rounding left), fp16 in one
+        uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float base = m[i] == -INFINITY ? 0.f : m[i];
+            const float a = ex2_approx(fmaf(s[n][2 * i], sc[i], -base));
+            const float b = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], -base));
+            l[i] += a + b;
             if constexpr (F8) {
-              // columns 64 cg + 16 t + 8 y + (0 .. 7)
+              const float bo = mo[i] == -INFINITY ? 0.f : mo[i];
+              const float x = ex2_approx(fmaf(s[n][2 * i], sc[i], ve[n][0] - bo));
+              const float y = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], ve[n][1] - bo));
+              hi[n >> 1][2 * (n & 1) + i] = pack_f16x2(x, y);
+            } else {
+              const uint32_t h = pack_bf16x2(a, b);
+              hi[n >> 1][2 * (n & 1) + i] = h;
+              lo[n >> 1][2 * (n & 1) + i] =
+                  pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+            }
+          }
+        const uint32_t vb0 = ring + sv * C::TILE + v_at0, vb1 = ring + sv * C::TILE + v_at1;
 #pragma unroll
-              for (int cg = 0; cg < D / 64; ++cg)
+        for (int kk = 0; kk < 2; ++kk) {  // 16 keys each
+            const uint32_t at = 16 * kk * C::ROW;
+            if constexpr (F8) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  uint32_t v[4];
+              for (int cg = 0; cg < D / 64; ++cg) {
+                // eight columns 64 cg + 8 g + i of keys 2t, 2t + 1, 2t + 8, 2t + 9
+                const uint32_t box = (cg * 64 / C::ROW) * C::BOX + at, x64 = cg * 64 % C::ROW;
+                const uint2 w0 = lds64((vb0 ^ x64) + box), w1 = lds64((vb1 ^ x64) + box);
+                const uint2 w2 = lds64((vb0 ^ x64) + box + 8 * C::ROW), w3 = lds64((vb1 ^ x64) + box + 8 * C::ROW);
 #pragma unroll
-                  for (int z = 0; z < 4; ++z)
-                    v[z] = pack_bf16x2(o[8 * cg + 2 * z][2 * i + y] * inv, o[8 * cg + 2 * z + 1][2 * i + y] * inv);
-                  *reinterpret_cast<uint4*>(dst + 2 * (64 * cg + 16 * t + 8 * y)) = make_uint4(v[0], v[1], v[2], v[3]);
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t a0 = h ? w0.y : w0.x, a1 = h ? w1.y : w1.x, a2 = h ? w2.y : w2.x, a3 = h ? w3.y : w3.x;
+                  uint32_t b0[4], b1[4];
+                  e4m3_to_f16(__byte_perm(a0, a1, 0x5140), b0[0], b0[1]);
+                  e4m3_to_f16(__byte_perm(a0, a1, 0x7362), b0[2], b0[3]);
+                  e4m3_to_f16(__byte_perm(a2, a3, 0x5140), b1[0], b1[1]);
+                  e4m3_to_f16(__byte_perm(a2, a3, 0x7362), b1[2], b1[3]);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    mma16816_f16(o[8 * cg + 4 * h + i], hi[kk], b0[i], b1[i]);
                 }
+              }
             } else {
 #pragma unroll
-              for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint32_t*>(dst + 2 * (8 * c + 2 * t)) =
-                    pack_bf16x2(o[c][2 * i] * inv, o[c][2 * i + 1] * inv);
+              for (int c = 0; c < D / 8; c += 2) {
+                uint32_t r[4];
+                ldmatrix4_trans((vb0 ^ (16 * (c & 7))) + (c >> 3) * C::BOX + at, r);
+                mma16816(o[c], hi[kk], r[0], r[1]);
+                mma16816(o[c + 1], hi[kk], r[2], r[3]);
+                mma16816(o[c], lo[kk], r[0], r[1]);
+                mma16816(o[c + 1], lo[kk], r[2], r[3]);
+              }
             }
-            if (t == 0)
-              p.out.lse[tok * p.out.H_q + head] = sum[i] == 0.f ? -INFINITY : top[i] * kLn2F + logf(sum[i]);
+        }
+      }
+      __syncwarp();
+      issue(2 * j + 1 + C::RING, sv);
+    }
+    copy_wait<0>();
+
+    // Join the four warps' (m, l, O): each leaves its own in its ring, which nothing
+    // uses any more, then every thread adds up four columns of a row at a time.
+    constexpr int LD = D + 8;  // floats of a row there: neighbouring rows start 8 banks apart
+    float* own = reinterpret_cast<float*>(smem + warp * C::RING * C::TILE);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(kAll, l[i], 1);
+      l[i] += __shfl_xor_sync(kAll, l[i], 2);
+      const int row = g + 8 * i;
+      // O's unit is 2^m, e4m3: 2^mo
+      if (t == 0) ml[warp * kFewRows + row] = make_float4(m[i], l[i], F8 ? mo[i] : m[i], 0.f);
+      if constexpr (F8) {
+        // columns 64 cg + 16 t + 8 y + (0 .. 7)
+#pragma unroll
+        for (int cg = 0; cg < D / 64; ++cg)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              *reinterpret_cast<float4*>(own + row * LD + 64 * cg + 16 * t + 8 * y + 4 * z) =
+                  make_float4(o[8 * cg + 4 * z][2 * i + y], o[8 * cg + 4 * z + 1][2 * i + y],
+                              o[8 * cg + 4 * z + 2][2 * i + y], o[8 * cg + 4 * z + 3][2 * i + y]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<float2*>(own + row * LD + 8 * c + 2 * t) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
+      }
+    }
+    __syncthreads();
+    {
+      const int row = threadIdx.x >> 3, c0 = threadIdx.x & 7, x = u.g0 + row;
+      if (row < u.nrows) {
+        float top = -INFINITY, sum = 0.f, w[kFewWarps];
+#pragma unroll
+        for (int k = 0; k < kFewWarps; ++k) top = fmaxf(top, ml[k * kFewRows + row].x);
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int k = 0; k < kFewWarps; ++k) {
+          const float4 v = ml[k * kFewRows + row];
+          sum += ex2_approx(v.x - base) * v.y;
+          w[k] = ex2_approx(v.z - base);
+        }
+        const bool whole = walk.whole();
+        const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        const int64_t tok = u.tok + x / G;
+        const int head = walk.h * G + x % G;
+        char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
+        float* part = p.w.part + p.w.part_floats * (2 * (size_t)blockIdx.x + walk.slot());
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const int col = 4 * (c0 + 8 * c);
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kFewWarps; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(
+                reinterpret_cast<const float*>(smem + k * C::RING * C::TILE) + row * LD + col);
+            a.x += w[k] * v.x;
+            a.y += w[k] * v.y;
+            a.z += w[k] * v.z;
+            a.w += w[k] * v.w;
+          }
+          if (whole)
+            *reinterpret_cast<uint2*>(dst + 2 * col) =
+                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          else
+            *reinterpret_cast<float4*>(part + (size_t)row * D + col) = a;
+        }
+        if (c0 == 0) {
+          if (whole) {
+            p.out.lse[tok * p.out.H_q + head] = sum == 0.f ? -INFINITY : top * kLn2F + logf(sum);
           } else {
-            float* dst = part + (size_t)row * D;
-            if constexpr (F8) {
-#pragma unroll
-              for (int cg = 0; cg < D / 64; ++cg)
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                  for (int z = 0; z < 2; ++z)
-                    *reinterpret_cast<float4*>(dst + 64 * cg + 16 * t + 8 * y + 4 * z) =
-                        make_float4(o[8 * cg + 4 * z][2 * i + y], o[8 * cg + 4 * z + 1][2 * i + y],
-                                    o[8 * cg + 4 * z + 2][2 * i + y], o[8 * cg + 4 * z + 3][2 * i + y]);
-            } else {
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<float2*>(dst + 8 * c + 2 * t) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
-            }
-            if (t == 0) {
-              part[(size_t)kFewRows * D + 2 * row] = top[i];
-              part[(size_t)kFewRows * D + 2 * row + 1] = sum[i];
-            }
+            part[(size_t)kFewRows * D + 2 * row] = top;
+            part[(size_t)kFewRows * D + 2 * row + 1] = sum;
           }
         }
       }
     }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------------- joining
 struct JoinParams {
   PagedWork w;
   PagedOut out;
-  int ctas, G, rows;  // rows of a slot
+  int G, rows;  // rows of a slot
 };
 
 // Block (c, y): where CTA c's range is the second one inside a unit and head,
 // their parts (CTA c - 1's last segment, then c .. last's first segments) are
-// joined, 8 rows a block, a row a warp. Parts are weighed 32 at a time (a lane
-// each), then read one after the other with their loads in flight together.
+// joined, a row (d = 64: two) a warp, four parts' loads in flight at a time.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
+  constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
   grid_dependency_wait();
   const int c = blockIdx.x + 1;
-  const PagedStart st = p.w.starts[c];
+  const PagedStart& st = p.w.starts[c];
   if (st.count <= 0 || st.kt == 0 || st.first != c - 1) return;
-  const PagedUnit u = p.w.units[st.u];
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= u.nrows) return;
+  const int lane = threadIdx.x & 31, col = 4 * (lane % LPR);
+  const int row = (blockIdx.y * 8 + (threadIdx.x >> 5)) * RPW + lane / LPR;
+  if (row >= st.unit.nrows) return;
   const size_t ml = (size_t)p.rows * D + 2 * row;
   const int parts = st.last - c + 2;
   // part i: slot 1 of CTA c - 1 (i = 0), slot 0 of CTA c - 1 + i
   auto part = [&](int i) { return p.w.part + p.w.part_floats * (2 * (size_t)(c - 1 + i) + (i == 0 ? 1 : 0)); };
-  float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, part(i)[ml]);
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[V];
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc[D / 32];
+  for (int x = 0; x < V; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < parts; i0 += 4) {
+    float2 w[4];
+    float4 v[4][V];
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) acc[x] = 0.f;
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    const int n = min(32, parts - i0);
-    float f = 0.f, l = 0.f;
-    if (lane < n) {
-      const float* s = part(i0 + lane);
-      f = ex2_approx(s[ml] - base);
-      l = f * s[ml + 1];
+    for (int k = 0; k < 4; ++k) {
+      w[k] = make_float2(-INFINITY, 0.f);
+      if (i0 + k < parts) {
+        const float* s = part(i0 + k);
+        w[k] = *reinterpret_cast<const float2*>(s + ml);
+#pragma unroll
+        for (int x = 0; x < V; ++x)
+          v[k][x] = *reinterpret_cast<const float4*>(s + (size_t)row * D + 4 * LPR * x + col);
+      }
     }
-    for (int i = 0; i < n; i += 8) {
-      float2 v[8][D / 64];
+    const float t = fmaxf(fmaxf(top, fmaxf(w[0].x, w[1].x)), fmaxf(w[2].x, w[3].x));
+    const float base = t == -INFINITY ? 0.f : t;
+    const float f = ex2_approx(top - base);
+    top = t;
+    sum *= f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i + k < n) {
-          const float* s = part(i0 + i + k) + (size_t)row * D + 2 * lane;
+    for (int x = 0; x < V; ++x) acc[x] = make_float4(acc[x].x * f, acc[x].y * f, acc[x].z * f, acc[x].w * f);
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x) v[k][x] = *reinterpret_cast<const float2*>(s + 64 * x);
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k < parts) {
+        const float y = ex2_approx(w[k].x - base);
+        sum += y * w[k].y;
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          acc[x].x += y * v[k][x].x;
+          acc[x].y += y * v[k][x].y;
+          acc[x].z += y * v[k][x].z;
+          acc[x].w += y * v[k][x].w;
         }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i + k < n) {
-          const float w = __shfl_sync(kAll, f, i + k);
-          sum += __shfl_sync(kAll, l, i + k);
-#pragma unroll
-          for (int x = 0; x < D / 64; ++x) {
-            acc[2 * x] += w * v[k][x].x;
-            acc[2 * x + 1] += w * v[k][x].y;
-          }
-        }
-    }
+      }
   }
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  const int x0 = u.g0 + row;
-  const int64_t tok = u.tok + x0 / p.G;
+  const int x0 = st.unit.g0 + row;
+  const int64_t tok = st.unit.tok + x0 / p.G;
   const int head = st.h * p.G + x0 % p.G;
   char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
 #pragma unroll
-  for (int x = 0; x < D / 64; ++x)
-    *reinterpret_cast<uint32_t*>(dst + 2 * (64 * x + 2 * lane)) = pack_bf16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv);
-  if (lane == 0) p.out.lse[tok * p.out.H_q + head] = sum == 0.f ? -INFINITY : top * kLn2F + logf(sum);
+  for (int x = 0; x < V; ++x)
+    *reinterpret_cast<uint2*>(dst + 2 * (4 * LPR * x + col)) =
+        make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+  if (col == 0) p.out.lse[tok * p.out.H_q + head] = sum == 0.f ? -INFINITY : top * kLn2F + logf(sum);
 }
 
 template <int D>
 cudaError_t launch_join(const PagedShape& s, const PagedWork& w, const PagedOut& out, int rows, cudaStream_t st) {
-  JoinParams j{w, out, s.ctas, s.G, rows};
-  const dim3 grid((unsigned)(s.ctas - 1), (unsigned)((rows + 7) / 8));
+  JoinParams j{w, out, s.G, rows};
+  const int per = 8 * (D == 64 ? 2 : 1);  // rows of a block
+  const dim3 grid((unsigned)(s.ctas - 1), (unsigned)((rows + per - 1) / per));
   if (s.ctas < 2) return cudaSuccess;
   count_launches(1);
   return launch_dependent(join_kernel<D>, grid, 256, 0, st, j);
@@ -840,11 +788,14 @@ cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cach
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(few_kernel<D, F8>), C::SMEM, ready);
   if (e != cudaSuccess) return e;
   FewParams p{s, w, static_cast<const char*>(q.ptr), q.st, q.sh, out,
-              {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, b.page_table,
+              {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, b.q_off, b.kv_len, b.page_table,
               scale * 1.4426950408889634f, err};
   count_launches(1);
   return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), kFewThreads, C::SMEM, st, p);
 }
+
+// tiles of a unit up to which it is not divided
+constexpr int kWholeFew = 8, kWholeChunk = 0;
 
 // Which kernel: chunk_kernel's tiles of 128 rows once the sequences have more
 // than 16 rows a KV head on average (few_kernel would read the keys again for
@@ -879,6 +830,13 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   s.least = chunk ? 1 : kFewWarps;  // a tile for each computing warp, and fewer parts to join
   s.ctas = sm_count() * (chunk || c.d == 256 ? 1 : 2);
   s.max_units = ((long long)T * s.G + s.step - 1) / s.step + b.R;
+  // Each CTA plans for itself where that is a few steps a thread; a plan kernel
+  // (one CTA, about 4 us of the stream) for larger batches.
+  const long long most = ((long long)b.width * s.page + s.tile - 1) / s.tile;  // tiles of a unit
+  s.local = b.R <= (chunk ? kLocalChunks : kLocalSeqs) && s.max_units <= kLocalUnits &&
+            s.max_units * most * s.H_kv * (s.ctas + 1) < (1ll << 31);
+  // Units of few tiles stay whole: one CTA takes less time for them than joining does.
+  s.whole = s.local && most <= (chunk ? kWholeChunk : kWholeFew);
   return s;
 }
 
@@ -900,11 +858,13 @@ cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, i
   const PagedShape s = shape_of(c, b, T, H_q, causal, window, sinks, chunk);
   const PagedWork w = paged_work(s, rows, ws);
   const PagedOut out{static_cast<char*>(o.ptr), o.st, o.sh, lse, H_q};
-  PlanParams pp{s, b.q_off, b.kv_len, w, err};
-  plan_kernel<<<1, kPlanThreads, 0, st>>>(pp);
-  count_launches(1);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!s.local) {
+    const PlanParams pp{s, b.q_off, b.kv_len, w, err};
+    count_launches(1);
+    e = launch_dependent(plan_kernel, dim3(1), kPlanThreads, 0, st, pp);
+    if (e != cudaSuccess) return e;
+  }
   const bool f8 = c.k_exp != nullptr;
   if (chunk)
     e = launch_paged_chunk(s, w, c, b, q, out, scale, st, err);
@@ -917,7 +877,7 @@ cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, i
   else
     e = f8 ? launch_few<256, true>(s, w, c, b, q, out, scale, st, err)
            : launch_few<256, false>(s, w, c, b, q, out, scale, st, err);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || s.whole) return e;
   return c.d == 64    ? launch_join<64>(s, w, out, rows, st)
          : c.d == 128 ? launch_join<128>(s, w, out, rows, st)
                       : launch_join<256>(s, w, out, rows, st);

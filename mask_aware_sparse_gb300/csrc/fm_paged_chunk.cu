@@ -72,6 +72,8 @@ struct ChunkParams {
   PagedOut out;
   const uint8_t* k_exp;
   const uint8_t* v_exp;
+  const int32_t* q_off;
+  const int32_t* kv_len;
   const int32_t* table;
   int tile_rows;  // rows of a query tile: whole tokens, at most 128
   float scale_log2;
@@ -139,11 +141,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  __shared__ PagedStart start;
+  __shared__ int4 seq[kLocalChunks];
   grid_dependency_wait();
   grid_launch_dependents();
+  if (p.s.local) {
+    // (the work list lies where the first keys will)
+    plan_locally(p.s, p.q_off, p.kv_len, seq, reinterpret_cast<unsigned*>(smem + C::K_OFF), &start, p.err);
+    if (threadIdx.x == 0 && !p.s.whole) p.w.starts[blockIdx.x] = start;  // for join_kernel
+    fence_proxy_async_smem();
+  } else {
+    if (threadIdx.x == 0) start = p.w.starts[blockIdx.x];
+  }
+  __syncthreads();
   const int G = p.s.G, TR = p.tile_rows;
   bool ok = *abort_flag == 0;
-  PagedWalk walk(p.w.units, p.w.starts[blockIdx.x], p.s.H_kv);
+  PagedWalk walk(p.s, p.w.units, seq, start);
 
   if (!ok) {
     // an unread timeout of an earlier launch: nothing is computed
@@ -583,7 +596,7 @@ cudaError_t launch(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c
   if (!make_tmap_tokens(&tq, q, s.T, s.H_kv, s.G, D, tokens) ||
       !make_tmap_pages(&tk, c.k, c, rows, F8 ? D : 128) || !make_tmap_pages(&tv, c.v, c, rows, F8 ? D : 128))
     return cudaErrorInvalidValue;
-  ChunkParams p{s, w, out, c.k_exp, c.v_exp, b.page_table, tokens * s.G, scale * 1.4426950408889634f, err};
+  ChunkParams p{s, w, out, c.k_exp, c.v_exp, b.q_off, b.kv_len, b.page_table, tokens * s.G, scale * 1.4426950408889634f, err};
   count_launches(1);
   return launch_dependent(chunk_kernel<D, F8>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, tq, tk, tv, p);
 }

@@ -26,10 +26,14 @@ struct __align__(16) PagedUnit {
   int ntiles, kv_len, lo, pad;  // lo: keys below it are visible as sinks only
 };
 
+// A CTA's range: `count` tiles from tile kt of head h of a unit on. The unit is
+// number u of the plan kernel's list, or, where each CTA plans for itself, unit i
+// of sequence u.
 struct __align__(16) PagedStart {
-  int u, h, kt, count;  // a CTA's first unit, head and tile, and its number of tiles
-  int first, last;      // where kt > 0: the first and the last CTA with tiles of that unit and head
-  int pad[2];
+  int u, i, h, kt, count;
+  int first, last;  // where kt > 0: the first and the last CTA with tiles of that unit and head
+  int pad;
+  PagedUnit unit;
 };
 
 struct PagedShape {
@@ -37,25 +41,164 @@ struct PagedShape {
   int causal, window, sinks;  // window 0: none
   int step, tile;  // query rows of a unit, keys of a tile
   int ctas, least;  // CTAs launched; tiles a CTA gets before another one does
+  int local;  // every CTA plans for itself: no plan kernel
+  int whole;  // (local) no unit and head is divided: nothing to join
   long long max_units;
 };
 
 // Tile number kt of a unit's list.
 __device__ __forceinline__ int tile_of(const PagedUnit& u, int kt) { return kt < u.ns ? kt : kt - u.ns + u.w0; }
 
+// The new tokens of sequence r, [a, a + n), kept inside [0, T] whatever q_off
+// holds, and its keys, kept inside the page table; true where either was not.
+__device__ __forceinline__ bool sequence_at(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int r,
+                                            int& a, int& n, int& L) {
+  const int b0 = q_off[r], e0 = q_off[r + 1], L0 = kv_len[r];
+  a = min(max(b0, 0), s.T);
+  const int e = min(max(e0, a), s.T);
+  n = e - a;
+  L = min(max(L0, 0), s.width * s.page);
+  return a != b0 || e != e0 || L != L0;
+}
+
+// Unit i of a sequence.
+__device__ __forceinline__ PagedUnit unit_at(const PagedShape& s, int r, int a, int n, int L, int i) {
+  const int row0 = i * s.step, tok = row0 / s.G;  // T * H_q stays below 2^30
+  PagedUnit q;
+  q.r = r;
+  q.tok = a + tok;
+  q.g0 = row0 - tok * s.G;
+  q.nrows = min(s.step, n * s.G - row0);
+  q.pos = L - n + tok;
+  q.kv_len = L;
+  const int last = q.pos + (q.g0 + q.nrows - 1) / s.G;
+  q.hi = s.causal ? min(max(last + 1, 0), L) : L;
+  q.lo = s.window > 0 ? max(0, q.pos - s.window + 1) : 0;
+  const int all = (q.hi + s.tile - 1) / s.tile;
+  q.ns = s.window > 0 ? min((s.sinks + s.tile - 1) / s.tile, all) : 0;
+  q.w0 = max(q.ns, min(q.lo / s.tile, all));
+  q.ntiles = q.ns + max(0, all - q.w0);
+  q.pad = 0;
+  return q;
+}
+
+// How many CTAs get ranges, [c total / used, (c + 1) total / used): all of them, or
+// as many as get s.least tiles each; and, for the tiles [f0, f0 + nt) of a unit and
+// head, the CTAs that share them: the CTA of tile x is the last c with
+// floor(c total / used) <= x. (I: unsigned where 32 bits hold ctas * total.)
+template <typename I>
+__device__ __forceinline__ I used_ctas(const PagedShape& s, I total) {
+  return max((I)1, min((I)s.ctas, total / (I)s.least));
+}
+template <typename I>
+__device__ __forceinline__ void sharers(PagedStart& st, I f0, I nt, I total, I used) {
+  st.first = (int)(((f0 + 1) * used - 1) / total);
+  st.last = (int)(((f0 + nt) * used - 1) / total);
+}
+
+// The plan as one CTA makes it for itself, for a few hundred units at most and a
+// total work that 32 bits hold: every sequence into seq (first token, tokens,
+// keys, units), its work into work (both shared memory, R entries), the CTA's
+// range into *out (shared memory).
+__device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int4* seq,
+                                             unsigned* work, PagedStart* out, int* err) {
+  bool bad = false;
+  for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
+    int a, n, L;
+    bad |= sequence_at(s, q_off, kv_len, r, a, n, L);
+    const int units = (n * s.G + s.step - 1) / s.step;
+    unsigned w = 0;
+    for (int i = 0; i < units; ++i) w += max(unit_at(s, r, a, n, L, i).ntiles, 1);
+    seq[r] = make_int4(a, n, L, units);
+    work[r] = w * s.H_kv;
+  }
+  if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
+  if (threadIdx.x == 0) *out = PagedStart{};
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (s.R + 31) / 32, r0 = lane * per, r1 = min(s.R, r0 + per);
+    unsigned mine = 0;
+    for (int r = r0; r < r1; ++r) mine += work[r];
+    unsigned upto = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, upto, m);
+      if (lane >= m) upto += x;
+    }
+    const unsigned total = __shfl_sync(0xffffffffu, upto, 31), used = used_ctas(s, total), c = blockIdx.x;
+    const bool some = c < used && total > 0;
+    const unsigned f = some ? total * c / used : 0, g = some ? total * (c + 1) / used : 0;
+    // tile x lies in this lane's sequences: sequence, unit, head and tile of it; the
+    // first tile of that unit and head into at; their number of tiles
+    auto find = [&](unsigned x, PagedStart& st, unsigned& at) -> unsigned {
+      at = upto - mine;
+      int r = r0;
+      while (r < r1 - 1 && at + work[r] <= x) at += work[r++];
+      const int4 q = seq[r];
+      unsigned nt = 1;
+      int i = 0;
+      for (;; ++i) {
+        st.unit = unit_at(s, r, q.x, q.y, q.z, i);
+        nt = max(st.unit.ntiles, 1);
+        if (i + 1 >= q.w || at + nt * s.H_kv > x) break;
+        at += nt * s.H_kv;
+      }
+      st.u = r;
+      st.i = i;
+      st.h = (x - at) / nt;
+      at += st.h * nt;
+      st.kt = x - at;
+      return nt;
+    };
+    auto holds = [&](unsigned x) { return some && x < total && upto - mine <= x && x < upto; };
+    // undivided units: a range begins and ends with the first unit and head at or after its ends
+    unsigned end = g;
+    if (s.whole) {
+      unsigned up = 0;
+      if (holds(g)) {
+        PagedStart st;
+        const unsigned nt = find(g, st, up);
+        up = st.kt ? up + nt : g;
+      }
+      end = max(g, __reduce_max_sync(0xffffffffu, up));
+    }
+    if (holds(f)) {
+      PagedStart st = {};
+      unsigned at, from = f;
+      const unsigned nt = find(f, st, at);
+      if (s.whole && st.kt) {
+        from = at + nt;
+        st.kt = 0;
+        if (++st.h == s.H_kv && from < end) {
+          st.h = 0;
+          int4 q = seq[st.u];
+          if (++st.i >= q.w) {
+            st.i = 0;
+            do q = seq[++st.u];
+            while (q.w == 0 && st.u + 1 < s.R);
+          }
+          st.unit = unit_at(s, st.u, q.x, q.y, q.z, st.i);
+        }
+      } else if (st.kt) {
+        sharers(st, at, nt, total, used);
+      }
+      st.count = (int)(end - from);
+      *out = st;
+    }
+  }
+  __syncthreads();
+}
+
 // A CTA's walk over its range of tiles: one (unit, head) at a time.
 struct PagedWalk {
-  const PagedUnit* units;
-  int H_kv, left;
-  int ui, h, kt, n;  // current segment: tiles [kt, kt + n) of unit ui, head h (n 0: a unit without keys)
+  const PagedShape& s;
+  const PagedUnit* units;  // the plan kernel's list
+  const int4* seq;         // or this CTA's own sequences
+  int left, at, i, h, kt, n;  // current segment: tiles [kt, kt + n) of head h (n 0: a unit without keys)
   PagedUnit u;
 
-  __device__ PagedWalk(const PagedUnit* units_, const PagedStart& s, int H_kv_)
-      : units(units_), H_kv(H_kv_), left(s.count), ui(s.u), h(s.h), kt(s.kt), n(0) {
-    if (left > 0) load();
-  }
-  __device__ void load() {
-    u = units[ui];
+  __device__ PagedWalk(const PagedShape& s_, const PagedUnit* units_, const int4* seq_, const PagedStart& st)
+      : s(s_), units(units_), seq(seq_), left(st.count), at(st.u), i(st.i), h(st.h), kt(st.kt), u(st.unit) {
     n = min(u.ntiles - kt, left);
   }
   __device__ bool more() const { return left > 0; }
@@ -66,15 +209,27 @@ struct PagedWalk {
     left -= max(n, 1);
     if (left <= 0) return;
     kt = 0;
-    if (++h == H_kv) {
+    if (++h == s.H_kv) {
       h = 0;
-      ++ui;
-      load();
-    } else {
-      n = min(u.ntiles, left);
+      if (s.local) {
+        int4 q = seq[at];
+        if (++i >= q.w) {
+          i = 0;
+          do q = seq[++at];
+          while (q.w == 0 && at + 1 < s.R);
+        }
+        u = unit_at(s, at, q.x, q.y, q.z, i);
+      } else {
+        u = units[++at];
+      }
     }
+    n = min(u.ntiles, left);
   }
 };
+
+constexpr int kLocalSeqs = 256;   // few_kernel: sequences that a CTA plans for by itself
+constexpr int kLocalChunks = 64;  // chunk_kernel: the same (its shared memory is nearly full)
+constexpr int kLocalUnits = 512;  // units, at most: a thread counts those of its sequences one by one
 
 // Workspace of one call: units, the running sum of their work, CTA starts, the
 // partial slots (two a CTA: rows x d sums, then rows x (m, l)).

@@ -11,9 +11,9 @@
 //
 //   warps 0-3, 4-7  softmax of query tile 0, 1: a thread a row
 //   warp 8          producer (TMA); warp 9: MMA issue and TMEM
-//   warps 12-15     e4m3 caches: each key tile's bytes to bf16, times the row's
-//                   scale, exact (a thread a row), from a staging ring to the
-//                   bf16 ring the tensor core reads
+//   warps 12-15, 16-19  e4m3 caches: the bytes of a tile's keys, and of its values,
+//                   to bf16, times the row's scale, exact (a thread a row), from a
+//                   staging ring to the bf16 ring the tensor core reads
 //
 // TMEM: S_0, S_1 (128 columns each; P overwrites S as bf16), O_0, O_1. With two
 // query tiles the tensor core works on one while the softmax works on the
@@ -45,8 +45,14 @@ constexpr float kLn2C = 0.69314718055994530942f;
 
 template <int D, bool F8>
 struct ChunkCfg {
-  // e4m3: 16 warps at 128 registers, redistributed: 8 softmax warps x 184, 8 others x 72
-  static constexpr int THREADS = F8 ? 512 : 320;
+  // e4m3: warpgroups that widen tiles, and the registers that the launch's are
+  // redistributed into: d = 128: 20 warps at 96, 8 softmax warps at 168, 12 others
+  // at 48 (one group, 16 warps: a 2048-token chunk over 32768 keys 1515 us instead
+  // of 1145); d = 64, half as much to widen for each product: 16 warps at 128, 184
+  // and 72 (two groups: 8000 tokens over 9000 keys 348 us instead of 315)
+  static constexpr int WIDEN = !F8 ? 0 : D == 128 ? 2 : 1;
+  static constexpr int SOFTMAX_REGS = WIDEN == 2 ? 168 : 184, OTHER_REGS = WIDEN == 2 ? 48 : 72;
+  static constexpr int THREADS = F8 ? 384 + 128 * WIDEN : 320;
   static constexpr int TILE = 128 * D * 2;
   static constexpr int BOXES = D / 64;
   static constexpr int STAGES = D == 64 ? 4 : 2;
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   if (!ok) {
     // an unread timeout of an earlier launch: nothing is computed
   } else if (warp < 8) {
-    if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
     const int row = ((warp & 3) << 5) + lane;
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
       }
     }
   } else if (warp < 12) {
-    if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 8) {
       // ------------------------------------------------------------- producer
       const int P = p.s.page, rows = min(P, 128), per = 128 / rows;
@@ -517,29 +523,32 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
       }
     }
   } else if constexpr (F8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     // -------------------------------------------------- e4m3 tiles to bf16
     constexpr int ROW = D;  // bytes of a staged row: 128 or 64, swizzled as wide
-    const int row = threadIdx.x - 384;
+    const int row = threadIdx.x & 127;
     uint32_t jt = 0;
     for (; walk.more() && ok; walk.next()) {
       const PagedUnit& u = walk.u;
       for (int j = 0; j < walk.n && ok; ++j, ++jt) {
         const int key = tile_of(u, walk.kt + j) * 128 + row;
+        // rows that no query of the unit sees become zeros, whatever they hold
         const bool dead = !(key < u.hi && (key >= u.lo || key < p.s.sinks));
+        const uint32_t mag = dead ? 0u : 0x07f007f0u, sign = dead ? 0u : 0x80008000u;
+        // keys and values in turn, or, with two groups, keys the first and values the second
 #pragma unroll 1
-        for (int v = 0; v < 2 && ok; ++v) {
+        for (int v = (warp - 12) >> 2; v < 2 && ok; v += C::WIDEN) {
           const uint32_t ri = 2 * jt + v, rs = ri % C::RAWS;
           ok = __all_sync(kAll, mbar_wait(&bars[C::RFULL + rs], (ri / C::RAWS) & 1u, abort_flag, p.err));
           if (ok)
-            ok = __all_sync(kAll, mbar_wait(&bars[(v ? C::VEMPTY : C::KEMPTY) + jt % S], ((jt / S) & 1u) ^ 1u,
-                                            abort_flag, p.err));
+            ok = __all_sync(kAll, mbar_wait(&bars[(v ? C::VEMPTY : C::KEMPTY) + jt % S], ((jt / S) & 1u) ^ 1u, abort_flag,
+                                            p.err));
           if (!ok) break;
           const uint32_t src = smem_u32(smem + C::RAW_OFF + rs * C::RAW);
           const uint32_t dst = smem_u32(smem + (v ? C::V_OFF : C::K_OFF) + (jt % S) * C::TILE) + row * 128;
           const uint32_t e = lds8(smem_u32(smem + C::EXP_OFF) + rs * 128 + row);
-          const uint32_t fl = factor_lo(e) * 0x10001u, fh = factor_hi(e) * 0x10001u;
-          const bool wide = __any_sync(kAll, e > 134u && e < 255u);
+          const uint32_t fl = dead ? 0u : factor_lo(e) * 0x10001u;
+          const bool wide = __any_sync(kAll, !dead && e > 134u && e < 255u);
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const uint4 r = lds128(src + in_box<ROW>(row, c));
@@ -547,16 +556,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
             uint32_t o[8];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              o[2 * x] = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x1404)), fl);
-              o[2 * x + 1] = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x3424)), fl);
+              o[2 * x] = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x1404), mag, sign), fl);
+              o[2 * x + 1] = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x3424), mag, sign), fl);
             }
             if (wide) {
+              const uint32_t fh = factor_hi(e) * 0x10001u;
 #pragma unroll
               for (int x = 0; x < 8; ++x) o[x] = mul_bf2(o[x], fh);
-            }
-            if (dead) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] = 0u;
             }
             const uint32_t at = dst + (c >> 2) * 16384;
             const int ch = 2 * (c & 3);

@@ -147,13 +147,21 @@ __device__ __forceinline__ uint4* at(const View& v, int64_t b, int h, int64_t n,
   return reinterpret_cast<uint4*>(v.p + 2 * (b * v.sb + h * v.sh + n * v.sn + off));
 }
 
-// TB tokens per block and step, kWarps / TB warps on each. BWD: the backward.
+// TB tokens per block and step, kWarps / TB warps on each; blockIdx.y 0: queries,
+// 1: keys and values. BWD: the backward.
+//
+// Loads in flight bound it: two rows' groups ahead of the one computed (kAhead),
+// three blocks an SM (backward: two, with twice as much to load), weights in
+// shared memory to leave registers for that. One group ahead at 118 registers
+// (two blocks an SM) moved 4.8 TB/s at 65536 tokens of 80 heads, d = 128.
 template <int D, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p, const int TB) {
+__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParams p, const int TB) {
   using C = Chunks<D, INTER>;
   constexpr int TG = C::TG, HPW = 32 / TG;  // threads per row, rows per warp
+  constexpr int kAhead = 2;
   __shared__ __align__(16) float4 cs[kWarps * D / 4];  // TB <= kWarps tokens, rot <= D
   __shared__ unsigned long long frac[D / 2];
+  __shared__ float4 ws[D / 4];
   __shared__ float red[BWD ? kWarps * D : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % TG, hl = lane / TG;
@@ -162,12 +170,25 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p, const in
   const int tw = warp / wpt, w0 = warp - tw * wpt;  // this warp's token of the step, its place among the token's warps
   const int64_t total = (int64_t)p.B * p.N;
   const int RT = p.rot / 16;
-  float acc[2][BWD ? 16 : 1];  // weight gradients of this thread's 16 columns (q, k)
+  const bool keys = blockIdx.y != 0;
+  const View in = keys ? p.k : p.q, out = keys ? p.ko : p.qo, src = keys ? p.xk : p.xq;
+  const int H = keys ? p.H_kv : p.H_q;
+  const void* wp = keys ? p.wk : p.wq;
+  float acc[BWD ? 16 : 1];  // weight gradients of this thread's 16 columns
   if constexpr (BWD) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   }
   load_fractions(p, frac);
+  if (wp && threadIdx.x < TG) {
+    // slot j * TG + c: a quarter of thread c's sixteen weights
+    const C mine(threadIdx.x, p.rot);
+    for (int j = 0; j < 4; ++j) {
+      const int o = (j < 2 ? mine.oa : mine.ob) + 4 * (j & 1);
+      ws[j * TG + threadIdx.x] = make_float4(weight_at(wp, p.w_f32, o), weight_at(wp, p.w_f32, o + 1),
+                                             weight_at(wp, p.w_f32, o + 2), weight_at(wp, p.w_f32, o + 3));
+    }
+  }
   __syncthreads();
   for (int64_t tok0 = (int64_t)blockIdx.x * TB; tok0 < total; tok0 += (int64_t)gridDim.x * TB) {
     load_angles(p, frac, cs, TB, tok0, total);
@@ -186,95 +207,93 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p, const in
           si[2 * j + 1] = t.w;
         }
       }
-#pragma unroll
-      for (int kind = 0; kind < 3; ++kind) {  // q, k, v
-        if (kind == 2 && !p.has_v) break;
-        const View& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-        const View& out = kind == 0 ? p.qo : kind == 1 ? p.ko : p.vo;
-        const View& src = kind == 0 ? p.xq : p.xk;
-        const int H = kind == 0 ? p.H_q : p.H_kv;
-        const void* wp = kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr;
-        float wa[8], wb[8];
-        if (wp) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            wa[i] = weight_at(wp, p.w_f32, ch.oa + i);
-            wb[i] = weight_at(wp, p.w_f32, ch.ob + i);
+      const int groups = (H + HPW - 1) / HPW;
+      // the next rows' loads are in flight while these are computed (a row is
+      // read and written by the same threads, so in and out may be one tensor)
+      uint4 ra[kAhead], rb[kAhead], xa[BWD ? kAhead : 1], xb[BWD ? kAhead : 1];
+      auto fetch = [&](int k, int g) {
+        const int h = g * HPW + hl;
+        if (h < H) {
+          ra[k] = *at(in, b, h, n, ch.oa);
+          rb[k] = *at(in, b, h, n, ch.ob);
+          if constexpr (BWD) {
+            if (wp) {
+              xa[k] = *at(src, b, h, n, ch.oa);
+              xb[k] = *at(src, b, h, n, ch.ob);
+            }
           }
         }
-        // the next rows' loads are in flight while these are computed (a row is
-        // read and written by the same threads, so in and out may be one tensor)
-        uint4 ra = {}, rb = {}, xa = {}, xb = {};
-        auto fetch = [&](int g) {
-          const int h = g * HPW + hl;
-          if (h < H) {
-            ra = *at(in, b, h, n, ch.oa);
-            rb = *at(in, b, h, n, ch.ob);
-            if (BWD && wp) {
-              xa = *at(src, b, h, n, ch.oa);
-              xb = *at(src, b, h, n, ch.ob);
-            }
-          }
-        };
-        const int groups = (H + HPW - 1) / HPW;
-        fetch(w0);
-        for (int g = w0; g < groups; g += wpt) {
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        ra[k] = rb[k] = make_uint4(0, 0, 0, 0);
+        if constexpr (BWD) xa[k] = xb[k] = make_uint4(0, 0, 0, 0);
+        fetch(k, w0 + k * wpt);
+      }
+      for (int g0 = w0; g0 < groups; g0 += kAhead * wpt) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int g = g0 + k * wpt;
+          if (g >= groups) break;
           const int h = g * HPW + hl;
           const bool live = h < H;
-          if (kind == 2) {
-            const uint4 ca = ra, cb = rb;
-            if (g + wpt < groups) fetch(g + wpt);
-            if (live) {
-              *at(out, b, h, n, ch.oa) = ca;
-              *at(out, b, h, n, ch.ob) = cb;
-            }
-            continue;
-          }
           float fa[8], fb[8];
-          unpack8(ra, fa);
-          unpack8(rb, fb);
+          unpack8(ra[k], fa);
+          unpack8(rb[k], fb);
           if constexpr (!BWD) {
-            if (g + wpt < groups) fetch(g + wpt);
+            fetch(k, g + kAhead * wpt);
             if (wp) {
               float ss = 0.f;
 #pragma unroll
               for (int i = 0; i < 8; ++i) ss += fa[i] * fa[i] + fb[i] * fb[i];
               const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                fa[i] = fa[i] * r * wa[i];
-                fb[i] = fb[i] * r * wb[i];
+              for (int j = 0; j < 4; ++j) {
+                const float4 w = ws[j * TG + c];
+                float* f = j < 2 ? fa + 4 * j : fb + 4 * (j - 2);
+                f[0] *= r * w.x;
+                f[1] *= r * w.y;
+                f[2] *= r * w.z;
+                f[3] *= r * w.w;
               }
             }
             if (ch.turned) turn<INTER, 1>(fa, fb, co, si);
           } else {
             float va[8], vb[8];
             if (wp) {
-              unpack8(xa, va);
-              unpack8(xb, vb);
+              unpack8(xa[k], va);
+              unpack8(xb[k], vb);
             }
-            if (g + wpt < groups) fetch(g + wpt);
+            fetch(k, g + kAhead * wpt);
             if (ch.turned) turn<INTER, -1>(fa, fb, co, si);
             if (wp) {
               float ss = 0.f, sg = 0.f;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                ss += va[i] * va[i] + vb[i] * vb[i];
-                sg += fa[i] * wa[i] * va[i] + fb[i] * wb[i] * vb[i];
-              }
+              for (int i = 0; i < 8; ++i) ss += va[i] * va[i] + vb[i] * vb[i];
               const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
-              const float t = row_sum<D>(sg) * (1.f / D) * r * r * r;
               if (live) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  acc[kind & 1][i] += fa[i] * va[i] * r;
-                  acc[kind & 1][8 + i] += fb[i] * vb[i] * r;
+                  acc[i] += fa[i] * va[i] * r;
+                  acc[8 + i] += fb[i] * vb[i] * r;
                 }
               }
 #pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 w = ws[j * TG + c];
+                float* f = j < 2 ? fa + 4 * j : fb + 4 * (j - 2);
+                const float* v = j < 2 ? va + 4 * j : vb + 4 * (j - 2);
+                f[0] *= w.x;
+                f[1] *= w.y;
+                f[2] *= w.z;
+                f[3] *= w.w;
+                sg += f[0] * v[0] + f[1] * v[1] + f[2] * v[2] + f[3] * v[3];
+              }
+              const float t = row_sum<D>(sg) * (1.f / D) * r * r * r;
+#pragma unroll
               for (int i = 0; i < 8; ++i) {
-                fa[i] = r * fa[i] * wa[i] - va[i] * t;
-                fb[i] = r * fb[i] * wb[i] - vb[i] * t;
+                fa[i] = r * fa[i] - va[i] * t;
+                fb[i] = r * fb[i] - vb[i] * t;
               }
             }
           }
@@ -284,17 +303,25 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p, const in
           }
         }
       }
+      if (keys && p.has_v) {
+        for (int g = w0; g < groups; g += wpt) {
+          const int h = g * HPW + hl;
+          if (h < H) {
+            const uint4 x = *at(p.v, b, h, n, 16 * c), y = *at(p.v, b, h, n, 16 * c + 8);
+            *at(p.vo, b, h, n, 16 * c) = x;
+            *at(p.vo, b, h, n, 16 * c + 8) = y;
+          }
+        }
+      }
     }
     __syncthreads();
   }
   if constexpr (BWD) {
     // one fixed order: lanes of a warp, then warps, then (next kernel) blocks
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      if (!(kind ? p.wk : p.wq)) continue;
+    if (wp) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float v = acc[kind][i];
+        float v = acc[i];
 #pragma unroll
         for (int m = TG; m < 32; m <<= 1) v += __shfl_xor_sync(kAll, v, m);
         if (hl == 0) red[warp * D + (i < 8 ? ch.oa + i : ch.ob + i - 8)] = v;
@@ -303,9 +330,8 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const QkParams p, const in
       for (int i = threadIdx.x; i < D; i += kThreads) {
         float v = 0.f;
         for (int w = 0; w < kWarps; ++w) v += red[w * D + i];
-        p.part[((int64_t)blockIdx.x * 2 + kind) * D + i] = v;
+        p.part[((int64_t)blockIdx.x * 2 + (keys ? 1 : 0)) * D + i] = v;
       }
-      __syncthreads();
     }
   }
 }
@@ -344,18 +370,18 @@ int tokens_per_step(int64_t total) {
   while (tb < kWarps && total >= 2ll * tb * 4 * sm_count()) tb *= 2;
   return tb;
 }
-// The forward keeps eight blocks an SM busy; the backward has a partial row per
-// block, so its grid is what an SM holds at once.
+// Two columns of blocks, queries and keys (with values); the backward has a
+// partial row per block, so its grid is what an SM holds at once.
 int grid_blocks(int64_t total, int tb, int per_sm) {
   const int64_t steps = (total + tb - 1) / tb;
   const int64_t most = (int64_t)sm_count() * per_sm;
   return (int)(steps < most ? steps : most);
 }
-constexpr int kBwdPerSm = 3;
+constexpr int kFwdPerSm = 8, kBwdPerSm = 2;
 
 template <bool BWD>
 cudaError_t launch_qk(const fm_qk_problem& P, const QkParams& p, int grid, int tb, cudaStream_t s) {
-  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p, tb); };
+  auto go = [&](auto kernel) { kernel<<<dim3((unsigned)grid, 2), kThreads, 0, s>>>(p, tb); };
   if (P.d == 64)
     P.interleaved ? go(qk_kernel<64, true, BWD>) : go(qk_kernel<64, false, BWD>);
   else if (P.d == 128)
@@ -398,7 +424,7 @@ cudaError_t launch_qk_fwd(const fm_qk_problem& P, const fm_view* q, const fm_vie
   p.has_v = v != nullptr;
   const int64_t total = (int64_t)P.B * P.N;
   const int tb = tokens_per_step(total);
-  return launch_qk<false>(P, p, grid_blocks(total, tb, 8), tb, s);
+  return launch_qk<false>(P, p, grid_blocks(total, tb, kFwdPerSm), tb, s);
 }
 
 size_t qk_bwd_ws_bytes(const fm_qk_problem& P) {

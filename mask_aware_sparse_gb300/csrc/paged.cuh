@@ -283,9 +283,10 @@ __device__ __forceinline__ uint32_t in_box(int row, int chunk) {
     return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-// e4m3 in the high bytes of two 16-bit lanes -> bf16 pair, times 2^-120
-__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) {
-  return ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+// e4m3 in the high bytes of two 16-bit lanes -> bf16 pair, times 2^-120 (masks
+// 0x07f007f0 and 0x80008000; zeros where they are zero)
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t, uint32_t mag, uint32_t sign) {
+  return ((t >> 4) & mag) | (t & sign);
 }
 __device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
   uint32_t r;

@@ -956,10 +956,10 @@ def fm_qk_norm_rope(q, k, v=None, *, positions=None, inv_freq=None, interleaved:
 
 
 @functools.lru_cache(maxsize=256)
-def _qk_bwd_bytes(dev, B, N, d):
-    """Workspace of a backward pass with normed sides (it goes by sizes alone)."""
+def _qk_bwd_bytes(dev, *sizes):
+    """Workspace of a backward pass with normed sides: it goes by the sizes (B, N, H_q, H_kv, d) alone."""
     with torch.cuda.device(dev):
-        return lib().fm_qk_norm_rope_bwd_workspace_bytes(fm_qk_problem(B, N, 1, 1, d, q_weight=16, k_weight=16))
+        return lib().fm_qk_norm_rope_bwd_workspace_bytes(fm_qk_problem(*sizes, q_weight=16, k_weight=16))
 
 
 def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, interleaved: bool = False,
@@ -994,7 +994,7 @@ def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, i
     dwk = None if k_weight is None else torch.empty_like(k_weight)
     ws, wsb = None, 0
     if dwq is not None or dwk is not None:
-        wsb = _qk_bwd_bytes(dev, qs[0], qs[2], qs[3])
+        wsb = _qk_bwd_bytes(dev, qs[0], qs[2], qs[1], ks[1], qs[3])
         ws = torch.empty(max(16, wsb), dtype=_U8, device=on)
     _enqueue("fm_qk_norm_rope_bwd", dev, stream, p, gq, gk, gv, qi, ki, qv, kv, vv,
              None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),

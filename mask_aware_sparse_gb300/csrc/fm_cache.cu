@@ -12,7 +12,8 @@
 // or an infinity gets e = 255 and reads as NaN throughout.
 //
 // What bounds both kernels: memory, each row read once and written once, 16
-// bytes of bf16 a thread; a block looks its tokens' pages up once for all heads.
+// bytes a load, four rows' loads in flight a thread; a block looks its tokens'
+// pages up once for all heads.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include "fm_internal.h"
@@ -34,27 +35,39 @@ struct CacheParams {
   const int32_t* kv_len;  // write: keys of each sequence, the new ones among them
   const int32_t* table;
   int R, width, n_pages, H_kv, page, T;
+  int wide;  // read: the output rows start on 32-byte boundaries
   int* err;
 };
 
-// The sequence whose rows [off[r], off[r + 1]) hold t, or -1.
-__device__ __forceinline__ int sequence_of(const int32_t* off, int R, int t) {
-  int lo = 0, hi = R;  // first r with off[r + 1] > t
-  while (lo < hi) {
+// The sequence whose rows [off[r], off[r + 1]) hold t = t0 + lane, or -1; called
+// by a whole warp, for its lanes below n. 32 of the offsets, one a lane, are
+// compared with each t at once, so that up to 32 sequences cost one load's latency
+// (a bisection's is what a block of a few tokens would mostly wait for), then a
+// bisection between two of them.
+__device__ __forceinline__ int sequence_of(const int32_t* off, int R, int t0, int n) {
+  const int lane = threadIdx.x & 31, t = t0 + lane, S = (R + 31) / 32;
+  const int ends = off[min((lane + 1) * S, R)];
+  int k = 0;  // parts of S sequences that end at or before t
+  for (int i = 0; i < n; ++i) {
+    const int x = __popc(__ballot_sync(kAll, lane * S < R && ends <= t0 + i));
+    if (i == lane) k = x;
+  }
+  int lo = min(k * S, R), hi = min(lo + S - 1, R);  // first r with off[r + 1] > t lies in [lo, hi]
+  while (lo < hi && lo < R) {
     const int mid = (lo + hi) >> 1;
-    if (off[mid + 1] > t)
+    if (off[min(mid + 1, R)] > t)
       hi = mid;
     else
       lo = mid + 1;
   }
-  return (lo < R && off[lo] <= t) ? lo : -1;
+  return (lane < n && lo < R && off[lo] <= t && t < off[lo + 1]) ? lo : -1;
 }
 
-// Cache row (head 0) of token t, or -1: a token of no sequence, or (flagged) one
+// Cache row (head 0) of this lane's token, or -1: a token of no sequence, or (flagged) one
 // whose place has no page.
 template <bool READ>
-__device__ __forceinline__ int64_t slot_of(const CacheParams& p, int t) {
-  const int r = sequence_of(p.off, p.R, t);
+__device__ __forceinline__ int64_t slot_of(const CacheParams& p, int t0, int n) {
+  const int r = sequence_of(p.off, p.R, t0, n), t = t0 + (threadIdx.x & 31);
   if (r < 0) return -1;
   const int a = t - p.off[r];
   const int64_t pos = READ ? a : (int64_t)p.kv_len[r] - (p.off[r + 1] - p.off[r]) + a;
@@ -71,8 +84,8 @@ __device__ __forceinline__ float scale_of(uint32_t e) {
 }
 
 // 8 e4m3 values times a power of two, as 8 bf16
-__device__ __forceinline__ uint4 dequant8(uint2 raw, float s) {
-  const uint32_t w[2] = {raw.x, raw.y};
+__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, float s) {
+  const uint32_t w[2] = {w0, w1};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -83,69 +96,135 @@ __device__ __forceinline__ uint4 dequant8(uint2 raw, float s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One block: TB tokens, every head, keys then values; d / 8 threads a row.
-template <int D, bool F8, bool READ>
-__global__ void __launch_bounds__(kThreads) cache_kernel(const CacheParams p, const int TB) {
-  constexpr int TR = D / 8, ES = F8 ? 1 : 2;
-  __shared__ int64_t slot[kThreads];
-  const int t0 = blockIdx.x * TB;
-  if (threadIdx.x < TB) slot[threadIdx.x] = (t0 + (int)threadIdx.x < p.T) ? slot_of<READ>(p, t0 + threadIdx.x) : -1;
+// What the loads of a step need: the cache row of this thread's row, or -1.
+struct Row {
+  int64_t s;  // cache row
+  int t, h, which;
+};
+
+// Row i of a block's rows: keys, then values, head by head, the tokens of a head
+// next to each other (TB = 2^log tokens: no division, of which four a step would
+// be a third of the write's instructions).
+__device__ __forceinline__ Row row_of(const CacheParams& p, const int64_t* slot, int log, int rows, int i) {
+  Row r;
+  r.t = i & ((1 << log) - 1);
+  r.h = i >> log;
+  r.which = r.h >= p.H_kv ? 1 : 0;
+  r.h -= r.which * p.H_kv;
+  const int64_t s = i < rows ? slot[r.t] : -1;
+  r.s = s < 0 ? -1 : s + (int64_t)r.h * p.page;
+  return r;
+}
+
+template <bool READ>
+__device__ __forceinline__ void look_up(const CacheParams& p, int64_t* slot, int t0, int TB) {
+  if (threadIdx.x < 32) {  // TB <= 32
+    const int64_t s = slot_of<READ>(p, t0, min(TB, p.T - t0));
+    if (threadIdx.x < TB) slot[threadIdx.x] = s;
+  }
   __syncthreads();
-  const int c = threadIdx.x % TR;
-  const int rows = TB * p.H_kv * 2;
+}
+
+constexpr int kAhead = 4;  // rows whose loads a thread has in flight (one: the 16K-key read of four sequences took 66 us)
+
+// One block: 2^log tokens, every head; d / 8 threads a row, 16 bytes of bf16 each.
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads) write_kernel(const CacheParams p, const int log) {
+  constexpr int TR = D / 8, STEP = kThreads / TR;
+  __shared__ int64_t slot[32];
+  const int TB = 1 << log, t0 = blockIdx.x * TB;
+  look_up<false>(p, slot, t0, TB);
+  const int c = threadIdx.x % TR, rows = TB * p.H_kv * 2;
   // every thread of a warp takes the same number of turns: the rows' maxima are exchanged
-  for (int i0 = 0; i0 < rows; i0 += kThreads / TR) {
-    const int i = i0 + threadIdx.x / TR;
-    const int which = i >= rows / 2 ? 1 : 0;
-    const int j = i - which * (rows / 2);
-    // write: neighbouring rows are heads of a token; read: tokens of a head
-    const int h = READ ? j / TB : j % p.H_kv;
-    const int t = READ ? j - h * TB : j / p.H_kv;
-    const int64_t s = i < rows ? slot[t] : -1;
-    const bool live = s >= 0;
-    const int64_t row = s + (int64_t)h * p.page;
-    if constexpr (READ) {
-      if (!live) continue;
-      uint4 r;
-      if constexpr (F8)
-        r = dequant8(reinterpret_cast<const uint2*>(p.c[which] + row * D)[c], scale_of(p.e[which][row]));
-      else
-        r = reinterpret_cast<const uint4*>(p.c[which] + row * D * 2)[c];
-      reinterpret_cast<uint4*>(p.out[which] + ((int64_t)h * p.T + t0 + t) * D * 2)[c] = r;
+  for (int i0 = 0; i0 < rows; i0 += kAhead * STEP) {
+    Row row[kAhead];
+    uint4 x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      row[k] = row_of(p, slot, log, rows, i0 + k * STEP + threadIdx.x / TR);
+      const Row& r = row[k];
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (r.s >= 0)
+        x[k] = *reinterpret_cast<const uint4*>(p.in[r.which] +
+                                               2 * ((int64_t)(t0 + r.t) * p.st[r.which] + r.h * p.sh[r.which] + 8 * c));
+    }
+    if constexpr (!F8) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (row[k].s >= 0) reinterpret_cast<uint4*>(p.c[row[k].which] + row[k].s * D * 2)[c] = x[k];
     } else {
-      uint4 r = make_uint4(0, 0, 0, 0);
-      if (live) r = *reinterpret_cast<const uint4*>(p.in[which] + 2 * ((int64_t)(t0 + t) * p.st[which] + h * p.sh[which] + 8 * c));
-      if constexpr (!F8) {
-        if (live) reinterpret_cast<uint4*>(p.c[which] + row * D * ES)[c] = r;
-      } else {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-        // the largest magnitude as bits: infinities and NaN are the largest of all
-        uint32_t m = 0;
+      // each row's largest magnitude as bits: infinities and NaN are the largest of all
+      uint32_t m[kAhead];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) m = __vmaxu2(m, w[x] & 0x7fff7fffu);
+      for (int k = 0; k < kAhead; ++k)
+        m[k] = __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                        __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
 #pragma unroll
-        for (int x = TR / 2; x > 0; x >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kAll, m, x));
-        const uint32_t top = max(m & 0xffffu, m >> 16);
+      for (int y = TR / 2; y > 0; y >>= 1)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) m[k] = __vmaxu2(m[k], __shfl_xor_sync(kAll, m[k], y));
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const Row& r = row[k];
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        const uint32_t top = max(m[k] & 0xffffu, m[k] >> 16);
         const int E = (int)(top >> 7);  // 448 = 1.75 * 2^8
-        int e = max(1, E - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0));
-        uint2 q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-        if (E == 255) {
-          e = 255;
-        } else {
-          const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-          float f[8];
+        const int e = max(1, E - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0));
+        const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+        float f[8];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            f[2 * x] = __uint_as_float(w[x] << 16) * inv;
-            f[2 * x + 1] = __uint_as_float(w[x] & 0xffff0000u) * inv;
-          }
-          q.x = pack_e4m3x4(f[0], f[1], f[2], f[3]);
-          q.y = pack_e4m3x4(f[4], f[5], f[6], f[7]);
+        for (int y = 0; y < 4; ++y) {
+          f[2 * y] = __uint_as_float(w[y] << 16) * inv;
+          f[2 * y + 1] = __uint_as_float(w[y] & 0xffff0000u) * inv;
         }
-        if (live) {
-          reinterpret_cast<uint2*>(p.c[which] + row * D)[c] = q;
-          if (c == 0) p.e[which][row] = (uint8_t)e;
+        uint2 q = make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+        if (E == 255) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (r.s >= 0) {
+          reinterpret_cast<uint2*>(p.c[r.which] + r.s * D)[c] = q;
+          if (c == 0) p.e[r.which][r.s] = (uint8_t)(E == 255 ? 255 : e);
         }
+      }
+    }
+  }
+}
+
+// One block: 2^log output rows of every head; 16 bytes of the cache a thread.
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p, const int log) {
+  constexpr int TR = D * (F8 ? 1 : 2) / 16, STEP = kThreads / TR;
+  __shared__ int64_t slot[32];
+  const int TB = 1 << log, t0 = blockIdx.x * TB;
+  look_up<true>(p, slot, t0, TB);
+  const int c = threadIdx.x % TR, rows = TB * p.H_kv * 2;
+  for (int i0 = 0; i0 < rows; i0 += kAhead * STEP) {
+    Row row[kAhead];
+    uint4 x[kAhead];
+    uint32_t e[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      row[k] = row_of(p, slot, log, rows, i0 + k * STEP + threadIdx.x / TR);
+      const Row& r = row[k];
+      if (r.s < 0) continue;
+      x[k] = reinterpret_cast<const uint4*>(p.c[r.which] + r.s * (D * (F8 ? 1 : 2)))[c];
+      if constexpr (F8) e[k] = p.e[r.which][r.s];
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const Row& r = row[k];
+      if (r.s < 0) continue;
+      uint4* to = reinterpret_cast<uint4*>(p.out[r.which] + ((int64_t)r.h * p.T + t0 + r.t) * D * 2);
+      if constexpr (F8) {
+        const float f = scale_of(e[k]);
+        const uint4 lo = dequant8(x[k].x, x[k].y, f), hi = dequant8(x[k].z, x[k].w, f);
+        if (p.wide) {
+          // one whole 32-byte sector a thread (two stores of 16 bytes: 62 us for the read of four 16K sequences)
+          stg_b32x8(to + 2 * c, lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w);
+        } else {
+          to[2 * c] = lo;
+          to[2 * c + 1] = hi;
+        }
+      } else {
+        to[c] = x[k];
       }
     }
   }
@@ -155,16 +234,22 @@ template <bool READ>
 cudaError_t launch(const CacheParams& p, int d, bool f8, cudaStream_t s) {
   // few tokens: one a block, so that the heads' rows spread over the SMs; many:
   // enough tokens a block that looking a page up is a small part of its work
-  int tb = 1;
-  while (tb < 32 && p.T >= 2ll * tb * 8 * sm_count()) tb *= 2;
-  const unsigned grid = (unsigned)((p.T + tb - 1) / tb);
-  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p, tb); };
+  int log = 0;
+  while (log < 5 && p.T >= (4ll << log) * sm_count()) ++log;
+  const unsigned grid = (unsigned)((p.T + (1 << log) - 1) >> log);
+  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p, log); };
+  auto pick = [&](auto write, auto read) {
+    if constexpr (READ)
+      go(read);
+    else
+      go(write);
+  };
   if (d == 64)
-    f8 ? go(cache_kernel<64, true, READ>) : go(cache_kernel<64, false, READ>);
+    f8 ? pick(write_kernel<64, true>, read_kernel<64, true>) : pick(write_kernel<64, false>, read_kernel<64, false>);
   else if (d == 128)
-    f8 ? go(cache_kernel<128, true, READ>) : go(cache_kernel<128, false, READ>);
+    f8 ? pick(write_kernel<128, true>, read_kernel<128, true>) : pick(write_kernel<128, false>, read_kernel<128, false>);
   else
-    f8 ? go(cache_kernel<256, true, READ>) : go(cache_kernel<256, false, READ>);
+    f8 ? pick(write_kernel<256, true>, read_kernel<256, true>) : pick(write_kernel<256, false>, read_kernel<256, false>);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -212,6 +297,7 @@ cudaError_t launch_cache_read(const fm_kv_cache& c, const int32_t* kv_off, const
   p.R = R;
   p.width = width;
   p.T = n_rows;
+  p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0;
   return launch<true>(p, c.d, c.k_exp != nullptr, s);
 }
 

@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+static_assert(kWarps == 8, "side_groups");
 constexpr unsigned kAll = 0xffffffffu;
 
 struct View {
@@ -102,6 +103,22 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
   }
 }
 
+// Tokens that a warp takes at a time, each with all of its H heads.
+__host__ __device__ __forceinline__ int tokens_per_warp(int H, int d) {
+  int t = 512 / d;  // rows a warp holds
+  while (t > 1 && t * H > 512 / d) t /= 2;
+  return t;
+}
+
+// Groups of such tokens per step of a side with H heads: TB, or as many as leave
+// each of a group's warps some of the heads.
+__host__ __device__ __forceinline__ int side_groups(int H, int d, int TB) {
+  const int rows = 512 / d, hs = rows / tokens_per_warp(H, d);
+  int wpt = 8 / TB;
+  while (wpt > 1 && (wpt / 2) * hs >= H) wpt /= 2;
+  return 8 / wpt;
+}
+
 template <int D>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -147,8 +164,10 @@ __device__ __forceinline__ uint4* at(const View& v, int64_t b, int h, int64_t n,
   return reinterpret_cast<uint4*>(v.p + 2 * (b * v.sb + h * v.sh + n * v.sn + off));
 }
 
-// TB tokens per block and step, kWarps / TB warps on each; blockIdx.y 0: queries,
-// 1: keys and values. BWD: the backward.
+// blockIdx.y 0: queries, 1: keys and values. BWD: the backward. A warp holds HPW
+// rows at a time: heads of one token, or, with fewer heads than that, those of
+// several tokens (two heads at d = 64 would leave three quarters of a warp idle).
+// A block and step: TB groups of such tokens, kWarps / TB warps on each.
 //
 // Loads in flight bound it: two rows' groups ahead of the one computed (kAhead),
 // three blocks an SM (backward: two, with twice as much to load), weights in
@@ -159,21 +178,24 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
   using C = Chunks<D, INTER>;
   constexpr int TG = C::TG, HPW = 32 / TG;  // threads per row, rows per warp
   constexpr int kAhead = 2;
-  __shared__ __align__(16) float4 cs[kWarps * D / 4];  // TB <= kWarps tokens, rot <= D
+  __shared__ __align__(16) float4 cs[kWarps * HPW * D / 4];  // at most kWarps * HPW tokens, rot <= D
   __shared__ unsigned long long frac[D / 2];
   __shared__ float4 ws[D / 4];
   __shared__ float red[BWD ? kWarps * D : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % TG, hl = lane / TG;
   const C ch(c, p.rot);
-  const int wpt = kWarps / TB;
-  const int tw = warp / wpt, w0 = warp - tw * wpt;  // this warp's token of the step, its place among the token's warps
   const int64_t total = (int64_t)p.B * p.N;
   const int RT = p.rot / 16;
   const bool keys = blockIdx.y != 0;
   const View in = keys ? p.k : p.q, out = keys ? p.ko : p.qo, src = keys ? p.xk : p.xq;
   const int H = keys ? p.H_kv : p.H_q;
   const void* wp = keys ? p.wk : p.wq;
+  const int TPW = tokens_per_warp(H, D), HS = HPW / TPW;  // tokens a warp, heads of each at a time
+  const int wpt = kWarps / side_groups(H, D, TB);
+  const int tw = warp / wpt, w0 = warp - tw * wpt;  // this warp's tokens of the step, its place among their warps
+  const int ti = tw * TPW + hl / HS, h0 = hl % HS;  // this thread's token of the step, its first head
+  const int tokens = kWarps / wpt * TPW;
   float acc[BWD ? 16 : 1];  // weight gradients of this thread's 16 columns
   if constexpr (BWD) {
 #pragma unroll
@@ -190,30 +212,31 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
     }
   }
   __syncthreads();
-  for (int64_t tok0 = (int64_t)blockIdx.x * TB; tok0 < total; tok0 += (int64_t)gridDim.x * TB) {
-    load_angles(p, frac, cs, TB, tok0, total);
+  for (int64_t tok0 = (int64_t)blockIdx.x * tokens; tok0 < total; tok0 += (int64_t)gridDim.x * tokens) {
+    load_angles(p, frac, cs, tokens, tok0, total);
     __syncthreads();
-    const int64_t tok = tok0 + tw;
-    if (tok < total) {
+    {
+      const int64_t tok = tok0 + ti;
+      const bool there = tok < total;
       const int64_t b = tok / p.N, n = tok - b * p.N;
       float co[8], si[8];
       if (ch.turned) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float4 t = cs[tw * (p.rot / 4) + j * RT + c];
+          const float4 t = there ? cs[ti * (p.rot / 4) + j * RT + c] : make_float4(0.f, 0.f, 0.f, 0.f);
           co[2 * j] = t.x;
           si[2 * j] = t.y;
           co[2 * j + 1] = t.z;
           si[2 * j + 1] = t.w;
         }
       }
-      const int groups = (H + HPW - 1) / HPW;
+      const int groups = (H + HS - 1) / HS;
       // the next rows' loads are in flight while these are computed (a row is
       // read and written by the same threads, so in and out may be one tensor)
       uint4 ra[kAhead], rb[kAhead], xa[BWD ? kAhead : 1], xb[BWD ? kAhead : 1];
       auto fetch = [&](int k, int g) {
-        const int h = g * HPW + hl;
-        if (h < H) {
+        const int h = g * HS + h0;
+        if (there && h < H) {
           ra[k] = *at(in, b, h, n, ch.oa);
           rb[k] = *at(in, b, h, n, ch.ob);
           if constexpr (BWD) {
@@ -235,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
         for (int k = 0; k < kAhead; ++k) {
           const int g = g0 + k * wpt;
           if (g >= groups) break;
-          const int h = g * HPW + hl;
-          const bool live = h < H;
+          const int h = g * HS + h0;
+          const bool live = there && h < H;
           float fa[8], fb[8];
           unpack8(ra[k], fa);
           unpack8(rb[k], fb);
@@ -305,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
       }
       if (keys && p.has_v) {
         for (int g = w0; g < groups; g += wpt) {
-          const int h = g * HPW + hl;
-          if (h < H) {
+          const int h = g * HS + h0;
+          if (there && h < H) {
             const uint4 x = *at(p.v, b, h, n, 16 * c), y = *at(p.v, b, h, n, 16 * c + 8);
             *at(p.vo, b, h, n, 16 * c) = x;
             *at(p.vo, b, h, n, 16 * c + 8) = y;
@@ -363,21 +386,25 @@ View view_of(const fm_view* v) {
   return View{static_cast<char*>(v->ptr), v->sb, v->sh, v->sn};
 }
 
-// Tokens per block and step: one warp per token once every SM has work (the
-// angles are then read once per token), more warps per token before that.
-int tokens_per_step(int64_t total) {
+// Groups of tokens per block and step: one warp on each once every SM has work
+// (the angles are then read once per token), more warps on each before that.
+int groups_per_step(const fm_qk_problem& P) {
+  const int64_t groups = (int64_t)P.B * P.N / tokens_per_warp(P.H_q, P.d);
   int tb = 1;
-  while (tb < kWarps && total >= 2ll * tb * 4 * sm_count()) tb *= 2;
+  while (tb < kWarps && groups >= 2ll * tb * 4 * sm_count()) tb *= 2;
   return tb;
 }
-// Two columns of blocks, queries and keys (with values); the backward has a
-// partial row per block, so its grid is what an SM holds at once.
-int grid_blocks(int64_t total, int tb, int per_sm) {
-  const int64_t steps = (total + tb - 1) / tb;
+// Two columns of blocks, queries and keys (with values), at most what the SMs hold
+// at once of each (forward, 8192 tokens of 48 heads: 43 us, 8 blocks an SM 45); the
+// backward has a partial row per block besides.
+int grid_blocks(const fm_qk_problem& P, int tb, int per_sm) {
+  const int H = P.H_q > P.H_kv ? P.H_q : P.H_kv;  // the side that needs more steps
+  const int tokens = side_groups(H, P.d, tb) * tokens_per_warp(H, P.d);
+  const int64_t steps = ((int64_t)P.B * P.N + tokens - 1) / tokens;
   const int64_t most = (int64_t)sm_count() * per_sm;
   return (int)(steps < most ? steps : most);
 }
-constexpr int kFwdPerSm = 8, kBwdPerSm = 2;
+constexpr int kFwdPerSm = 3, kBwdPerSm = 2;
 
 template <bool BWD>
 cudaError_t launch_qk(const fm_qk_problem& P, const QkParams& p, int grid, int tb, cudaStream_t s) {
@@ -422,15 +449,11 @@ cudaError_t launch_qk_fwd(const fm_qk_problem& P, const fm_view* q, const fm_vie
   p.ko = view_of(ko);
   p.vo = view_of(vo);
   p.has_v = v != nullptr;
-  const int64_t total = (int64_t)P.B * P.N;
-  const int tb = tokens_per_step(total);
-  return launch_qk<false>(P, p, grid_blocks(total, tb, kFwdPerSm), tb, s);
+  const int tb = groups_per_step(P);
+  return launch_qk<false>(P, p, grid_blocks(P, tb, kFwdPerSm), tb, s);
 }
 
-size_t qk_bwd_ws_bytes(const fm_qk_problem& P) {
-  const int64_t total = (int64_t)P.B * P.N;
-  return (size_t)grid_blocks(total, tokens_per_step(total), kBwdPerSm) * 2 * P.d * sizeof(float);
-}
+size_t qk_bwd_ws_bytes(const fm_qk_problem& P) { return (size_t)sm_count() * kBwdPerSm * 2 * P.d * sizeof(float); }
 
 cudaError_t launch_qk_bwd(const fm_qk_problem& P, const fm_view* dqo, const fm_view* dko, const fm_view* dvo,
                           const fm_view* q, const fm_view* k, const fm_view* dq, const fm_view* dk, const fm_view* dv,
@@ -446,9 +469,8 @@ cudaError_t launch_qk_bwd(const fm_qk_problem& P, const fm_view* dqo, const fm_v
   p.vo = view_of(dv);
   p.has_v = dvo != nullptr;
   p.part = static_cast<float*>(ws);
-  const int64_t total = (int64_t)P.B * P.N;
-  const int tb = tokens_per_step(total);
-  const int grid = grid_blocks(total, tb, kBwdPerSm);
+  const int tb = groups_per_step(P);
+  const int grid = grid_blocks(P, tb, kBwdPerSm);
   cudaError_t e = launch_qk<true>(P, p, grid, tb, s);
   if (e != cudaSuccess || (!P.q_weight && !P.k_weight)) return e;
   qk_weights_kernel<<<2 * P.d / 32, 1024, 0, s>>>(p.part, grid, P.d, P.q_weight ? dwq : nullptr,

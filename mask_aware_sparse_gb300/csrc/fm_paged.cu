@@ -10,12 +10,12 @@
 // few_kernel, one unit = 16 query rows of a KV head (a token's query heads of
 // the group, then the next token's): bound by memory, each key and value byte
 // is read once for all query heads of its group and 16 rows cost few
-// operations, so the design is about loads in flight. Each of a CTA's four warps
-// takes a quarter of the segment's key tiles (32 keys) and brings them in itself,
+// operations, so the design is about loads in flight. Each of a CTA's warps
+// takes its share of the segment's key tiles (32 keys) and brings them in itself,
 // 16 bytes a lane and copy, into a ring of its own (keys and values as entries of
-// their own; 96 KB a CTA, two CTAs an SM), with its own running (m, l, O) in
+// their own; about 200 KB an SM), with its own running (m, l, O) in
 // registers (m16n8k16 products): every byte in shared memory is read once, and
-// no warp waits for another before a segment's end, where the four are joined.
+// no warp waits for another before a segment's end, where they are joined.
 // Measured against TMA boxes issued by a producer warp (e4m3, pages of 64, loads
 // alone, nothing computed): boxes of 32 rows and the exponents' own bulk copies
 // reach 3.9 TB/s; the copies also cost the same for pages of any size, and fill
@@ -173,10 +173,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 }
 
 // -------------------------------------------------------------- few query rows
-constexpr int kFewWarps = 4;
-constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRows = 16;
 constexpr int kTileKeys = 32;
+
+constexpr int few_warps(int d, bool f8) { return d == 256 && f8 ? 8 : 4; }
+constexpr int few_ctas(int d, bool f8) { return d == 256 ? 1 : d == 64 && f8 ? 3 : 2; }
 
 template <int D, bool F8>
 struct FewCfg {
@@ -187,13 +188,20 @@ struct FewCfg {
   static constexpr int BOX = kTileKeys * ROW;
   static constexpr int TILE = BOXES * BOX;           // one ring entry: a tile's keys, or its values
   static constexpr int EXP = F8 ? kTileKeys : 0;
-  static constexpr int PER_SM = D == 256 ? 1 : 2;
-  static constexpr int RING = D == 64 ? (F8 ? 8 : 6) : (F8 ? 6 : 3);  // entries of a warp's ring
-  static constexpr int ENTRIES = kFewWarps * RING;
+  // Warps, CTAs an SM and entries of a warp's ring: what fills shared memory with
+  // loads in flight. e4m3 rows are short for the work on each, so more warps help
+  // where registers allow: d = 64 three CTAs (step of 32 sequences 98 us with two),
+  // d = 256 eight warps (406 us with four).
+  static constexpr int WARPS = few_warps(D, F8), THREADS = 32 * WARPS;
+  static constexpr int PER_SM = few_ctas(D, F8);
+  static constexpr int RING = D == 256 ? 3 : D == 64 ? (F8 ? 8 : 6) : (F8 ? 6 : 3);
+  static constexpr int ENTRIES = WARPS * RING;
   static constexpr int EXP_OFF = ENTRIES * TILE;
   static constexpr int ML_OFF = EXP_OFF + ENTRIES * EXP;
-  static constexpr int SMEM = ML_OFF + kFewWarps * kFewRows * 16 + 1024;
-  static_assert(RING * TILE >= kFewRows * (D + 8) * 4, "a warp's ring holds its O at a segment's end");
+  static constexpr int SMEM = ML_OFF + WARPS * kFewRows * 16 + 1024;
+  // entries that hold a warp's O at a segment's end, and those free for the next segment's first loads
+  static constexpr int MERGE = (kFewRows * D * 4 + TILE - 1) / TILE, AHEAD = RING - MERGE;
+  static_assert(AHEAD >= 1, "the ring is more than what the join needs");
   static constexpr int KSTEPS = D / 16;
   static constexpr int CHUNKS = ROW / 64;  // 16-byte chunks a thread reads of a box's row
   static constexpr int SPC = F8 ? 4 : 2;   // k-steps of a chunk
@@ -276,7 +284,7 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM) few_kernel(const FewParams p) {
   using C = FewCfg<D, F8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -284,17 +292,20 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ PagedStart start;
   __shared__ int4 seq[kLocalSeqs];
+  __shared__ uint16_t first[kLocalSeqs + 1], order[kWholeUnits];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (p.s.local) {
+  if (p.s.whole) {
+    plan_whole(p.s, p.q_off, p.kv_len, seq, first, order, reinterpret_cast<uint16_t*>(smem), &start, p.err);
+  } else if (p.s.local) {
     plan_locally(p.s, p.q_off, p.kv_len, seq, reinterpret_cast<unsigned*>(smem), &start, p.err);
-    if (threadIdx.x == 0 && !p.s.whole) p.w.starts[blockIdx.x] = start;  // for join_kernel
+    if (threadIdx.x == 0) p.w.starts[blockIdx.x] = start;  // for join_kernel
   } else {
     if (threadIdx.x == 0) start = p.w.starts[blockIdx.x];
     __syncthreads();
   }
   const int G = p.s.G, P = p.s.page;
-  PagedWalk walk(p.s, p.w.units, seq, start);
+  PagedWalk walk(p.s, p.w.units, seq, first, order, start);
   const int g = lane >> 2, t = lane & 3;
   const float sl2 = p.scale_log2;
   const uint32_t ring = smem_u32(smem) + warp * C::RING * C::TILE;
@@ -310,63 +321,75 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
   const int l_row = lane / C::CPR, l_chunk = lane % C::CPR;
   const uint32_t l_at = (l_chunk * 16 / C::ROW) * C::BOX + in_box<C::ROW>(l_row, l_chunk % (C::ROW / 16));
   PageWindow pages;
-
-  for (; walk.more(); walk.next()) {
+  // The warp's tiles of the segment: [j0, j0 + nt), its entries 0 .. 2 nt - 1 (keys
+  // and values in turn), RING of them in the ring or on their way. A segment's
+  // first AHEAD entries are asked for before the last segment's results are joined
+  // (200 sequences of 64 keys, five segments a CTA: 34 us instead of 62).
+  int j0 = 0, nt = 0;
+  int64_t src_a = 0, src_b = 0;  // rows of the cache: the tile's first 16 (or all) keys, its last 16
+  bool bad_a = false, bad_b = false;
+  auto begin = [&] {
+    j0 = walk.n * warp / C::WARPS;
+    nt = walk.n * (warp + 1) / C::WARPS - j0;
+    pages.reset(p.table, walk.u.r, p.s.width);
+  };
+  auto issue = [&](int e, int slot) {
     const PagedUnit& u = walk.u;
-    // the warp's tiles of the segment: [j0, j0 + nt), its entries 0 .. 2 nt - 1
-    // (keys and values in turn), RING of them in the ring or on their way
-    const int j0 = walk.n * warp / kFewWarps, nt = walk.n * (warp + 1) / kFewWarps - j0;
-    pages.reset(p.table, u.r, p.s.width);
-    int64_t src_a = 0, src_b = 0;  // rows of the cache: the tile's first 16 (or all) keys, its last 16
-    bool bad_a = false, bad_b = false;
-    auto issue = [&](int e, int slot) {
-      if (e < 2 * nt) {
-        const int key0 = tile_of(u, walk.kt + j0 + (e >> 1)) * kTileKeys;
-        const int which = e & 1;
-        if (which == 0) {
-          const int pg0 = key0 / P, per = P < kTileKeys ? 2 : 1;
-          pages.hold(pg0, per, lane);
-          const int a = __shfl_sync(kAll, pages.held, pg0 - pages.base);
-          const int b = __shfl_sync(kAll, pages.held, pg0 + per - 1 - pages.base);
-          const bool two = per == 2 && key0 + 16 < u.kv_len;  // the second page holds keys
-          bad_a = a < 0 || a >= p.s.n_pages;
-          bad_b = per == 2 ? !two || b < 0 || b >= p.s.n_pages : bad_a;
-          if (bad_a || (two && bad_b)) record_error(p.err, FM_DEV_ERR_RANGE);
-          src_a = ((int64_t)(bad_a ? 0 : a) * p.s.H_kv + walk.h) * P + (key0 - pg0 * P);
-          src_b = per == 2 ? ((int64_t)(bad_b ? 0 : b) * p.s.H_kv + walk.h) * P : src_a + 16;
-        }
-        // keys that no row of the unit sees (past the sequence's end: anything may lie there) become zeros
-        const bool edge = key0 + kTileKeys > u.hi || (p.s.window > 0 && key0 < u.lo) || bad_a || bad_b;
-        const char* base = p.kv[which] + l_chunk * 16;
-        const uint32_t dst = ring + slot * C::TILE + l_at;
-        const char* from_a = base + (src_a + l_row) * C::RB;
-        const char* from_b = base + (src_b + l_row) * C::RB;
-        auto copies = [&](auto whole) {
-#pragma unroll
-          for (int i = 0; i < C::LOADS; ++i) {
-            const int r0 = i * C::RPI;
-            const char* from = r0 < 16 ? from_a + r0 * C::RB : from_b + (r0 - 16) * C::RB;
-            const uint32_t x = C::ROW == 128 ? (uint32_t)((r0 & 7) << 4) : (uint32_t)(((r0 >> 1) & 3) << 4);
-            if constexpr (whole.value) {
-              copy16((dst ^ x) + r0 * C::ROW, from);
-            } else {
-              const int key = key0 + r0 + l_row;
-              copy16((dst ^ x) + r0 * C::ROW, from,
-                     key < u.hi && (key >= u.lo || key < p.s.sinks) && !(r0 < 16 ? bad_a : bad_b));
-            }
-          }
-        };
-        if (edge)
-          copies(std::false_type{});
-        else
-          copies(std::true_type{});
-        if (F8 && lane < 2)
-          copy16(ring_exp + slot * C::EXP + 16 * lane, p.exps[which] + (lane ? src_b : src_a), !(lane ? bad_b : bad_a));
+    if (e < 2 * nt) {
+      const int key0 = tile_of(u, walk.kt + j0 + (e >> 1)) * kTileKeys;
+      const int which = e & 1;
+      if (which == 0) {
+        const int pg0 = key0 / P, per = P < kTileKeys ? 2 : 1;
+        pages.hold(pg0, per, lane);
+        const int a = __shfl_sync(kAll, pages.held, pg0 - pages.base);
+        const int b = __shfl_sync(kAll, pages.held, pg0 + per - 1 - pages.base);
+        const bool two = per == 2 && key0 + 16 < u.kv_len;  // the second page holds keys
+        bad_a = a < 0 || a >= p.s.n_pages;
+        bad_b = per == 2 ? !two || b < 0 || b >= p.s.n_pages : bad_a;
+        if (bad_a || (two && bad_b)) record_error(p.err, FM_DEV_ERR_RANGE);
+        src_a = ((int64_t)(bad_a ? 0 : a) * p.s.H_kv + walk.h) * P + (key0 - pg0 * P);
+        src_b = per == 2 ? ((int64_t)(bad_b ? 0 : b) * p.s.H_kv + walk.h) * P : src_a + 16;
       }
-      copy_commit();
-    };
+      // keys that no row of the unit sees (past the sequence's end: anything may lie there) become zeros
+      const bool edge = key0 + kTileKeys > u.hi || (p.s.window > 0 && key0 < u.lo) || bad_a || bad_b;
+      const char* base = p.kv[which] + l_chunk * 16;
+      const uint32_t dst = ring + slot * C::TILE + l_at;
+      const char* from_a = base + (src_a + l_row) * C::RB;
+      const char* from_b = base + (src_b + l_row) * C::RB;
+      auto copies = [&](auto whole) {
+#pragma unroll
+        for (int i = 0; i < C::LOADS; ++i) {
+          const int r0 = i * C::RPI;
+          const char* from = r0 < 16 ? from_a + r0 * C::RB : from_b + (r0 - 16) * C::RB;
+          const uint32_t x = C::ROW == 128 ? (uint32_t)((r0 & 7) << 4) : (uint32_t)(((r0 >> 1) & 3) << 4);
+          if constexpr (whole.value) {
+            copy16((dst ^ x) + r0 * C::ROW, from);
+          } else {
+            const int key = key0 + r0 + l_row;
+            copy16((dst ^ x) + r0 * C::ROW, from,
+                   key < u.hi && (key >= u.lo || key < p.s.sinks) && !(r0 < 16 ? bad_a : bad_b));
+          }
+        }
+      };
+      if (edge)
+        copies(std::false_type{});
+      else
+        copies(std::true_type{});
+      if (F8 && lane < 2)
+        copy16(ring_exp + slot * C::EXP + 16 * lane, p.exps[which] + (lane ? src_b : src_a), !(lane ? bad_b : bad_a));
+    }
+    copy_commit();
+  };
+  if (walk.more()) {
+    begin();
 #pragma unroll 1
-    for (int e = 0; e < C::RING; ++e) issue(e, e);
+    for (int e = 0; e < C::AHEAD; ++e) issue(e, e);
+  }
+
+  while (walk.more()) {
+    const PagedUnit& u = walk.u;
+#pragma unroll 1
+    for (int e = C::AHEAD; e < C::RING; ++e) issue(e, e);
     // this thread's rows g and g + 8: their positions (-1: no such row), their Q
     int pos[2];
     uint32_t qf[C::KSTEPS][4];
@@ -613,10 +636,18 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
     }
     copy_wait<0>();
 
-    // Join the four warps' (m, l, O): each leaves its own in its ring, which nothing
-    // uses any more, then every thread adds up four columns of a row at a time.
-    constexpr int LD = D + 8;  // floats of a row there: neighbouring rows start 8 banks apart
-    float* own = reinterpret_cast<float*>(smem + warp * C::RING * C::TILE);
+    // Join the warps' (m, l, O): each leaves its own in the last entries of its
+    // ring, then every thread adds up four columns of a row at a time. Column c of
+    // row r lies at c ^ 8 (r % 4): four rows start 8 banks apart.
+    const int tok0 = u.tok, g0 = u.g0, nrows = u.nrows, h = walk.h, part_slot = walk.slot();
+    const bool whole = walk.whole();
+    walk.next();
+    if (walk.more()) {
+      begin();
+#pragma unroll 1
+      for (int e = 0; e < C::AHEAD; ++e) issue(e, e);
+    }
+    float* own = reinterpret_cast<float*>(smem + (warp * C::RING + C::AHEAD) * C::TILE);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(kAll, l[i], 1);
@@ -632,43 +663,44 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, F8>::PER_SM) few_kernel
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int z = 0; z < 2; ++z)
-              *reinterpret_cast<float4*>(own + row * LD + 64 * cg + 16 * t + 8 * y + 4 * z) =
+              *reinterpret_cast<float4*>(own + row * D + ((64 * cg + 16 * t + 8 * y + 4 * z) ^ (8 * (row & 3)))) =
                   make_float4(o[8 * cg + 4 * z][2 * i + y], o[8 * cg + 4 * z + 1][2 * i + y],
                               o[8 * cg + 4 * z + 2][2 * i + y], o[8 * cg + 4 * z + 3][2 * i + y]);
       } else {
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<float2*>(own + row * LD + 8 * c + 2 * t) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
+          *reinterpret_cast<float2*>(own + row * D + ((8 * c + 2 * t) ^ (8 * (row & 3)))) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
       }
     }
     __syncthreads();
     {
-      const int row = threadIdx.x >> 3, c0 = threadIdx.x & 7, x = u.g0 + row;
-      if (row < u.nrows) {
-        float top = -INFINITY, sum = 0.f, w[kFewWarps];
+      constexpr int TPR = C::THREADS / kFewRows;  // threads a row
+      const int row = threadIdx.x / TPR, c0 = threadIdx.x % TPR, x = g0 + row;
+      if (row < nrows) {
+        float top = -INFINITY, sum = 0.f, w[C::WARPS];
 #pragma unroll
-        for (int k = 0; k < kFewWarps; ++k) top = fmaxf(top, ml[k * kFewRows + row].x);
+        for (int k = 0; k < C::WARPS; ++k) top = fmaxf(top, ml[k * kFewRows + row].x);
         const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int k = 0; k < kFewWarps; ++k) {
+        for (int k = 0; k < C::WARPS; ++k) {
           const float4 v = ml[k * kFewRows + row];
           sum += ex2_approx(v.x - base) * v.y;
           w[k] = ex2_approx(v.z - base);
         }
-        const bool whole = walk.whole();
         const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        const int64_t tok = u.tok + x / G;
-        const int head = walk.h * G + x % G;
+        const int64_t tok = tok0 + x / G;
+        const int head = h * G + x % G;
         char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
-        float* part = p.w.part + p.w.part_floats * (2 * (size_t)blockIdx.x + walk.slot());
+        float* part = p.w.part + p.w.part_floats * (2 * (size_t)blockIdx.x + part_slot);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const int col = 4 * (c0 + 8 * c);
+        for (int c = 0; c < D / (4 * TPR); ++c) {
+          const int col = 4 * (c0 + TPR * c);
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < kFewWarps; ++k) {
+          for (int k = 0; k < C::WARPS; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(
-                reinterpret_cast<const float*>(smem + k * C::RING * C::TILE) + row * LD + col);
+                reinterpret_cast<const float*>(smem + (k * C::RING + C::AHEAD) * C::TILE) + row * D +
+                (col ^ (8 * (row & 3))));
             a.x += w[k] * v.x;
             a.y += w[k] * v.y;
             a.z += w[k] * v.z;
@@ -703,80 +735,109 @@ struct JoinParams {
 
 // Block (c, y): where CTA c's range is the second one inside a unit and head,
 // their parts (CTA c - 1's last segment, then c .. last's first segments) are
-// joined, a row (d = 64: two) a warp, four parts' loads in flight at a time.
-template <int D>
+// joined: a warp has ROWS rows (d = 64: twice as many), several parts of each in
+// flight at a time. Four rows and two parts for chunk_kernel's slots of 256 rows,
+// where the blocks of one row a warp were several times what the SMs hold; one row
+// and eight parts for the 16 rows of few_kernel's, which long caches split finely.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
+  constexpr int PARTS = ROWS == 1 ? 8 : 2;
   grid_dependency_wait();
   const int c = blockIdx.x + 1;
   const PagedStart& st = p.w.starts[c];
   if (st.count <= 0 || st.kt == 0 || st.first != c - 1) return;
   const int lane = threadIdx.x & 31, col = 4 * (lane % LPR);
-  const int row = (blockIdx.y * 8 + (threadIdx.x >> 5)) * RPW + lane / LPR;
-  if (row >= st.unit.nrows) return;
-  const size_t ml = (size_t)p.rows * D + 2 * row;
+  const int row0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * ROWS * RPW + lane / LPR;  // then every RPW-th
+  const int nrows = st.unit.nrows;
+  if (row0 >= nrows) return;
   const int parts = st.last - c + 2;
   // part i: slot 1 of CTA c - 1 (i = 0), slot 0 of CTA c - 1 + i
   auto part = [&](int i) { return p.w.part + p.w.part_floats * (2 * (size_t)(c - 1 + i) + (i == 0 ? 1 : 0)); };
-  float top = -INFINITY, sum = 0.f;
-  float4 acc[V];
+  float top[ROWS], sum[ROWS];
+  float4 acc[ROWS][V];
 #pragma unroll
-  for (int x = 0; x < V; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < parts; i0 += 4) {
-    float2 w[4];
-    float4 v[4][V];
+  for (int r = 0; r < ROWS; ++r) {
+    top[r] = -INFINITY;
+    sum[r] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[k] = make_float2(-INFINITY, 0.f);
-      if (i0 + k < parts) {
-        const float* s = part(i0 + k);
-        w[k] = *reinterpret_cast<const float2*>(s + ml);
+    for (int x = 0; x < V; ++x) acc[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int i0 = 0; i0 < parts; i0 += PARTS) {
+    float2 w[ROWS][PARTS];
+    float4 v[ROWS][PARTS][V];
 #pragma unroll
-        for (int x = 0; x < V; ++x)
-          v[k][x] = *reinterpret_cast<const float4*>(s + (size_t)row * D + 4 * LPR * x + col);
-      }
-    }
-    const float t = fmaxf(fmaxf(top, fmaxf(w[0].x, w[1].x)), fmaxf(w[2].x, w[3].x));
-    const float base = t == -INFINITY ? 0.f : t;
-    const float f = ex2_approx(top - base);
-    top = t;
-    sum *= f;
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-    for (int x = 0; x < V; ++x) acc[x] = make_float4(acc[x].x * f, acc[x].y * f, acc[x].z * f, acc[x].w * f);
+      for (int k = 0; k < PARTS; ++k) {
+        const int row = row0 + r * RPW;
+        w[r][k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i0 + k < parts) {
-        const float y = ex2_approx(w[k].x - base);
-        sum += y * w[k].y;
+        for (int x = 0; x < V; ++x) v[r][k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + k < parts && row < nrows) {
+          const float* s = part(i0 + k);
+          w[r][k] = *reinterpret_cast<const float2*>(s + (size_t)p.rows * D + 2 * row);
 #pragma unroll
-        for (int x = 0; x < V; ++x) {
-          acc[x].x += y * v[k][x].x;
-          acc[x].y += y * v[k][x].y;
-          acc[x].z += y * v[k][x].z;
-          acc[x].w += y * v[k][x].w;
+          for (int x = 0; x < V; ++x)
+            v[r][k][x] = *reinterpret_cast<const float4*>(s + (size_t)row * D + 4 * LPR * x + col);
         }
       }
-  }
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  const int x0 = st.unit.g0 + row;
-  const int64_t tok = st.unit.tok + x0 / p.G;
-  const int head = st.h * p.G + x0 % p.G;
-  char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
 #pragma unroll
-  for (int x = 0; x < V; ++x)
-    *reinterpret_cast<uint2*>(dst + 2 * (4 * LPR * x + col)) =
-        make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
-  if (col == 0) p.out.lse[tok * p.out.H_q + head] = sum == 0.f ? -INFINITY : top * kLn2F + logf(sum);
+    for (int r = 0; r < ROWS; ++r) {
+      float t = top[r];
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k) t = fmaxf(t, w[r][k].x);
+      const float base = t == -INFINITY ? 0.f : t;
+      const float f = ex2_approx(top[r] - base);
+      top[r] = t;
+      sum[r] *= f;
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        acc[r][x].x *= f;
+        acc[r][x].y *= f;
+        acc[r][x].z *= f;
+        acc[r][x].w *= f;
+      }
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k) {
+        const float y = ex2_approx(w[r][k].x - base);
+        sum[r] += y * w[r][k].y;
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          acc[r][x].x += y * v[r][k][x].x;
+          acc[r][x].y += y * v[r][k][x].y;
+          acc[r][x].z += y * v[r][k][x].z;
+          acc[r][x].w += y * v[r][k][x].w;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int row = row0 + r * RPW;
+    if (row >= nrows) continue;
+    const float inv = sum[r] > 0.f ? 1.f / sum[r] : (sum[r] == 0.f ? 0.f : sum[r]);
+    const int x0 = st.unit.g0 + row;
+    const int64_t tok = st.unit.tok + x0 / p.G;
+    const int head = st.h * p.G + x0 % p.G;
+    char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
+#pragma unroll
+    for (int x = 0; x < V; ++x)
+      *reinterpret_cast<uint2*>(dst + 2 * (4 * LPR * x + col)) = make_uint2(
+          pack_bf16x2(acc[r][x].x * inv, acc[r][x].y * inv), pack_bf16x2(acc[r][x].z * inv, acc[r][x].w * inv));
+    if (col == 0) p.out.lse[tok * p.out.H_q + head] = sum[r] == 0.f ? -INFINITY : top[r] * kLn2F + logf(sum[r]);
+  }
 }
 
 template <int D>
 cudaError_t launch_join(const PagedShape& s, const PagedWork& w, const PagedOut& out, int rows, cudaStream_t st) {
-  JoinParams j{w, out, s.G, rows};
-  const int per = 8 * (D == 64 ? 2 : 1);  // rows of a block
-  const dim3 grid((unsigned)(s.ctas - 1), (unsigned)((rows + per - 1) / per));
   if (s.ctas < 2) return cudaSuccess;
+  const JoinParams j{w, out, s.G, rows};
+  const int per = 8 * (D == 64 ? 2 : 1) * (rows == kChunkRows ? 4 : 1);  // rows of a block
+  const dim3 grid((unsigned)(s.ctas - 1), (unsigned)((rows + per - 1) / per));
   count_launches(1);
-  return launch_dependent(join_kernel<D>, grid, 256, 0, st, j);
+  if (rows == kChunkRows) return launch_dependent(join_kernel<D, 4>, grid, 256, 0, st, j);
+  return launch_dependent(join_kernel<D, 1>, grid, 256, 0, st, j);
 }
 
 template <int D, bool F8>
@@ -791,11 +852,28 @@ cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cach
               {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, b.q_off, b.kv_len, b.page_table,
               scale * 1.4426950408889634f, err};
   count_launches(1);
-  return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), kFewThreads, C::SMEM, st, p);
+  return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, p);
 }
 
-// tiles of a unit up to which it is not divided
-constexpr int kWholeFew = 8, kWholeChunk = 0;
+// Whether units stay whole, one CTA each, or ranges of tiles may end inside them.
+// Whole units leave CTAs idle in the last round, `most` tiles each at worst;
+// divided ones cost the parts' writing and joining, and a start and an end for every
+// part. What the host knows decides: the units that T tokens make, the keys that
+// the page table has room for. chunk_kernel (tiles of 128 keys, about 1.9 us):
+// 2048 tokens of 32 / 8 heads over themselves 40 us whole, 90 divided; 4096 over
+// themselves 122, 233; 2048 over 4096 keys 95, 113; 256 over 2048 keys 37, 30; a
+// full prompt's units grow from one tile to `most`, so less is left idle. few_kernel
+// (tiles of 32 keys): 64 sequences of 500 keys 22 whole, 25 divided; one 11.7, 8.6.
+bool stay_whole(const PagedShape& s, const fm_paged_batch& b, long long most, bool chunk) {
+  const double units = (double)s.H_kv * (chunk ? ((double)s.T * s.G / s.step + b.R / 2.0)
+                                               : std::max((double)b.R, (double)s.T * s.G / s.step));
+  const double rounds = units / s.ctas;
+  double idle = most * (std::ceil(rounds) - rounds);
+  if (s.causal && s.window == 0 && 2ll * s.T >= (long long)b.R * b.width * s.page)
+    idle /= 4 * std::max(1.0, rounds);
+  if (!chunk) idle /= std::max(1.0, rounds);  // ragged lengths even out over the rounds
+  return idle <= (chunk ? 5 + 8 * std::min(1.0, rounds) : 8);
+}
 
 // Which kernel: chunk_kernel's tiles of 128 rows once the sequences have more
 // than 16 rows a KV head on average (few_kernel would read the keys again for
@@ -827,16 +905,17 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   s.sinks = window > 0 ? std::min(sinks, 1 << 30) : 0;
   s.step = chunk ? 2 * (128 / s.G) * s.G : kFewRows;
   s.tile = chunk ? 128 : kTileKeys;
-  s.least = chunk ? 1 : kFewWarps;  // a tile for each computing warp, and fewer parts to join
-  s.ctas = sm_count() * (chunk || c.d == 256 ? 1 : 2);
+  s.least = chunk ? 1 : few_warps(c.d, c.k_exp != nullptr);  // a tile for each computing warp, and fewer parts to join
+  s.ctas = sm_count() * (chunk ? 1 : few_ctas(c.d, c.k_exp != nullptr));
   s.max_units = ((long long)T * s.G + s.step - 1) / s.step + b.R;
-  // Each CTA plans for itself where that is a few steps a thread; a plan kernel
-  // (one CTA, about 4 us of the stream) for larger batches.
+  // Each CTA plans for itself where that is a few steps a thread (a thread counts the
+  // units of its sequences one by one: 257 of one sequence took 60 us); a plan
+  // kernel (one CTA, about 4 us of the stream) for larger batches.
   const long long most = ((long long)b.width * s.page + s.tile - 1) / s.tile;  // tiles of a unit
-  s.local = b.R <= (chunk ? kLocalChunks : kLocalSeqs) && s.max_units <= kLocalUnits &&
-            s.max_units * most * s.H_kv * (s.ctas + 1) < (1ll << 31);
-  // Units of few tiles stay whole: one CTA takes less time for them than joining does.
-  s.whole = s.local && most <= (chunk ? kWholeChunk : kWholeFew);
+  const bool few_seqs = b.R <= (chunk ? kLocalChunks : kLocalSeqs);
+  s.whole = few_seqs && (b.R == 1 || s.max_units <= kWholeUnits) && stay_whole(s, b, most, chunk);
+  s.local = s.whole || (few_seqs && s.max_units - b.R <= kLocalUnits &&
+                        s.max_units * most * s.H_kv * (s.ctas + 1) < (1ll << 31));
   return s;
 }
 

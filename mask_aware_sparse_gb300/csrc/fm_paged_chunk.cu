@@ -82,6 +82,7 @@ struct ChunkParams {
   const int32_t* kv_len;
   const int32_t* table;
   int tile_rows;  // rows of a query tile: whole tokens, at most 128
+  int wide;       // output rows start on 32-byte boundaries
   float scale_log2;
   int* err;
 };
@@ -149,20 +150,23 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   const uint32_t tbase = *tmem_slot;
   __shared__ PagedStart start;
   __shared__ int4 seq[kLocalChunks];
+  __shared__ uint16_t first[kLocalChunks + 1], order[kWholeUnits];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (p.s.local) {
-    // (the work list lies where the first keys will)
+  // (the plans' scratch lies where the first keys will)
+  if (p.s.whole) {
+    plan_whole(p.s, p.q_off, p.kv_len, seq, first, order, reinterpret_cast<uint16_t*>(smem + C::K_OFF), &start, p.err);
+  } else if (p.s.local) {
     plan_locally(p.s, p.q_off, p.kv_len, seq, reinterpret_cast<unsigned*>(smem + C::K_OFF), &start, p.err);
-    if (threadIdx.x == 0 && !p.s.whole) p.w.starts[blockIdx.x] = start;  // for join_kernel
-    fence_proxy_async_smem();
+    if (threadIdx.x == 0) p.w.starts[blockIdx.x] = start;  // for join_kernel
   } else {
     if (threadIdx.x == 0) start = p.w.starts[blockIdx.x];
   }
+  fence_proxy_async_smem();
   __syncthreads();
   const int G = p.s.G, TR = p.tile_rows;
   bool ok = *abort_flag == 0;
-  PagedWalk walk(p.s, p.w.units, seq, start);
+  PagedWalk walk(p.s, p.w.units, seq, first, order, start);
 
   if (!ok) {
     // an unread timeout of an earlier launch: nothing is computed
@@ -308,7 +312,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
         tc_fence_after();
       }
       if (!warp_live) continue;
-      // the row's result, 32 columns at a time: O / l, or the partial sums
+      // The row's result, 32 columns at a time: O / l, or the partial sums. A lane's
+      // row is its own, so a store of 16 bytes a lane would touch every sector twice:
+      // whole sectors (32 bytes) where the output allows.
       const bool whole = walk.whole();
       const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
       char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
@@ -329,13 +335,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           uint32_t w[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(f[2 * c] * inv, f[2 * c + 1] * inv);
+          if (p.wide) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            reinterpret_cast<uint4*>(dst + 2 * c0)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            for (int c = 0; c < 16; c += 8)
+              stg_b32x8(dst + 2 * c0 + 4 * c, w[c], w[c + 1], w[c + 2], w[c + 3], w[c + 4], w[c + 5], w[c + 6], w[c + 7]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              reinterpret_cast<uint4*>(dst + 2 * c0)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          }
         } else {
-          float4* at = reinterpret_cast<float4*>(part + (size_t)rr * D + c0);
+          float* at = part + (size_t)rr * D + c0;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) at[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+          for (int c = 0; c < 32; c += 8)
+            stg_b32x8(at + c, r[c], r[c + 1], r[c + 2], r[c + 3], r[c + 4], r[c + 5], r[c + 6], r[c + 7]);
         }
       }
       if (live) {
@@ -602,7 +615,8 @@ cudaError_t launch(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c
   if (!make_tmap_tokens(&tq, q, s.T, s.H_kv, s.G, D, tokens) ||
       !make_tmap_pages(&tk, c.k, c, rows, F8 ? D : 128) || !make_tmap_pages(&tv, c.v, c, rows, F8 ? D : 128))
     return cudaErrorInvalidValue;
-  ChunkParams p{s, w, out, c.k_exp, c.v_exp, b.q_off, b.kv_len, b.page_table, tokens * s.G, scale * 1.4426950408889634f, err};
+  const int wide = reinterpret_cast<uintptr_t>(out.o) % 32 == 0 && out.st % 16 == 0 && out.sh % 16 == 0;
+  ChunkParams p{s, w, out, c.k_exp, c.v_exp, b.q_off, b.kv_len, b.page_table, tokens * s.G, wide, scale * 1.4426950408889634f, err};
   count_launches(1);
   return launch_dependent(chunk_kernel<D, F8>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, tq, tk, tv, p);
 }

@@ -42,7 +42,7 @@ struct PagedShape {
   int step, tile;  // query rows of a unit, keys of a tile
   int ctas, least;  // CTAs launched; tiles a CTA gets before another one does
   int local;  // every CTA plans for itself: no plan kernel
-  int whole;  // (local) no unit and head is divided: nothing to join
+  int whole;  // no unit and head is divided (every CTA plans for itself): nothing to join
   long long max_units;
 };
 
@@ -151,63 +151,132 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
       return nt;
     };
     auto holds = [&](unsigned x) { return some && x < total && upto - mine <= x && x < upto; };
-    // undivided units: a range begins and ends with the first unit and head at or after its ends
-    unsigned end = g;
-    if (s.whole) {
-      unsigned up = 0;
-      if (holds(g)) {
-        PagedStart st;
-        const unsigned nt = find(g, st, up);
-        up = st.kt ? up + nt : g;
-      }
-      end = max(g, __reduce_max_sync(0xffffffffu, up));
-    }
     if (holds(f)) {
       PagedStart st = {};
-      unsigned at, from = f;
+      unsigned at;
       const unsigned nt = find(f, st, at);
-      if (s.whole && st.kt) {
-        from = at + nt;
-        st.kt = 0;
-        if (++st.h == s.H_kv && from < end) {
-          st.h = 0;
-          int4 q = seq[st.u];
-          if (++st.i >= q.w) {
-            st.i = 0;
-            do q = seq[++st.u];
-            while (q.w == 0 && st.u + 1 < s.R);
-          }
-          st.unit = unit_at(s, st.u, q.x, q.y, q.z, st.i);
-        }
-      } else if (st.kt) {
-        sharers(st, at, nt, total, used);
-      }
-      st.count = (int)(end - from);
+      if (st.kt) sharers(st, at, nt, total, used);
+      st.count = (int)(g - f);
       *out = st;
     }
   }
   __syncthreads();
 }
 
-// A CTA's walk over its range of tiles: one (unit, head) at a time.
+// The same where no unit and head is divided (s.whole): they are dealt to the CTAs
+// largest first, forth and back, so that each CTA's tiles add up to about the same.
+// Several sequences (one's units are in order as they are): first: R + 1 running sums of the sequences' units; order: the units from the
+// largest on; sizes: their tiles (scratch); all shared memory.
+__device__ __forceinline__ void plan_whole(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int4* seq,
+                                           uint16_t* first, uint16_t* order, uint16_t* sizes, PagedStart* out, int* err) {
+  bool bad = false;
+  for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
+    int a, n, L;
+    bad |= sequence_at(s, q_off, kv_len, r, a, n, L);
+    seq[r] = make_int4(a, n, L, (n * s.G + s.step - 1) / s.step);
+  }
+  if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
+  __syncthreads();
+  int units = seq[0].w;
+  if (s.R > 1) {
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x, per = (s.R + 31) / 32, r0 = lane * per, r1 = min(s.R, r0 + per);
+      const int cap = (int)s.max_units;  // spans that overlap may hold more
+      int mine = 0;
+      for (int r = r0; r < r1; ++r) mine = min(mine + seq[r].w, cap);
+      int upto = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, m);
+        if (lane >= m) upto = min(upto + x, cap);
+      }
+      int sum = __shfl_up_sync(0xffffffffu, upto, 1);
+      if (lane == 0) sum = 0;
+      for (int r = r0; r < r1; ++r) {
+        first[r] = (uint16_t)sum;
+        sum = min(sum + seq[r].w, cap);
+      }
+      if (r0 < s.R && r1 == s.R) first[s.R] = (uint16_t)sum;
+    }
+    __syncthreads();
+    units = first[s.R];
+    for (int u = threadIdx.x; u < units; u += blockDim.x) {
+      int r = 0;
+      for (int hi = s.R - 1; r < hi;) {
+        const int mid = (r + hi) >> 1;
+        if (first[mid + 1] <= u)
+          r = mid + 1;
+        else
+          hi = mid;
+      }
+      sizes[u] = (uint16_t)unit_at(s, r, seq[r].x, seq[r].y, seq[r].z, u - first[r]).ntiles;
+    }
+    __syncthreads();
+    for (int u = threadIdx.x; u < units; u += blockDim.x) {
+      int rank = 0;
+      for (int v = 0; v < units; ++v) rank += (sizes[v] > sizes[u] || (sizes[v] == sizes[u] && v < u)) ? 1 : 0;
+      order[rank] = (uint16_t)u;
+    }
+  }
+  if (threadIdx.x == 0) {
+    // this CTA's items: number c of every even row of ctas items, ctas - 1 - c of every odd one
+    const int items = units * s.H_kv, rows = items / s.ctas, rest = items - rows * s.ctas, c = blockIdx.x;
+    PagedStart st = {};
+    st.count = rows + ((rows & 1 ? s.ctas - 1 - c : c) < rest ? 1 : 0);
+    *out = st;
+  }
+  __syncthreads();
+}
+
+// A CTA's walk over its range of tiles, or its units: one (unit, head) at a time.
 struct PagedWalk {
   const PagedShape& s;
   const PagedUnit* units;  // the plan kernel's list
   const int4* seq;         // or this CTA's own sequences
+  const uint16_t* first;   // (whole) their first units
+  const uint16_t* order;   // (whole) the units, largest first
   int left, at, i, h, kt, n;  // current segment: tiles [kt, kt + n) of head h (n 0: a unit without keys)
   PagedUnit u;
 
-  __device__ PagedWalk(const PagedShape& s_, const PagedUnit* units_, const int4* seq_, const PagedStart& st)
-      : s(s_), units(units_), seq(seq_), left(st.count), at(st.u), i(st.i), h(st.h), kt(st.kt), u(st.unit) {
-    n = min(u.ntiles - kt, left);
+  __device__ PagedWalk(const PagedShape& s_, const PagedUnit* units_, const int4* seq_, const uint16_t* first_,
+                       const uint16_t* order_, const PagedStart& st)
+      : s(s_), units(units_), seq(seq_), first(first_), order(order_), left(st.count), at(st.u), i(st.i), h(st.h),
+        kt(st.kt), u(st.unit) {
+    if (s.whole && left > 0) deal();
+    n = s.whole ? u.ntiles : min(u.ntiles - kt, left);
   }
   __device__ bool more() const { return left > 0; }
   // the segment covers its unit wholly
-  __device__ bool whole() const { return kt == 0 && n == u.ntiles; }
+  __device__ bool whole() const { return s.whole || (kt == 0 && n == u.ntiles); }
   __device__ int slot() const { return kt == 0 ? 1 : 0; }
+  // (whole) row number `at` of the items
+  __device__ void deal() {
+    const int k = at * s.ctas + (at & 1 ? s.ctas - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    h = k % s.H_kv;
+    int v = k / s.H_kv, r = 0;
+    if (s.R == 1) {
+      v = seq[0].w - 1 - v;  // one sequence: its last units are its largest
+    } else {
+      v = order[v];
+      for (int hi = s.R - 1; r < hi;) {  // the sequence of unit v
+        const int mid = (r + hi) >> 1;
+        if (first[mid + 1] <= v)
+          r = mid + 1;
+        else
+          hi = mid;
+      }
+    }
+    u = unit_at(s, r, seq[r].x, seq[r].y, seq[r].z, s.R == 1 ? v : v - first[r]);
+  }
   __device__ void next() {
-    left -= max(n, 1);
+    left -= s.whole ? 1 : max(n, 1);
     if (left <= 0) return;
+    if (s.whole) {
+      ++at;
+      deal();
+      n = u.ntiles;
+      return;
+    }
     kt = 0;
     if (++h == s.H_kv) {
       h = 0;
@@ -227,9 +296,12 @@ struct PagedWalk {
   }
 };
 
-constexpr int kLocalSeqs = 256;   // few_kernel: sequences that a CTA plans for by itself
-constexpr int kLocalChunks = 64;  // chunk_kernel: the same (its shared memory is nearly full)
-constexpr int kLocalUnits = 512;  // units, at most: a thread counts those of its sequences one by one
+// Limits of a CTA's own plan: sequences (kLocalChunks: chunk_kernel, whose shared
+// memory is nearly full), units more than one a sequence, all units where those of
+// several sequences are dealt whole (each is ranked against all others).
+constexpr int kLocalSeqs = 256, kLocalChunks = 32;
+constexpr int kLocalUnits = 64;
+constexpr int kWholeUnits = 320;
 
 // Workspace of one call: units, the running sum of their work, CTA starts, the
 // partial slots (two a CTA: rows x d sums, then rows x (m, l)).

@@ -735,22 +735,24 @@ struct JoinParams {
 
 // Block (c, y): where CTA c's range is the second one inside a unit and head,
 // their parts (CTA c - 1's last segment, then c .. last's first segments) are
-// joined: a warp has ROWS rows (d = 64: twice as many), several parts of each in
-// flight at a time. Four rows and two parts for chunk_kernel's slots of 256 rows,
-// where the blocks of one row a warp were several times what the SMs hold; one row
-// and eight parts for the 16 rows of few_kernel's, which long caches split finely.
-template <int D, int ROWS>
+// joined. Latency bounds it, so it goes by what there is more of: many rows of a
+// few parts each (MANY_ROWS): four rows (d = 64: eight) a warp, two parts of each in
+// flight; or few rows of many parts, a long cache's: a row by four warps, eight
+// parts in flight in each (one token over 32000 keys, 38 parts: 32 us for the call,
+// 35 with one warp a row).
+template <int D, bool MANY_ROWS>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
-  constexpr int PARTS = ROWS == 1 ? 8 : 2;
+  constexpr int ROWS = MANY_ROWS ? 4 : 1, PARTS = MANY_ROWS ? 2 : 8, WPR = MANY_ROWS ? 1 : 4;
+  __shared__ float4 other[WPR > 1 ? 8 * 32 * V : 1];
+  __shared__ float2 other_ml[WPR > 1 ? 8 * RPW : 1];
   grid_dependency_wait();
   const int c = blockIdx.x + 1;
   const PagedStart& st = p.w.starts[c];
   if (st.count <= 0 || st.kt == 0 || st.first != c - 1) return;
-  const int lane = threadIdx.x & 31, col = 4 * (lane % LPR);
-  const int row0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * ROWS * RPW + lane / LPR;  // then every RPW-th
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 4 * (lane % LPR);
+  const int row0 = (blockIdx.y * (8 / WPR) + warp / WPR) * ROWS * RPW + lane / LPR;  // then every RPW-th
   const int nrows = st.unit.nrows;
-  if (row0 >= nrows) return;
   const int parts = st.last - c + 2;
   // part i: slot 1 of CTA c - 1 (i = 0), slot 0 of CTA c - 1 + i
   auto part = [&](int i) { return p.w.part + p.w.part_floats * (2 * (size_t)(c - 1 + i) + (i == 0 ? 1 : 0)); };
@@ -763,7 +765,21 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 #pragma unroll
     for (int x = 0; x < V; ++x) acc[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  for (int i0 = 0; i0 < parts; i0 += PARTS) {
+  // a row so far and one more part of it
+  auto add = [&](float& t, float& s, float4 (&a)[V], float pt, float ps, const float4 (&pv)[V]) {
+    const float m = fmaxf(t, pt), base = m == -INFINITY ? 0.f : m;
+    const float f = ex2_approx(t - base), y = ex2_approx(pt - base);
+    t = m;
+    s = s * f + y * ps;
+#pragma unroll
+    for (int x = 0; x < V; ++x) {
+      a[x].x = a[x].x * f + y * pv[x].x;
+      a[x].y = a[x].y * f + y * pv[x].y;
+      a[x].z = a[x].z * f + y * pv[x].z;
+      a[x].w = a[x].w * f + y * pv[x].w;
+    }
+  };
+  for (int i0 = PARTS * (warp % WPR); i0 < parts; i0 += PARTS * WPR) {
     float2 w[ROWS][PARTS];
     float4 v[ROWS][PARTS][V];
 #pragma unroll
@@ -783,33 +799,23 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
         }
       }
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      float t = top[r];
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) t = fmaxf(t, w[r][k].x);
-      const float base = t == -INFINITY ? 0.f : t;
-      const float f = ex2_approx(top[r] - base);
-      top[r] = t;
-      sum[r] *= f;
+      for (int k = 0; k < PARTS; ++k) add(top[r], sum[r], acc[r], w[r][k].x, w[r][k].y, v[r][k]);
+  }
+  if constexpr (WPR > 1) {
 #pragma unroll
-      for (int x = 0; x < V; ++x) {
-        acc[r][x].x *= f;
-        acc[r][x].y *= f;
-        acc[r][x].z *= f;
-        acc[r][x].w *= f;
-      }
+    for (int x = 0; x < V; ++x) other[(warp * V + x) * 32 + lane] = acc[0][x];
+    if (col == 0) other_ml[warp * RPW + lane / LPR] = make_float2(top[0], sum[0]);
+    __syncthreads();
+    if (warp % WPR) return;
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) {
-        const float y = ex2_approx(w[r][k].x - base);
-        sum[r] += y * w[r][k].y;
+    for (int k = 1; k < WPR; ++k) {
+      float4 v[V];
 #pragma unroll
-        for (int x = 0; x < V; ++x) {
-          acc[r][x].x += y * v[r][k][x].x;
-          acc[r][x].y += y * v[r][k][x].y;
-          acc[r][x].z += y * v[r][k][x].z;
-          acc[r][x].w += y * v[r][k][x].w;
-        }
-      }
+      for (int x = 0; x < V; ++x) v[x] = other[((warp + k) * V + x) * 32 + lane];
+      const float2 w = other_ml[(warp + k) * RPW + lane / LPR];
+      add(top[0], sum[0], acc[0], w.x, w.y, v);
     }
   }
 #pragma unroll
@@ -833,11 +839,13 @@ template <int D>
 cudaError_t launch_join(const PagedShape& s, const PagedWork& w, const PagedOut& out, int rows, cudaStream_t st) {
   if (s.ctas < 2) return cudaSuccess;
   const JoinParams j{w, out, s.G, rows};
-  const int per = 8 * (D == 64 ? 2 : 1) * (rows == kChunkRows ? 4 : 1);  // rows of a block
+  // few parts a unit: units enough that a CTA's range ends inside one about once
+  const bool many = rows == kChunkRows && 4 * (s.max_units - s.R / 2) * s.H_kv >= s.ctas;
+  const int per = (D == 64 ? 2 : 1) * (many ? 8 * 4 : 8 / 4);  // rows of a block
   const dim3 grid((unsigned)(s.ctas - 1), (unsigned)((rows + per - 1) / per));
   count_launches(1);
-  if (rows == kChunkRows) return launch_dependent(join_kernel<D, 4>, grid, 256, 0, st, j);
-  return launch_dependent(join_kernel<D, 1>, grid, 256, 0, st, j);
+  if (many) return launch_dependent(join_kernel<D, true>, grid, 256, 0, st, j);
+  return launch_dependent(join_kernel<D, false>, grid, 256, 0, st, j);
 }
 
 template <int D, bool F8>
@@ -908,9 +916,8 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   s.least = chunk ? 1 : few_warps(c.d, c.k_exp != nullptr);  // a tile for each computing warp, and fewer parts to join
   s.ctas = sm_count() * (chunk ? 1 : few_ctas(c.d, c.k_exp != nullptr));
   s.max_units = ((long long)T * s.G + s.step - 1) / s.step + b.R;
-  // Each CTA plans for itself where that is a few steps a thread (a thread counts the
-  // units of its sequences one by one: 257 of one sequence took 60 us); a plan
-  // kernel (one CTA, about 4 us of the stream) for larger batches.
+  // Each CTA plans for itself where that is a few steps a warp; a plan kernel (one
+  // CTA, about 4 us of the stream) for larger batches.
   const long long most = ((long long)b.width * s.page + s.tile - 1) / s.tile;  // tiles of a unit
   const bool few_seqs = b.R <= (chunk ? kLocalChunks : kLocalSeqs);
   s.whole = few_seqs && (b.R == 1 || s.max_units <= kWholeUnits) && stay_whole(s, b, most, chunk);

@@ -103,20 +103,24 @@ __device__ __forceinline__ void sharers(PagedStart& st, I f0, I nt, I total, I u
 __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int4* seq,
                                              unsigned* work, PagedStart* out, int* err) {
   bool bad = false;
-  for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < s.R; r += blockDim.x >> 5) {  // a warp a sequence, a lane a unit
     int a, n, L;
     bad |= sequence_at(s, q_off, kv_len, r, a, n, L);
     const int units = (n * s.G + s.step - 1) / s.step;
     unsigned w = 0;
-    for (int i = 0; i < units; ++i) w += max(unit_at(s, r, a, n, L, i).ntiles, 1);
-    seq[r] = make_int4(a, n, L, units);
-    work[r] = w * s.H_kv;
+    for (int i = lane; i < units; i += 32) w += max(unit_at(s, r, a, n, L, i).ntiles, 1);
+    w = __reduce_add_sync(0xffffffffu, w);
+    if (lane == 0) {
+      seq[r] = make_int4(a, n, L, units);
+      work[r] = w * s.H_kv;
+    }
   }
   if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
   if (threadIdx.x == 0) *out = PagedStart{};
   __syncthreads();
   if (threadIdx.x < 32) {
-    const int lane = threadIdx.x, per = (s.R + 31) / 32, r0 = lane * per, r1 = min(s.R, r0 + per);
+    const int per = (s.R + 31) / 32, r0 = lane * per, r1 = min(s.R, r0 + per);
     unsigned mine = 0;
     for (int r = r0; r < r1; ++r) mine += work[r];
     unsigned upto = mine;
@@ -126,38 +130,47 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
       if (lane >= m) upto += x;
     }
     const unsigned total = __shfl_sync(0xffffffffu, upto, 31), used = used_ctas(s, total), c = blockIdx.x;
-    const bool some = c < used && total > 0;
-    const unsigned f = some ? total * c / used : 0, g = some ? total * (c + 1) / used : 0;
-    // tile x lies in this lane's sequences: sequence, unit, head and tile of it; the
-    // first tile of that unit and head into at; their number of tiles
-    auto find = [&](unsigned x, PagedStart& st, unsigned& at) -> unsigned {
-      at = upto - mine;
+    if (c < used && total > 0) {  // (the same for every lane)
+      const unsigned f = total * c / used, g = total * (c + 1) / used;
+      // tile f: its sequence, in the range of the one lane whose sequences hold it
       int r = r0;
-      while (r < r1 - 1 && at + work[r] <= x) at += work[r++];
+      unsigned at = upto - mine;
+      const bool holds = at <= f && f < upto;
+      if (holds)
+        while (r < r1 - 1 && at + work[r] <= f) at += work[r++];
+      const int owner = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
+      r = __shfl_sync(0xffffffffu, r, owner);
+      at = __shfl_sync(0xffffffffu, at, owner);
+      // its unit, 32 at a time
       const int4 q = seq[r];
-      unsigned nt = 1;
-      int i = 0;
-      for (;; ++i) {
-        st.unit = unit_at(s, r, q.x, q.y, q.z, i);
-        nt = max(st.unit.ntiles, 1);
-        if (i + 1 >= q.w || at + nt * s.H_kv > x) break;
-        at += nt * s.H_kv;
+      for (int i0 = 0; i0 < q.w; i0 += 32) {
+        const int i = i0 + lane;
+        PagedStart st = {};
+        unsigned nt = 0;
+        if (i < q.w) {
+          st.unit = unit_at(s, r, q.x, q.y, q.z, i);
+          nt = max(st.unit.ntiles, 1);
+        }
+        unsigned end = nt * s.H_kv;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const unsigned x = __shfl_up_sync(0xffffffffu, end, m);
+          if (lane >= m) end += x;
+        }
+        const unsigned from = at + end - nt * s.H_kv;  // this lane's unit: tiles [from, at + end)
+        if (i < q.w && from <= f && f < at + end) {
+          st.u = r;
+          st.i = i;
+          st.h = (f - from) / nt;
+          const unsigned f0 = from + st.h * nt;
+          st.kt = f - f0;
+          st.count = g - f;
+          if (st.kt) sharers(st, f0, nt, total, used);
+          *out = st;
+        }
+        at += __shfl_sync(0xffffffffu, end, 31);
+        if (at > f) break;
       }
-      st.u = r;
-      st.i = i;
-      st.h = (x - at) / nt;
-      at += st.h * nt;
-      st.kt = x - at;
-      return nt;
-    };
-    auto holds = [&](unsigned x) { return some && x < total && upto - mine <= x && x < upto; };
-    if (holds(f)) {
-      PagedStart st = {};
-      unsigned at;
-      const unsigned nt = find(f, st, at);
-      if (st.kt) sharers(st, at, nt, total, used);
-      st.count = (int)(g - f);
-      *out = st;
     }
   }
   __syncthreads();
@@ -300,7 +313,7 @@ struct PagedWalk {
 // memory is nearly full), units more than one a sequence, all units where those of
 // several sequences are dealt whole (each is ranked against all others).
 constexpr int kLocalSeqs = 256, kLocalChunks = 32;
-constexpr int kLocalUnits = 64;
+constexpr int kLocalUnits = 512;
 constexpr int kWholeUnits = 320;
 
 // Workspace of one call: units, the running sum of their work, CTA starts, the

@@ -735,15 +735,16 @@ struct JoinParams {
 
 // Block (c, y): where CTA c's range is the second one inside a unit and head,
 // their parts (CTA c - 1's last segment, then c .. last's first segments) are
-// joined. Latency bounds it, so it goes by what there is more of: many rows of a
-// few parts each (MANY_ROWS): four rows (d = 64: eight) a warp, two parts of each in
-// flight; or few rows of many parts, a long cache's: a row by four warps, eight
-// parts in flight in each (one token over 32000 keys, 38 parts: 32 us for the call,
-// 35 with one warp a row).
-template <int D, bool MANY_ROWS>
+// joined. Latency bounds it, so it goes by what there is more of. Many rows of a
+// few parts each (chunk_kernel's slots of 256 rows): ROWS = 4 rows (d = 64: eight) a
+// warp, two parts of each in flight. Few rows: one a warp, eight parts in flight, or,
+// of many parts, a long cache's, one by WPR = 4 warps (one token over 32000 keys, 38
+// parts: 32 us for the call, 35 with one warp a row; but where one warp is enough,
+// three times the blocks cost about 2 us).
+template <int D, int ROWS, int WPR>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
-  constexpr int ROWS = MANY_ROWS ? 4 : 1, PARTS = MANY_ROWS ? 2 : 8, WPR = MANY_ROWS ? 1 : 4;
+  constexpr int PARTS = ROWS > 1 ? 2 : 8;
   __shared__ float4 other[WPR > 1 ? 8 * 32 * V : 1];
   __shared__ float2 other_ml[WPR > 1 ? 8 * RPW : 1];
   grid_dependency_wait();
@@ -839,13 +840,19 @@ template <int D>
 cudaError_t launch_join(const PagedShape& s, const PagedWork& w, const PagedOut& out, int rows, cudaStream_t st) {
   if (s.ctas < 2) return cudaSuccess;
   const JoinParams j{w, out, s.G, rows};
-  // few parts a unit: units enough that a CTA's range ends inside one about once
-  const bool many = rows == kChunkRows && 4 * (s.max_units - s.R / 2) * s.H_kv >= s.ctas;
-  const int per = (D == 64 ? 2 : 1) * (many ? 8 * 4 : 8 / 4);  // rows of a block
-  const dim3 grid((unsigned)(s.ctas - 1), (unsigned)((rows + per - 1) / per));
-  count_launches(1);
-  if (many) return launch_dependent(join_kernel<D, true>, grid, 256, 0, st, j);
-  return launch_dependent(join_kernel<D, false>, grid, 256, 0, st, j);
+  // units and heads, and the parts that each comes in, about
+  const double units = (double)(s.max_units - s.R / 2) * s.H_kv;
+  const double tiles = (double)s.width * s.page / s.tile;
+  const double parts = std::min(s.ctas / units, tiles / s.least) + 1;
+  auto go = [&](auto kernel, int per) {  // rows of a block
+    const dim3 grid((unsigned)(s.ctas - 1), (unsigned)((rows + per - 1) / per));
+    count_launches(1);
+    return launch_dependent(kernel, grid, 256, 0, st, j);
+  };
+  constexpr int RPW = D == 64 ? 2 : 1;
+  if (parts > 9) return go(join_kernel<D, 1, 4>, 2 * RPW);
+  if (rows == kChunkRows) return go(join_kernel<D, 4, 1>, 32 * RPW);
+  return go(join_kernel<D, 1, 1>, 8 * RPW);
 }
 
 template <int D, bool F8>

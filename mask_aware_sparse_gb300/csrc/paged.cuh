@@ -104,19 +104,26 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
                                              unsigned* work, PagedStart* out, int* err) {
   bool bad = false;
   const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < s.R; r += blockDim.x >> 5) {  // a warp a sequence, a lane a unit
+  constexpr int kAlone = 4;  // units that a thread counts by itself
+  for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
     int a, n, L;
     bad |= sequence_at(s, q_off, kv_len, r, a, n, L);
     const int units = (n * s.G + s.step - 1) / s.step;
     unsigned w = 0;
-    for (int i = lane; i < units; i += 32) w += max(unit_at(s, r, a, n, L, i).ntiles, 1);
-    w = __reduce_add_sync(0xffffffffu, w);
-    if (lane == 0) {
-      seq[r] = make_int4(a, n, L, units);
-      work[r] = w * s.H_kv;
-    }
+    for (int i = 0; i < units && units <= kAlone; ++i) w += max(unit_at(s, r, a, n, L, i).ntiles, 1);
+    seq[r] = make_int4(a, n, L, units);
+    work[r] = w * s.H_kv;
   }
   if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
+  __syncthreads();
+  for (int r = threadIdx.x >> 5; r < s.R; r += blockDim.x >> 5) {  // longer ones: a lane a unit
+    const int4 q = seq[r];
+    if (q.w <= kAlone) continue;
+    unsigned w = 0;
+    for (int i = lane; i < q.w; i += 32) w += max(unit_at(s, r, q.x, q.y, q.z, i).ntiles, 1);
+    w = __reduce_add_sync(0xffffffffu, w);
+    if (lane == 0) work[r] = w * s.H_kv;
+  }
   if (threadIdx.x == 0) *out = PagedStart{};
   __syncthreads();
   if (threadIdx.x < 32) {

@@ -766,7 +766,8 @@ def fm_balance_chunks(w, P: int, kappa: int, phases: int = 3, node_budget: int =
 # ------------------------------------------------ norm, rotation, paged cache
 # These calls are made many times a token, on tensors whose kernels take a few
 # microseconds, so their checks are plain comparisons (messages are built only
-# on failure) and their structures are packed bytes, passed by address.
+# on failure) and their structures are packed bytes, passed by address. All of them
+# take a keyword `stream`.
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 _pack_view, _pack_rows = struct.Struct("=Qqqq").pack, struct.Struct("=Qqq").pack  # fm_view, fm_rows
 _pack_qk = struct.Struct("=8i2fQqQQQ").pack  # fm_qk_problem
@@ -788,21 +789,32 @@ def _fast_fn(name):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _enqueue(name, dev, stream, *args):
-    """Call a library function whose last argument is the stream: the given one, or
-    the current stream of device `dev` (an index), with that device current."""
+def _enqueue(name, dev, *args):
+    """Call a library function whose last argument is the stream: the current stream
+    of device `dev` (an index), with that device current."""
     if dev < 0:
         raise ValueError("the tensors must be CUDA tensors: the library computes on the GPU only")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _enqueue(name, dev, stream, *args)
-    if stream is not None:
-        s = stream.cuda_stream
-    else:
-        s = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+            return _enqueue(name, dev, *args)
+    s = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     st = _fast_fn(name)(*args, s)
     if st != FM_OK:
         raise FMError(st, name)
+
+
+def _streamed(f):
+    """f with a `stream` argument: everything it does, new tensors and workspaces
+    included, belongs to that stream (None: the current one)."""
+
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+
+    return call
 
 
 def _tensor(t, name, dims):
@@ -924,8 +936,9 @@ def _qk_args(q, k, positions, inv_freq, interleaved, rot_scale, q_weight, k_weig
     return _pack_qk(B, N, Hq, Hkv, d, rot, 1 if interleaved else 0, f32, eps, rot_scale, pos, sb, fr, *w), dev
 
 
+@_streamed
 def fm_qk_norm_rope(q, k, v=None, *, positions=None, inv_freq=None, interleaved: bool = False, rot_scale: float = 1.0,
-                    q_weight=None, k_weight=None, eps: float = 1e-6, out=None, stream=None):
+                    q_weight=None, k_weight=None, eps: float = 1e-6, out=None):
     """Per-head norm and rotation of queries and keys in one pass: q (B, H_q, N, d),
     k, v (B, H_kv, N, d) bf16 views of any strides (rows contiguous), e.g. of a
     fused projection's output, to (q', k') or (q', k', v') contiguous (B, H, N, d),
@@ -951,7 +964,7 @@ def fm_qk_norm_rope(q, k, v=None, *, positions=None, inv_freq=None, interleaved:
         qv, kv = _view(out[0], "output q", qs, dev, True), _view(out[1], "output k", ks, dev, True)
         vv = None if v is None else _view(out[2], "output v", ks, dev, True)
         out = tuple(out)
-    _enqueue("fm_qk_norm_rope", dev, stream, p, qi, ki, vi, qv, kv, vv)
+    _enqueue("fm_qk_norm_rope", dev, p, qi, ki, vi, qv, kv, vv)
     return out
 
 
@@ -962,9 +975,9 @@ def _qk_bwd_bytes(dev, *sizes):
         return lib().fm_qk_norm_rope_bwd_workspace_bytes(fm_qk_problem(*sizes, q_weight=16, k_weight=16))
 
 
+@_streamed
 def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, interleaved: bool = False,
-                        rot_scale: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6, out=None,
-                        stream=None):
+                        rot_scale: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6, out=None):
     """Backward of fm_qk_norm_rope: the gradients dqo, dko, dvo (or None) of its
     outputs and its inputs q, k give (dq, dk, dv, dq_weight, dk_weight); None
     where there is no such input. dq, dk, dv are (B, H, N, d) views of contiguous
@@ -996,7 +1009,7 @@ def fm_qk_norm_rope_bwd(dqo, dko, dvo, q, k, *, positions=None, inv_freq=None, i
     if dwq is not None or dwk is not None:
         wsb = _qk_bwd_bytes(dev, qs[0], qs[2], qs[1], ks[1], qs[3])
         ws = torch.empty(max(16, wsb), dtype=_U8, device=on)
-    _enqueue("fm_qk_norm_rope_bwd", dev, stream, p, gq, gk, gv, qi, ki, qv, kv, vv,
+    _enqueue("fm_qk_norm_rope_bwd", dev, p, gq, gk, gv, qi, ki, qv, kv, vv,
              None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
              None if ws is None else ws.data_ptr(), wsb)
     return dq, dk, dv, dwq, dwk
@@ -1075,17 +1088,19 @@ def _serve_args(cache, batch):
     return cache.index
 
 
-def fm_cache_write(k, v, cache: KVCache, batch: PagedBatch, stream=None):
+@_streamed
+def fm_cache_write(k, v, cache: KVCache, batch: PagedBatch):
     """Put the rows of T new tokens, k and v (T, H_kv, d) bf16 views, in their places
     in the cache (rounded to e4m3 with a scale a row where the cache is e4m3)."""
     dev = _serve_args(cache, batch)
     _tensor(k, "k", 3)
     shape = (k.shape[0], cache.H_kv, cache.d)
     kr, vr = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
-    _enqueue("fm_cache_write", dev, stream, cache.at, batch.at, shape[0], kr, vr)
+    _enqueue("fm_cache_write", dev, cache.at, batch.at, shape[0], kr, vr)
 
 
-def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=None, stream=None):
+@_streamed
+def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=None):
     """Keys and values as packed bf16 rows (1, H_kv, n_rows, d): sequence r's keys from 0
     on become rows [kv_off[r], kv_off[r + 1]). kv_off (R + 1,) and page_table (R, width)
     int32. Rows that no sequence has are left as they were (undefined in new tensors)."""
@@ -1097,6 +1112,8 @@ def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=
     _expect(page_table, "page_table", (R, width), _I32, dev)
     _expect(kv_off, "kv_off", (R + 1,), _I32, dev)
     shape = (1, cache.H_kv, int(n_rows), cache.d)
+    if not 0 <= shape[2] <= 1 << 30:
+        raise ValueError(f"n_rows must be in [0, 2^30], got {n_rows}")
     if k is None:
         k = torch.empty(shape, dtype=_BF16, device=cache.device)
     else:
@@ -1105,7 +1122,7 @@ def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=
         v = torch.empty(shape, dtype=_BF16, device=cache.device)
     else:
         _expect(v, "v", shape, _BF16, dev)
-    _enqueue("fm_cache_read", dev, stream, cache.at, kv_off.data_ptr(), page_table.data_ptr(), R, width, shape[2],
+    _enqueue("fm_cache_read", dev, cache.at, kv_off.data_ptr(), page_table.data_ptr(), R, width, shape[2],
              k.data_ptr(), v.data_ptr())
     return k, v
 
@@ -1124,8 +1141,9 @@ def fm_attn_paged_workspace_bytes(cache: KVCache, batch: PagedBatch, T: int, H_q
                         cache.page_size, cache.d, cache.k_exp is not None)
 
 
+@_streamed
 def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal: bool = True, window: int = 0,
-                  sinks: int = 0, o=None, lse=None, ws=None, stream=None):
+                  sinks: int = 0, o=None, lse=None, ws=None):
     """Attention of T new tokens q (T, H_q, d) over the paged cache, their own keys and
     values written before (fm_cache_write): (O bf16 (T, H_q, d), LSE fp32 (T, H_q)).
     Position p sees key j < kv_len iff j <= p (when causal) and, with a window,
@@ -1139,6 +1157,9 @@ def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal:
         raise ValueError(f"q has d={d}, the cache d={cache.d}")
     if Hq <= 0 or Hq % cache.H_kv:
         raise ValueError(f"H_q={Hq} must be a multiple of H_kv={cache.H_kv}")
+    if not (0 <= window and 0 <= sinks):
+        raise ValueError(f"window and sinks must not be negative, got {window} and {sinks}")
+    window, sinks = min(window, 1 << 30), min(sinks, 1 << 30)  # (all positions are below)
     qr = _rows(q, "q", shape, dev)
     if o is None:
         o = torch.empty(shape, dtype=_BF16, device=cache.device)
@@ -1155,7 +1176,7 @@ def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal:
     elif (not isinstance(ws, torch.Tensor) or not ws.is_contiguous() or ws.dtype != _U8 or ws.numel() < wsb
           or ws.get_device() != dev):
         raise ValueError(f"ws must be a contiguous uint8 tensor of at least {wsb} bytes on the cache's device")
-    _enqueue("fm_attn_paged", dev, stream, cache.at, batch.at, T, Hq, qr, scale, 1 if causal else 0, window, sinks,
+    _enqueue("fm_attn_paged", dev, cache.at, batch.at, T, Hq, qr, scale, 1 if causal else 0, window, sinks,
              orow, lse.data_ptr(), ws.data_ptr(), wsb)
     return o, lse
 

@@ -871,20 +871,21 @@ cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cach
 }
 
 // Whether units stay whole, one CTA each, or ranges of tiles may end inside them.
-// Whole units leave CTAs idle in the last round, `most` tiles each at worst;
-// divided ones cost the parts' writing and joining, and a start and an end for every
-// part. What the host knows decides: the units that T tokens make, the keys that
-// the page table has room for. chunk_kernel (tiles of 128 keys, about 1.9 us):
-// 2048 tokens of 32 / 8 heads over themselves 40 us whole, 90 divided; 4096 over
-// themselves 122, 233; 2048 over 4096 keys 95, 113; 256 over 2048 keys 37, 30; a
+// Whole units leave CTAs idle in the last round, `most` tiles each at worst (and
+// sequences are taken to be ragged: two fifths of it at least, where there are
+// several); divided ones cost the parts' writing and joining, and a start and an end
+// for every part. What the host knows decides: the units that T tokens make, the
+// keys that the page table has room for. chunk_kernel (tiles of 128 keys, about 1.9
+// us): 2048 tokens of 32 / 8 heads over themselves 38 us whole, 90 divided; 4096
+// over themselves 121, 233; 2048 over 4096 keys 95, 113; 256 over 2048 keys 37, 30; a
 // full prompt's units grow from one tile to `most`, so less is left idle. few_kernel
-// (tiles of 32 keys): 64 sequences of 500 keys 22 whole, 25 divided; one 11.7, 8.6.
+// (tiles of 32 keys): 64 sequences of 500 keys 18 us whole, 25 divided; one 11.7, 8.6.
 bool stay_whole(const PagedShape& s, const fm_paged_batch& b, long long most, bool chunk) {
   const double units = (double)s.H_kv * (chunk ? ((double)s.T * s.G / s.step + b.R / 2.0)
                                                : std::max((double)b.R, (double)s.T * s.G / s.step));
   const double rounds = units / s.ctas;
-  double idle = most * (std::ceil(rounds) - rounds);
-  if (s.causal && s.window == 0 && 2ll * s.T >= (long long)b.R * b.width * s.page)
+  double idle = most * std::max(std::ceil(rounds) - rounds, b.R > 1 ? 0.4 : 0.0);
+  if (b.R == 1 && s.causal && s.window == 0 && 2ll * s.T >= (long long)b.width * s.page)
     idle /= 4 * std::max(1.0, rounds);
   if (!chunk) idle /= std::max(1.0, rounds);  // ragged lengths even out over the rounds
   return idle <= (chunk ? 5 + 8 * std::min(1.0, rounds) : 8);

@@ -370,3 +370,114 @@ def test_a_served_sequence_is_the_trained_one():
             at += n
         assert at == N
     assert fm.fm_device_status() == (fm.FM_OK, 0)
+
+
+@pytest.mark.parametrize("d, f8", [(64, True), (128, False), (128, True)])
+def test_many_chunks_of_ragged_lengths(d, f8):
+    # more sequences than a CTA plans for by itself: chunks of every size beside single tokens
+    g = torch.Generator().manual_seed(12)
+    new = torch.randint(0, 60, (45,), generator=g).tolist()
+    new[3], new[7], new[20] = 400, 1, 0
+    keys = [n + int(x) for n, x in zip(new, torch.randint(0, 300, (45,), generator=g))]
+    s = Setup(keys, new, 2, d, 32, f8, seed=13)
+    s.attend(6)
+
+
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("d, Hq, Hkv, n", [(128, 8, 2, 1300), (64, 2, 2, 2000)])
+def test_a_prompt_over_itself(d, Hq, Hkv, n, window):
+    # whole units, dealt largest first: one per CTA and more
+    s = Setup([n], [n], Hkv, d, 64, False, seed=14)
+    s.attend(Hq, window=window, sinks=3 if window else 0)
+    s = Setup([n, 77], [n, 50], Hkv, d, 64, False, seed=15)
+    s.attend(Hq, window=window)
+
+
+def test_one_long_sequence_among_short_ones():
+    s = Setup([4000] + [20] * 30, [1] * 31, 2, 64, 16, False, seed=16)
+    s.attend(8)
+    s = Setup([3000] + [40] * 20, [40] + [30] * 20, 1, 64, 16, True, seed=17)
+    s.attend(4)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [1, 50])
+def test_new_tokens_without_keys(n, causal):
+    s = Setup([64, 30], [0, 0], 2, 64, 16, False, seed=18)
+    kv_len = torch.tensor([0, 30], dtype=torch.int32).cuda()
+    b = fm.PagedBatch(torch.tensor([0, n, 2 * n], dtype=torch.int32).cuda(), kv_len, s.table)
+    q = torch.randn(2 * n, 4, 64, generator=s.g).to(torch.bfloat16).cuda()
+    o, lse = fm.fm_attn_paged(q, s.cache, b, scale=0.125, causal=causal)
+    assert (o[:n] == 0).all() and torch.isneginf(lse[:n]).all()
+    k, v = s.values()
+    ref = paged(q[n:].double().cpu(), [k[1]], [v[1]], [0, n], [30], 0.125, causal, 0, 0)
+    assert_paged(o[n:], lse[n:], ref, 64)
+    # no tokens at all
+    o, lse = fm.fm_attn_paged(q[:0], s.cache, b, scale=0.125)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    fm.fm_cache_write(q[:0, :2], q[:0, :2], s.cache, b)
+    assert fm.fm_device_status() == (fm.FM_OK, 0)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 30, 60]])
+@pytest.mark.parametrize("f8", [False, True])
+def test_a_visible_nan_stays_in_its_sequence(new, f8):
+    s = Setup([100, 90, 200], new, 2, 64, 16, f8, seed=19)
+    q, o, lse = s.attend(4)
+    for which in (s.k, s.v):
+        bad = which.clone()
+        bad[100 + 5] = float("nan")  # key 5 of the second sequence
+        fm.fm_cache_write(*((bad.cuda(), s.v.cuda()) if which is s.k else (s.k.cuda(), bad.cuda())), s.cache,
+                          fm.PagedBatch(s.kv_off, s.kv_len, s.table))
+        o2, l2 = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=64 ** -0.5)
+        a, b = s.q_off.tolist()[1:3]
+        assert torch.isnan(o2[a:b]).all()
+        for part in (slice(0, a), slice(b, None)):
+            assert torch.equal(o2[part], o[part]) and torch.equal(l2[part], lse[part])
+
+
+def test_a_given_stream_owns_what_a_call_allocates():
+    # a slow stream: memory that the call's outputs and workspace came from is not
+    # handed out again before the stream has passed
+    s = Setup([3000], [1], 2, 128, 16, False, seed=20)
+    q, o, lse = s.attend(8)
+    q = q.cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    outs = [fm.fm_attn_paged(q, s.cache, s.batch, scale=128 ** -0.5, stream=side) for _ in range(3)]
+    junk = [torch.full((1 << 22,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(40)]
+    side.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, o) and torch.equal(b, lse)
+    del junk
+
+
+def test_arguments_refused():
+    s = Setup([20], [2], 2, 64, 16, False)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16).cuda()
+    for kw in (dict(window=-1), dict(sinks=-1), dict(window=-(2 ** 40)), dict(o=q.float()), dict(o=q[:1]),
+               dict(lse=torch.zeros(2, 4)), dict(lse=torch.zeros(4, 2).cuda()), dict(ws=torch.zeros(8).cuda()),
+               dict(o=q[:, :1].expand(2, 4, 64))):
+        with pytest.raises(ValueError):
+            fm.fm_attn_paged(q, s.cache, s.batch, scale=0.1, **kw)
+    for bad in (q[:, :3], q[..., :32], q.float(), q[0]):
+        with pytest.raises((ValueError, fm.FMError)):
+            fm.fm_attn_paged(bad, s.cache, s.batch, scale=0.1)
+    for kw in (dict(scale=0.0), dict(scale=0.1, causal=False, window=3), dict(scale=float("nan"))):
+        with pytest.raises(fm.FMError):
+            fm.fm_attn_paged(q, s.cache, s.batch, **kw)
+    with pytest.raises(ValueError):
+        fm.fm_cache_read(s.cache, s.kv_off, s.table, -1)
+    with pytest.raises(ValueError):
+        fm.fm_cache_write(q, q[:1], s.cache, s.batch)
+    # broadcast queries (a stride of zero) are read like any others
+    one = torch.randn(1, 1, 64, generator=s.g).to(torch.bfloat16).cuda()
+    a = fm.fm_attn_paged(one.expand(2, 4, 64), s.cache, s.batch, scale=0.1)
+    b = fm.fm_attn_paged(one.expand(2, 4, 64).contiguous(), s.cache, s.batch, scale=0.1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    big = fm.PagedBatch(torch.tensor([0, 20], dtype=torch.int32).cuda(), s.kv_len, s.table)
+    a = fm.fm_attn_paged(one.expand(20, 4, 64), s.cache, big, scale=0.1)
+    b = fm.fm_attn_paged(one.expand(20, 4, 64).contiguous(), s.cache, big, scale=0.1)
+    assert float((a[0].float() - b[0].float()).abs().max()) <= 2 ** -6 * float(s.v.abs().max())

@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
             qf[k][x] = pack_f16x2(__uint_as_float(qf[k][x] << 16) * f, __uint_as_float(qf[k][x] & 0xffff0000u) * f);
       }
     }
+    const bool many = u.nrows > 8;  // some thread has a second row (half the softmax otherwise)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float mo[2] = {-INFINITY, -INFINITY};  // e4m3: the running maximum of score + exponent of the value's scale
     float o[D / 8][4];
@@ -532,10 +533,11 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
           }
         }
         // a running maximum moves only when it is passed by more than 8 (weights stay below 2^8)
-        float f[2];
+        float f[2] = {1.f, 1.f};
         bool moved = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          if (i == 1 && !many) break;
           float x = -INFINITY, z = -INFINITY;
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
@@ -547,7 +549,6 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
           if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 1));
           x = fmaxf(x, __shfl_xor_sync(kAll, x, 2)) * sc[i];
           if constexpr (F8) z = fmaxf(z, __shfl_xor_sync(kAll, z, 2));
-          f[i] = 1.f;
           if (x > m[i] + 8.f) {
             const float y = ex2_approx(m[i] - x);
             l[i] *= y;
@@ -573,17 +574,17 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
           }
         }
         // weights: bf16 in two terms (p and what its rounding left), fp16 in one
-        uint32_t hi[2][4], lo[2][4];
+        uint32_t hi[2][4] = {}, lo[2][4] = {};
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int i = 0; i < 2; ++i) {
+          if (i == 1 && !many) break;
+          const float base = m[i] == -INFINITY ? 0.f : m[i], bo = mo[i] == -INFINITY ? 0.f : mo[i];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float base = m[i] == -INFINITY ? 0.f : m[i];
+          for (int n = 0; n < 4; ++n) {
             const float a = ex2_approx(fmaf(s[n][2 * i], sc[i], -base));
             const float b = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], -base));
             l[i] += a + b;
             if constexpr (F8) {
-              const float bo = mo[i] == -INFINITY ? 0.f : mo[i];
               const float x = ex2_approx(fmaf(s[n][2 * i], sc[i], ve[n][0] - bo));
               const float y = ex2_approx(fmaf(s[n][2 * i + 1], sc[i], ve[n][1] - bo));
               hi[n >> 1][2 * (n & 1) + i] = pack_f16x2(x, y);
@@ -594,6 +595,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
                   pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
             }
           }
+        }
         const uint32_t vb0 = ring + sv * C::TILE + v_at0, vb1 = ring + sv * C::TILE + v_at1;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {  // 16 keys each

@@ -337,9 +337,11 @@ struct PagedWork {
 
 inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// (wherever the workspace starts: its parts start on 256-byte boundaries, for which the
+// size has room; the parts' rows are stored 32 bytes at a time)
 inline PagedWork paged_work(const PagedShape& s, int rows, void* ws) {
   PagedWork w = {};
-  char* p = static_cast<char*>(ws);
+  char* p = reinterpret_cast<char*>(round256(reinterpret_cast<uintptr_t>(ws)));
   size_t o = 0;
   auto take = [&](size_t bytes) {
     char* at = p ? p + o : nullptr;
@@ -352,7 +354,7 @@ inline PagedWork paged_work(const PagedShape& s, int rows, void* ws) {
   w.starts = reinterpret_cast<PagedStart*>(take(sizeof(PagedStart) * (size_t)s.ctas));
   w.part_floats = (size_t)rows * (s.d + 2);
   w.part = reinterpret_cast<float*>(take(sizeof(float) * w.part_floats * 2 * (size_t)s.ctas));
-  w.bytes = o;
+  w.bytes = o + 255;
   return w;
 }
 

@@ -225,6 +225,20 @@ def test_same_bits_padding_rows_and_views(new, keys):
         fm.fm_attn_paged(wide[:, :4], s.cache, s.batch, scale=1.0, ws=ws[:-1])
 
 
+@pytest.mark.parametrize("new, keys, d", [([1], [3000], 128), ([70], [3000], 128), ([90], [2500], 64)])
+def test_a_workspace_at_any_16_byte_boundary(new, keys, d):
+    # divided units leave parts there
+    s = Setup(keys, new, 2, d, 32, False, seed=21)
+    T = new[0]
+    need = fm.fm_attn_paged_workspace_bytes(s.cache, s.batch, T, 8)
+    buf = torch.full((need + 512,), 0x5a, dtype=torch.uint8).cuda()
+    q, o, lse = s.attend(8)
+    for at in (16, 48, 240):
+        o2, l2 = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=d ** -0.5, ws=buf[at:at + need])
+        assert torch.equal(o2, o) and torch.equal(l2, lse)
+        assert (buf[:at] == 0x5a).all() and (buf[at + need:] == 0x5a).all()
+
+
 def test_quantised_is_the_cache_read_back():
     # an e4m3 cache gives what its bf16 copy gives, up to the order of the same sums
     s = Setup([500, 77], [40, 1], 2, 128, 32, True, seed=5)

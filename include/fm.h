@@ -495,7 +495,7 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  * All device int32. Tokens from q_off[R] on belong to no sequence: their rows are
  * neither read nor written. Values that no such batch has (a page outside
  * [0, n_pages), a length outside [0, width * page_size], offsets that descend or
- * pass T) set FM_DEVERR_RANGE; their rows are then left out or read as zeros,
+ * pass T) set FM_DEVERR_RANGE; what rows of such a batch receive is then undefined,
  * nothing outside the tensors is touched.
  *
  * fm_cache_write puts the new tokens' rows k, v (element strides st a token, sh

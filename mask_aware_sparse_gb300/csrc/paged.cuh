@@ -97,17 +97,19 @@ __device__ __forceinline__ void sharers(PagedStart& st, I f0, I nt, I total, I u
 }
 
 // The plan as one CTA makes it for itself, for a few hundred units at most and a
-// total work that 32 bits hold: every sequence into seq (first token, tokens,
+// total work that 32 bits hold (offsets that descend, whose spans may overlap and add
+// up to more, plan nothing): every sequence into seq (first token, tokens,
 // keys, units), its work into work (both shared memory, R entries), the CTA's
 // range into *out (shared memory).
 __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int4* seq,
                                              unsigned* work, PagedStart* out, int* err) {
-  bool bad = false;
+  bool bad = false, descends = false;
   const int lane = threadIdx.x & 31;
   constexpr int kAlone = 4;  // units that a thread counts by itself
   for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
     int a, n, L;
     bad |= sequence_at(s, q_off, kv_len, r, a, n, L);
+    descends |= q_off[r + 1] < q_off[r];
     const int units = (n * s.G + s.step - 1) / s.step;
     unsigned w = 0;
     for (int i = 0; i < units && units <= kAlone; ++i) w += max(unit_at(s, r, a, n, L, i).ntiles, 1);
@@ -115,7 +117,7 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
     work[r] = w * s.H_kv;
   }
   if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
-  __syncthreads();
+  const bool none = __syncthreads_or(descends);
   for (int r = threadIdx.x >> 5; r < s.R; r += blockDim.x >> 5) {  // longer ones: a lane a unit
     const int4 q = seq[r];
     if (q.w <= kAlone) continue;
@@ -137,7 +139,7 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
       if (lane >= m) upto += x;
     }
     const unsigned total = __shfl_sync(0xffffffffu, upto, 31), used = used_ctas(s, total), c = blockIdx.x;
-    if (c < used && total > 0) {  // (the same for every lane)
+    if (c < used && total > 0 && !none) {  // (the same for every lane)
       const unsigned f = total * c / used, g = total * (c + 1) / used;
       // tile f: its sequence, in the range of the one lane whose sequences hold it
       int r = r0;

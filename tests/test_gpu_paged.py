@@ -155,6 +155,23 @@ def test_bad_metadata_is_flagged_and_stays_inside():
     assert fm.fm_device_status() == (fm.FM_ERR_DEVICE, fm.FM_DEVERR_RANGE)
 
 
+def test_overlapping_spans_of_a_large_batch_plan_nothing():
+    # descending offsets: five spans of all nine tokens, whose tiles times the CTAs pass 32 bits
+    R, Hkv, width = 9, 64, 1000
+    cache = fm.fm_cache_new(1, Hkv, 128, 64)
+    cache.k.zero_(), cache.v.fill_(1.0)
+    kv_len = torch.full((R,), 128 * width, dtype=torch.int32).cuda()
+    table = torch.zeros(R, width, dtype=torch.int32).cuda()
+    q = torch.zeros(R, 16 * Hkv, 64, dtype=torch.bfloat16).cuda()
+    bad = fm.PagedBatch(torch.tensor([0, R] * 5, dtype=torch.int32).cuda(), kv_len, table)
+    fm.fm_attn_paged(q, cache, bad, scale=1.0)
+    assert fm.fm_device_status() == (fm.FM_ERR_DEVICE, fm.FM_DEVERR_RANGE)
+    good = fm.PagedBatch(torch.arange(R + 1, dtype=torch.int32).cuda(), kv_len // 100, table)
+    o, lse = fm.fm_attn_paged(q, cache, good, scale=1.0)
+    assert (o == 1).all() and float((lse - np.log(1280)).abs().max()) <= 1e-5
+    assert fm.fm_device_status() == (fm.FM_OK, 0)
+
+
 # single tokens: keys of each sequence, heads, head dim, page
 STEPS = [
     ([1], 1, 1, 64, 16), ([17], 4, 1, 128, 16), ([64, 65, 63], 8, 8, 128, 64), ([5, 700, 0, 129, 128], 6, 3, 64, 32),

@@ -491,7 +491,9 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  * call's T packed tokens, ascending from 0; kv_len (R), its keys in the cache,
  * the new tokens' own included; page_table (R, width): entry i of row r is the
  * page of its keys [i * page_size, (i + 1) * page_size). New token a of n has
- * position kv_len - n + a. Entries past a sequence's last page are not read.
+ * position kv_len - n + a. An entry matters to a call only where the call writes, reads
+ * back or (fm_attn_paged) shows some new token a key of that page: entries past a
+ * sequence's end or behind its window may hold anything.
  * All device int32. Tokens from q_off[R] on belong to no sequence: their rows are
  * neither read nor written. Values that no such batch has (a page outside
  * [0, n_pages), a length outside [0, width * page_size], offsets that descend or

@@ -343,10 +343,11 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
         pages.hold(pg0, per, lane);
         const int a = __shfl_sync(kAll, pages.held, pg0 - pages.base);
         const int b = __shfl_sync(kAll, pages.held, pg0 + per - 1 - pages.base);
-        const bool two = per == 2 && key0 + 16 < u.kv_len;  // the second page holds keys
-        bad_a = a < 0 || a >= p.s.n_pages;
-        bad_b = per == 2 ? !two || b < 0 || b >= p.s.n_pages : bad_a;
-        if (bad_a || (two && bad_b)) record_error(p.err, FM_DEV_ERR_RANGE);
+        const bool see_a = per == 1 || any_seen(p.s, u, key0, key0 + 16);
+        const bool see_b = per == 2 && any_seen(p.s, u, key0 + 16, key0 + 32);
+        bad_a = !see_a || a < 0 || a >= p.s.n_pages;
+        bad_b = per == 2 ? !see_b || b < 0 || b >= p.s.n_pages : bad_a;
+        if ((see_a && bad_a) || (see_b && bad_b)) record_error(p.err, FM_DEV_ERR_RANGE);
         src_a = ((int64_t)(bad_a ? 0 : a) * p.s.H_kv + walk.h) * P + (key0 - pg0 * P);
         src_b = per == 2 ? ((int64_t)(bad_b ? 0 : b) * p.s.H_kv + walk.h) * P : src_a + 16;
       }

@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           const int pg = __shfl_sync(kAll, pages.held, pg0 + b - pages.base);
           const bool mine = lane < boxes * XS;
           const bool good = pg >= 0 && pg < p.s.n_pages;
-          if (mine && !good) record_error(p.err, FM_DEV_ERR_RANGE);
+          if (mine && !good && any_seen(p.s, u, key0 + b * rows, key0 + (b + 1) * rows))
+            record_error(p.err, FM_DEV_ERR_RANGE);
           const int z = good ? pg * p.s.H_kv + walk.h : zmax;  // zmax: out of range, reads as zero
 #pragma unroll
           for (int v = 0; v < 2; ++v) {

@@ -82,6 +82,11 @@ __device__ __forceinline__ PagedUnit unit_at(const PagedShape& s, int r, int a, 
   return q;
 }
 
+// Some row of the unit sees some of the keys [a, b): only then does it matter which page holds them.
+__device__ __forceinline__ bool any_seen(const PagedShape& s, const PagedUnit& u, int a, int b) {
+  return a < u.hi && (b > u.lo || a < s.sinks);
+}
+
 // How many CTAs get ranges, [c total / used, (c + 1) total / used): all of them, or
 // as many as get s.least tiles each; and, for the tiles [f0, f0 + nt) of a unit and
 // head, the CTAs that share them: the CTA of tile x is the last c with

@@ -213,6 +213,24 @@ def test_windows(window, sinks, new, keys, G, d):
     s.attend(2 * G, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("new, keys", [([1, 1], [900, 333]), ([30, 40], [700, 333])])
+def test_pages_behind_the_window_may_be_gone(page, f8, new, keys):
+    window, sinks = 100, 5
+    s = Setup(keys, new, 2, 64, page, f8, seed=22)
+    q, o, lse = s.attend(4, window=window, sinks=sinks)
+    for r, (n, L) in enumerate(zip(new, keys)):
+        lo = L - n - window + 1  # the first key that the first new token sees in its window
+        for i in range(s.table.shape[1]):
+            if i * page >= sinks and (i + 1) * page <= lo:
+                s.table[r, i] = -1 if r else 2 ** 30
+    assert int((s.table[:, :5] == -1).sum()) >= 2
+    o2, l2 = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=64 ** -0.5, window=window, sinks=sinks)
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+    assert fm.fm_device_status() == (fm.FM_OK, 0)
+
+
 def test_large_window_is_no_window():
     s = Setup([333, 90], [9, 90], 2, 64, 16, True)
     q, o, lse = s.attend(4)

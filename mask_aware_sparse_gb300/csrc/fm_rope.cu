@@ -8,7 +8,8 @@
 //   (a, b) -> (a c_i - b s_i, a s_i + b c_i)            for pair i < rot / 2
 // with pairs (i, i + rot/2) (half layout) or (2i, 2i + 1) (interleaved); the
 // elements from rot on pass through. Backward, with g the rotation's transpose
-// applied to dy:  dw = sum g x r,  dx = r g w - x r^3 / d sum(g w x).
+// applied to dy and z = x r:  dw = sum g z,  dx = r (g w - z / d sum(g w z)); r^3, which
+// that spares, would leave fp32's range for rows far from 1.
 // Sums, norms and the rotation are fp32; each output is rounded to bf16 once.
 //
 // What bounds it: memory, one read and one write of every element (backward:
@@ -294,11 +295,16 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
 #pragma unroll
               for (int i = 0; i < 8; ++i) ss += va[i] * va[i] + vb[i] * vb[i];
               const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                va[i] *= r;
+                vb[i] *= r;
+              }
               if (live) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  acc[i] += fa[i] * va[i] * r;
-                  acc[8 + i] += fb[i] * vb[i] * r;
+                  acc[i] += fa[i] * va[i];
+                  acc[8 + i] += fb[i] * vb[i];
                 }
               }
 #pragma unroll
@@ -312,11 +318,11 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
                 f[3] *= w.w;
                 sg += f[0] * v[0] + f[1] * v[1] + f[2] * v[2] + f[3] * v[3];
               }
-              const float t = row_sum<D>(sg) * (1.f / D) * r * r * r;
+              const float t = row_sum<D>(sg) * (1.f / D);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                fa[i] = r * fa[i] - va[i] * t;
-                fb[i] = r * fb[i] - vb[i] * t;
+                fa[i] = r * (fa[i] - va[i] * t);
+                fb[i] = r * (fb[i] - vb[i] * t);
               }
             }
           }

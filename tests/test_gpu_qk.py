@@ -167,6 +167,54 @@ def test_zero_and_non_finite_rows_stay_in_their_rows():
     assert torch.equal(got[0][0][keep.cuda()], want[0][0][keep.cuda()])
 
 
+@pytest.mark.parametrize("power", [-50, -20, 20, 50])
+def test_rows_far_from_one(power):
+    # squares stay in fp32's range, cubes of the norm's factor do not
+    q, k, _ = _inputs(1, 5, 2, 2, 64, 7, fused=False)
+    q, k = q * 2.0 ** power, k * 2.0 ** power
+    w = torch.linspace(0.5, 1.5, 64).cuda()
+    g = torch.Generator().manual_seed(3)
+    dy = torch.randn(q.shape, generator=g).to(torch.bfloat16)
+    dq, dk, _, dwq, _ = fm.fm_qk_norm_rope_bwd(dy.cuda(), dy.cuda(), None, q, k, q_weight=w, k_weight=w, eps=0.0)
+    for x, dx in ((q, dq), (k, dk)):
+        x = x.double().cpu().requires_grad_()
+        want = torch.autograd.grad(qk_rows(x, w.cpu(), 0.0, None, None, 1.0, False), x, dy.double())[0]
+        xd, gw = x.detach(), dy.double().abs() * w.double().cpu()
+        r = 1 / torch.sqrt((xd * xd).mean(-1, keepdim=True))
+        _close(dx, want, r * gw + xd.abs() * r ** 3 * (gw * xd.abs()).mean(-1, keepdim=True))
+
+
+def test_captured_forward_and_backward():
+    # a captured pass, replayed with other values beside an eager one on a second stream
+    q, k, v = _inputs(2, 33, 4, 2, 128, 10)
+    g = torch.Generator().manual_seed(5)
+    grads = [torch.randn(t.shape, generator=g).to(torch.bfloat16).cuda() for t in (q, k, v)]
+    f, _ = fm.fm_rope_freqs(128, device="cuda")
+    w = torch.linspace(0.5, 1.5, 128).cuda()
+    pos = torch.arange(33, dtype=torch.int32).cuda()
+    how = dict(positions=pos, inv_freq=f, q_weight=w, k_weight=w)
+
+    def step(stream=None):
+        return (*fm.fm_qk_norm_rope(q, k, v, stream=stream, **how),
+                *fm.fm_qk_norm_rope_bwd(*grads, q, k, stream=stream, **how))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    side = torch.cuda.Stream()
+    for i in range(3):
+        pos += 1000 * i
+        q.copy_(torch.randn(q.shape, generator=g))
+        torch.cuda.synchronize()
+        graph.replay()
+        beside = step(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, beside))
+    assert not torch.equal(held[0], q)
+
+
 def test_flashmask_attention_with_norm_and_rotation():
     # the attention call's own path: same outputs and gradients as the steps
     # one by one, and as the differentiated 64-bit form within the parity bound

@@ -428,9 +428,9 @@ fm_status fm_needed_chunks(const uint8_t* tile_class, int32_t B, int32_t nQ, int
  * a projection's (B, N, heads, d) output and the attention calls' contiguous
  * (B, H, N, d) are both such views. An output may be its own input (the same
  * view); apart from that no tensors overlap. d is 64, 128 or 256; rot a multiple
- * of 16, 0 <= rot <= d (0: no rotation; pos and inv_freq are then not read). pos: int32, entry b * pos_sb + n
- * (pos_sb 0: one row for every batch entry); inv_freq: rot / 2 finite fp32
- * values. q_weight / k_weight: d values each, fp32 when w_f32 != 0 else bf16;
+ * of 16, 0 <= rot <= d (0: no rotation; pos and inv_freq are then not read). pos:
+ * int32, entry b * pos_sb + n (pos_sb 0: one row for every batch entry); inv_freq:
+ * rot / 2 finite fp32 values. q_weight / k_weight: d values each, fp32 when w_f32 != 0 else bf16;
  * NULL: that side is not normed. v and vo both NULL: no values.
  *
  * Backward: dqo, dko, dvo are the gradients of the outputs; dq, dk, dv and the
@@ -484,8 +484,9 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  *
  * k, v: (n_pages, H_kv, page_size, d), contiguous, bf16 or (k_exp, v_exp not
  * NULL) e4m3 with one scale a row: exponent bytes (n_pages, H_kv, page_size),
- * value = stored * 2^(exponent - 127), 1 to 254; 255 goes with a row of NaN. page_size is 16, 32, 64 or 128, d 64, 128
- * or 256. Addresses 16-byte aligned.
+ * value = stored * 2^(exponent - 127), 1 to 254; 255 goes with a row of NaN.
+ * page_size is 16, 32, 64 or 128, d 64, 128 or 256, H_kv at most 65536. Addresses
+ * 16-byte aligned.
  *
  * A batch of R sequences: q_off (R + 1), the first new token of each in the
  * call's T packed tokens, ascending from 0; kv_len (R), its keys in the cache,
@@ -554,8 +555,9 @@ fm_status fm_cache_read(const fm_kv_cache* cache, const int32_t* kv_off, const i
  * sequence in the call.
  *
  * q, o: bf16 rows (T, H_q, d) of element strides st, sh (multiples of 8,
- * 16-byte aligned); lse: (T, H_q) fp32, contiguous. GQA as fm_attn_fwd. e4m3
- * caches give what the cache read back in bf16 gives. scale > 0. The joining
+ * 16-byte aligned); lse: (T, H_q) fp32, contiguous. o overlaps no input. GQA
+ * as fm_attn_fwd. e4m3 caches give what the same values in a bf16 cache give, up to
+ * 32-bit rounding and that of the weights. scale > 0. The joining
  * order of a sequence's parts is fixed by the lengths: the same call gives the
  * same bits. Workspace: fm_attn_paged_workspace_bytes (on the current device),
  * rewritten by every call: calls that may overlap need one each.

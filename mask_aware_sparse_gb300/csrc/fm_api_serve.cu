@@ -36,6 +36,7 @@ fm_status check_cache(const fm_kv_cache* c) {
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return FM_ERR_UNSUPPORTED;
   if ((c->k_exp == nullptr) != (c->v_exp == nullptr)) return FM_ERR_INVALID_ARG;
   if ((int64_t)c->n_pages * c->H_kv > INT32_MAX) return FM_ERR_UNSUPPORTED;
+  if (c->H_kv > 65536) return FM_ERR_UNSUPPORTED;  // rows of a block, key tiles of a call are counted
   if (c->n_pages == 0) return FM_ERR_INVALID_ARG;
   if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_exp) || !aligned16(c->v_exp))
     return FM_ERR_INVALID_ARG;
@@ -127,7 +128,7 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
     return FM_ERR_INVALID_ARG;
   if (dvo && (!view_ok(dvo) || !view_ok(dv))) return FM_ERR_INVALID_ARG;
   if ((p->q_weight && !view_ok(q)) || (p->k_weight && !view_ok(k))) return FM_ERR_INVALID_ARG;
-  if (normed && (!ws || ws_bytes < qk_bwd_ws_bytes(*p))) return FM_ERR_WORKSPACE;
+  if (normed && (!ws || !aligned16(ws) || ws_bytes < qk_bwd_ws_bytes(*p))) return FM_ERR_WORKSPACE;
   return from_cuda(launch_qk_bwd(*p, dqo, dko, dvo, q, k, dq, dk, dv, dq_weight, dk_weight, ws,
                                  static_cast<cudaStream_t>(stream)));
 }

@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
         top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(kAll, top, 2));
         const int E = (int)(max(top & 0xffffu, top >> 16) >> 7);
-        // 2^(142 - E), kept finite; a row of zeros, infinities or NaN stays as it is
-        const int up = (E == 0 || E == 255) ? 0 : min(142 - E, 126);
+        // 2^(142 - E), kept finite; a row with infinities or NaN stays as it is
+        const int up = E == 255 ? 0 : min(142 - E, 126);
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
         sc[i] = sl2 * __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll

@@ -300,6 +300,16 @@ def test_large_and_outlying_values(new, f8):
     s.attend(4)
 
 
+def test_subnormal_queries_of_large_quantised_keys():
+    s = Setup([90, 33], [1, 1], 2, 64, 16, True, seed=23)
+    s.k = (s.k.double() * 2.0 ** 118).to(torch.bfloat16)
+    fm.fm_cache_write(s.k.cuda(), s.v.cuda(), s.cache, fm.PagedBatch(s.kv_off, s.kv_len, s.table))
+    q = (torch.randn(2, 4, 64, generator=s.g).double() * 2.0 ** -129).to(torch.bfloat16)
+    o, lse = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=512.0)
+    k, v = s.values()
+    assert_paged(o, lse, paged(q.double(), k, v, s.q_off.tolist(), s.keys, 512.0, True, 0, 0), 64)
+
+
 def test_long_cache_offsets_beyond_32_bits():
     # pages at the end of a cache whose byte offsets pass 2^32
     for f8 in (False, True):

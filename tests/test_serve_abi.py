@@ -39,7 +39,7 @@ ROWS = fm.fm_rows(A, 128, 64)
     (dict(k_exp=A + 4, v_exp=A), "INVALID_ARG"), (dict(n_pages=0), "INVALID_ARG"), (dict(H_kv=0), "INVALID_ARG"),
     (dict(n_pages=-1), "INVALID_ARG"), (dict(page_size=8), "UNSUPPORTED"), (dict(page_size=48), "UNSUPPORTED"),
     (dict(page_size=256), "UNSUPPORTED"), (dict(d=96), "UNSUPPORTED"), (dict(d=0), "UNSUPPORTED"),
-    (dict(n_pages=1 << 30, H_kv=4), "UNSUPPORTED"),
+    (dict(n_pages=1 << 30, H_kv=4), "UNSUPPORTED"), (dict(n_pages=1, H_kv=65537), "UNSUPPORTED"),
 ])
 def test_caches_refused(lib, over, want):
     want = getattr(fm, "FM_ERR_" + want)
@@ -126,6 +126,7 @@ def test_norm_rotation_arguments_refused(lib):
     assert bwd(prob(), dwq=0) == I and bwd(prob(), dwk=0) == I
     need = lib.fm_qk_norm_rope_bwd_workspace_bytes(prob())
     assert need > 0 and lib.fm_qk_norm_rope_bwd_workspace_bytes(prob(q_weight=0, k_weight=0)) == 0
+    assert bwd(prob(), ws=A + 4) == fm.FM_ERR_WORKSPACE
     assert bwd(prob(), ws=0) == fm.FM_ERR_WORKSPACE and bwd(prob(), wsb=need - 1) == fm.FM_ERR_WORKSPACE
     assert fwd(prob(B=0), q=None, k=None) == fm.FM_OK and fwd(prob(N=0)) == fm.FM_OK
     assert bwd(prob(B=0, q_weight=0, k_weight=0)) == fm.FM_OK

@@ -25,6 +25,7 @@
 // memory, for all heads.
 #include <cmath>
 #include <cuda_bf16.h>
+#include "dependent.cuh"
 #include "fm_internal.h"
 
 namespace fm {
@@ -202,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   }
+  grid_dependency_wait();
+  grid_launch_dependents();
   load_fractions(p, frac);
   if (wp && threadIdx.x < TG) {
     // slot j * TG + c: a quarter of thread c's sixteen weights
@@ -369,6 +372,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
 __global__ void __launch_bounds__(1024) qk_weights_kernel(const float* part, int blocks, int D, void* dwq, void* dwk,
                                                           int f32) {
   __shared__ float red[32][33];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
   const int kind = col / D, i = col - kind * D;
   void* dst = kind ? dwk : dwq;
@@ -414,15 +419,13 @@ constexpr int kFwdPerSm = 3, kBwdPerSm = 2;
 
 template <bool BWD>
 cudaError_t launch_qk(const fm_qk_problem& P, const QkParams& p, int grid, int tb, cudaStream_t s) {
-  auto go = [&](auto kernel) { kernel<<<dim3((unsigned)grid, 2), kThreads, 0, s>>>(p, tb); };
-  if (P.d == 64)
-    P.interleaved ? go(qk_kernel<64, true, BWD>) : go(qk_kernel<64, false, BWD>);
-  else if (P.d == 128)
-    P.interleaved ? go(qk_kernel<128, true, BWD>) : go(qk_kernel<128, false, BWD>);
-  else
-    P.interleaved ? go(qk_kernel<256, true, BWD>) : go(qk_kernel<256, false, BWD>);
+  auto go = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)grid, 2), kThreads, 0, s, p, tb); };
   count_launches(1);
-  return cudaGetLastError();
+  if (P.d == 64)
+    return P.interleaved ? go(qk_kernel<64, true, BWD>) : go(qk_kernel<64, false, BWD>);
+  if (P.d == 128)
+    return P.interleaved ? go(qk_kernel<128, true, BWD>) : go(qk_kernel<128, false, BWD>);
+  return P.interleaved ? go(qk_kernel<256, true, BWD>) : go(qk_kernel<256, false, BWD>);
 }
 
 QkParams params_of(const fm_qk_problem& P) {
@@ -479,10 +482,9 @@ cudaError_t launch_qk_bwd(const fm_qk_problem& P, const fm_view* dqo, const fm_v
   const int grid = grid_blocks(P, tb, kBwdPerSm);
   cudaError_t e = launch_qk<true>(P, p, grid, tb, s);
   if (e != cudaSuccess || (!P.q_weight && !P.k_weight)) return e;
-  qk_weights_kernel<<<2 * P.d / 32, 1024, 0, s>>>(p.part, grid, P.d, P.q_weight ? dwq : nullptr,
-                                                  P.k_weight ? dwk : nullptr, P.w_f32);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_dependent(qk_weights_kernel, dim3(2 * P.d / 32), 1024, 0, s, p.part, grid, P.d,
+                          P.q_weight ? dwq : nullptr, P.k_weight ? dwk : nullptr, P.w_f32);
 }
 
 }  // namespace fm

@@ -13,6 +13,7 @@
 #include <atomic>
 #include <climits>
 #include <cstdint>
+#include "dependent.cuh"
 #include "fm_internal.h"
 #include "sm100.cuh"
 
@@ -420,9 +421,6 @@ struct PageWindow {
   }
 };
 
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
-
 // Where a row's output goes.
 struct PagedOut {
   char* o;
@@ -446,24 +444,5 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
 constexpr int kChunkRows = 256;  // rows of a chunk_kernel partial slot: two tiles
 cudaError_t launch_paged_chunk(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const fm_paged_batch& b,
                                const fm_rows& q, const PagedOut& out, float scale, cudaStream_t st, int* err);
-
-// Launch with the programmatic dependency on the kernel before it: the new
-// grid's prologue runs while that kernel ends, and its grid_dependency_wait
-// returns once it has.
-template <typename... Args, typename... Given>
-cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
-                             Given&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, Args(args)...);
-}
 
 }  // namespace fm

@@ -12,10 +12,10 @@
 // or an infinity gets e = 255 and reads as NaN throughout.
 //
 // What bounds both kernels: memory, each row read once and written once, 16
-// bytes a load, four rows' loads in flight a thread; a block looks its tokens'
-// pages up once for all heads.
+// bytes a load; a block looks its tokens' pages up once for all heads.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include "dependent.cuh"
 #include "fm_internal.h"
 #include "sm100.cuh"
 
@@ -96,28 +96,9 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, float s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// What the loads of a step need: the cache row of this thread's row, or -1.
-struct Row {
-  int64_t s;  // cache row
-  int t, h, which;
-};
-
-// Row i of a block's rows: keys, then values, head by head, the tokens of a head
-// next to each other (TB = 2^log tokens: no division, of which four a step would
-// be a third of the write's instructions).
-__device__ __forceinline__ Row row_of(const CacheParams& p, const int64_t* slot, int log, int rows, int i) {
-  Row r;
-  r.t = i & ((1 << log) - 1);
-  r.h = i >> log;
-  r.which = r.h >= p.H_kv ? 1 : 0;
-  r.h -= r.which * p.H_kv;
-  const int64_t s = i < rows ? slot[r.t] : -1;
-  r.s = s < 0 ? -1 : s + (int64_t)r.h * p.page;
-  return r;
-}
-
 template <bool READ>
 __device__ __forceinline__ void look_up(const CacheParams& p, int64_t* slot, int t0, int TB) {
+  grid_dependency_wait();
   if (threadIdx.x < 32) {  // TB <= 32
     const int64_t s = slot_of<READ>(p, t0, min(TB, p.T - t0));
     if (threadIdx.x < TB) slot[threadIdx.x] = s;
@@ -125,106 +106,153 @@ __device__ __forceinline__ void look_up(const CacheParams& p, int64_t* slot, int
   __syncthreads();
 }
 
-constexpr int kAhead = 4;  // rows whose loads a thread has in flight (one: the 16K-key read of four sequences took 66 us)
+// A block: TB = 2^log tokens, keys of every head, then values. Its rows go by token
+// first, and a step's rows are a multiple of TB, so that each thread stays with one
+// token: what belongs to the token is worked out once, a head costs a multiplication
+// and an addition (with places and addresses from each row's number, the write of
+// 8192 tokens took 12.4 us, and more with more loads ahead: its instructions bound it).
+template <int TR>
+struct Rows {
+  static constexpr int STEP = kThreads / TR;  // rows
+  int c, t, h, heads;                         // this thread's part of a row, token, first head; heads of a step
+  __device__ Rows(int log) {
+    const int r = threadIdx.x / TR;
+    c = threadIdx.x % TR;
+    t = r & ((1 << log) - 1);
+    h = r >> log;
+    heads = STEP >> log;
+  }
+};
+constexpr int most_log(int tr) { return kThreads / tr >= 32 ? 5 : kThreads / tr >= 16 ? 4 : 3; }
 
-// One block: 2^log tokens, every head; d / 8 threads a row, 16 bytes of bf16 each.
+// Rows whose loads a thread has in flight (reading, one: the 16K-key read of four
+// sequences took 66 us).
+constexpr int kWriteAhead = 2, kReadAhead = 4;
+
+// D / 16 threads a row, 32 bytes of bf16 each: neighbouring ones where they become 16
+// bytes of e4m3, else two pieces half a row apart, so that each load and store of a
+// row's threads covers whole lines (side by side: 8192 tokens 13.2 us instead of 9.3).
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) write_kernel(const CacheParams p, const int log) {
-  constexpr int TR = D / 8, STEP = kThreads / TR;
+  constexpr int TR = D / 16, kAhead = kWriteAhead, PIECE = F8 ? 32 : 16, NEXT = F8 ? 1 : TR;
   __shared__ int64_t slot[32];
-  const int TB = 1 << log, t0 = blockIdx.x * TB;
-  look_up<false>(p, slot, t0, TB);
-  const int c = threadIdx.x % TR, rows = TB * p.H_kv * 2;
+  const int t0 = blockIdx.x << log;
+  look_up<false>(p, slot, t0, 1 << log);
+  const Rows<TR> own(log);
+  const int64_t s = slot[own.t];
+  const char* in[2];
+  char* out[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    in[i] = p.in[i] + 2 * ((int64_t)(t0 + own.t) * p.st[i]) + PIECE * own.c;
+    out[i] = p.c[i] + s * D * (F8 ? 1 : 2) + 16 * own.c;
+  }
   // every thread of a warp takes the same number of turns: the rows' maxima are exchanged
-  for (int i0 = 0; i0 < rows; i0 += kAhead * STEP) {
-    Row row[kAhead];
-    uint4 x[kAhead];
+  for (int g = 0; g < 2 * p.H_kv; g += kAhead * own.heads) {
+    uint4 x[kAhead][2];
+    int h[kAhead], which[kAhead];
+    bool live[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      row[k] = row_of(p, slot, log, rows, i0 + k * STEP + threadIdx.x / TR);
-      const Row& r = row[k];
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (r.s >= 0)
-        x[k] = *reinterpret_cast<const uint4*>(p.in[r.which] +
-                                               2 * ((int64_t)(t0 + r.t) * p.st[r.which] + r.h * p.sh[r.which] + 8 * c));
+      h[k] = g + k * own.heads + own.h;
+      live[k] = s >= 0 && h[k] < 2 * p.H_kv;
+      which[k] = h[k] >= p.H_kv ? 1 : 0;
+      h[k] -= which[k] * p.H_kv;
+      x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
+      if (live[k]) {
+        const uint4* from = reinterpret_cast<const uint4*>((which[k] ? in[1] : in[0]) + 2 * (h[k] * p.sh[which[k]]));
+        x[k][0] = from[0];
+        x[k][1] = from[NEXT];
+      }
     }
     if constexpr (!F8) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
-        if (row[k].s >= 0) reinterpret_cast<uint4*>(p.c[row[k].which] + row[k].s * D * 2)[c] = x[k];
+        if (live[k]) {
+          uint4* to = reinterpret_cast<uint4*>((which[k] ? out[1] : out[0]) + (int64_t)h[k] * p.page * D * 2);
+          to[0] = x[k][0];
+          to[NEXT] = x[k][1];
+        }
     } else {
       // each row's largest magnitude as bits: infinities and NaN are the largest of all
       uint32_t m[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        m[k] = __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
-                        __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
+      for (int k = 0; k < kAhead; ++k) {
+        m[k] = 0;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          m[k] = __vmaxu2(m[k], __vmaxu2(__vmaxu2(x[k][y].x & 0x7fff7fffu, x[k][y].y & 0x7fff7fffu),
+                                         __vmaxu2(x[k][y].z & 0x7fff7fffu, x[k][y].w & 0x7fff7fffu)));
+      }
 #pragma unroll
       for (int y = TR / 2; y > 0; y >>= 1)
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) m[k] = __vmaxu2(m[k], __shfl_xor_sync(kAll, m[k], y));
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const Row& r = row[k];
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
         const uint32_t top = max(m[k] & 0xffffu, m[k] >> 16);
         const int E = (int)(top >> 7);  // 448 = 1.75 * 2^8
         const int e = max(1, E - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0));
         const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-        float f[8];
+        uint32_t q[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          f[2 * y] = __uint_as_float(w[y] << 16) * inv;
-          f[2 * y + 1] = __uint_as_float(w[y] & 0xffff0000u) * inv;
+          const uint4& v = x[k][y >> 1];
+          const uint32_t a = y & 1 ? v.z : v.x, b = y & 1 ? v.w : v.y;
+          q[y] = pack_e4m3x4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
+                             __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv);
+          if (E == 255) q[y] = 0x7f7f7f7fu;
         }
-        uint2 q = make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
-        if (E == 255) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-        if (r.s >= 0) {
-          reinterpret_cast<uint2*>(p.c[r.which] + r.s * D)[c] = q;
-          if (c == 0) p.e[r.which][r.s] = (uint8_t)(E == 255 ? 255 : e);
+        if (live[k]) {
+          *reinterpret_cast<uint4*>((which[k] ? out[1] : out[0]) + (int64_t)h[k] * p.page * D) =
+              make_uint4(q[0], q[1], q[2], q[3]);
+          if (own.c == 0) p.e[which[k]][s + (int64_t)h[k] * p.page] = (uint8_t)(E == 255 ? 255 : e);
         }
       }
     }
   }
 }
 
-// One block: 2^log output rows of every head; 16 bytes of the cache a thread.
+// 16 bytes of the cache a thread.
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p, const int log) {
-  constexpr int TR = D * (F8 ? 1 : 2) / 16, STEP = kThreads / TR;
+  constexpr int TR = D * (F8 ? 1 : 2) / 16, kAhead = kReadAhead;
   __shared__ int64_t slot[32];
-  const int TB = 1 << log, t0 = blockIdx.x * TB;
-  look_up<true>(p, slot, t0, TB);
-  const int c = threadIdx.x % TR, rows = TB * p.H_kv * 2;
-  for (int i0 = 0; i0 < rows; i0 += kAhead * STEP) {
-    Row row[kAhead];
+  const int t0 = blockIdx.x << log;
+  look_up<true>(p, slot, t0, 1 << log);
+  const Rows<TR> own(log);
+  const int64_t s = slot[own.t];
+  if (s < 0) return;
+  const char* in[2] = {p.c[0] + s * D * (F8 ? 1 : 2) + 16 * own.c, p.c[1] + s * D * (F8 ? 1 : 2) + 16 * own.c};
+  for (int g = own.h; g < 2 * p.H_kv; g += kAhead * own.heads) {
     uint4 x[kAhead];
     uint32_t e[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      row[k] = row_of(p, slot, log, rows, i0 + k * STEP + threadIdx.x / TR);
-      const Row& r = row[k];
-      if (r.s < 0) continue;
-      x[k] = reinterpret_cast<const uint4*>(p.c[r.which] + r.s * (D * (F8 ? 1 : 2)))[c];
-      if constexpr (F8) e[k] = p.e[r.which][r.s];
+      const int h = g + k * own.heads, which = h >= p.H_kv ? 1 : 0;
+      if (h >= 2 * p.H_kv) continue;
+      const int64_t row = (int64_t)(h - which * p.H_kv) * p.page;
+      x[k] = *reinterpret_cast<const uint4*>((which ? in[1] : in[0]) + row * D * (F8 ? 1 : 2));
+      if constexpr (F8) e[k] = p.e[which][s + row];
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const Row& r = row[k];
-      if (r.s < 0) continue;
-      uint4* to = reinterpret_cast<uint4*>(p.out[r.which] + ((int64_t)r.h * p.T + t0 + r.t) * D * 2);
+      const int h = g + k * own.heads, which = h >= p.H_kv ? 1 : 0;
+      if (h >= 2 * p.H_kv) continue;
+      uint4* to = reinterpret_cast<uint4*>(p.out[which] +
+                                           ((int64_t)(h - which * p.H_kv) * p.T + t0 + own.t) * D * 2);
       if constexpr (F8) {
         const float f = scale_of(e[k]);
         const uint4 lo = dequant8(x[k].x, x[k].y, f), hi = dequant8(x[k].z, x[k].w, f);
         if (p.wide) {
           // one whole 32-byte sector a thread (two stores of 16 bytes: 62 us for the read of four 16K sequences)
-          stg_b32x8(to + 2 * c, lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w);
+          stg_b32x8(to + 2 * own.c, lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w);
         } else {
-          to[2 * c] = lo;
-          to[2 * c + 1] = hi;
+          to[2 * own.c] = lo;
+          to[2 * own.c + 1] = hi;
         }
       } else {
-        to[c] = x[k];
+        to[own.c] = x[k];
       }
     }
   }
@@ -232,26 +260,29 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p, con
 
 template <bool READ>
 cudaError_t launch(const CacheParams& p, int d, bool f8, cudaStream_t s) {
-  // few tokens: one a block, so that the heads' rows spread over the SMs; many:
-  // enough tokens a block that looking a page up is a small part of its work
+  // Tokens of a block: as many as fill its threads' loads once, if that leaves two
+  // blocks an SM; then more of them (fewer look-ups) while that leaves more than fill
+  // an SM. Writing 1000 / 8192 / 12000 tokens of 8 heads, d = 128: 3.2 / 8.5 / 11.2 us;
+  // with one step less 3.4 / 8.7 / 13.8 (fewer, larger blocks) or 4.6 / 8.9 / 11.3 us.
+  const int tr = READ ? d * (f8 ? 1 : 2) / 16 : d / 16, full = kThreads / tr * (READ ? kReadAhead : kWriteAhead);
   int log = 0;
-  while (log < 5 && p.T >= (4ll << log) * sm_count()) ++log;
+  while (log < most_log(tr) && p.T >= (((2ll * p.H_kv << log) < full ? 2ll : READ ? 4 : 8) << log) * sm_count()) ++log;
   const unsigned grid = (unsigned)((p.T + (1 << log) - 1) >> log);
-  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p, log); };
   auto pick = [&](auto write, auto read) {
     if constexpr (READ)
-      go(read);
+      return launch_dependent(read, dim3(grid), kThreads, 0, s, p, log);
     else
-      go(write);
+      return launch_dependent(write, dim3(grid), kThreads, 0, s, p, log);
   };
-  if (d == 64)
-    f8 ? pick(write_kernel<64, true>, read_kernel<64, true>) : pick(write_kernel<64, false>, read_kernel<64, false>);
-  else if (d == 128)
-    f8 ? pick(write_kernel<128, true>, read_kernel<128, true>) : pick(write_kernel<128, false>, read_kernel<128, false>);
-  else
-    f8 ? pick(write_kernel<256, true>, read_kernel<256, true>) : pick(write_kernel<256, false>, read_kernel<256, false>);
   count_launches(1);
-  return cudaGetLastError();
+  if (d == 64)
+    return f8 ? pick(write_kernel<64, true>, read_kernel<64, true>)
+              : pick(write_kernel<64, false>, read_kernel<64, false>);
+  if (d == 128)
+    return f8 ? pick(write_kernel<128, true>, read_kernel<128, true>)
+              : pick(write_kernel<128, false>, read_kernel<128, false>);
+  return f8 ? pick(write_kernel<256, true>, read_kernel<256, true>)
+            : pick(write_kernel<256, false>, read_kernel<256, false>);
 }
 
 CacheParams params_of(const fm_kv_cache& c, int* err) {

@@ -142,30 +142,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     if (tid == kPlanThreads - 1) carry = in;
     __syncthreads();
   }
-  const long long total = carry;
-  if (tid == 0) p.w.sum[units] = total;
-  __syncthreads();
-  const long long used = used_ctas(s, total);
+  const PagedDivision<long long> div(s, carry, units);
+  const long long ex = div.extra * s.H_kv;
   for (int c = tid; c < s.ctas; c += kPlanThreads) {
     PagedStart st = {};
-    if (c < used && total > 0) {
-      const long long f = total * c / used;
+    if (c < div.used && div.total > 0) {
+      const long long f = div.begin(c);
       int lo = 0, hi = units - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.w.sum[mid] <= f)
+        if (p.w.sum[mid] + mid * ex <= f)
           lo = mid;
         else
           hi = mid - 1;
       }
-      const long long rem = f - p.w.sum[lo];
+      const long long from = p.w.sum[lo] + lo * ex;
       st.unit = p.w.units[lo];
-      const int nt = max(st.unit.ntiles, 1);
+      const long long nt = max(st.unit.ntiles, 1);
       st.u = lo;
-      st.h = (int)(rem / nt);
-      st.kt = (int)(rem - (long long)st.h * nt);
-      st.count = (int)(total * (c + 1) / used - f);
-      sharers(st, f - st.kt, (long long)nt, total, used);
+      st.h = (int)((f - from) / (nt + div.extra));
+      div.set(st, c, from + st.h * (nt + div.extra), nt);
     }
     p.w.starts[c] = st;
   }
@@ -672,7 +668,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
       } else {
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<float2*>(own + row * D + ((8 * c + 2 * t) ^ (8 * (row & 3)))) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
+          *reinterpret_cast<float2*>(own + row * D + ((8 * c + 2 * t) ^ (8 * (row & 3)))) =
+              make_float2(o[c][2 * i], o[c][2 * i + 1]);
       }
     }
     __syncthreads();
@@ -867,8 +864,8 @@ cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cach
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(few_kernel<D, F8>), C::SMEM, ready);
   if (e != cudaSuccess) return e;
   FewParams p{s, w, static_cast<const char*>(q.ptr), q.st, q.sh, out,
-              {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, b.q_off, b.kv_len, b.page_table,
-              scale * 1.4426950408889634f, err};
+              {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, b.q_off, b.kv_len,
+              b.page_table, scale * 1.4426950408889634f, err};
   count_launches(1);
   return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, p);
 }
@@ -925,6 +922,7 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   s.step = chunk ? 2 * (128 / s.G) * s.G : kFewRows;
   s.tile = chunk ? 128 : kTileKeys;
   s.least = chunk ? 1 : few_warps(c.d, c.k_exp != nullptr);  // a tile for each computing warp, and fewer parts to join
+  s.extra = chunk ? (c.k_exp ? 3 : 2) : (c.k_exp ? 10 : 4);
   s.ctas = sm_count() * (chunk ? 1 : few_ctas(c.d, c.k_exp != nullptr));
   s.max_units = ((long long)T * s.G + s.step - 1) / s.step + b.R;
   // Each CTA plans for itself where that is a few steps a warp; a plan kernel (one
@@ -933,7 +931,7 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   const bool few_seqs = b.R <= (chunk ? kLocalChunks : kLocalSeqs);
   s.whole = few_seqs && (b.R == 1 || s.max_units <= kWholeUnits) && stay_whole(s, b, most, chunk);
   s.local = s.whole || (few_seqs && s.max_units - b.R <= kLocalUnits &&
-                        s.max_units * most * s.H_kv * (s.ctas + 1) < (1ll << 31));
+                        s.max_units * (most + s.extra) * s.H_kv * (s.ctas + 1) < (1ll << 31));
   return s;
 }
 

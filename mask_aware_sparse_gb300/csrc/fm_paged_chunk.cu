@@ -338,11 +338,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           if (p.wide) {
 #pragma unroll
             for (int c = 0; c < 16; c += 8)
-              stg_b32x8(dst + 2 * c0 + 4 * c, w[c], w[c + 1], w[c + 2], w[c + 3], w[c + 4], w[c + 5], w[c + 6], w[c + 7]);
+              stg_b32x8(dst + 2 * c0 + 4 * c, w[c], w[c + 1], w[c + 2], w[c + 3], w[c + 4], w[c + 5], w[c + 6],
+                        w[c + 7]);
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              reinterpret_cast<uint4*>(dst + 2 * c0)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+              reinterpret_cast<uint4*>(dst + 2 * c0)[c] =
+                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
           }
         } else {
           float* at = part + (size_t)rr * D + c0;
@@ -473,7 +475,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           const uint32_t tO = tbase + 256u + (uint32_t)(t * D);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ts(tO, tbase + (uint32_t)(buf * 128 + k * 8), vd + (uint64_t)(k * 128), id_o, (!first || k > 0) ? 1u : 0u);
+            mma_ts(tO, tbase + (uint32_t)(buf * 128 + k * 8), vd + (uint64_t)(k * 128), id_o,
+                   (!first || k > 0) ? 1u : 0u);
           mma_commit(&bars[C::ODONE + t]);
           return true;
         };
@@ -555,8 +558,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           const uint32_t ri = 2 * jt + v, rs = ri % C::RAWS;
           ok = __all_sync(kAll, mbar_wait(&bars[C::RFULL + rs], (ri / C::RAWS) & 1u, abort_flag, p.err));
           if (ok)
-            ok = __all_sync(kAll, mbar_wait(&bars[(v ? C::VEMPTY : C::KEMPTY) + jt % S], ((jt / S) & 1u) ^ 1u, abort_flag,
-                                            p.err));
+            ok = __all_sync(
+                kAll, mbar_wait(&bars[(v ? C::VEMPTY : C::KEMPTY) + jt % S], ((jt / S) & 1u) ^ 1u, abort_flag, p.err));
           if (!ok) break;
           const uint32_t src = smem_u32(smem + C::RAW_OFF + rs * C::RAW);
           const uint32_t dst = smem_u32(smem + (v ? C::V_OFF : C::K_OFF) + (jt % S) * C::TILE) + row * 128;
@@ -617,7 +620,9 @@ cudaError_t launch(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c
       !make_tmap_pages(&tk, c.k, c, rows, F8 ? D : 128) || !make_tmap_pages(&tv, c.v, c, rows, F8 ? D : 128))
     return cudaErrorInvalidValue;
   const int wide = reinterpret_cast<uintptr_t>(out.o) % 32 == 0 && out.st % 16 == 0 && out.sh % 16 == 0;
-  ChunkParams p{s, w, out, c.k_exp, c.v_exp, b.q_off, b.kv_len, b.page_table, tokens * s.G, wide, scale * 1.4426950408889634f, err};
+  ChunkParams p{s,        w,            out,           c.k_exp, c.v_exp,
+                b.q_off,  b.kv_len,     b.page_table,  tokens * s.G,
+                wide,     scale * 1.4426950408889634f, err};
   count_launches(1);
   return launch_dependent(chunk_kernel<D, F8>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, tq, tk, tv, p);
 }

@@ -33,7 +33,7 @@ struct __align__(16) PagedUnit {
 struct __align__(16) PagedStart {
   int u, i, h, kt, count;
   int first, last;  // where kt > 0: the first and the last CTA with tiles of that unit and head
-  int pad;
+  int extra;        // places that a unit and head takes besides its tiles'
   PagedUnit unit;
 };
 
@@ -42,6 +42,7 @@ struct PagedShape {
   int causal, window, sinks;  // window 0: none
   int step, tile;  // query rows of a unit, keys of a tile
   int ctas, least;  // CTAs launched; tiles a CTA gets before another one does
+  int extra;  // tiles that a segment's start and end are counted as
   int local;  // every CTA plans for itself: no plan kernel
   int whole;  // no unit and head is divided (every CTA plans for itself): nothing to join
   long long max_units;
@@ -88,27 +89,48 @@ __device__ __forceinline__ bool any_seen(const PagedShape& s, const PagedUnit& u
   return a < u.hi && (b > u.lo || a < s.sinks);
 }
 
-// How many CTAs get ranges, [c total / used, (c + 1) total / used): all of them, or
-// as many as get s.least tiles each; and, for the tiles [f0, f0 + nt) of a unit and
-// head, the CTAs that share them: the CTA of tile x is the last c with
-// floor(c total / used) <= x. (I: unsigned where 32 bits hold ctas * total.)
+// Units are divided on a line: each unit and head takes `extra` places, for what
+// starting on it costs, then one a tile (one in all where it has none). CTA c of
+// `used` gets the tiles that lie on its places, [c total / used, (c + 1) total / used)
+// of all of them. Used are all CTAs, or as many as get s.least tiles each; extra is
+// then 0, for equal parts (one token over 1021 keys 10.1 us, with 4 11.9). Where all
+// have work, CTAs that took up a second or third segment were up to 10 us later than
+// the others (a segment's end, the next one's first loads), and the grid waits for them: 32 ragged sequences of up to
+// 4096 keys, e4m3: 46.6 us with extra = 0, 43.3 with 10; bf16 62.9, with 4 61.6;
+// chunks of 1111 tokens over 3000 keys, e4m3, 38.3, with 3 34.4. Long ranges gain
+// less: up to 16384 keys, e4m3, 119.6, 117.5; bf16 199, 202.
+// (I: unsigned where 32 bits hold ctas * total.)
 template <typename I>
-__device__ __forceinline__ I used_ctas(const PagedShape& s, I total) {
-  return max((I)1, min((I)s.ctas, total / (I)s.least));
-}
-template <typename I>
-__device__ __forceinline__ void sharers(PagedStart& st, I f0, I nt, I total, I used) {
-  st.first = (int)(((f0 + 1) * used - 1) / total);
-  st.last = (int)(((f0 + nt) * used - 1) / total);
-}
+struct PagedDivision {
+  I total, used, extra;
+  __device__ PagedDivision(const PagedShape& s, I tiles, I units) {
+    used = max((I)1, min((I)s.ctas, tiles / (I)s.least));
+    extra = used == (I)s.ctas ? (I)s.extra : (I)0;
+    total = tiles + units * (I)s.H_kv * extra;
+  }
+  __device__ I begin(I c) const { return total * c / used; }
+  // The range of CTA c, from the unit and head whose places [f0, f0 + extra + nt) hold
+  // its first one on, and the CTAs that share its tiles: those with places f0 + extra
+  // on. (The CTA of place x is the last c with begin(c) <= x.)
+  __device__ void set(PagedStart& st, I c, I f0, I nt) const {
+    const I f = begin(c), g = begin(c + 1), tile0 = f0 + extra;
+    st.extra = (int)extra;
+    st.kt = f > tile0 ? (int)(f - tile0) : 0;
+    st.count = f < tile0 ? (g > tile0 ? (int)(g - tile0) : 0) : (int)(g - f);
+    if (st.kt) {
+      st.first = (int)(((tile0 + 1) * used - 1) / total);
+      st.last = (int)(((tile0 + nt) * used - 1) / total);
+    }
+  }
+};
 
 // The plan as one CTA makes it for itself, for a few hundred units at most and a
 // total work that 32 bits hold (offsets that descend, whose spans may overlap and add
 // up to more, plan nothing): every sequence into seq (first token, tokens,
 // keys, units), its work into work (both shared memory, R entries), the CTA's
 // range into *out (shared memory).
-__device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int4* seq,
-                                             unsigned* work, PagedStart* out, int* err) {
+__device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len,
+                                             int4* seq, unsigned* work, PagedStart* out, int* err) {
   bool bad = false, descends = false;
   const int lane = threadIdx.x & 31;
   constexpr int kAlone = 4;  // units that a thread counts by itself
@@ -136,23 +158,30 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
   __syncthreads();
   if (threadIdx.x < 32) {
     const int per = (s.R + 31) / 32, r0 = lane * per, r1 = min(s.R, r0 + per);
-    unsigned mine = 0;
-    for (int r = r0; r < r1; ++r) mine += work[r];
+    unsigned tiles = 0, units = 0;
+    for (int r = r0; r < r1; ++r) {
+      tiles += work[r];
+      units += seq[r].w;
+    }
+    const PagedDivision<unsigned> div(s, __reduce_add_sync(0xffffffffu, tiles), __reduce_add_sync(0xffffffffu, units));
+    const unsigned ex = div.extra * s.H_kv, mine = tiles + units * ex, c = blockIdx.x;
     unsigned upto = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const unsigned x = __shfl_up_sync(0xffffffffu, upto, m);
       if (lane >= m) upto += x;
     }
-    const unsigned total = __shfl_sync(0xffffffffu, upto, 31), used = used_ctas(s, total), c = blockIdx.x;
-    if (c < used && total > 0 && !none) {  // (the same for every lane)
-      const unsigned f = total * c / used, g = total * (c + 1) / used;
-      // tile f: its sequence, in the range of the one lane whose sequences hold it
+    if (c < div.used && div.total > 0 && !none) {  // (the same for every lane)
+      const unsigned f = div.begin(c);
+      // place f: its sequence, in the range of the one lane whose sequences hold it
       int r = r0;
       unsigned at = upto - mine;
       const bool holds = at <= f && f < upto;
       if (holds)
-        while (r < r1 - 1 && at + work[r] <= f) at += work[r++];
+        while (r < r1 - 1 && at + work[r] + seq[r].w * ex <= f) {
+          at += work[r] + seq[r].w * ex;
+          ++r;
+        }
       const int owner = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
       r = __shfl_sync(0xffffffffu, r, owner);
       at = __shfl_sync(0xffffffffu, at, owner);
@@ -166,21 +195,19 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
           st.unit = unit_at(s, r, q.x, q.y, q.z, i);
           nt = max(st.unit.ntiles, 1);
         }
-        unsigned end = nt * s.H_kv;
+        const unsigned places = i < q.w ? nt + div.extra : 0;
+        unsigned end = places * s.H_kv;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
           const unsigned x = __shfl_up_sync(0xffffffffu, end, m);
           if (lane >= m) end += x;
         }
-        const unsigned from = at + end - nt * s.H_kv;  // this lane's unit: tiles [from, at + end)
+        const unsigned from = at + end - places * s.H_kv;  // this lane's unit: places [from, at + end)
         if (i < q.w && from <= f && f < at + end) {
           st.u = r;
           st.i = i;
-          st.h = (f - from) / nt;
-          const unsigned f0 = from + st.h * nt;
-          st.kt = f - f0;
-          st.count = g - f;
-          if (st.kt) sharers(st, f0, nt, total, used);
+          st.h = (f - from) / places;
+          div.set(st, c, from + st.h * places, nt);
           *out = st;
         }
         at += __shfl_sync(0xffffffffu, end, 31);
@@ -193,10 +220,12 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
 
 // The same where no unit and head is divided (s.whole): they are dealt to the CTAs
 // largest first, forth and back, so that each CTA's tiles add up to about the same.
-// Several sequences (one's units are in order as they are): first: R + 1 running sums of the sequences' units; order: the units from the
-// largest on; sizes: their tiles (scratch); all shared memory.
-__device__ __forceinline__ void plan_whole(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int4* seq,
-                                           uint16_t* first, uint16_t* order, uint16_t* sizes, PagedStart* out, int* err) {
+// For several sequences (one's units are in order as they are): first: R + 1 running
+// sums of the sequences' units; order: the units from the largest on; sizes: their
+// tiles (scratch); all shared memory.
+__device__ __forceinline__ void plan_whole(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len,
+                                           int4* seq, uint16_t* first, uint16_t* order, uint16_t* sizes,
+                                           PagedStart* out, int* err) {
   bool bad = false;
   for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
     int a, n, L;
@@ -264,12 +293,13 @@ struct PagedWalk {
   const uint16_t* first;   // (whole) their first units
   const uint16_t* order;   // (whole) the units, largest first
   int left, at, i, h, kt, n;  // current segment: tiles [kt, kt + n) of head h (n 0: a unit without keys)
+  int extra;
   PagedUnit u;
 
   __device__ PagedWalk(const PagedShape& s_, const PagedUnit* units_, const int4* seq_, const uint16_t* first_,
                        const uint16_t* order_, const PagedStart& st)
       : s(s_), units(units_), seq(seq_), first(first_), order(order_), left(st.count), at(st.u), i(st.i), h(st.h),
-        kt(st.kt), u(st.unit) {
+        kt(st.kt), extra(st.extra), u(st.unit) {
     if (s.whole && left > 0) deal();
     n = s.whole ? u.ntiles : min(u.ntiles - kt, left);
   }
@@ -297,7 +327,7 @@ struct PagedWalk {
     u = unit_at(s, r, seq[r].x, seq[r].y, seq[r].z, s.R == 1 ? v : v - first[r]);
   }
   __device__ void next() {
-    left -= s.whole ? 1 : max(n, 1);
+    left -= s.whole ? 1 : max(n, 1) + extra;
     if (left <= 0) return;
     if (s.whole) {
       ++at;

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
       const int key0 = tile_of(u, walk.kt + j0 + (e >> 1)) * kTileKeys;
       const int which = e & 1;
       if (which == 0) {
-        const int pg0 = key0 / P, per = P < kTileKeys ? 2 : 1;
+        const int pg0 = key0 >> p.s.page_log, per = P < kTileKeys ? 2 : 1;
         pages.hold(pg0, per, lane);
         const int a = __shfl_sync(kAll, pages.held, pg0 - pages.base);
         const int b = __shfl_sync(kAll, pages.held, pg0 + per - 1 - pages.base);
@@ -914,13 +914,16 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   s.d = c.d;
   s.width = b.width;
   s.page = c.page_size;
+  s.page_log = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
   s.n_pages = c.n_pages;
   s.causal = causal;
   // positions stay below 2^30: larger windows and sinks hide nothing more
   s.window = std::min(window, 1 << 30);
   s.sinks = window > 0 ? std::min(sinks, 1 << 30) : 0;
   s.step = chunk ? 2 * (128 / s.G) * s.G : kFewRows;
-  s.tile = chunk ? 128 : kTileKeys;
+  s.tile_log = chunk ? 7 : 5;
+  s.tile = 1 << s.tile_log;
+  static_assert(kTileKeys == 32, "tile_log");
   s.least = chunk ? 1 : few_warps(c.d, c.k_exp != nullptr);  // a tile for each computing warp, and fewer parts to join
   s.extra = chunk ? (c.k_exp ? 3 : 2) : (c.k_exp ? 10 : 4);
   s.ctas = sm_count() * (chunk ? 1 : few_ctas(c.d, c.k_exp != nullptr));

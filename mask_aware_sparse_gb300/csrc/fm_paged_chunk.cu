@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
     if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 8) {
       // ------------------------------------------------------------- producer
-      const int P = p.s.page, rows = min(P, 128), per = 128 / rows;
+      const int P = p.s.page, rows = P, per = 128 >> p.s.page_log;  // P <= 128
       const int zmax = p.s.n_pages * p.s.H_kv;
       uint32_t jt = 0, seg = 0;  // key tiles, segments with keys so far
       PageWindow pages;
@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
         ++seg;
         for (int j = 0; j < walk.n && ok; ++j, ++jt) {
           const int key0 = tile_of(u, walk.kt + j) * 128;
-          const int pg0 = key0 / P;
+          const int pg0 = key0 >> p.s.page_log;
           pages.hold(pg0, per, lane);
-          const int boxes = min(per, (u.kv_len - key0 + rows - 1) / rows);
+          const int boxes = min(per, (u.kv_len - key0 + rows - 1) >> p.s.page_log);
           // lane i copies the i-th box of the tile's keys (x fastest), then of its values
           constexpr int XS = F8 ? 1 : C::BOXES;
           const int b = min(lane / XS, boxes - 1), x = lane % XS;

@@ -41,6 +41,7 @@ struct PagedShape {
   int T, R, H_q, H_kv, G, d, width, page, n_pages;
   int causal, window, sinks;  // window 0: none
   int step, tile;  // query rows of a unit, keys of a tile
+  int tile_log, page_log;  // tile = 2^tile_log, page = 2^page_log
   int ctas, least;  // CTAs launched; tiles a CTA gets before another one does
   int extra;  // tiles that a segment's start and end are counted as
   int local;  // every CTA plans for itself: no plan kernel
@@ -76,9 +77,9 @@ __device__ __forceinline__ PagedUnit unit_at(const PagedShape& s, int r, int a, 
   const int last = q.pos + (q.g0 + q.nrows - 1) / s.G;
   q.hi = s.causal ? min(max(last + 1, 0), L) : L;
   q.lo = s.window > 0 ? max(0, q.pos - s.window + 1) : 0;
-  const int all = (q.hi + s.tile - 1) / s.tile;
-  q.ns = s.window > 0 ? min((s.sinks + s.tile - 1) / s.tile, all) : 0;
-  q.w0 = max(q.ns, min(q.lo / s.tile, all));
+  const int all = (q.hi + s.tile - 1) >> s.tile_log;
+  q.ns = s.window > 0 ? min((s.sinks + s.tile - 1) >> s.tile_log, all) : 0;
+  q.w0 = max(q.ns, min(q.lo >> s.tile_log, all));
   q.ntiles = q.ns + max(0, all - q.w0);
   q.pad = 0;
   return q;

@@ -31,8 +31,9 @@
 // exponent - mo) with a running maximum mo of its own, so that the weight of
 // the largest summand is near 1 whatever the rows' scales are. One fp16 term
 // (2^-12 of a weight; weights below 2^-14 of the largest are off by 2^-25 of it
-// at most) is finer than bf16's 2^-9. Measured at 32 sequences of 4K to 16K keys, 32 / 8 heads, d = 128: 258 us
-// with the values widened to bf16 by integer operations (867 instructions for 16 keys).
+// at most) is finer than bf16's 2^-9. Measured at 32 ragged sequences of up to 16384
+// keys, 32 / 8 heads, d = 128 (bytes alone 99 us): 114 us; 261 with the values widened
+// to bf16 by integer operations, whose instructions bounded it.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -186,8 +187,8 @@ struct FewCfg {
   static constexpr int EXP = F8 ? kTileKeys : 0;
   // Warps, CTAs an SM and entries of a warp's ring: what fills shared memory with
   // loads in flight. e4m3 rows are short for the work on each, so more warps help
-  // where registers allow: d = 64 three CTAs (step of 32 sequences 98 us with two),
-  // d = 256 eight warps (406 us with four).
+  // where registers allow: d = 64 three CTAs (step of 32 sequences 87 us, with two
+  // 98), d = 256 eight warps (292 us, with four 406).
   static constexpr int WARPS = few_warps(D, F8), THREADS = 32 * WARPS;
   static constexpr int PER_SM = few_ctas(D, F8);
   static constexpr int RING = D == 256 ? 3 : D == 64 ? (F8 ? 8 : 6) : (F8 ? 6 : 3);
@@ -439,7 +440,9 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
             qf[k][x] = pack_f16x2(__uint_as_float(qf[k][x] << 16) * f, __uint_as_float(qf[k][x] & 0xffff0000u) * f);
       }
     }
-    const bool many = u.nrows > 8;  // some thread has a second row (half the softmax otherwise)
+    // Some thread has a second row (half the softmax otherwise: e4m3 steps of 4 rows a
+    // unit 118 us instead of 120, d = 64 82 instead of 87; of 16 rows 130 instead of 124).
+    const bool many = u.nrows > 8;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float mo[2] = {-INFINITY, -INFINITY};  // e4m3: the running maximum of score + exponent of the value's scale
     float o[D / 8][4];
@@ -875,11 +878,12 @@ cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cach
 // sequences are taken to be ragged: two fifths of it at least, where there are
 // several); divided ones cost the parts' writing and joining, and a start and an end
 // for every part. What the host knows decides: the units that T tokens make, the
-// keys that the page table has room for. chunk_kernel (tiles of 128 keys, about 1.9
-// us): 2048 tokens of 32 / 8 heads over themselves 38 us whole, 90 divided; 4096
-// over themselves 121, 233; 2048 over 4096 keys 95, 113; 256 over 2048 keys 37, 30; a
-// full prompt's units grow from one tile to `most`, so less is left idle. few_kernel
-// (tiles of 32 keys): 64 sequences of 500 keys 18 us whole, 25 divided; one 11.7, 8.6.
+// keys that the page table has room for. chunk_kernel (tiles of 128 keys, about 1.5
+// us): 2048 tokens of 32 / 8 heads over themselves 33 us whole, 51 divided; 4096
+// over themselves 100, 131; 2048 over 4096 keys 77, 92; 256 over 2048 keys 31, 27; 512
+// over 4096 keys 53, 43; a full prompt's units grow from one tile to `most`, so less is
+// left idle. few_kernel (tiles of 32 keys): 64 sequences of 500 keys 17 us whole, 23
+// divided; one of 300 keys 9.1, 12.0; one of 1021 17.7, 10.0.
 bool stay_whole(const PagedShape& s, const fm_paged_batch& b, long long most, bool chunk) {
   const double units = (double)s.H_kv * (chunk ? ((double)s.T * s.G / s.step + b.R / 2.0)
                                                : std::max((double)b.R, (double)s.T * s.G / s.step));
@@ -887,8 +891,8 @@ bool stay_whole(const PagedShape& s, const fm_paged_batch& b, long long most, bo
   double idle = most * std::max(std::ceil(rounds) - rounds, b.R > 1 ? 0.4 : 0.0);
   if (b.R == 1 && s.causal && s.window == 0 && 2ll * s.T >= (long long)b.width * s.page)
     idle /= 4 * std::max(1.0, rounds);
-  if (!chunk) idle /= std::max(1.0, rounds);  // ragged lengths even out over the rounds
-  return idle <= (chunk ? 5 + 8 * std::min(1.0, rounds) : 8);
+  if (!chunk || b.R > 1) idle /= std::max(1.0, rounds);  // ragged lengths even out over the rounds
+  return idle <= (chunk ? 5 + 8 * std::min(1.0, rounds) : 12);
 }
 
 // Which kernel: chunk_kernel's tiles of 128 rows once the sequences have more

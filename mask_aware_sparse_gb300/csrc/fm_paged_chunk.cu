@@ -47,9 +47,10 @@ template <int D, bool F8>
 struct ChunkCfg {
   // e4m3: warpgroups that widen tiles, and the registers that the launch's are
   // redistributed into: d = 128: 20 warps at 96, 8 softmax warps at 168, 12 others
-  // at 48 (one group, 16 warps: a 2048-token chunk over 32768 keys 1515 us instead
-  // of 1145); d = 64, half as much to widen for each product: 16 warps at 128, 184
-  // and 72 (two groups: 8000 tokens over 9000 keys 348 us instead of 315)
+  // at 48 (one group, 16 warps: a 2048-token chunk over 32768 keys 1031 us instead
+  // of 958); d = 64, half as much to widen for each product: 16 warps at 128, 184 and
+  // 72 (two groups: ragged chunks of 1111 tokens 32.1 us instead of 30.7, but 2048
+  // tokens over 32768 keys 666 instead of 695)
   static constexpr int WIDEN = !F8 ? 0 : D == 128 ? 2 : 1;
   static constexpr int SOFTMAX_REGS = WIDEN == 2 ? 168 : 184, OTHER_REGS = WIDEN == 2 ? 48 : 72;
   static constexpr int THREADS = F8 ? 384 + 128 * WIDEN : 320;

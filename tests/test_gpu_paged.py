@@ -87,6 +87,21 @@ def test_write_and_read(d, page, f8):
     assert fm.fm_device_status() == (fm.FM_OK, 0)
 
 
+@pytest.mark.parametrize("d, page, Hkv", [(64, 16, 5), (128, 64, 2), (256, 128, 1)])
+@pytest.mark.parametrize("f8", [False, True])
+def test_write_and_read_of_many_rows(d, page, Hkv, f8):
+    # blocks of many tokens, and one with a few left; rows at an odd 16 bytes
+    s = Setup([9001, 3, 0, 2500], [1, 1, 0, 1], Hkv, d, page, f8, seed=24)
+    n = sum(s.keys)
+    buf = torch.empty(2, Hkv * n * d + 8, dtype=torch.bfloat16).cuda()
+    k, v = fm.fm_cache_read(s.cache, s.kv_off, s.table, n, k=buf[0, 8:].view(1, Hkv, n, d),
+                            v=buf[1, :-8].view(1, Hkv, n, d))
+    for got, x in ((k, s.k), (v, s.v)):
+        want = quantised(x.double())[0] if f8 else x.double()
+        assert torch.equal(got[0].double().cpu(), want.transpose(0, 1))
+    assert fm.fm_device_status() == (fm.FM_OK, 0)
+
+
 def test_quantisation_edges():
     d = 64
     rows = torch.zeros(12, 1, d)

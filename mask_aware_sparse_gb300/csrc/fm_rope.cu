@@ -440,7 +440,7 @@ int groups_per_step(const fm_qk_problem& P) {
   return tb;
 }
 // Two columns of blocks, queries and keys (with values), at most what the SMs hold
-// at once of each (forward, 8192 tokens of 48 heads: 43 us, 8 blocks an SM 45); the
+// at once of each (forward, 8192 tokens of 48 heads: 44.7 us, 8 blocks an SM 46.6); the
 // backward has a partial row per block besides.
 int grid_blocks(const fm_qk_problem& P, int tb, int per_sm) {
   const int H = P.H_q > P.H_kv ? P.H_q : P.H_kv;  // the side that needs more steps

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % TG, hl = lane / TG;
   const C ch(c, p.rot);
-  const int64_t total = (int64_t)p.B * p.N;
+  const int total = p.B * p.N;
   const int RT = p.rot / 16;
   const bool keys = blockIdx.y != 0;
   const View in = keys ? p.k : p.q, out = keys ? p.ko : p.qo, src = keys ? p.xk : p.xq;
@@ -238,13 +238,44 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
     }
   }
   __syncthreads();
-  for (int64_t tok0 = (int64_t)blockIdx.x * tokens; tok0 < total; tok0 += (int64_t)gridDim.x * tokens) {
+  const int groups = (H + HS - 1) / HS;
+  const int stride = gridDim.x * tokens;  // (no more than 2^30 tokens)
+  int tok0 = blockIdx.x * tokens, b = 0, n = 0;
+  bool there = false;
+  // The next rows' loads are in flight while these are computed, and the next step's
+  // first ones while its angles are (a row is read and written by the same threads, so
+  // in and out may be one tensor).
+  uint4 ra[kAhead], rb[kAhead], xa[BWD ? kAhead : 1], xb[BWD ? kAhead : 1];
+  auto fetch = [&](int k, int g) {
+    const int h = g * HS + h0;
+    if (there && h < H) {
+      ra[k] = *at(in, b, h, n, ch.oa);
+      rb[k] = *at(in, b, h, n, ch.ob);
+      if constexpr (BWD) {
+        if (wp) {
+          xa[k] = *at(src, b, h, n, ch.oa);
+          xb[k] = *at(src, b, h, n, ch.ob);
+        }
+      }
+    }
+  };
+  auto begin = [&] {
+    there = tok0 + ti < total;
+    b = (tok0 + ti) / p.N;
+    n = tok0 + ti - b * p.N;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(k, w0 + k * wpt);
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    ra[k] = rb[k] = make_uint4(0, 0, 0, 0);
+    if constexpr (BWD) xa[k] = xb[k] = make_uint4(0, 0, 0, 0);
+  }
+  begin();
+  while (tok0 < total) {
     load_angles(p, frac, cs, tokens, tok0, total);
     __syncthreads();
     {
-      const int64_t tok = tok0 + ti;
-      const bool there = tok < total;
-      const int64_t b = tok / p.N, n = tok - b * p.N;
       F2 co[4], si[4];
       if (ch.turned) {
 #pragma unroll
@@ -253,29 +284,6 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
           co[j] = f2_pack(t.x, t.y);
           si[j] = f2_pack(t.z, t.w);
         }
-      }
-      const int groups = (H + HS - 1) / HS;
-      // the next rows' loads are in flight while these are computed (a row is
-      // read and written by the same threads, so in and out may be one tensor)
-      uint4 ra[kAhead], rb[kAhead], xa[BWD ? kAhead : 1], xb[BWD ? kAhead : 1];
-      auto fetch = [&](int k, int g) {
-        const int h = g * HS + h0;
-        if (there && h < H) {
-          ra[k] = *at(in, b, h, n, ch.oa);
-          rb[k] = *at(in, b, h, n, ch.ob);
-          if constexpr (BWD) {
-            if (wp) {
-              xa[k] = *at(src, b, h, n, ch.oa);
-              xb[k] = *at(src, b, h, n, ch.ob);
-            }
-          }
-        }
-      };
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        ra[k] = rb[k] = make_uint4(0, 0, 0, 0);
-        if constexpr (BWD) xa[k] = xb[k] = make_uint4(0, 0, 0, 0);
-        fetch(k, w0 + k * wpt);
       }
       for (int g0 = w0; g0 < groups; g0 += kAhead * wpt) {
 #pragma unroll
@@ -365,13 +373,17 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(const QkParam
           }
         }
       }
+      const int64_t vb = b, vn = n;
+      const bool v_there = there;
+      tok0 += stride;
+      begin();
       if (keys && p.has_v) {
         for (int g = w0; g < groups; g += wpt) {
           const int h = g * HS + h0;
-          if (there && h < H) {
-            const uint4 x = *at(p.v, b, h, n, 16 * c), y = *at(p.v, b, h, n, 16 * c + 8);
-            *at(p.vo, b, h, n, 16 * c) = x;
-            *at(p.vo, b, h, n, 16 * c + 8) = y;
+          if (v_there && h < H) {
+            const uint4 x = *at(p.v, vb, h, vn, 16 * c), y = *at(p.v, vb, h, vn, 16 * c + 8);
+            *at(p.vo, vb, h, vn, 16 * c) = x;
+            *at(p.vo, vb, h, vn, 16 * c + 8) = y;
           }
         }
       }

@@ -59,7 +59,7 @@ struct QkParams {
 };
 
 // Two fp32 numbers as one operand: half the instructions (8192 tokens of 48 heads,
-// both ways: 114.3 us, 112.3 so).
+// both ways: 110 us, 2 us more one by one).
 using F2 = uint64_t;
 __device__ __forceinline__ F2 f2_both(float x) { return f2_pack(x, x); }
 __device__ __forceinline__ float f2_sum(F2 a) {
@@ -443,8 +443,8 @@ View view_of(const fm_view* v) {
 
 // Groups of tokens per block and step: one warp on each (the angles are then read once
 // per token) once that leaves a block for every other SM, more warps on each before
-// that. 512 / 1000 tokens of 48 heads, d = 128, both ways: 14.5 / 21.6 us; only when
-// four blocks an SM are left: 16.6 / 23.0, eight: 20.6 / 27.7.
+// that. 512 / 1000 tokens of 48 heads, d = 128, both ways: 14.0 / 20.8 us; only when
+// four blocks an SM are left 2 us more, eight 6 us more.
 int groups_per_step(const fm_qk_problem& P) {
   const int64_t groups = (int64_t)P.B * P.N / tokens_per_warp(P.H_q, P.d);
   int tb = 1;
@@ -452,7 +452,7 @@ int groups_per_step(const fm_qk_problem& P) {
   return tb;
 }
 // Two columns of blocks, queries and keys (with values), at most what the SMs hold
-// at once of each (forward, 8192 tokens of 48 heads: 44.7 us, 8 blocks an SM 46.6); the
+// at once of each (forward, 8192 tokens of 48 heads: 43.3 us, with 8 blocks an SM 2 us more); the
 // backward has a partial row per block besides.
 int grid_blocks(const fm_qk_problem& P, int tb, int per_sm) {
   const int H = P.H_q > P.H_kv ? P.H_q : P.H_kv;  // the side that needs more steps

@@ -873,9 +873,9 @@ def _new_view(shape, device):
 
 def _new_token_view(shape, device):
     """The same, laid out (B, N, H, d)."""
-    B, H, N, d = shape
-    t = torch.empty((B, N, H, d), dtype=_BF16, device=device)
-    return t.transpose(1, 2), _pack_view(t.data_ptr(), H * N * d, d, H * d)
+    _, H, N, d = shape
+    t = torch.empty_strided(shape, (H * N * d, d, H * d, 1), dtype=_BF16, device=device)
+    return t, _pack_view(t.data_ptr(), H * N * d, d, H * d)
 
 
 def _rows(t, name, shape, dev, out=False):

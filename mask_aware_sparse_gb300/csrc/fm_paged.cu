@@ -739,15 +739,16 @@ struct JoinParams {
 // Block (c, y): where CTA c's range is the second one inside a unit and head,
 // their parts (CTA c - 1's last segment, then c .. last's first segments) are
 // joined. Latency bounds it, so it goes by what there is more of. Many rows of a
-// few parts each (chunk_kernel's slots of 256 rows): ROWS = 4 rows (d = 64: eight) a
-// warp, two parts of each in flight. Few rows: one a warp, eight parts in flight, or,
+// few parts each (chunk_kernel's slots of 256 rows): ROWS = 2 rows (d = 64: four) a
+// warp, four parts of each in flight (256 tokens over 4096 keys 32.5 us; four rows, two
+// parts 33.1; one row, eight parts 33.4). Few rows: one a warp, eight parts in flight, or,
 // of many parts, a long cache's, one by WPR = 4 warps (one token over 32000 keys, 38
 // parts: 32 us for the call, 35 with one warp a row; but where one warp is enough,
 // three times the blocks cost about 2 us).
 template <int D, int ROWS, int WPR>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
-  constexpr int PARTS = ROWS > 1 ? 2 : 8;
+  constexpr int PARTS = ROWS > 1 ? 4 : 8;
   __shared__ float4 other[WPR > 1 ? 8 * 32 * V : 1];
   __shared__ float2 other_ml[WPR > 1 ? 8 * RPW : 1];
   grid_dependency_wait();
@@ -854,7 +855,7 @@ cudaError_t launch_join(const PagedShape& s, const PagedWork& w, const PagedOut&
   };
   constexpr int RPW = D == 64 ? 2 : 1;
   if (parts > 9) return go(join_kernel<D, 1, 4>, 2 * RPW);
-  if (rows == kChunkRows) return go(join_kernel<D, 4, 1>, 32 * RPW);
+  if (rows == kChunkRows) return go(join_kernel<D, 2, 1>, 16 * RPW);
   return go(join_kernel<D, 1, 1>, 8 * RPW);
 }
 

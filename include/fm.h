@@ -430,8 +430,8 @@ fm_status fm_needed_chunks(const uint8_t* tile_class, int32_t B, int32_t nQ, int
  * view); apart from that no tensors overlap. d is 64, 128 or 256; rot a multiple
  * of 16, 0 <= rot <= d (0: no rotation; pos and inv_freq are then not read). pos:
  * int32, entry b * pos_sb + n (pos_sb 0: one row for every batch entry); inv_freq:
- * rot / 2 finite fp32 values. q_weight / k_weight: d values each, fp32 when w_f32 != 0 else bf16;
- * NULL: that side is not normed. v and vo both NULL: no values.
+ * rot / 2 finite fp32 values. q_weight / k_weight: d values each, fp32 when
+ * w_f32 != 0 else bf16; NULL: that side is not normed. v and vo both NULL: no values.
  *
  * Backward: dqo, dko, dvo are the gradients of the outputs; dq, dk, dv and the
  * weights' gradients (type of the weights) are written. q and k, the forward's
@@ -492,11 +492,11 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  * call's T packed tokens, ascending from 0; kv_len (R), its keys in the cache,
  * the new tokens' own included; page_table (R, width): entry i of row r is the
  * page of its keys [i * page_size, (i + 1) * page_size). New token a of n has
- * position kv_len - n + a. An entry matters to a call only where the call writes, reads
- * back or (fm_attn_paged) shows some new token a key of that page: entries past a
- * sequence's end or behind its window may hold anything.
- * All device int32. Tokens from q_off[R] on belong to no sequence: their rows are
- * neither read nor written. Values that no such batch has (a page outside
+ * position kv_len - n + a. An entry matters to a call only where the call writes,
+ * reads back or (fm_attn_paged) shows some new token a key of that page: entries
+ * past a sequence's end or behind its window may hold anything. All device int32.
+ * Tokens from q_off[R] on belong to no sequence: what their rows hold has no effect,
+ * and nothing is written for them. Values that no such batch has (a page outside
  * [0, n_pages), a length outside [0, width * page_size], offsets that descend or
  * pass T) set FM_DEVERR_RANGE; what rows of such a batch receive is then undefined,
  * nothing outside the tensors is touched.

@@ -350,7 +350,8 @@ def test_many_sequences_and_shared_pages():
     q_off = torch.cat((torch.zeros(1, dtype=torch.int32), new.cumsum(0).int()))
     T = int(q_off[-1])
     q = torch.randn(T, 2, 64, generator=g).to(torch.bfloat16)
-    o, lse = fm.fm_attn_paged(q.cuda(), cache, fm.PagedBatch(q_off.cuda(), keys.int().cuda(), table.cuda()), scale=0.125)
+    batch = fm.PagedBatch(q_off.cuda(), keys.int().cuda(), table.cuda())
+    o, lse = fm.fm_attn_paged(q.cuda(), cache, batch, scale=0.125)
     assert fm.fm_device_status() == (fm.FM_OK, 0)
     seq = lambda c, r: torch.cat((c[0, 0], c[r + 1, 0]))[: int(keys[r])].double()[None]  # noqa: E731
     ref = paged(q.double(), [seq(kv[0], r) for r in range(R)], [seq(kv[1], r) for r in range(R)], q_off.tolist(),

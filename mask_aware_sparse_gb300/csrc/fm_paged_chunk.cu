@@ -48,9 +48,9 @@ struct ChunkCfg {
   // e4m3: warpgroups that widen tiles, and the registers that the launch's are
   // redistributed into: d = 128: 20 warps at 96, 8 softmax warps at 168, 12 others
   // at 48 (one group, 16 warps: a 2048-token chunk over 32768 keys 1031 us instead
-  // of 958); d = 64, half as much to widen for each product: 16 warps at 128, 184 and
-  // 72 (two groups: ragged chunks of 1111 tokens 32.1 us instead of 30.7, but 2048
-  // tokens over 32768 keys 666 instead of 695)
+  // of 936); d = 64, half as much to widen for each product: 16 warps at 128, 184 and
+  // 72 (two groups: ragged chunks of 1111 tokens 31.8 us instead of 30.2, 20 of 4000 tokens
+  // over up to 8000 keys 137 instead of 132, 2048 tokens over 32768 keys 681 instead of 685)
   static constexpr int WIDEN = !F8 ? 0 : D == 128 ? 2 : 1;
   static constexpr int SOFTMAX_REGS = WIDEN == 2 ? 168 : 184, OTHER_REGS = WIDEN == 2 ? 48 : 72;
   static constexpr int THREADS = F8 ? 384 + 128 * WIDEN : 320;
@@ -554,7 +554,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
         const int key = tile_of(u, walk.kt + j) * 128 + row;
         // rows that no query of the unit sees become zeros, whatever they hold
         const bool dead = !(key < u.hi && (key >= u.lo || key < p.s.sinks));
-        const uint32_t mag = dead ? 0u : 0x07f007f0u, sign = dead ? 0u : 0x80008000u;
         // keys and values in turn, or, with two groups, keys the first and values the second
 #pragma unroll 1
         for (int v = (warp - 12) >> 2; v < 2 && ok; v += C::WIDEN) {
@@ -567,34 +566,60 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           const uint32_t src = smem_u32(smem + C::RAW_OFF + rs * C::RAW);
           const uint32_t dst = smem_u32(smem + (v ? C::V_OFF : C::K_OFF) + (jt % S) * C::TILE) + row * 128;
           const uint32_t e = lds8(smem_u32(smem + C::EXP_OFF) + rs * 128 + row);
-          const uint32_t fl = dead ? 0u : factor_lo(e) * 0x10001u;
+          const uint32_t fl = dead ? 0u : factor_lo(e) * 0x10001u;  // (the bits it multiplies are finite)
           const bool wide = __any_sync(kAll, !dead && e > 134u && e < 255u);
+          // 64 bytes of the row at a time: the staged tile is free for the next one as soon as
+          // the last of them are in registers (its load is otherwise waited for: 2048 tokens
+          // over 32768 keys, d = 128, 1016 us instead of 934, d = 64 715 instead of 684)
+          constexpr int kPart = 4;
+          uint32_t top = 0;  // the row's largest magnitudes, before its scale
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const uint4 r = lds128(src + in_box<ROW>(row, c));
-            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-            uint32_t o[8];
+          for (int part = 0; part < D / 64; ++part) {
+            uint4 rr[kPart];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              o[2 * x] = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x1404), mag, sign), fl);
-              o[2 * x + 1] = mul_bf2(e4m3_bits(__byte_perm(w[x], 0, 0x3424), mag, sign), fl);
+            for (int c = 0; c < kPart; ++c) rr[c] = lds128(src + in_box<ROW>(row, part * kPart + c));
+            if (part == D / 64 - 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[C::REMPTY + rs]);
             }
-            if (wide) {
-              const uint32_t fh = factor_hi(e) * 0x10001u;
 #pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] = mul_bf2(o[x], fh);
+            for (int cc = 0; cc < kPart; ++cc) {
+              const int c = part * kPart + cc;
+              const uint32_t w[4] = {rr[cc].x, rr[cc].y, rr[cc].z, rr[cc].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t a = __byte_perm(w[x], 0, 0x1404), b = __byte_perm(w[x], 0, 0x3424);
+                const uint32_t ma = (a >> 4) & kE4m3Mag, mb = (b >> 4) & kE4m3Mag;
+                top = __vimax3_u16x2(top, ma, mb);
+                o[2 * x] = mul_bf2(ma | (a & kE4m3Sign), fl);
+                o[2 * x + 1] = mul_bf2(mb | (b & kE4m3Sign), fl);
+              }
+              if (wide) {
+                const uint32_t fh = factor_hi(e) * 0x10001u;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) o[x] = mul_bf2(o[x], fh);
+              }
+              const uint32_t at = dst + (c >> 2) * 16384;
+              const int ch = 2 * (c & 3);
+              sts_b32x4(at + (((ch) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+              sts_b32x4(at + (((ch + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
             }
-            const uint32_t at = dst + (c >> 2) * 16384;
-            const int ch = 2 * (c & 3);
-            sts_b32x4(at + (((ch) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-            sts_b32x4(at + (((ch + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+          }
+          // The row holds NaN, which was widened like a number, 480, that e4m3 does not have:
+          // back to NaN (with it, at scales of 2^120 and more, what bf16 has no number for)
+          if (max(top & 0xffffu, top >> 16) == (kE4m3Mag & 0xffffu) && !dead) {
+            const uint32_t lo = mul_bf2(kE4m3Mag, fl);
+            const uint32_t n480 = (wide ? mul_bf2(lo, factor_hi(e) * 0x10001u) : lo) & 0x7fffu;
+#pragma unroll 1
+            for (int i = 0; i < D; ++i) {
+              const uint32_t at = dst + (i >> 6) * 16384 + ((((i >> 3) & 7) ^ (row & 7)) << 4) + 2 * (i & 7);
+              if (((lds8(at) | lds8(at + 1) << 8) & 0x7fffu) == n480) sts_b16(at, 0x7fffu);
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars[(v ? C::VFULL : C::KFULL) + jt % S]);
-            mbar_arrive(&bars[C::REMPTY + rs]);
-          }
+          if (lane == 0) mbar_arrive(&bars[(v ? C::VFULL : C::KFULL) + jt % S]);
         }
       }
     }

@@ -416,11 +416,14 @@ __device__ __forceinline__ uint32_t in_box(int row, int chunk) {
     return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-// e4m3 in the high bytes of two 16-bit lanes -> bf16 pair, times 2^-120 (masks
-// 0x07f007f0 and 0x80008000; zeros where they are zero)
-__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t, uint32_t mag, uint32_t sign) {
-  return ((t >> 4) & mag) | (t & sign);
+__device__ __forceinline__ void sts_b16(uint32_t addr, uint32_t v) {
+  if (!FM_DBG(smem_range(addr, 2, 2))) return;
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
+
+// e4m3 in the high byte of a 16-bit lane, t: (t >> 4) & kE4m3Mag | t & kE4m3Sign is the
+// value as bf16, times 2^-120, and NaN (all magnitude bits) becomes 480 times that
+constexpr uint32_t kE4m3Mag = 0x07f007f0u, kE4m3Sign = 0x80008000u;
 __device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -35,3 +35,58 @@ def test_nan_bytes_of_rows_with_an_ordinary_exponent(d, new, byte):
         assert torch.equal(torch.isnan(got).cpu(), hit)
         c[at] = was
     assert fm.fm_device_status() == (fm.FM_OK, 0)
+
+
+def _i32(*v):
+    return torch.tensor(v, dtype=torch.int32).cuda()
+
+
+RANGE = (fm.FM_ERR_DEVICE, fm.FM_DEVERR_RANGE)
+
+
+@pytest.mark.parametrize("off", [(0, 6, 5), (0, 3, 9), (3, 1, 5), (-4, 3, 5), (2, 3, 5), (0, 3, 2 ** 31 - 1),
+                                 (0, -1, 5), (5, 0, 0)])
+@pytest.mark.parametrize("f8", [False, True])
+def test_cache_calls_flag_offsets_and_write_nothing(off, f8):
+    cache = fm.fm_cache_new(4, 2, 16, 64, dtype=torch.float8_e4m3fn if f8 else torch.bfloat16)
+    table, kv_len = _i32(0, 1, 2, 3).view(2, 2), _i32(20, 5)
+    held = torch.randn(2, 52, 2, 64, generator=torch.Generator().manual_seed(31)).to(torch.bfloat16).cuda()
+    fm.fm_cache_write(held[0], held[1], cache, fm.PagedBatch(_i32(0, 32, 52), _i32(32, 20), table))
+    state = [t.view(torch.uint8).clone() for t in (cache.k, cache.v, cache.k_exp, cache.v_exp) if t is not None]
+    x = torch.ones(5, 2, 64, dtype=torch.bfloat16).cuda()
+    assert fm.fm_device_status() == (fm.FM_OK, 0)
+    fm.fm_cache_write(x, x, cache, fm.PagedBatch(_i32(*off), kv_len, table))
+    assert fm.fm_device_status() == RANGE
+    now = [t.view(torch.uint8) for t in (cache.k, cache.v, cache.k_exp, cache.v_exp) if t is not None]
+    assert all(torch.equal(a, b) for a, b in zip(state, now))
+    fm.fm_cache_read(cache, _i32(*off), table, 5)
+    assert fm.fm_device_status() == RANGE
+
+
+@pytest.mark.parametrize("kv_len, new", [((33, 5), (0, 2, 5)), ((-1, 5), (0, 0, 3)), ((20, 2 ** 31 - 1), (0, 2, 2)),
+                                         ((-(2 ** 31), 5), (0, 2, 5))])
+def test_a_write_flags_lengths_and_writes_nothing(kv_len, new):
+    cache = fm.fm_cache_new(4, 2, 16, 64)
+    cache.k.zero_(), cache.v.zero_()
+    x = torch.ones(5, 2, 64, dtype=torch.bfloat16).cuda()
+    fm.fm_cache_write(x, x, cache, fm.PagedBatch(_i32(*new), _i32(*kv_len), _i32(0, 1, 2, 3).view(2, 2)))
+    assert fm.fm_device_status() == RANGE
+    assert not cache.k.any() and not cache.v.any()
+
+
+def test_offsets_of_many_sequences_are_looked_at():
+    # more than a block has threads; one pair of offsets descends where no token of most blocks is
+    R = 1000
+    cache = fm.fm_cache_new(R, 1, 16, 64)
+    cache.k.zero_(), cache.v.zero_()
+    off = torch.arange(R + 1, dtype=torch.int32)
+    kv_len, table = torch.ones(R, dtype=torch.int32).cuda(), torch.arange(R, dtype=torch.int32)[:, None].contiguous().cuda()
+    x = torch.ones(R, 1, 64, dtype=torch.bfloat16).cuda()
+    bad = off.clone()
+    bad[700], bad[701] = 701, 700
+    fm.fm_cache_write(x, x, cache, fm.PagedBatch(bad.cuda(), kv_len, table))
+    assert fm.fm_device_status() == RANGE
+    assert not cache.k.any() and not cache.v.any()
+    fm.fm_cache_write(x, x, cache, fm.PagedBatch(off.cuda(), kv_len, table))
+    assert fm.fm_device_status() == (fm.FM_OK, 0)
+    assert (cache.k[:, 0, 0] == 1).all() and not cache.k[:, 0, 1:].any()

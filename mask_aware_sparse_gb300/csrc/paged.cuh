@@ -53,7 +53,8 @@ struct PagedShape {
 __device__ __forceinline__ int tile_of(const PagedUnit& u, int kt) { return kt < u.ns ? kt : kt - u.ns + u.w0; }
 
 // The new tokens of sequence r, [a, a + n), kept inside [0, T] whatever q_off
-// holds, and its keys, kept inside the page table; true where either was not.
+// holds, and its keys, kept inside the page table; true where either was not, or the
+// first sequence's tokens do not start at 0.
 __device__ __forceinline__ bool sequence_at(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len, int r,
                                             int& a, int& n, int& L) {
   const int b0 = q_off[r], e0 = q_off[r + 1], L0 = kv_len[r];
@@ -61,7 +62,7 @@ __device__ __forceinline__ bool sequence_at(const PagedShape& s, const int32_t* 
   const int e = min(max(e0, a), s.T);
   n = e - a;
   L = min(max(L0, 0), s.width * s.page);
-  return a != b0 || e != e0 || L != L0;
+  return a != b0 || e != e0 || L != L0 || (r == 0 && b0 != 0);
 }
 
 // Unit i of a sequence.

@@ -90,3 +90,14 @@ def test_offsets_of_many_sequences_are_looked_at():
     fm.fm_cache_write(x, x, cache, fm.PagedBatch(off.cuda(), kv_len, table))
     assert fm.fm_device_status() == (fm.FM_OK, 0)
     assert (cache.k[:, 0, 0] == 1).all() and not cache.k[:, 0, 1:].any()
+
+
+@pytest.mark.parametrize("new, keys", [([3, 2], [20, 5]), ([300, 200], [700, 300]), ([1] * 300, [20] * 300)])
+def test_attention_flags_offsets_that_do_not_start_at_0(new, keys):
+    # planned by every CTA (whole units, divided ones) and by a kernel of its own
+    s = Setup(keys, new, 2, 64, 16, False, seed=32)
+    q = torch.ones(sum(new) + 1, 4, 64, dtype=torch.bfloat16).cuda()
+    fm.fm_attn_paged(q, s.cache, s.batch, scale=0.1)
+    assert fm.fm_device_status() == (fm.FM_OK, 0)
+    fm.fm_attn_paged(q, s.cache, fm.PagedBatch(s.q_off + 1, s.kv_len, s.table), scale=0.1)
+    assert fm.fm_device_status() == RANGE

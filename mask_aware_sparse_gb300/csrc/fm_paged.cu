@@ -32,9 +32,10 @@
 // the largest summand is near 1 whatever the rows' scales are. One fp16 term
 // (2^-12 of a weight; weights below 2^-14 of the largest are off by 2^-25 of it
 // at most) is finer than bf16's 2^-9. Measured at 32 ragged sequences of up to 16384
-// keys, 32 / 8 heads, d = 128 (bytes alone 99 us): 114 us; 261 with the values widened
+// keys, 32 / 8 heads, d = 128 (bytes alone 99 us): 112 us; 261 with the values widened
 // to bf16 by integer operations, whose instructions bounded it.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -432,7 +433,12 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
         // 2^(142 - E), kept finite; a row with infinities or NaN stays as it is
         const int up = E == 255 ? 0 : min(142 - E, 126);
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-        sc[i] = sl2 * __uint_as_float((uint32_t)(127 - up) << 23);
+        // 2^-up: on the sums (below 2^33) ahead of a key's scale, so that no score passes
+        // fp32's range on the way to one inside it, what is above 2^80 after it. In
+        // shared memory until the segment's end (d = 256: 272 us, in registers 295).
+        const int back = min(-up, 80);
+        if (t == 0) ml[warp * kFewRows + g + 8 * i].x = __uint_as_float((uint32_t)(127 + back) << 23);
+        sc[i] = fminf(sl2 * __uint_as_float((uint32_t)(127 - up - back) << 23), FLT_MAX);
 #pragma unroll
         for (int k = 0; k < C::KSTEPS; ++k)
 #pragma unroll
@@ -484,14 +490,15 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
               }
             }
         if constexpr (F8) {
+          const float down[2] = {ml[warp * kFewRows + g].x, ml[warp * kFewRows + g + 8].x};
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             const uint32_t ek = lds16(ring_exp + sk * C::EXP + 8 * n + 2 * t);
-            const float f0 = scale_of(ek & 255u), f1 = scale_of(ek >> 8);
-            s[n][0] *= f0;
-            s[n][1] *= f1;
-            s[n][2] *= f0;
-            s[n][3] *= f1;
+            const uint64_t f = f2_pack(scale_of(ek & 255u), scale_of(ek >> 8));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              f2_unpack(f2_mul(f2_mul(f2_pack(s[n][2 * i], s[n][2 * i + 1]), f2_pack(down[i], down[i])), f), s[n][2 * i],
+                        s[n][2 * i + 1]);
           }
         }
       }

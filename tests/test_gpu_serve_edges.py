@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import mask_aware_sparse_gb300 as fm
+from serve_ref import assert_paged, paged
 from test_gpu_paged import Setup
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +102,26 @@ def test_attention_flags_offsets_that_do_not_start_at_0(new, keys):
     assert fm.fm_device_status() == (fm.FM_OK, 0)
     fm.fm_attn_paged(q, s.cache, fm.PagedBatch(s.q_off + 1, s.kv_len, s.table), scale=0.1)
     assert fm.fm_device_status() == RANGE
+
+
+@pytest.mark.parametrize("d, Hq", [(64, 4), (128, 32), (256, 4)])
+@pytest.mark.parametrize("power, scale", [(-112, 0.125), (-100, 0.125), (112, 0.125), (0, 1e-30)])
+def test_steps_over_quantised_keys_far_from_one(d, Hq, power, scale):
+    # scores near 1 from queries near 2^power and keys near 2^-power; a scale so small that all weights are alike
+    s = Setup([150, 33], [1, 1], 2, d, 16, True, seed=33)
+    s.k = (s.k.double() * 2.0 ** -power).to(torch.bfloat16)
+    fm.fm_cache_write(s.k.cuda(), s.v.cuda(), s.cache, fm.PagedBatch(s.kv_off, s.kv_len, s.table))
+    q = (torch.randn(2, Hq, d, generator=s.g).double() * 2.0 ** power).to(torch.bfloat16)
+    o, lse = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=scale)
+    k, v = s.values()
+    assert_paged(o, lse, paged(q.double(), k, v, s.q_off.tolist(), s.keys, scale, True, 0, 0), d)
+
+
+@pytest.mark.parametrize("scale", [0.125, 1e-9, 1e-30])
+def test_queries_of_zero_over_quantised_keys(scale):
+    s = Setup([150, 33], [1, 1], 2, 64, 16, True, seed=34)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    q[1, 2] = 1.0
+    o, lse = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=scale)
+    k, v = s.values()
+    assert_paged(o, lse, paged(q.double(), k, v, s.q_off.tolist(), s.keys, scale, True, 0, 0), 64)

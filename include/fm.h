@@ -558,10 +558,15 @@ fm_status fm_cache_read(const fm_kv_cache* cache, const int32_t* kv_off, const i
  *
  * q, o: bf16 rows (T, H_q, d) of element strides st, sh (multiples of 8,
  * 16-byte aligned); lse: (T, H_q) fp32, contiguous. o overlaps no input. GQA
- * as fm_attn_fwd. e4m3 caches give what the same values in a bf16 cache give, up to
- * 32-bit rounding and that of the weights. scale > 0. The joining
- * order of a sequence's parts is fixed by the lengths: the same call gives the
- * same bits. Workspace: fm_attn_paged_workspace_bytes (on the current device),
+ * as fm_attn_fwd. scale > 0. Weights are rounded to bf16 for their product with the
+ * values (2^-9 of each; calls of few rows a sequence keep two terms, 2^-18). e4m3
+ * caches give what the same values in a bf16 cache give up to that and 32-bit rounding,
+ * but in calls of few rows for fp16 in place of bf16: a weight times its value's scale
+ * is off by 2^-12 of it or 2^-32 of the row's largest such product, and elements of a
+ * query below 2^-32 of its largest one lose bits. The joining order of a sequence's parts
+ * is fixed by the lengths: the same call gives the same bits. Which kernel a call takes
+ * goes by T, R, the heads and the cache's type: in another batch a sequence's last bits
+ * may be others. Workspace: fm_attn_paged_workspace_bytes (on the current device),
  * rewritten by every call: calls that may overlap need one each.
  * ------------------------------------------------------------------------- */
 size_t fm_attn_paged_workspace_bytes(const fm_kv_cache* cache, const fm_paged_batch* batch, int32_t T, int32_t H_q);

@@ -28,10 +28,10 @@
 // e4m3 caches: e4m3 is exact in fp16, one conversion for two values, so the
 // products run in fp16 on the stored values and the rows' power-of-two scales
 // stay outside: a key's on its score, a value's in its weight, 2^(score +
-// exponent - mo) with a running maximum mo of its own, so that the weight of
-// the largest summand is near 1 whatever the rows' scales are. One fp16 term
-// (2^-12 of a weight; weights below 2^-14 of the largest are off by 2^-25 of it
-// at most) is finer than bf16's 2^-9. Measured at 32 ragged sequences of up to 16384
+// exponent - mo) with a running maximum of its own less 7 as mo, so that the weight
+// of the largest summand lies near the top of fp16's range (2^7 to 2^15) whatever the
+// rows' scales are. One fp16 term (2^-12 of a weight; weights below 2^-21 of the
+// largest are off by 2^-32 of it at most) is finer than bf16's 2^-9. Measured at 32 ragged sequences of up to 16384
 // keys, 32 / 8 heads, d = 128 (bytes alone 99 us): 112 us; 261 with the values widened
 // to bf16 by integer operations, whose instructions bounded it.
 #include <algorithm>
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 // -------------------------------------------------------------- few query rows
 constexpr int kFewRows = 16;
 constexpr int kTileKeys = 32;
+constexpr float kTopBits = 7.f;  // e4m3: weights go up to 2^(7 + 8)
 
 constexpr int few_warps(int d, bool f8) { return d == 256 && f8 ? 8 : 4; }
 constexpr int few_ctas(int d, bool f8) { return d == 256 ? 1 : d == 64 && f8 ? 3 : 2; }
@@ -450,7 +451,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
     // unit 118 us instead of 120, d = 64 82 instead of 87; of 16 rows 130 instead of 124).
     const bool many = u.nrows > 8;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float mo[2] = {-INFINITY, -INFINITY};  // e4m3: the running maximum of score + exponent of the value's scale
+    // e4m3: the running maximum of score + exponent of the value's scale, less kTopBits
+    float mo[2] = {-INFINITY, -INFINITY};
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -565,9 +567,9 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
               moved = true;
             }
           }
-          if (F8 && z > mo[i] + 8.f) {
-            f[i] = ex2_approx(mo[i] - z);
-            mo[i] = z;
+          if (F8 && z > mo[i] + kTopBits + 8.f) {
+            f[i] = ex2_approx(mo[i] + kTopBits - z);
+            mo[i] = z - kTopBits;
             moved = true;
           }
         }

@@ -125,3 +125,16 @@ def test_queries_of_zero_over_quantised_keys(scale):
     o, lse = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=scale)
     k, v = s.values()
     assert_paged(o, lse, paged(q.double(), k, v, s.q_off.tolist(), s.keys, scale, True, 0, 0), 64)
+
+
+@pytest.mark.parametrize("d, Hq", [(64, 2), (128, 32), (256, 4)])
+@pytest.mark.parametrize("keys", [30, 500])
+def test_quantised_values_of_rows_with_far_scales(d, Hq, keys):
+    # a row 2^20 times the others' size, zero in some columns: there the others' values count
+    s = Setup([keys, 20], [1, 1], 2, d, 16, True, seed=35)
+    v = s.v.clone()
+    v[3] = v[3] * 2.0 ** 20
+    v[3, :, ::3] = 0
+    s.v = v
+    fm.fm_cache_write(s.k.cuda(), s.v.cuda(), s.cache, fm.PagedBatch(s.kv_off, s.kv_len, s.table))
+    s.attend(Hq)

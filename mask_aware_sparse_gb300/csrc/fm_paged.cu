@@ -30,8 +30,8 @@
 // stay outside: a key's on its score, a value's in its weight, 2^(score +
 // exponent - mo) with a running maximum of its own less 7 as mo, so that the weight
 // of the largest summand lies near the top of fp16's range (2^7 to 2^15) whatever the
-// rows' scales are. One fp16 term (2^-12 of a weight; weights below 2^-21 of the
-// largest are off by 2^-32 of it at most) is finer than bf16's 2^-9. Measured at 32 ragged sequences of up to 16384
+// rows' scales are. One fp16 term (2^-11 of a weight; weights below 2^-21 of the
+// largest are off by 2^-32 of it at most) is finer than bf16's 2^-8. Measured at 32 ragged sequences of up to 16384
 // keys, 32 / 8 heads, d = 128 (bytes alone 99 us): 112 us; 261 with the values widened
 // to bf16 by integer operations, whose instructions bounded it.
 #include <algorithm>
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
     float sc[2] = {sl2, sl2};  // per row: scores to log2 units
     if constexpr (F8) {
       // Q in fp16, each row times the power of two that puts its largest value at
-      // the top of fp16's range: values down to 2^-29 of it keep all their bits
+      // the top of fp16's range: values down to 2^-32 of it keep all their bits
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t top = 0;

@@ -117,7 +117,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   FM_DEBUG_BEGIN();
   if (threadIdx.x == 0) {
-    *abort_flag = timeout_pending(p.err) ? 1 : 0;
     mbar_init(&bars[C::QFULL], 1);
     mbar_init(&bars[C::QFREE], 1);
     for (int i = 0; i < 2; ++i) {
@@ -154,6 +153,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   __shared__ uint16_t first[kLocalChunks + 1], order[kWholeUnits];
   grid_dependency_wait();
   grid_launch_dependents();
+  if (threadIdx.x == 0) *abort_flag = timeout_pending(p.err) ? 1 : 0;  // (the kernel before may have set it)
   // (the plans' scratch lies where the first keys will)
   if (p.s.whole) {
     plan_whole(p.s, p.q_off, p.kv_len, seq, first, order, reinterpret_cast<uint16_t*>(smem + C::K_OFF), &start, p.err);

@@ -68,7 +68,8 @@ struct ChunkCfg {
   static constexpr int ODONE = 10, OEND = 12;                        // [tile]
   static constexpr int KFULL = 14, KEMPTY = KFULL + STAGES, VFULL = KEMPTY + STAGES, VEMPTY = VFULL + STAGES;
   static constexpr int RFULL = VEMPTY + STAGES, REMPTY = RFULL + RAWS;
-  static constexpr int NBAR = REMPTY + RAWS;
+  static constexpr int MEND = REMPTY + RAWS;  // all products done
+  static constexpr int NBAR = MEND + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;
 };
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars[C::QFULL], 1);
     mbar_init(&bars[C::QFREE], 1);
+    mbar_init(&bars[C::MEND], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[C::SFULL + i], 1);
       mbar_init(&bars[C::PREADY + i], 128);
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
       const int P = p.s.page, rows = P, per = 128 >> p.s.page_log;  // P <= 128
       const int zmax = p.s.n_pages * p.s.H_kv;
       uint32_t jt = 0, seg = 0;  // key tiles, segments with keys so far
+      uint32_t asked = 0, asked_q = 0;  // tiles of keys and of values, and of queries, whose copies were started
       PageWindow pages;
       for (; walk.more() && ok; walk.next()) {
         if (walk.n == 0) continue;
@@ -386,6 +389,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
               for (int x = 0; x < C::BOXES; ++x)
                 tma_load_4d(smem + t * C::TILE + x * 16384, &tq, &bars[C::QFULL], x * 64, 0, walk.h,
                             u.tok + t * (TR / G));
+            ++asked_q;
           }
         }
         ok = __shfl_sync(kAll, ok, 0);
@@ -425,6 +429,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(fb, boxes * rows * (F8 ? D + 1 : 2 * D));
             __syncwarp();
+            ++asked;
             if (mine) {
               if constexpr (F8) {
                 tma_load_3d(at + b * rows * D, v ? &tv : &tk, fb, 0, key0 - pg0 * P, z);
@@ -437,17 +442,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           }
         }
       }
-      if (!ok && lane == 0) {
-        // leave with no copy in flight: what was handed out has landed, or a second bound passed
+      if (lane == 0) {
+        // The CTA ends with no copy in flight, however its other warps end: the last ones
+        // have landed, or a second bound passed.
         volatile int none = 0;
-        if constexpr (F8) {
-          for (uint32_t r = 2 * jt > C::RAWS ? 2 * jt - C::RAWS : 0; r < 2 * jt; ++r)
-            mbar_wait(&bars[C::RFULL + r % C::RAWS], (r / C::RAWS) & 1u, &none, p.err);
-        } else {
-          for (uint32_t r = jt > S ? jt - S : 0; r < jt; ++r) {
-            mbar_wait(&bars[C::KFULL + r % S], (r / S) & 1u, &none, p.err);
-            mbar_wait(&bars[C::VFULL + r % S], (r / S) & 1u, &none, p.err);
-          }
+        constexpr uint32_t kRing = F8 ? C::RAWS : 2 * S;
+        if (asked_q > 0) mbar_wait(&bars[C::QFULL], (asked_q - 1) & 1u, &none, p.err);
+        for (uint32_t r = asked > kRing ? asked - kRing : 0; r < asked; ++r) {
+          uint64_t* full = F8 ? &bars[C::RFULL + r % kRing] : &bars[(r & 1 ? C::VFULL : C::KFULL) + (r >> 1) % S];
+          mbar_wait(full, (r / kRing) & 1u, &none, p.err);
         }
       }
     } else if (warp == 9) {
@@ -540,6 +543,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           }
           mma_commit(&bars[C::VEMPTY + last]);
         }
+        // nor with a product in flight, which would use its memory after it
+        volatile int none = 0;
+        mma_commit(&bars[C::MEND]);
+        mbar_wait(&bars[C::MEND], 0u, &none, p.err);
       }
     }
   } else if constexpr (F8) {
@@ -570,7 +577,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           const bool wide = __any_sync(kAll, !dead && e > 134u && e < 255u);
           // 64 bytes of the row at a time: the staged tile is free for the next one as soon as
           // the last of them are in registers (its load is otherwise waited for: 2048 tokens
-          // over 32768 keys, d = 128, 1016 us instead of 934, d = 64 715 instead of 684)
+          // over 32768 keys, d = 128, 1016 us instead of 936, d = 64 715 instead of 685)
           constexpr int kPart = 4;
           uint32_t top = 0;  // the row's largest magnitudes, before its scale
 #pragma unroll

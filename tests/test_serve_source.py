@@ -39,3 +39,17 @@ def test_no_memory_of_earlier_kernels_before_the_wait(name, body):
     # the error word, tensors and plans all come through the parameter p
     for use in re.findall(r"[=(,;{!]\s*\*\s*p\.\w+|p\.[\w.]+\s*\[|\(p\.err|timeout_pending", before):
         pytest.fail(f"{name} touches {use.strip()} before it waits")
+
+
+def test_the_chunk_kernel_ends_with_nothing_in_flight():
+    # a wait that ran out elsewhere in the CTA must not let it end under its own copies or products:
+    # the last acts of the warp that starts each kind are waits for all of them, whatever `ok` says
+    body = dict(_kernels())["chunk_kernel"]
+    copies = body[body.index("uint32_t asked"):body.index("else if (warp == 9)")]
+    for started in ("++asked_q;", "++asked;"):
+        assert copies.count(started) == 1
+    end = copies[copies.rindex("if (lane == 0) {"):]
+    assert all(x in end for x in ("asked_q > 0", "C::QFULL", "C::RFULL", "C::VFULL", "C::KFULL", "r < asked"))
+    assert "ok" not in re.findall(r"\b\w+\b", end)
+    products = body[body.index("else if (warp == 9)"):]
+    assert re.search(r"mma_commit\(&bars\[C::MEND\]\);\s*mbar_wait\(&bars\[C::MEND\]", products)

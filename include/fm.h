@@ -420,8 +420,8 @@ fm_status fm_needed_chunks(const uint8_t* tile_class, int32_t B, int32_t nQ, int
  *     (a, b) -> rot_scale * (a cos theta - b sin theta, a sin theta + b cos theta)
  *   pairs are elements (i, i + rot / 2), or (2i, 2i + 1) when interleaved != 0;
  *   elements from rot on pass through. v rows are copied.
- * Computed in fp32 (theta exact modulo a turn for any int32 position), each
- * output rounded to bf16 once.
+ * Computed in fp32 (theta modulo a turn within |pos| 2^-64 turns of the exact one,
+ * before its own rounding to fp32), each output rounded to bf16 once.
  *
  * Tensors are bf16 views (B, H, N, d) of any element strides sb, sh, sn that are
  * multiples of 8, the d elements of a row contiguous, addresses 16-byte aligned:
@@ -430,7 +430,7 @@ fm_status fm_needed_chunks(const uint8_t* tile_class, int32_t B, int32_t nQ, int
  * view); apart from that no tensors overlap. d is 64, 128 or 256; rot a multiple
  * of 16, 0 <= rot <= d (0: no rotation; pos and inv_freq are then not read). pos:
  * int32, entry b * pos_sb + n (pos_sb 0: one row for every batch entry); inv_freq:
- * rot / 2 finite fp32 values. q_weight / k_weight: d values each, fp32 when
+ * rot / 2 fp32 values of magnitude below 2^32. q_weight / k_weight: d values each, fp32 when
  * w_f32 != 0 else bf16; NULL: that side is not normed. v and vo both NULL: no values.
  *
  * Backward: dqo, dko, dvo are the gradients of the outputs; dq, dk, dv and the

@@ -19,8 +19,8 @@
 // the rotation in registers, one 16-byte store per chunk.
 //
 // Angles: f_i / 2 pi is turned once per block into a 64-bit fraction of a turn;
-// pos times it, modulo 2^64, is the exact fraction of theta (error below
-// |pos| 2^-65 turns, against |pos| 2^-24 for an fp32 product), which
+// pos times it, modulo 2^64, is the fraction of theta (error below |pos| 2^-64
+// turns for |f_i| < 2^32, against |pos| f_i 2^-25 for an fp32 product), which
 // sincospif takes. A block computes the angles of its tokens once, in shared
 // memory, for all heads.
 #include <cmath>
@@ -152,13 +152,25 @@ __device__ __forceinline__ float weight_at(const void* w, int f32, int i) {
   return f32 ? static_cast<const float*>(w)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
 
-// The block's frequencies as fractions of a turn (in units of 2^-64).
+// x / (2 pi) modulo 1, in units of 2^-64: x = m 2^k times 1 / (2 pi) to 128 bits, for
+// |x| < 2^32 within one unit (below 2^24 half of one).
+__device__ __forceinline__ unsigned long long turn_fraction(float x) {
+  constexpr unsigned long long hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;  // 1 / (2 pi)
+  const uint32_t u = __float_as_uint(x);
+  const int e = (int)(u >> 23) & 255, k = (e ? e : 1) - 150;
+  const unsigned long long m = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const unsigned __int128 p = (unsigned __int128)m * hi + __umul64hi(m, lo);  // m / (2 pi)
+  unsigned long long t = 0;
+  if (k > 0)
+    t = k < 64 ? (unsigned long long)p << k | m * lo >> (64 - k) : 0;
+  else if (k > -128)
+    t = (unsigned long long)(k ? (p + ((unsigned __int128)1 << (-k - 1))) >> -k : p);
+  return u >> 31 ? 0 - t : t;
+}
+
+// The block's frequencies as fractions of a turn.
 __device__ __forceinline__ void load_fractions(const QkParams& p, unsigned long long* frac) {
-  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
-    double t = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    t -= floor(t);
-    frac[i] = (t < 1.0) ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;  // t < 1: below 2^64
-  }
+  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) frac[i] = turn_fraction(p.inv_freq[i]);
 }
 
 // cos and sin (times rot_scale) of the block's TB tokens from tok0 on. Slot

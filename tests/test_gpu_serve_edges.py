@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import mask_aware_sparse_gb300 as fm
-from serve_ref import assert_paged, paged
+from serve_ref import BF16_HALF, assert_paged, paged
 from test_gpu_paged import Setup
 
 pytestmark = pytest.mark.gpu
@@ -138,3 +138,38 @@ def test_quantised_values_of_rows_with_far_scales(d, Hq, keys):
     s.v = v
     fm.fm_cache_write(s.k.cuda(), s.v.cuda(), s.cache, fm.PagedBatch(s.kv_off, s.kv_len, s.table))
     s.attend(Hq)
+
+
+def _two_pi(bits):
+    """2 pi * 2^bits by Machin's formula, in whole numbers."""
+    def arctan(n):  # arctan(1 / n)
+        t = s = (1 << bits + 32) // n
+        k = 1
+        while t:
+            t, k = t // (n * n), k + 2
+            s += t // k if k % 4 == 1 else -(t // k)
+        return s
+    return 8 * (4 * arctan(5) - arctan(239)) >> 32
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_angles_at_far_positions_of_any_frequency(inter):
+    # theta = pos * f exactly, modulo a turn: neither the product nor 1 / (2 pi) has enough of 64 bits
+    f = torch.tensor([1.0, 0.7, 50.0, 1000.0, 1e6, 4e9, 1e-6, -1.0, -0.3, -1e5, 2.0 ** -40, 0.0, 1e-42, 16777217.0,
+                      2.0 ** 24, 3.0], dtype=torch.float32)
+    pos = torch.tensor([0, 1, -1, 12345, 2 ** 24 + 1, 2 ** 31 - 1, -(2 ** 31), 999999937], dtype=torch.int32)
+    turn = _two_pi(200)
+    theta = torch.empty(len(pos), len(f), dtype=torch.float64)
+    for i, p in enumerate(pos.tolist()):
+        for j, x in enumerate(f.tolist()):
+            num, den = x.as_integer_ratio()
+            theta[i, j] = ((p * num << 200) // den % turn) / (1 << 200)
+    c, s = torch.cos(theta), torch.sin(theta)
+    q = torch.ones(1, 1, len(pos), 64, dtype=torch.bfloat16).cuda()
+    out = fm.fm_qk_norm_rope(q, q.clone(), positions=pos.cuda(), inv_freq=f.cuda(), interleaved=inter)[0]
+    got = out[0, 0].double().cpu()
+    a, b = (got[:, 0:32:2], got[:, 1:32:2]) if inter else (got[:, :16], got[:, 16:32])
+    for x, want in ((a, c - s), (b, c + s)):
+        # theta's rounding to fp32 (2^-24 of half a turn), cos and sin (2^-22), one bf16 rounding
+        assert bool(((x - want).abs() <= BF16_HALF * want.abs() * 1.01 + 2.0 ** -20).all())
+    assert (got[:, 32:] == 1).all()

@@ -1194,6 +1194,24 @@ class QKNormRope:
     eps: float = 1e-6
 
 
+class _FirstOnly(torch.autograd.Function):
+    """n gradients, and the tensors that they depend on: passes the gradients on, so
+    that a gradient of theirs raises instead of missing the library calls' part.
+    (once_differentiable goes by the incoming gradients alone.)"""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(None if t is None else t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("flashmask_attention has no second derivatives: its gradients cannot be differentiated")
+
+
+def _first_only(grads, *depends_on):
+    return _FirstOnly.apply(len(grads), *grads, *depends_on) if torch.is_grad_enabled() else grads
+
+
 class _QKNormRopeFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, wq, wk, positions, inv_freq, interleaved, rot_scale, eps):
@@ -1207,6 +1225,7 @@ class _QKNormRopeFn(torch.autograd.Function):
         q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
         grads = fm_qk_norm_rope_bwd(dqo.contiguous(), dko.contiguous(), dvo.contiguous(), q, k, positions=positions,
                                     inv_freq=inv_freq, q_weight=wq, k_weight=wk, **ctx.how)
+        grads = _first_only(grads, dqo, dko, dvo, q, k, wq, wk)
         return (*grads, None, None, None, None, None)
 
 
@@ -1225,12 +1244,14 @@ class _FlashMaskFn(torch.autograd.Function):
         q, k, v, o, lse, lts, lte, uts, ute = ctx.saved_tensors
         dq, dk, dv = fm_attn_bwd(q, k, v, o, lse, do.contiguous(), lts, lte, uts, ute, ctx.queues, scale=ctx.scale,
                                  causal=ctx.causal)
+        dq, dk, dv = _first_only((dq, dk, dv), do, q, k, v)
         return dq, dk, dv, None, None, None, None, None, None
 
 
 def flashmask_attention(q, k, v, lts, lte, uts, ute, *, causal: bool, scale: float | None = None,
                         qk: QKNormRope | None = None):
-    """Masked SDPA with the FlashMask column-wise mask; differentiable in q, k, v.
+    """Masked SDPA with the FlashMask column-wise mask; differentiable in q, k, v, once
+    (a gradient of its gradients is refused).
 
     qk: norm and rotate the queries and keys first (fm_qk_norm_rope, in one pass
     that also lays q, k, v out): q, k, v may then be strided views, e.g. of a fused

@@ -208,3 +208,29 @@ def test_binding_checks_before_any_library_call(lib):
         fm.fm_qk_norm_rope_bwd(q, k, k, q, k, positions=pos, inv_freq=f)
     with pytest.raises(ValueError, match="shape"):
         fm.fm_qk_norm_rope_bwd(k, k, k, q, k, positions=pos, inv_freq=f)
+
+
+def test_second_derivatives_are_refused(monkeypatch):
+    # the library's calls stand for themselves here: what matters is that a gradient's own
+    # gradient raises, where it used to leave the calls' part out
+    x = torch.randn(3, 1, 2, 4, 64, dtype=torch.float64)
+    monkeypatch.setattr(fm, "fm_qk_norm_rope", lambda q, k, v, **kw: (2 * q, 3 * k, v.clone()))
+    monkeypatch.setattr(fm, "fm_qk_norm_rope_bwd", lambda a, b, c, q, k, **kw: (2 * a * q, 3 * b, c, None, None))
+    monkeypatch.setattr(fm, "attn_tiling", lambda: (128, 128))
+    monkeypatch.setattr(fm, "fm_classify_tiles", lambda *a, **kw: None)
+    monkeypatch.setattr(fm, "fm_attn_fwd", lambda q, k, v, *a, **kw: (q * k * v, None))
+    monkeypatch.setattr(fm, "fm_attn_bwd", lambda q, k, v, o, lse, do, *a, **kw: (do * k * v, do * q * v, do * q * k))
+    for spec in (None, fm.QKNormRope()):
+        for of in (lambda o: o.sum(), lambda o: (o * o).sum()):
+            q, k, v = (t.clone().requires_grad_() for t in x)
+            o = fm.flashmask_attention(q, k, v, None, None, None, None, causal=True, qk=spec)
+            first = torch.autograd.grad(of(o), (q, k, v), create_graph=True)
+            assert all(g.abs().sum() > 0 for g in first)
+            for again in (lambda: torch.autograd.grad(sum(g.sum() for g in first), (q, k, v)),
+                          lambda: (of(o) + sum((g * g).sum() for g in first)).backward()):
+                with pytest.raises(RuntimeError, match="second derivatives"):
+                    again()
+            # the gradients by themselves are as without create_graph
+            o = fm.flashmask_attention(q, k, v, None, None, None, None, causal=True, qk=spec)
+            for a, b in zip(first, torch.autograd.grad(of(o), (q, k, v))):
+                assert torch.equal(a, b) and not b.requires_grad

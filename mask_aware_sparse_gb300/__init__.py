@@ -32,6 +32,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 from dataclasses import dataclass
 
 import numpy as np
@@ -787,6 +788,7 @@ def _fast_fn(name):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_given = threading.local()  # .stream: the running call was given one
 
 
 def _enqueue(name, dev, *args):
@@ -795,6 +797,8 @@ def _enqueue(name, dev, *args):
     if dev < 0:
         raise ValueError("the tensors must be CUDA tensors: the library computes on the GPU only")
     if dev != torch.cuda.current_device():
+        if getattr(_given, "stream", False):
+            raise ValueError("stream belongs to another device than the tensors")
         with torch.cuda.device(dev):
             return _enqueue(name, dev, *args)
     s = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
@@ -812,7 +816,11 @@ def _streamed(f):
         if stream is None:
             return f(*args, **kw)
         with torch.cuda.stream(stream):
-            return f(*args, **kw)
+            _given.stream = True
+            try:
+                return f(*args, **kw)
+            finally:
+                _given.stream = False
 
     return call
 

@@ -234,3 +234,36 @@ def test_second_derivatives_are_refused(monkeypatch):
             o = fm.flashmask_attention(q, k, v, None, None, None, None, causal=True, qk=spec)
             for a, b in zip(first, torch.autograd.grad(of(o), (q, k, v))):
                 assert torch.equal(a, b) and not b.requires_grad
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    # torch's and the library's calls stand for themselves: two devices, the first one current
+    import contextlib
+
+    at = [0]
+
+    @contextlib.contextmanager
+    def on(dev):
+        was, at[0] = at[0], dev
+        yield
+        at[0] = was
+
+    ran = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: at[0])
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(torch.cuda, "stream", on)  # a stream is its device's index here
+    monkeypatch.setattr(fm, "_raw_stream", lambda dev: 100 + dev)
+    monkeypatch.setattr(fm, "_fast_fn", lambda name: lambda *a: ran.append((at[0], a)) or fm.FM_OK)
+    call = fm._streamed(lambda dev: fm._enqueue("fm_cache_write", dev, 7))
+    call(0)
+    call(1)  # the tensors' device, its current stream
+    call(1, stream=1)
+    assert ran == [(0, (7, 100)), (1, (7, 101)), (1, (7, 101))]
+    for dev, stream in ((0, 1), (1, 0)):
+        if stream == 0:
+            at[0] = 1
+        with pytest.raises(ValueError, match="another device"):
+            call(dev, stream=stream)
+    at[0] = 0
+    call(1)  # a refused call leaves nothing behind
+    assert len(ran) == 4

@@ -66,7 +66,7 @@ fm_status fm_rope_freqs(int32_t rot, double base, int32_t kind, double factor, i
     return FM_ERR_INVALID_ARG;
   if (kind == FM_ROPE_NTK && rot == 2) return FM_ERR_INVALID_ARG;
   if (kind == FM_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
-  double first = 0, last = 0;
+  double first = 0, last = 0, slow = 0;
   if (kind == FM_ROPE_YARN) {
     if (orig_len <= 0 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast))
       return FM_ERR_INVALID_ARG;
@@ -75,14 +75,16 @@ fm_status fm_rope_freqs(int32_t rot, double base, int32_t kind, double factor, i
       return rot * std::log((double)orig_len / (turns * 2 * M_PI)) / (2 * std::log(base));
     };
     first = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
-    last = std::fmin(std::ceil(pair_of(beta_slow)), rot - 1.0);
+    slow = pair_of(beta_slow);
+    last = std::fmin(std::ceil(slow), rot - 1.0);
   }
   for (int i = 0; i < rot / 2; ++i) {
     const double f = std::pow(base, -2.0 * i / rot);
     double v = f;
     if (kind == FM_ROPE_LINEAR) v = f / factor;
     if (kind == FM_ROPE_YARN) {
-      const double ramp = std::fmin(std::fmax((i - first) / std::fmax(last - first, 1e-3), 0.0), 1.0);
+      // (where even pair 0 is slow, last <= 0 = first leaves no room for the ramp)
+      const double ramp = i > slow ? 1.0 : std::fmin(std::fmax((i - first) / std::fmax(last - first, 1e-3), 0.0), 1.0);
       v = f / factor * ramp + f * (1 - ramp);
     }
     inv_freq[i] = (float)v;

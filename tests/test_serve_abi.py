@@ -267,3 +267,14 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     at[0] = 0
     call(1)  # a refused call leaves nothing behind
     assert len(ran) == 4
+
+
+@pytest.mark.parametrize("rot, base, orig_len", [(64, 10000.0, 1), (64, 10000.0, 6), (16, 500000.0, 5),
+                                                 (64, 10000.0, 2 ** 40), (32, 1.5, 10 ** 6)])
+def test_yarn_where_all_pairs_are_slow_or_fast(lib, rot, base, orig_len):
+    # every pair turns less than once, or more than 32 times, within the trained length
+    plain = base ** (-2.0 * np.arange(rot // 2) / rot)
+    turns = orig_len * plain / (2 * math.pi)
+    assert (turns < 1).all() or (turns > 32).all()
+    f, _ = fm.fm_rope_freqs(rot, base=base, kind="yarn", factor=8.0, orig_len=orig_len)
+    np.testing.assert_allclose(f.numpy(), plain / (8.0 if turns[0] < 1 else 1.0), rtol=2 ** -23)

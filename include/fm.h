@@ -558,7 +558,7 @@ fm_status fm_cache_read(const fm_kv_cache* cache, const int32_t* kv_off, const i
  *
  * q, o: bf16 rows (T, H_q, d) of element strides st, sh (multiples of 8,
  * 16-byte aligned); lse: (T, H_q) fp32, contiguous. o overlaps no input. GQA
- * as fm_attn_fwd. scale > 0. Weights are rounded to bf16 for their product with the
+ * as fm_attn_fwd. scale > 0, at most 2^127. Weights are rounded to bf16 for their product with the
  * values (2^-8 of each; calls of few rows a sequence keep two terms, 2^-16). e4m3
  * caches give what the same values in a bf16 cache give up to that and 32-bit rounding,
  * but in calls of few rows for fp16 in place of bf16: a weight times its value's scale

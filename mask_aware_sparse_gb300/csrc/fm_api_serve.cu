@@ -181,7 +181,8 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
                         const fm_rows* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
   fm_status st = check_paged(cache, batch, T, H_q);
   if (st != FM_OK) return st;
-  if (!(scale > 0.f) || !std::isfinite(scale) || window < 0 || sinks < 0 || (!causal && (window || sinks)))
+  // (kernels take scale in log2 units)
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f) || window < 0 || sinks < 0 || (!causal && (window || sinks)))
     return FM_ERR_INVALID_ARG;
   if (T == 0) return FM_OK;
   if (!rows_ok(q) || !rows_ok(o) || !lse) return FM_ERR_INVALID_ARG;

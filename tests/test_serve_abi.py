@@ -278,3 +278,9 @@ def test_yarn_where_all_pairs_are_slow_or_fast(lib, rot, base, orig_len):
     assert (turns < 1).all() or (turns > 32).all()
     f, _ = fm.fm_rope_freqs(rot, base=base, kind="yarn", factor=8.0, orig_len=orig_len)
     np.testing.assert_allclose(f.numpy(), plain / (8.0 if turns[0] < 1 else 1.0), rtol=2 ** -23)
+
+
+@pytest.mark.parametrize("scale, want", [(2.0 ** 127, "WORKSPACE"), (2.5e38, "INVALID_ARG"), (3.4e38, "INVALID_ARG"),
+                                         (1e-45, "WORKSPACE")])
+def test_scales_that_leave_fp32_in_log2_units_refused(lib, scale, want):
+    assert lib.fm_attn_paged(_cache(), _batch(), 3, 4, ROWS, scale, 1, 0, 0, ROWS, A, 0, 0, 0) == getattr(fm, "FM_ERR_" + want)

@@ -1064,6 +1064,9 @@ def fm_cache_new(n_pages: int, H_kv: int, page_size: int, d: int, *, dtype=torch
     return KVCache(*kv, *ex)
 
 
+_MOST = 1 << 30  # counts are handed to the library as 32 bits, which keep the low ones of more
+
+
 class PagedBatch:
     """A batch of R sequences over a cache, int32 CUDA tensors: q_off (R + 1,) first new
     token of each among a call's packed tokens, kv_len (R,) keys of each (new ones
@@ -1076,6 +1079,7 @@ class PagedBatch:
         _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, "page_table must be (R, width)")
         R, width = page_table.shape
         _need(R > 0 and width > 0, "a batch needs sequences and pages")
+        _need(R <= _MOST and width <= _MOST, f"a batch has at most 2^30 sequences and pages of each, got {R} and {width}")
         _like(page_table, "page_table", (R, width), torch.int32)
         _like(q_off, "q_off", (R + 1,), torch.int32)
         _like(kv_len, "kv_len", (R,), torch.int32)
@@ -1103,6 +1107,8 @@ def fm_cache_write(k, v, cache: KVCache, batch: PagedBatch):
     dev = _serve_args(cache, batch)
     _tensor(k, "k", 3)
     shape = (k.shape[0], cache.H_kv, cache.d)
+    if shape[0] > _MOST:
+        raise ValueError(f"a call takes at most 2^30 tokens, got {shape[0]}")
     kr, vr = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
     _enqueue("fm_cache_write", dev, cache.at, batch.at, shape[0], kr, vr)
 
@@ -1120,8 +1126,8 @@ def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=
     _expect(page_table, "page_table", (R, width), _I32, dev)
     _expect(kv_off, "kv_off", (R + 1,), _I32, dev)
     shape = (1, cache.H_kv, int(n_rows), cache.d)
-    if not 0 <= shape[2] <= 1 << 30:
-        raise ValueError(f"n_rows must be in [0, 2^30], got {n_rows}")
+    if not (0 <= shape[2] <= _MOST and R <= _MOST and width <= _MOST):
+        raise ValueError(f"n_rows must be in [0, 2^30], and so must the table's sizes, got {n_rows}, {R}, {width}")
     if k is None:
         k = torch.empty(shape, dtype=_BF16, device=cache.device)
     else:
@@ -1145,6 +1151,8 @@ def _paged_bytes(dev, T, Hq, R, width, n_pages, H_kv, page, d, f8):
 
 def fm_attn_paged_workspace_bytes(cache: KVCache, batch: PagedBatch, T: int, H_q: int) -> int:
     """Bytes of workspace an fm_attn_paged call of these shapes needs."""
+    if not (0 <= T <= _MOST and 0 < H_q <= _MOST):
+        raise ValueError(f"T must be in [0, 2^30], H_q in [1, 2^30], got {T} and {H_q}")
     return _paged_bytes(_serve_args(cache, batch), T, H_q, batch.R, batch.width, cache.n_pages, cache.H_kv,
                         cache.page_size, cache.d, cache.k_exp is not None)
 
@@ -1169,6 +1177,7 @@ def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal:
         raise ValueError(f"window and sinks must not be negative, got {window} and {sinks}")
     window, sinks = min(window, 1 << 30), min(sinks, 1 << 30)  # (all positions are below)
     qr = _rows(q, "q", shape, dev)
+    wsb = fm_attn_paged_workspace_bytes(cache, batch, T, Hq)
     if o is None:
         o = torch.empty(shape, dtype=_BF16, device=cache.device)
         orow = _pack_rows(o.data_ptr(), Hq * d, d)
@@ -1178,7 +1187,6 @@ def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal:
         lse = torch.empty((T, Hq), dtype=_F32, device=cache.device)
     else:
         _expect(lse, "lse", (T, Hq), _F32, dev)
-    wsb = fm_attn_paged_workspace_bytes(cache, batch, T, Hq)
     if ws is None:
         ws = torch.empty(max(16, wsb), dtype=_U8, device=cache.device)
     elif (not isinstance(ws, torch.Tensor) or not ws.is_contiguous() or ws.dtype != _U8 or ws.numel() < wsb

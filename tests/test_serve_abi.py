@@ -284,3 +284,28 @@ def test_yarn_where_all_pairs_are_slow_or_fast(lib, rot, base, orig_len):
                                          (1e-45, "WORKSPACE")])
 def test_scales_that_leave_fp32_in_log2_units_refused(lib, scale, want):
     assert lib.fm_attn_paged(_cache(), _batch(), 3, 4, ROWS, scale, 1, 0, 0, ROWS, A, 0, 0, 0) == getattr(fm, "FM_ERR_" + want)
+
+
+def test_counts_beyond_32_bits_refused_by_the_binding(lib, monkeypatch):
+    # ctypes keeps the low 32 bits of a larger number: 2^32 + 5 tokens would be five
+    i32, big = torch.int32, 2 ** 32 + 5
+    on_meta = lambda *s, dt=i32: torch.empty(*s, dtype=dt, device="meta")  # noqa: E731
+    for R, width in ((1, big), (big, 1)):
+        with pytest.raises(ValueError, match="2\\^30"):
+            fm.PagedBatch(on_meta(R + 1), on_meta(R), on_meta(R, width))
+    # handles as they are after their checks, without a GPU
+    cache, batch = object.__new__(fm.KVCache), object.__new__(fm.PagedBatch)
+    for name, x in dict(index=-1, H_kv=1, d=64, n_pages=1, page_size=16, k_exp=None, at=0, device="cpu").items():
+        setattr(cache, name, x)
+    for name, x in dict(index=-1, R=1, width=1, at=0).items():
+        setattr(batch, name, x)
+    rows = torch.zeros(1, 1, 64, dtype=torch.bfloat16).expand(big, 1, 64)
+    monkeypatch.setattr(fm, "_enqueue", lambda *a: pytest.fail("reached the library"))
+    monkeypatch.setattr(fm, "_paged_bytes", lambda *a: pytest.fail("reached the library"))
+    with pytest.raises(ValueError, match="2\\^30"):
+        fm.fm_cache_write(rows, rows, cache, batch)
+    with pytest.raises(ValueError, match="2\\^30"):
+        fm.fm_attn_paged(rows, cache, batch, scale=0.1)
+    for T, H in ((big, 1), (-1, 1), (1, big), (1, 0)):
+        with pytest.raises(ValueError, match="2\\^30"):
+            fm.fm_attn_paged_workspace_bytes(cache, batch, T, H)

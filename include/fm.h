@@ -421,7 +421,8 @@ fm_status fm_needed_chunks(const uint8_t* tile_class, int32_t B, int32_t nQ, int
  *   pairs are elements (i, i + rot / 2), or (2i, 2i + 1) when interleaved != 0;
  *   elements from rot on pass through. v rows are copied.
  * Computed in fp32 (theta modulo a turn within |pos| 2^-64 turns of the exact one,
- * before its own rounding to fp32), each output rounded to bf16 once.
+ * before its own rounding to fp32; a normed row's mean square has to lie in fp32's
+ * range), each output rounded to bf16 once.
  *
  * Tensors are bf16 views (B, H, N, d) of any element strides sb, sh, sn that are
  * multiples of 8, the d elements of a row contiguous, addresses 16-byte aligned:

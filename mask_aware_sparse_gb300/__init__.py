@@ -907,6 +907,7 @@ def fm_rope_freqs(rot: int, *, base: float = 10000.0, kind: str = "plain", facto
     the factor of its cos and sin. kind: "plain", or for contexts `factor` times
     longer than the trained ones "linear", "ntk" or "yarn" (orig_len: the trained length)."""
     _need(kind in _ROPE_KINDS, f"kind must be one of {sorted(_ROPE_KINDS)}, got {kind!r}")
+    _need(int(rot) <= _MOST and int(orig_len) <= 1 << 62, f"rot={rot} or orig_len={orig_len} is too large")
     f = np.empty(max(1, int(rot) // 2), dtype=np.float32)
     sc = ctypes.c_float()
     _check(lib().fm_rope_freqs(int(rot), float(base), _ROPE_KINDS[kind], float(factor), int(orig_len),

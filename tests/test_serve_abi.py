@@ -309,3 +309,9 @@ def test_counts_beyond_32_bits_refused_by_the_binding(lib, monkeypatch):
     for T, H in ((big, 1), (-1, 1), (1, big), (1, 0)):
         with pytest.raises(ValueError, match="2\\^30"):
             fm.fm_attn_paged_workspace_bytes(cache, batch, T, H)
+
+
+@pytest.mark.parametrize("how", [dict(rot=2 ** 32 + 64), dict(rot=64, kind="yarn", factor=2.0, orig_len=2 ** 64 + 4096)])
+def test_rotations_beyond_the_librarys_integers_refused(lib, how):
+    with pytest.raises(ValueError, match="too large"):
+        fm.fm_rope_freqs(**how)

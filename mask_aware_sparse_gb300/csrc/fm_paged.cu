@@ -189,8 +189,8 @@ struct FewCfg {
   static constexpr int EXP = F8 ? kTileKeys : 0;
   // Warps, CTAs an SM and entries of a warp's ring: what fills shared memory with
   // loads in flight. e4m3 rows are short for the work on each, so more warps help
-  // where registers allow: d = 64 three CTAs (step of 32 sequences 87 us, with two
-  // 98), d = 256 eight warps (292 us, with four 406).
+  // where registers allow: d = 64 three CTAs (step of 32 sequences 77 us, with two
+  // 91), d = 256 eight warps (271 us, with four 355).
   static constexpr int WARPS = few_warps(D, F8), THREADS = 32 * WARPS;
   static constexpr int PER_SM = few_ctas(D, F8);
   static constexpr int RING = D == 256 ? 3 : D == 64 ? (F8 ? 8 : 6) : (F8 ? 6 : 3);
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
         // 2^-up: on the sums (below 2^33) ahead of a key's scale, so that no score passes
         // fp32's range on the way to one inside it, what is above 2^80 after it. In
-        // shared memory until the segment's end (d = 256: 272 us, in registers 295).
+        // shared memory until the segment's end (d = 128 112 us, d = 256 271; in registers 116, 293).
         const int back = min(-up, 80);
         if (t == 0) ml[warp * kFewRows + g + 8 * i].x = __uint_as_float((uint32_t)(127 + back) << 23);
         sc[i] = fminf(sl2 * __uint_as_float((uint32_t)(127 - up - back) << 23), FLT_MAX);
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
       }
     }
     // Some thread has a second row (half the softmax otherwise: e4m3 steps of 4 rows a
-    // unit 118 us instead of 120, d = 64 82 instead of 87; of 16 rows 130 instead of 124).
+    // unit 112 us instead of 119, d = 64 77 instead of 83; of 16 rows 124 instead of 122).
     const bool many = u.nrows > 8;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     // e4m3: the running maximum of score + exponent of the value's scale, less kTopBits

@@ -1218,7 +1218,8 @@ class _FirstOnly(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, n, *tensors):
-        return tuple(None if t is None else t.view_as(t) for t in tensors[:n])
+        ctx.mark_dirty(*(t for t in tensors[:n] if t is not None))  # the same tensors, no views of them
+        return tensors[:n]
 
     @staticmethod
     def backward(ctx, *grads):

@@ -230,7 +230,8 @@ def test_second_derivatives_are_refused(monkeypatch):
                           lambda: (of(o) + sum((g * g).sum() for g in first)).backward()):
                 with pytest.raises(RuntimeError, match="second derivatives"):
                     again()
-            # the gradients by themselves are as without create_graph
+            # the gradients by themselves are as without create_graph: tensors of their own, no views
+            assert not any(g._is_view() for g in first)
             o = fm.flashmask_attention(q, k, v, None, None, None, None, causal=True, qk=spec)
             for a, b in zip(first, torch.autograd.grad(of(o), (q, k, v))):
                 assert torch.equal(a, b) and not b.requires_grad

@@ -97,10 +97,11 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, float s) {
 }
 
 // The block's tokens' places, by its first warp, and by the others whether the batch is
-// one at all: offsets that do not ascend from 0 or pass T, lengths outside the table
-// (8192 tokens of 4 sequences 8.5 -> 8.7 us, of 4096 sequences 10.3 -> 11.9).
+// one at all: offsets that do not ascend from 0 or pass T, lengths outside the table.
 // False (flagged once): nothing is written, as tokens would be taken for those of other
-// places.
+// places. Every block reads all of them, which a few thousand sequences hardly notice
+// (8192 tokens of 4 sequences 8.5 -> 8.6 us, of 4096 10.4 -> 11.9; 65536 tokens of as
+// many sequences 91 -> 257).
 template <bool READ>
 __device__ __forceinline__ bool look_up(const CacheParams& p, int64_t* slot, int t0, int TB) {
   grid_dependency_wait();
@@ -281,7 +282,7 @@ cudaError_t launch(const CacheParams& p, int d, bool f8, cudaStream_t s) {
   // Tokens of a block: as many as fill its threads' loads once, if that leaves two
   // blocks an SM; then more of them (fewer look-ups) while that leaves more than fill
   // an SM. Writing 1000 / 8192 / 12000 tokens of 8 heads, d = 128: 3.2 / 8.5 / 11.2 us
-  // (3.4 / 8.7 / - with the batch looked at); with one step less 3.4 / 8.7 / 13.8 (fewer,
+  // (before the batch was looked at, 0.1 us); with one step less 3.4 / 8.7 / 13.8 (fewer,
   // larger blocks) or 4.6 / 8.9 / 11.3 us.
   const int tr = READ ? d * (f8 ? 1 : 2) / 16 : d / 16, full = kThreads / tr * (READ ? kReadAhead : kWriteAhead);
   int log = 0;

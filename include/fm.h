@@ -499,10 +499,10 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  * Tokens from q_off[R] on belong to no sequence: what their rows hold has no effect,
  * and nothing is written for them. Values that no such batch has (a page outside
  * [0, n_pages), a length outside [0, width * page_size], offsets that do not ascend
- * from 0 or pass T) set FM_DEVERR_RANGE. fm_cache_write then writes nothing if an
- * offset or a length is one of them, and leaves out the tokens whose page is; what
- * rows of O, LSE and fm_cache_read such a batch receives is undefined. Nothing
- * outside the tensors is touched.
+ * from 0 or pass T, those of fm_cache_read n_rows) set FM_DEVERR_RANGE. The cache
+ * calls then write nothing if an offset or a length is one of them, and leave out
+ * the tokens whose page is; what rows of O and LSE such a batch receives is
+ * undefined. Nothing outside the tensors is touched.
  *
  * fm_cache_write puts the new tokens' rows k, v (element strides st a token, sh
  * a head, multiples of 8) in their places, rounded to e4m3 with the smallest

@@ -1118,7 +1118,8 @@ def fm_cache_write(k, v, cache: KVCache, batch: PagedBatch):
 def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=None):
     """Keys and values as packed bf16 rows (1, H_kv, n_rows, d): sequence r's keys from 0
     on become rows [kv_off[r], kv_off[r + 1]). kv_off (R + 1,) and page_table (R, width)
-    int32. Rows that no sequence has are left as they were (undefined in new tensors)."""
+    int32, kv_off[R] at most n_rows. Rows that no sequence has are left as they were
+    (undefined in new tensors)."""
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
     dev = cache.index

@@ -516,6 +516,22 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  * from 0, sequence r's keys 0 .. kv_off[r + 1] - kv_off[r] - 1 become rows
  * [kv_off[r], kv_off[r + 1]) of k, v, contiguous (H_kv, n_rows, d): the packed
  * documents that fm_attn_fwd takes. Rows from kv_off[R] on are left as they were.
+ *
+ * fm_cache_append is fm_qk_norm_rope and fm_cache_write in one pass: q (T, H_q, d) and
+ * k, v (T, H_kv, d) bf16 rows of a projection's output (views of any strides); queries and
+ * keys normed and rotated as p says (B = 1, N = T, H_kv and d the cache's; pos (T), or NULL:
+ * a token's position in its sequence, kv_len - n + a; pos_sb is not used), queries to qo
+ * (q itself is allowed; it overlaps nothing else), keys and values to their places in the
+ * cache, with no tensor of theirs in between. Queries, values and the keys of a bf16 cache
+ * have the bits of the two calls; keys of an e4m3 cache are rounded once, from 32 bits.
+ * What no batch has is handled as by fm_cache_write (no row of qo is written either); the
+ * queries of a token without a page are written.
+ *
+ * fm_cache_copy makes page dst[i] a copy of page src[i], keys, values and exponents, for
+ * i < n (device int32): a sequence that forks gets its own copy of a page it will write
+ * to. A pair of two -1 copies nothing; any other page outside [0, n_pages) sets
+ * FM_DEVERR_RANGE and its pair is left out. A page that is copied to may be in no other
+ * pair (its contents are undefined if it is).
  * ------------------------------------------------------------------------- */
 typedef struct fm_rows {
   void* ptr;
@@ -541,6 +557,9 @@ fm_status fm_cache_write(const fm_kv_cache* cache, const fm_paged_batch* batch, 
                          const fm_rows* v, void* stream);
 fm_status fm_cache_read(const fm_kv_cache* cache, const int32_t* kv_off, const int32_t* page_table, int32_t R,
                         int32_t width, int32_t n_rows, void* k, void* v, void* stream);
+fm_status fm_cache_append(const fm_kv_cache* cache, const fm_paged_batch* batch, const fm_qk_problem* p,
+                          const fm_rows* q, const fm_rows* k, const fm_rows* v, const fm_rows* qo, void* stream);
+fm_status fm_cache_copy(const fm_kv_cache* cache, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Attention of new tokens over the paged cache (their own keys and values
@@ -574,6 +593,37 @@ size_t fm_attn_paged_workspace_bytes(const fm_kv_cache* cache, const fm_paged_ba
 fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, int32_t T, int32_t H_q,
                         const fm_rows* q, float scale, int32_t causal, int32_t window, int32_t sinks,
                         const fm_rows* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The same attention where groups of the batch's sequences share their first keys
+ * (responses to one prompt, questions behind one system prompt): keys that a group
+ * shares are read once for all of its new tokens.
+ *
+ * Sequences [seq_off[g], seq_off[g + 1]) hold the same first prefix_len[g] keys:
+ * seq_off (S + 1) ascending from 0 to R, prefix_len (S), device int32; prefix_len[g] is
+ * at most kv_len - n of each of them that has new tokens (n of them). The whole pages
+ * below it, prefix_len[g] / page_size rounded down, are the same pages in their rows of
+ * the page table; the call reads them by the row of one of them that has new tokens (or
+ * by each one's own). What is left of the prefix each sequence holds in a page of its
+ * own (fm_cache_copy). A group may be one sequence, or none (its length does not matter);
+ * prefix_len 0 shares nothing.
+ * O and LSE are fm_attn_paged's without a window, up to the rounding of weights named
+ * there and 32-bit rounding. Offsets and lengths that no such batch has set
+ * FM_DEVERR_RANGE, if the call is one that shares (more sequences than groups, fewer than
+ * 128 query rows of a KV head a sequence on average); the rows of O and LSE are then
+ * undefined. Workspace: fm_attn_shared_workspace_bytes.
+ * ------------------------------------------------------------------------- */
+typedef struct fm_shared_prefix {
+  const int32_t* seq_off;
+  const int32_t* prefix_len;
+  int32_t S;
+} fm_shared_prefix;
+
+size_t fm_attn_shared_workspace_bytes(const fm_kv_cache* cache, const fm_paged_batch* batch,
+                                      const fm_shared_prefix* shared, int32_t T, int32_t H_q);
+fm_status fm_attn_shared(const fm_kv_cache* cache, const fm_paged_batch* batch, const fm_shared_prefix* shared,
+                         int32_t T, int32_t H_q, const fm_rows* q, float scale, int32_t causal, const fm_rows* o,
+                         float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Device error word. Synchronizes `stream`, returns the accumulated FM_DEVERR_*

@@ -17,9 +17,11 @@ Functions carry the names of the C entry points:
   K / V exchange plan for context parallelism);
   fm_rope_freqs, fm_qk_norm_rope, fm_qk_norm_rope_bwd (per-head norm and rotation of
   queries and keys), fm_cache_write, fm_cache_read, fm_attn_paged (the paged key /
-  value cache and the attention of new tokens over it);
-plus KVCache, PagedBatch and fm_cache_new (a cache and a batch, checked once and
-kept by a serving program), QKNormRope (the norm and rotation of a
+  value cache and the attention of new tokens over it), fm_cache_append (norm, rotation
+  and the cache's write in one pass), fm_cache_copy, fm_attn_shared (the attention where
+  groups of sequences share their first keys);
+plus KVCache, PagedBatch, SharedPrefix and fm_cache_new (a cache, a batch and its groups,
+checked once and kept by a serving program), QKNormRope (the norm and rotation of a
 flashmask_attention call), fm_classify_tiles_heads (fm_classify_tiles over the B * H_q rows of
 per-head vectors), fm_attn_multi_interval and fm_attn_per_head (the library
 calls of a multi-interval / per-head forward and backward in sequence) and
@@ -89,6 +91,10 @@ class fm_paged_batch(ctypes.Structure):
                 ("R", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
+class fm_shared_prefix(ctypes.Structure):
+    _fields_ = [("seq_off", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("S", ctypes.c_int32)]
+
+
 class FMError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} (status {status})")
@@ -99,7 +105,7 @@ _lib = None
 
 _P = ctypes.c_void_p
 _VIEW, _ROWS = ctypes.POINTER(fm_view), ctypes.POINTER(fm_rows)
-_CACHE, _BATCH = ctypes.POINTER(fm_kv_cache), ctypes.POINTER(fm_paged_batch)
+_CACHE, _BATCH, _SHARED = (ctypes.POINTER(t) for t in (fm_kv_cache, fm_paged_batch, fm_shared_prefix))
 _SIGS = {
     "fm_rope_freqs": (ctypes.c_int, [ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_int64,
                                      ctypes.c_double, ctypes.c_double, _P, ctypes.POINTER(ctypes.c_float)]),
@@ -113,6 +119,11 @@ _SIGS = {
     "fm_attn_paged": (ctypes.c_int, [_CACHE, _BATCH, ctypes.c_int32, ctypes.c_int32, _ROWS, ctypes.c_float,
                                      ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _ROWS, _P, _P, ctypes.c_size_t,
                                      _P]),
+    "fm_cache_append": (ctypes.c_int, [_CACHE, _BATCH, ctypes.POINTER(fm_qk_problem)] + [_ROWS] * 4 + [_P]),
+    "fm_cache_copy": (ctypes.c_int, [_CACHE, _P, _P, ctypes.c_int32, _P]),
+    "fm_attn_shared_workspace_bytes": (ctypes.c_size_t, [_CACHE, _BATCH, _SHARED, ctypes.c_int32, ctypes.c_int32]),
+    "fm_attn_shared": (ctypes.c_int, [_CACHE, _BATCH, _SHARED, ctypes.c_int32, ctypes.c_int32, _ROWS, ctypes.c_float,
+                                      ctypes.c_int32, _ROWS, _P, _P, ctypes.c_size_t, _P]),
     "fm_abi_version": (ctypes.c_int32, []),
     "fm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fm_attn_tiling": (ctypes.c_int, [ctypes.POINTER(fm_tiling)]),
@@ -915,24 +926,9 @@ def fm_rope_freqs(rot: int, *, base: float = 10000.0, kind: str = "plain", facto
     return torch.from_numpy(f).to("cpu" if device is None else device), sc.value
 
 
-def _qk_args(q, k, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps):
-    """The packed problem of a norm-and-rotation call, its shapes, dtypes and devices checked."""
-    _tensor(q, "q", 4)
-    _tensor(k, "k", 4)
-    B, Hq, N, d = q.shape
-    Hkv, dev = k.shape[1], q.get_device()
-    if k.shape != (B, Hkv, N, d):
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected (B={B}, H_kv, N={N}, d={d})")
-    rot = pos = sb = fr = f32 = 0
-    if inv_freq is not None:
-        _tensor(inv_freq, "inv_freq", 1)
-        _expect(inv_freq, "inv_freq", inv_freq.shape, _F32, dev)
-        if not isinstance(positions, torch.Tensor) or positions.shape not in ((N,), (B, N)):
-            raise ValueError(f"positions must be an int32 tensor of shape (N={N},) or (B={B}, N={N})")
-        _expect(positions, "positions", positions.shape, _I32, dev)
-        rot, pos, fr = 2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr()
-        sb = N if positions.dim() == 2 else 0
-    w = [0, 0]
+def _norm_weights(q_weight, k_weight, d, dev):
+    """Addresses of the norms' weights (0: no norm), and whether they are fp32."""
+    w, f32 = [0, 0], 0
     for i, t in enumerate((q_weight, k_weight)):
         if t is not None:
             name = "k_weight" if i else "q_weight"
@@ -942,6 +938,27 @@ def _qk_args(q, k, positions, inv_freq, interleaved, rot_scale, q_weight, k_weig
             w[i], f32 = t.data_ptr(), 1 if t.dtype == _F32 else 0
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise ValueError("q_weight and k_weight must have one dtype")
+    return w, f32
+
+
+def _qk_args(q, k, positions, inv_freq, interleaved, rot_scale, q_weight, k_weight, eps):
+    """The packed problem of a norm-and-rotation call, its shapes, dtypes and devices checked."""
+    _tensor(q, "q", 4)
+    _tensor(k, "k", 4)
+    B, Hq, N, d = q.shape
+    Hkv, dev = k.shape[1], q.get_device()
+    if k.shape != (B, Hkv, N, d):
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected (B={B}, H_kv, N={N}, d={d})")
+    rot = pos = sb = fr = 0
+    if inv_freq is not None:
+        _tensor(inv_freq, "inv_freq", 1)
+        _expect(inv_freq, "inv_freq", inv_freq.shape, _F32, dev)
+        if not isinstance(positions, torch.Tensor) or positions.shape not in ((N,), (B, N)):
+            raise ValueError(f"positions must be an int32 tensor of shape (N={N},) or (B={B}, N={N})")
+        _expect(positions, "positions", positions.shape, _I32, dev)
+        rot, pos, fr = 2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr()
+        sb = N if positions.dim() == 2 else 0
+    w, f32 = _norm_weights(q_weight, k_weight, d, dev)
     return _pack_qk(B, N, Hq, Hkv, d, rot, 1 if interleaved else 0, f32, eps, rot_scale, pos, sb, fr, *w), dev
 
 
@@ -1143,6 +1160,63 @@ def fm_cache_read(cache: KVCache, kv_off, page_table, n_rows: int, *, k=None, v=
     return k, v
 
 
+@_streamed
+def fm_cache_append(q, k, v, cache: KVCache, batch: PagedBatch, *, positions=None, inv_freq=None,
+                    interleaved: bool = False, rot_scale: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    out=None):
+    """fm_qk_norm_rope and fm_cache_write in one pass: T new tokens' q (T, H_q, d) and
+    k, v (T, H_kv, d), bf16 views of any strides (rows contiguous), e.g. of a fused
+    projection's output; keys and values go to their places in the cache, the queries
+    to q' (T, H_q, d), or to `out` (a view; q itself is allowed). positions: int32 (T,),
+    None: each token's position in its sequence; inv_freq: fp32 (rot / 2,), None: no
+    rotation; q_weight / k_weight: (d,), None: no norm. Rows of tokens past q_off[R] are
+    left as they were (undefined in a new tensor)."""
+    dev = _serve_args(cache, batch)
+    _tensor(q, "q", 3)
+    T, Hq, d = shape = q.shape
+    if d != cache.d:
+        raise ValueError(f"q has d={d}, the cache d={cache.d}")
+    if T > _MOST:
+        raise ValueError(f"a call takes at most 2^30 tokens, got {T}")
+    if not 0 < Hq <= 1 << 20:
+        raise ValueError(f"H_q must be in [1, 2^20], got {Hq}")
+    rot = pos = fr = 0
+    if inv_freq is not None:
+        _tensor(inv_freq, "inv_freq", 1)
+        _expect(inv_freq, "inv_freq", inv_freq.shape, _F32, dev)
+        rot, fr = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+    if positions is not None:
+        _expect(positions, "positions", (T,), _I32, dev)
+        pos = positions.data_ptr()
+    w, f32 = _norm_weights(q_weight, k_weight, d, dev)
+    p = _pack_qk(1, T, Hq, cache.H_kv, d, rot, 1 if interleaved else 0, f32, eps, rot_scale, pos, 0, fr, *w)
+    kv = (T, cache.H_kv, d)
+    qr, kr, vr = _rows(q, "q", shape, dev), _rows(k, "k", kv, dev), _rows(v, "v", kv, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=cache.device)
+        orow = _pack_rows(out.data_ptr(), Hq * d, d)
+    else:
+        orow = _rows(out, "out", shape, dev, True)
+    _enqueue("fm_cache_append", dev, cache.at, batch.at, p, qr, kr, vr, orow)
+    return out
+
+
+@_streamed
+def fm_cache_copy(cache: KVCache, src, dst):
+    """Make page dst[i] a copy of page src[i] (int32 CUDA (n,); a pair of two -1 copies
+    nothing). A page that is copied to may be in no other pair."""
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    dev = cache.index
+    _tensor(src, "src", 1)
+    n = src.shape[0]
+    if n > _MOST:
+        raise ValueError(f"a call copies at most 2^30 pages, got {n}")
+    _expect(src, "src", (n,), _I32, dev)
+    _expect(dst, "dst", (n,), _I32, dev)
+    _enqueue("fm_cache_copy", dev, cache.at, src.data_ptr(), dst.data_ptr(), n)
+
+
 @functools.lru_cache(maxsize=1024)
 def _paged_bytes(dev, T, Hq, R, width, n_pages, H_kv, page, d, f8):
     """Workspace of an attention call (it goes by sizes alone; the addresses only have to be set)."""
@@ -1196,6 +1270,83 @@ def fm_attn_paged(q, cache: KVCache, batch: PagedBatch, *, scale: float, causal:
         raise ValueError(f"ws must be a contiguous uint8 tensor of at least {wsb} bytes on the cache's device")
     _enqueue("fm_attn_paged", dev, cache.at, batch.at, T, Hq, qr, scale, 1 if causal else 0, window, sinks,
              orow, lse.data_ptr(), ws.data_ptr(), wsb)
+    return o, lse
+
+
+class SharedPrefix:
+    """Groups of a batch's sequences that share their first keys, int32 CUDA tensors:
+    sequences [seq_off[g], seq_off[g + 1]) hold the same first prefix_len[g] keys, the
+    whole pages of them as the same pages. seq_off (S + 1,) ascends from 0 to R. Checked
+    once; the tensors' values may change between calls (their addresses may not)."""
+
+    __slots__ = ("seq_off", "prefix_len", "S", "index", "c", "at")
+
+    def __init__(self, seq_off, prefix_len):
+        _need(isinstance(prefix_len, torch.Tensor) and prefix_len.dim() == 1, "prefix_len must be (S,)")
+        S = prefix_len.shape[0]
+        _need(0 < S <= _MOST, f"there must be 1 to 2^30 groups, got {S}")
+        _like(prefix_len, "prefix_len", (S,), torch.int32)
+        _like(seq_off, "seq_off", (S + 1,), torch.int32)
+        _same_cuda(seq_off=seq_off, prefix_len=prefix_len)
+        self.seq_off, self.prefix_len, self.S, self.index = seq_off, prefix_len, S, seq_off.get_device()
+        self.c = fm_shared_prefix(seq_off.data_ptr(), prefix_len.data_ptr(), S)
+        self.at = ctypes.addressof(self.c)
+
+
+@functools.lru_cache(maxsize=1024)
+def _shared_bytes(dev, T, Hq, R, width, S, n_pages, H_kv, page, d, f8):
+    c = fm_kv_cache(16, 16, 16 if f8 else 0, 16 if f8 else 0, n_pages, H_kv, page, d)
+    with torch.cuda.device(dev):
+        return lib().fm_attn_shared_workspace_bytes(c, fm_paged_batch(16, 16, 16, R, width),
+                                                    fm_shared_prefix(16, 16, S), T, Hq)
+
+
+def fm_attn_shared_workspace_bytes(cache: KVCache, batch: PagedBatch, shared: SharedPrefix, T: int, H_q: int) -> int:
+    """Bytes of workspace an fm_attn_shared call of these shapes needs."""
+    if not (0 <= T <= _MOST and 0 < H_q <= _MOST):
+        raise ValueError(f"T must be in [0, 2^30], H_q in [1, 2^30], got {T} and {H_q}")
+    dev = _serve_args(cache, batch)
+    if not isinstance(shared, SharedPrefix):
+        raise ValueError("shared must be a SharedPrefix")
+    if shared.index != dev:
+        raise ValueError("the groups are on another device than the cache")
+    return _shared_bytes(dev, T, H_q, batch.R, batch.width, shared.S, cache.n_pages, cache.H_kv, cache.page_size,
+                         cache.d, cache.k_exp is not None)
+
+
+@_streamed
+def fm_attn_shared(q, cache: KVCache, batch: PagedBatch, shared: SharedPrefix, *, scale: float, causal: bool = True,
+                   o=None, lse=None, ws=None):
+    """fm_attn_paged of a batch whose sequences share prefixes, as `shared` says: each
+    group's shared keys are read once for all of its new tokens. (O bf16 (T, H_q, d),
+    LSE fp32 (T, H_q)). Rows of tokens past q_off[R] are left as they were (undefined in
+    new tensors). ws: a uint8 workspace of fm_attn_shared_workspace_bytes, one for each
+    call that may run at once."""
+    dev = _serve_args(cache, batch)
+    _tensor(q, "q", 3)
+    T, Hq, d = shape = q.shape
+    if d != cache.d:
+        raise ValueError(f"q has d={d}, the cache d={cache.d}")
+    if Hq <= 0 or Hq % cache.H_kv:
+        raise ValueError(f"H_q={Hq} must be a multiple of H_kv={cache.H_kv}")
+    qr = _rows(q, "q", shape, dev)
+    wsb = fm_attn_shared_workspace_bytes(cache, batch, shared, T, Hq)
+    if o is None:
+        o = torch.empty(shape, dtype=_BF16, device=cache.device)
+        orow = _pack_rows(o.data_ptr(), Hq * d, d)
+    else:
+        orow = _rows(o, "o", shape, dev, True)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=_F32, device=cache.device)
+    else:
+        _expect(lse, "lse", (T, Hq), _F32, dev)
+    if ws is None:
+        ws = torch.empty(max(16, wsb), dtype=_U8, device=cache.device)
+    elif (not isinstance(ws, torch.Tensor) or not ws.is_contiguous() or ws.dtype != _U8 or ws.numel() < wsb
+          or ws.get_device() != dev):
+        raise ValueError(f"ws must be a contiguous uint8 tensor of at least {wsb} bytes on the cache's device")
+    _enqueue("fm_attn_shared", dev, cache.at, batch.at, shared.at, T, Hq, qr, scale, 1 if causal else 0, orow,
+             lse.data_ptr(), ws.data_ptr(), wsb)
     return o, lse
 
 

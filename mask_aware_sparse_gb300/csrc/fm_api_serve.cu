@@ -161,6 +161,38 @@ fm_status fm_cache_read(const fm_kv_cache* cache, const int32_t* kv_off, const i
                                      static_cast<cudaStream_t>(stream), err));
 }
 
+fm_status fm_cache_append(const fm_kv_cache* cache, const fm_paged_batch* batch, const fm_qk_problem* p,
+                          const fm_rows* q, const fm_rows* k, const fm_rows* v, const fm_rows* qo, void* stream) {
+  fm_status st = check_cache(cache);
+  if (st == FM_OK && !p) st = FM_ERR_INVALID_ARG;
+  if (st == FM_OK) st = check_batch(cache, batch, p->N);
+  if (st != FM_OK) return st;
+  bool empty = false;
+  fm_qk_problem x = *p;
+  if (!x.pos) x.pos = batch->q_off;  // (checked as given: the places in the cache stand in for them)
+  st = check_qk(&x, &empty);
+  if (st != FM_OK) return st;
+  if (p->B != 1 || p->H_kv != cache->H_kv || p->d != cache->d) return FM_ERR_INVALID_ARG;
+  if (p->H_q > (1 << 20)) return FM_ERR_UNSUPPORTED;  // rows of a block's tokens are counted in 32 bits
+  if (empty) return FM_OK;
+  if (!rows_ok(q) || !rows_ok(k) || !rows_ok(v) || !rows_ok(qo)) return FM_ERR_INVALID_ARG;
+  int* err = device_error_word();
+  if (!err) return FM_ERR_CUDA;
+  return from_cuda(launch_cache_append(*cache, *batch, *p, *q, *k, *v, *qo, static_cast<cudaStream_t>(stream), err));
+}
+
+fm_status fm_cache_copy(const fm_kv_cache* cache, const int32_t* src, const int32_t* dst, int32_t n, void* stream) {
+  fm_status st = check_cache(cache);
+  if (st != FM_OK) return st;
+  if (n < 0) return FM_ERR_INVALID_ARG;
+  if (n > (1 << 30)) return FM_ERR_UNSUPPORTED;
+  if (n == 0) return FM_OK;
+  if (!src || !dst) return FM_ERR_INVALID_ARG;
+  int* err = device_error_word();
+  if (!err) return FM_ERR_CUDA;
+  return from_cuda(launch_cache_copy(*cache, src, dst, n, static_cast<cudaStream_t>(stream), err));
+}
+
 // Shapes of an attention call over the cache; its pointers are checked apart.
 static fm_status check_paged(const fm_kv_cache* c, const fm_paged_batch* b, int32_t T, int32_t H_q) {
   fm_status st = check_cache(c);
@@ -191,6 +223,36 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
   if (!err) return FM_ERR_CUDA;
   return from_cuda(launch_paged(*cache, *batch, T, H_q, *q, *o, lse, scale, causal ? 1 : 0, window, sinks, ws,
                                 static_cast<cudaStream_t>(stream), err));
+}
+
+static fm_status check_shared(const fm_kv_cache* c, const fm_paged_batch* b, const fm_shared_prefix* x, int32_t T,
+                              int32_t H_q) {
+  const fm_status st = check_paged(c, b, T, H_q);
+  if (st != FM_OK) return st;
+  if (!x || x->S <= 0 || !x->seq_off || !x->prefix_len) return FM_ERR_INVALID_ARG;
+  if ((int64_t)T * H_q + b->R + x->S > (1 << 30)) return FM_ERR_UNSUPPORTED;
+  return FM_OK;
+}
+
+size_t fm_attn_shared_workspace_bytes(const fm_kv_cache* cache, const fm_paged_batch* batch,
+                                      const fm_shared_prefix* shared, int32_t T, int32_t H_q) {
+  if (check_shared(cache, batch, shared, T, H_q) != FM_OK || T == 0) return 0;
+  return shared_ws_bytes(*cache, *batch, shared->S, T, H_q);
+}
+
+fm_status fm_attn_shared(const fm_kv_cache* cache, const fm_paged_batch* batch, const fm_shared_prefix* shared,
+                         int32_t T, int32_t H_q, const fm_rows* q, float scale, int32_t causal, const fm_rows* o,
+                         float* lse, void* ws, size_t ws_bytes, void* stream) {
+  fm_status st = check_shared(cache, batch, shared, T, H_q);
+  if (st != FM_OK) return st;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return FM_ERR_INVALID_ARG;
+  if (T == 0) return FM_OK;
+  if (!rows_ok(q) || !rows_ok(o) || !lse) return FM_ERR_INVALID_ARG;
+  if (!ws || !aligned16(ws) || ws_bytes < shared_ws_bytes(*cache, *batch, shared->S, T, H_q)) return FM_ERR_WORKSPACE;
+  int* err = device_error_word();
+  if (!err) return FM_ERR_CUDA;
+  return from_cuda(launch_shared(*cache, *batch, *shared, T, H_q, *q, *o, lse, scale, causal ? 1 : 0, ws,
+                                 static_cast<cudaStream_t>(stream), err));
 }
 
 }  // extern "C"

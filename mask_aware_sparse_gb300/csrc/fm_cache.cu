@@ -13,6 +13,9 @@
 //
 // What bounds both kernels: memory, each row read once and written once, 16
 // bytes a load; a block looks its tokens' pages up once for all heads.
+//
+// Pages are copied to pages as they are (copy_kernel): a sequence that forks takes
+// copies of the pages it will write, beams change places.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include "dependent.cuh"
@@ -277,6 +280,58 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p, con
   }
 }
 
+// A page's keys lie together, so do its values and its exponents: pieces of 16 KB, and
+// both exponents as one, dealt to blocks in turn. Memory bounds it: 4096 pages of 64
+// e4m3 rows of 8 heads, d = 128. A pair outside the cache is flagged and left out.
+struct CopyParams {
+  char* c[2];
+  uint8_t* e[2];
+  const int32_t* src;
+  const int32_t* dst;
+  int n, n_pages;
+  int64_t bytes, exps;  // of a page's keys, of their exponents (0: a bf16 cache)
+  int* err;
+};
+
+constexpr int kPiece = kThreads * 16 * 4;
+
+__global__ void __launch_bounds__(kThreads) copy_kernel(const CopyParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int each = (int)((p.bytes + kPiece - 1) / kPiece), all = 2 * each + (p.exps ? 1 : 0);  // pieces of a page
+  for (int64_t i = blockIdx.x; i < (int64_t)p.n * all; i += gridDim.x) {
+    const int64_t pair = i / all;
+    const int piece = (int)(i - pair * all), which = piece >= each ? 1 : 0;
+    const int from = p.src[pair], to = p.dst[pair];
+    if (from == -1 && to == -1) continue;
+    if (from < 0 || to < 0 || from >= p.n_pages || to >= p.n_pages) {
+      if (piece == 0 && threadIdx.x == 0) record_error(p.err, FM_DEV_ERR_RANGE);
+      continue;
+    }
+    if (piece == 2 * each) {
+      for (int64_t x = 16 * threadIdx.x; x < 2 * p.exps; x += 16 * kThreads) {
+        uint8_t* e = x < p.exps ? p.e[0] : p.e[1];
+        const int64_t at = x < p.exps ? x : x - p.exps;
+        *reinterpret_cast<uint4*>(e + to * p.exps + at) = *reinterpret_cast<const uint4*>(e + from * p.exps + at);
+      }
+      continue;
+    }
+    char* c = which ? p.c[1] : p.c[0];
+    const int64_t x0 = (int64_t)(piece - which * each) * kPiece + 16 * threadIdx.x;
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t x = x0 + k * 16 * kThreads;
+      if (x < p.bytes) v[k] = *reinterpret_cast<const uint4*>(c + from * p.bytes + x);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t x = x0 + k * 16 * kThreads;
+      if (x < p.bytes) *reinterpret_cast<uint4*>(c + to * p.bytes + x) = v[k];
+    }
+  }
+}
+
 template <bool READ>
 cudaError_t launch(const CacheParams& p, int d, bool f8, cudaStream_t s) {
   // Tokens of a block: as many as fill its threads' loads once, if that leaves two
@@ -336,6 +391,27 @@ cudaError_t launch_cache_write(const fm_kv_cache& c, const fm_paged_batch& b, in
   p.width = b.width;
   p.T = T;
   return launch<false>(p, c.d, c.k_exp != nullptr, s);
+}
+
+cudaError_t launch_cache_copy(const fm_kv_cache& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s,
+                              int* err) {
+  CopyParams p = {};
+  p.c[0] = static_cast<char*>(c.k);
+  p.c[1] = static_cast<char*>(c.v);
+  p.e[0] = c.k_exp;
+  p.e[1] = c.v_exp;
+  p.src = src;
+  p.dst = dst;
+  p.n = n;
+  p.n_pages = c.n_pages;
+  const int64_t rows = (int64_t)c.H_kv * c.page_size;
+  p.bytes = rows * c.d * (c.k_exp ? 1 : 2);
+  p.exps = c.k_exp ? rows : 0;
+  p.err = err;
+  const int64_t pieces = (int64_t)n * (2 * ((p.bytes + kPiece - 1) / kPiece) + (p.exps ? 1 : 0));
+  const int64_t most = 8ll * sm_count();
+  count_launches(1);
+  return launch_dependent(copy_kernel, dim3((unsigned)(pieces < most ? pieces : most)), kThreads, 0, s, p);
 }
 
 cudaError_t launch_cache_read(const fm_kv_cache& c, const int32_t* kv_off, const int32_t* table, int R, int width,

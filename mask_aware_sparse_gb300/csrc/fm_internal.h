@@ -139,6 +139,19 @@ cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, i
                          const fm_rows& o, float* lse, float scale, int causal, int window, int sinks, void* ws,
                          cudaStream_t st, int* err);
 
+// The same where groups of sequences share their first keys (fm_paged.cu).
+size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q);
+cudaError_t launch_shared(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q,
+                          const fm_rows& q, const fm_rows& o, float* lse, float scale, int causal, void* ws,
+                          cudaStream_t st, int* err);
+
+// New tokens' queries normed and rotated, their keys and values into the cache (fm_append.cu).
+cudaError_t launch_cache_append(const fm_kv_cache& c, const fm_paged_batch& b, const fm_qk_problem& P, const fm_rows& q,
+                                const fm_rows& k, const fm_rows& v, const fm_rows& qo, cudaStream_t s, int* err);
+// Pages copied to pages (fm_cache.cu).
+cudaError_t launch_cache_copy(const fm_kv_cache& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t s,
+                              int* err);
+
 constexpr int kTile = 128;  // attention tile (block_m = block_n)
 
 // Key / value rows of a problem (N_kv = 0 stands for N_kv = N).

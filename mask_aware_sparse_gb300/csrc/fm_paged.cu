@@ -54,8 +54,7 @@ constexpr float kLn2F = 0.69314718055994530942f;
 // ------------------------------------------------------------------ the plan
 struct PlanParams {
   PagedShape s;
-  const int32_t* q_off;
-  const int32_t* kv_len;
+  PagedLists in;
   PagedWork w;
   int* err;
 };
@@ -86,6 +85,7 @@ __device__ __forceinline__ V block_scan(V v, V* warp_sums) {  // inclusive
   return v;
 }
 
+template <bool SH>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   __shared__ long long sums[32];
   __shared__ long long carry;
@@ -94,22 +94,38 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   grid_dependency_wait();
   grid_launch_dependents();
   bool bad = false;
+  // sequence r of the plan
+  auto sequence = [&](int r, int4& q, int2& more) -> bool {
+    if constexpr (SH) {
+      const int vs = prefixes(s);
+      int s0, s1, P;
+      if (r < vs) return prefix_at(s, p.in, r, q, more, s0);
+      const int g = last_at(p.in.seq_off, s.S, r - vs);
+      const bool off = group_at(s, p.in, g, s0, s1, P);
+      return rest_at(s, p.in, r - vs, P, p.in.prefix_len[g], q, more) || off;
+    } else {
+      const bool off = sequence_at(s, p.in.q_off, p.in.kv_len, r, q.x, q.y, q.z);
+      q.w = (int)(((long long)q.y * s.G + s.step - 1) / s.step);
+      return off;
+    }
+  };
   // units of each sequence
   if (tid == 0) {
     carry = 0;
     p.w.first[0] = 0;
   }
   __syncthreads();
-  for (int r0 = 0; r0 < s.R; r0 += kPlanThreads) {
+  for (int r0 = 0; r0 < s.V; r0 += kPlanThreads) {
     const int r = r0 + tid;
     long long n = 0;
-    if (r < s.R) {
-      int a, k, L;
-      bad |= sequence_at(s, p.q_off, p.kv_len, r, a, k, L);
-      n = ((long long)k * s.G + s.step - 1) / s.step;
+    if (r < s.V) {
+      int4 q;
+      int2 more;
+      bad |= sequence(r, q, more);
+      n = q.w;
     }
     const long long in = block_scan(n, sums) + carry;
-    if (r < s.R) p.w.first[r + 1] = (int)min(in, s.max_units);
+    if (r < s.V) p.w.first[r + 1] = (int)min(in, s.max_units);
     __syncthreads();
     if (tid == kPlanThreads - 1) carry = in;
     __syncthreads();
@@ -124,19 +140,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     const int u = u0 + tid;
     long long work = 0;
     if (u < units) {
-      int lo = 0, hi = s.R - 1;  // last r with first[r] <= u
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.w.first[mid] <= u)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      int a, n, L;
-      sequence_at(s, p.q_off, p.kv_len, lo, a, n, L);
-      const PagedUnit q = unit_at(s, lo, a, n, L, u - p.w.first[lo]);
-      p.w.units[u] = q;
-      work = (long long)max(q.ntiles, 1) * s.H_kv;
+      const int r = last_at(p.w.first, s.V, u);
+      int4 q;
+      int2 more;
+      sequence(r, q, more);
+      PagedUnit unit;
+      if constexpr (SH)
+        unit = shared_unit_at(s, r, q, more, u - p.w.first[r]);
+      else
+        unit = unit_at(s, r, q.x, q.y, q.z, u - p.w.first[r]);
+      p.w.units[u] = unit;
+      work = (long long)max(unit.ntiles, 1) * s.H_kv;
     }
     const long long in = block_scan(work, sums) + carry;
     if (u < units) p.w.sum[u] = in - work;
@@ -216,8 +230,8 @@ struct FewParams {
   PagedOut out;
   const char* kv[2];
   const uint8_t* exps[2];
-  const int32_t* q_off;
-  const int32_t* kv_len;
+  PagedLists in;
+  SharedOut sh;
   const int32_t* table;
   float scale_log2;
   int* err;
@@ -282,7 +296,7 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "r"(addr));
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool SH>
 __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM) few_kernel(const FewParams p) {
   using C = FewCfg<D, F8>;
   extern __shared__ uint8_t smem_raw[];
@@ -291,20 +305,21 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ PagedStart start;
   __shared__ int4 seq[kLocalSeqs];
-  __shared__ uint16_t first[kLocalSeqs + 1], order[kWholeUnits];
+  __shared__ int2 more[SH ? kLocalSeqs : 1];
+  __shared__ uint16_t first[SH ? 1 : kLocalSeqs + 1], order[SH ? 1 : kWholeUnits];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (p.s.whole) {
-    plan_whole(p.s, p.q_off, p.kv_len, seq, first, order, reinterpret_cast<uint16_t*>(smem), &start, p.err);
+  if (!SH && p.s.whole) {
+    plan_whole(p.s, p.in, seq, first, order, reinterpret_cast<uint16_t*>(smem), &start, p.err);
   } else if (p.s.local) {
-    plan_locally(p.s, p.q_off, p.kv_len, seq, reinterpret_cast<unsigned*>(smem), &start, p.err);
-    if (threadIdx.x == 0) p.w.starts[blockIdx.x] = start;  // for join_kernel
+    plan_locally<SH>(p.s, p.in, seq, more, reinterpret_cast<unsigned*>(smem), &start, p.err);
+    if (!SH && threadIdx.x == 0) p.w.starts[blockIdx.x] = start;  // for join_kernel
   } else {
     if (threadIdx.x == 0) start = p.w.starts[blockIdx.x];
     __syncthreads();
   }
   const int G = p.s.G, P = p.s.page;
-  PagedWalk walk(p.s, p.w.units, seq, first, order, start);
+  PagedWalk<SH> walk(p.s, p.w.units, seq, more, first, order, start);
   const int g = lane >> 2, t = lane & 3;
   const float sl2 = p.scale_log2;
   const uint32_t ring = smem_u32(smem) + warp * C::RING * C::TILE;
@@ -335,7 +350,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
   auto issue = [&](int e, int slot) {
     const PagedUnit& u = walk.u;
     if (e < 2 * nt) {
-      const int key0 = tile_of(u, walk.kt + j0 + (e >> 1)) * kTileKeys;
+      const int key0 = key_of<SH, kTileKeys>(u, walk.kt + j0 + (e >> 1));
       const int which = e & 1;
       if (which == 0) {
         const int pg0 = key0 >> p.s.page_log, per = P < kTileKeys ? 2 : 1;
@@ -380,13 +395,13 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
     }
     copy_commit();
   };
-  if (walk.more()) {
+  if (walk.going()) {
     begin();
 #pragma unroll 1
     for (int e = 0; e < C::AHEAD; ++e) issue(e, e);
   }
 
-  while (walk.more()) {
+  while (walk.going()) {
     const PagedUnit& u = walk.u;
 #pragma unroll 1
     for (int e = C::AHEAD; e < C::RING; ++e) issue(e, e);
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
 
     int slot = 0;  // of the next entry
     for (int j = 0; j < nt; ++j) {
-      const int key0 = tile_of(u, walk.kt + j0 + j) * kTileKeys;
+      const int key0 = key_of<SH, kTileKeys>(u, walk.kt + j0 + j);
       const int sk = slot, sv = slot + 1 == C::RING ? 0 : slot + 1;
       slot = sv + 1 == C::RING ? 0 : sv + 1;
       copy_wait<C::RING - 1>();
@@ -652,8 +667,10 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
     // row r lies at c ^ 8 (r % 4): four rows start 8 banks apart.
     const int tok0 = u.tok, g0 = u.g0, nrows = u.nrows, h = walk.h, part_slot = walk.slot();
     const bool whole = walk.whole();
+    const uint32_t mark = SH ? shared_mark(whole, walk.kt, start) : 0u;
+    const int kind = u.ns;  // (SH)
     walk.next();
-    if (walk.more()) {
+    if (walk.going()) {
       begin();
 #pragma unroll 1
       for (int e = 0; e < C::AHEAD; ++e) issue(e, e);
@@ -699,11 +716,13 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
           sum += ex2_approx(v.x - base) * v.y;
           w[k] = ex2_approx(v.z - base);
         }
-        const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        const float inv = SH || !whole ? 1.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
         const int64_t tok = tok0 + x / G;
         const int head = h * G + x % G;
         char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
         float* part = p.w.part + p.w.part_floats * (2 * (size_t)blockIdx.x + part_slot);
+        const long long at = SH ? kind * p.sh.rows + tok * p.out.H_q + head : 0;
+        float* to = SH && whole ? p.sh.full + at * D : part + (size_t)row * D;
 #pragma unroll
         for (int c = 0; c < D / (4 * TPR); ++c) {
           const int col = 4 * (c0 + TPR * c);
@@ -718,14 +737,18 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
             a.z += w[k] * v.z;
             a.w += w[k] * v.w;
           }
-          if (whole)
+          if (!SH && whole)
             *reinterpret_cast<uint2*>(dst + 2 * col) =
                 make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
           else
-            *reinterpret_cast<float4*>(part + (size_t)row * D + col) = a;
+            *reinterpret_cast<float4*>(to + col) = a;
         }
         if (c0 == 0) {
-          if (whole) {
+          if constexpr (SH) {
+            *(whole ? p.sh.full_ml + at : reinterpret_cast<float2*>(part + (size_t)kFewRows * D) + row) =
+                make_float2(top, sum);
+            if (mark) p.sh.where[at] = whole ? mark : mark | (uint32_t)row;
+          } else if (whole) {
             p.out.lse[tok * p.out.H_q + head] = sum == 0.f ? -INFINITY : top * kLn2F + logf(sum);
           } else {
             part[(size_t)kFewRows * D + 2 * row] = top;
@@ -744,6 +767,35 @@ struct JoinParams {
   PagedOut out;
   int G, rows;  // rows of a slot
 };
+
+// A row so far, and one more part of it.
+template <int V>
+__device__ __forceinline__ void add_part(float& t, float& s, float4 (&a)[V], const float2& ml, const float4 (&v)[V]) {
+  const float m = fmaxf(t, ml.x), base = m == -INFINITY ? 0.f : m;
+  const float f = ex2_approx(t - base), y = ex2_approx(ml.x - base);
+  t = m;
+  s = s * f + y * ml.y;
+#pragma unroll
+  for (int x = 0; x < V; ++x) {
+    a[x].x = a[x].x * f + y * v[x].x;
+    a[x].y = a[x].y * f + y * v[x].y;
+    a[x].z = a[x].z * f + y * v[x].z;
+    a[x].w = a[x].w * f + y * v[x].w;
+  }
+}
+
+// A whole row, LPR lanes on it, four columns of V places each.
+template <int LPR, int V>
+__device__ __forceinline__ void store_row(const PagedOut& out, int64_t tok, int head, int col, float top, float sum,
+                                          const float4 (&acc)[V]) {
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  char* dst = out.o + 2 * (tok * out.st + head * out.sh);
+#pragma unroll
+  for (int x = 0; x < V; ++x)
+    *reinterpret_cast<uint2*>(dst + 2 * (4 * LPR * x + col)) =
+        make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+  if (col == 0) out.lse[tok * out.H_q + head] = sum == 0.f ? -INFINITY : top * kLn2F + logf(sum);
+}
 
 // Block (c, y): where CTA c's range is the second one inside a unit and head,
 // their parts (CTA c - 1's last segment, then c .. last's first segments) are
@@ -779,20 +831,6 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 #pragma unroll
     for (int x = 0; x < V; ++x) acc[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  // a row so far and one more part of it
-  auto add = [&](float& t, float& s, float4 (&a)[V], float pt, float ps, const float4 (&pv)[V]) {
-    const float m = fmaxf(t, pt), base = m == -INFINITY ? 0.f : m;
-    const float f = ex2_approx(t - base), y = ex2_approx(pt - base);
-    t = m;
-    s = s * f + y * ps;
-#pragma unroll
-    for (int x = 0; x < V; ++x) {
-      a[x].x = a[x].x * f + y * pv[x].x;
-      a[x].y = a[x].y * f + y * pv[x].y;
-      a[x].z = a[x].z * f + y * pv[x].z;
-      a[x].w = a[x].w * f + y * pv[x].w;
-    }
-  };
   for (int i0 = PARTS * (warp % WPR); i0 < parts; i0 += PARTS * WPR) {
     float2 w[ROWS][PARTS];
     float4 v[ROWS][PARTS][V];
@@ -815,7 +853,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) add(top[r], sum[r], acc[r], w[r][k].x, w[r][k].y, v[r][k]);
+      for (int k = 0; k < PARTS; ++k) add_part(top[r], sum[r], acc[r], w[r][k], v[r][k]);
   }
   if constexpr (WPR > 1) {
 #pragma unroll
@@ -829,23 +867,15 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 #pragma unroll
       for (int x = 0; x < V; ++x) v[x] = other[((warp + k) * V + x) * 32 + lane];
       const float2 w = other_ml[(warp + k) * RPW + lane / LPR];
-      add(top[0], sum[0], acc[0], w.x, w.y, v);
+      add_part(top[0], sum[0], acc[0], w, v);
     }
   }
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     const int row = row0 + r * RPW;
     if (row >= nrows) continue;
-    const float inv = sum[r] > 0.f ? 1.f / sum[r] : (sum[r] == 0.f ? 0.f : sum[r]);
     const int x0 = st.unit.g0 + row;
-    const int64_t tok = st.unit.tok + x0 / p.G;
-    const int head = st.h * p.G + x0 % p.G;
-    char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
-#pragma unroll
-    for (int x = 0; x < V; ++x)
-      *reinterpret_cast<uint2*>(dst + 2 * (4 * LPR * x + col)) = make_uint2(
-          pack_bf16x2(acc[r][x].x * inv, acc[r][x].y * inv), pack_bf16x2(acc[r][x].z * inv, acc[r][x].w * inv));
-    if (col == 0) p.out.lse[tok * p.out.H_q + head] = sum[r] == 0.f ? -INFINITY : top[r] * kLn2F + logf(sum[r]);
+    store_row<LPR>(p.out, st.unit.tok + x0 / p.G, st.h * p.G + x0 % p.G, col, top[r], sum[r], acc[r]);
   }
 }
 
@@ -868,19 +898,134 @@ cudaError_t launch_join(const PagedShape& s, const PagedWork& w, const PagedOut&
   return go(join_kernel<D, 1, 1>, 8 * RPW);
 }
 
-template <int D, bool F8>
-cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const fm_paged_batch& b,
-                       const fm_rows& q, const PagedOut& out, float scale, cudaStream_t st, int* err) {
+// Rows of sequences that share a prefix: each row's parts over the prefix, then those over
+// the rest, WPR warps a row. Latency bounds it (where the parts are, then the parts);
+// eight parts are in flight.
+struct MergeParams {
+  PagedOut out;
+  SharedOut sh;
+  const float* part[2];  // of each kind: slots, floats of one, rows of one, CTAs
+  size_t part_floats[2];
+  int slot_rows[2], ctas[2];
+  const int32_t* q_off;
+  int R, T;
+};
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) merge_kernel(const MergeParams p) {
+  constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
+  constexpr int PARTS = 8;
+  __shared__ float4 other[WPR > 1 ? 8 * 32 * V : 1];
+  __shared__ float2 other_ml[WPR > 1 ? 8 * RPW : 1];
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 4 * (lane % LPR);
+  const long long i = ((long long)blockIdx.x * (8 / WPR) + warp / WPR) * RPW + lane / LPR;
+  // tokens of no sequence keep their rows
+  const bool live = i < p.sh.rows && i < (long long)min(max(p.q_off[p.R], 0), p.T) * p.out.H_q;
+  int first[2] = {0, 0}, row[2] = {0, 0}, n[2] = {0, 0};
+  if (live) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w = p.sh.where[k * p.sh.rows + i];
+      if (w == 0xffffffffu) {
+        first[k] = -1;
+        n[k] = 1;
+      } else {
+        first[k] = (int)(w >> 20);
+        n[k] = (int)(w >> 8 & 0xfffu);
+        row[k] = (int)(w & 0xffu);
+        // (what a batch that is none left there)
+        if (first[k] + n[k] > p.ctas[k] || row[k] >= p.slot_rows[k]) n[k] = 0;
+      }
+    }
+  }
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[V];
+#pragma unroll
+  for (int x = 0; x < V; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int parts = n[0] + n[1];
+  for (int i0 = PARTS * (warp % WPR); i0 < parts; i0 += PARTS * WPR) {
+    float2 w[PARTS];
+    float4 v[PARTS][V];
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+      w[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int x = 0; x < V; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + k < parts) {
+        const bool rest = i0 + k >= n[0];
+        const int j = rest ? i0 + k - n[0] : i0 + k, f = rest ? first[1] : first[0], r = rest ? row[1] : row[0];
+        const float *from, *ml;
+        if (f < 0) {
+          const long long at = rest ? p.sh.rows + i : i;
+          from = p.sh.full + at * D;
+          ml = reinterpret_cast<const float*>(p.sh.full_ml + at);
+        } else {  // slot 1 of the first CTA, slot 0 of the others
+          const float* s = (rest ? p.part[1] : p.part[0]) +
+                           (rest ? p.part_floats[1] : p.part_floats[0]) * (2 * (size_t)(f + j) + (j == 0 ? 1 : 0));
+          from = s + (size_t)r * D;
+          ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * r;
+        }
+        w[k] = *reinterpret_cast<const float2*>(ml);
+#pragma unroll
+        for (int x = 0; x < V; ++x) v[k][x] = *reinterpret_cast<const float4*>(from + 4 * LPR * x + col);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) add_part(top, sum, acc, w[k], v[k]);
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int x = 0; x < V; ++x) other[(warp * V + x) * 32 + lane] = acc[x];
+    if (col == 0) other_ml[warp * RPW + lane / LPR] = make_float2(top, sum);
+    __syncthreads();
+    if (warp % WPR) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      float4 v[V];
+#pragma unroll
+      for (int x = 0; x < V; ++x) v[x] = other[((warp + k) * V + x) * 32 + lane];
+      add_part(top, sum, acc, other_ml[(warp + k) * RPW + lane / LPR], v);
+    }
+  }
+  if (live) store_row<LPR>(p.out, i / p.out.H_q, (int)(i % p.out.H_q), col, top, sum, acc);
+}
+
+template <int D, bool F8, bool SH>
+cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const PagedLists& in,
+                       const int32_t* table, const fm_rows& q, const PagedOut& out, const SharedOut& sh, float scale,
+                       cudaStream_t st, int* err) {
   using C = FewCfg<D, F8>;
   static_assert(C::SMEM <= 232448 && C::PER_SM * (C::SMEM + 1024) <= 233472, "few_kernel: shared memory of an SM");
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(few_kernel<D, F8>), C::SMEM, ready);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(few_kernel<D, F8, SH>), C::SMEM, ready);
   if (e != cudaSuccess) return e;
   FewParams p{s, w, static_cast<const char*>(q.ptr), q.st, q.sh, out,
-              {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, b.q_off, b.kv_len,
-              b.page_table, scale * 1.4426950408889634f, err};
+              {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, in, sh, table,
+              scale * 1.4426950408889634f, err};
   count_launches(1);
-  return launch_dependent(few_kernel<D, F8>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, p);
+  return launch_dependent(few_kernel<D, F8, SH>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, p);
+}
+
+// The plan, where no CTA makes its own, and the attention kernel.
+template <bool SH>
+cudaError_t launch_attention(bool chunk, const PagedShape& s, const PagedWork& w, const fm_kv_cache& c,
+                             const PagedLists& in, const int32_t* table, const fm_rows& q, const PagedOut& out,
+                             const SharedOut& sh, float scale, cudaStream_t st, int* err) {
+  if (!s.local) {
+    const PlanParams pp{s, in, w, err};
+    count_launches(1);
+    const cudaError_t e = launch_dependent(plan_kernel<SH>, dim3(1), kPlanThreads, 0, st, pp);
+    if (e != cudaSuccess) return e;
+  }
+  if (chunk) return launch_paged_chunk(s, w, c, in, table, q, out, SH ? &sh : nullptr, scale, st, err);
+  auto go = [&](auto d) {
+    return c.k_exp ? launch_few<d.value, true, SH>(s, w, c, in, table, q, out, sh, scale, st, err)
+                   : launch_few<d.value, false, SH>(s, w, c, in, table, q, out, sh, scale, st, err);
+  };
+  return c.d == 64    ? go(std::integral_constant<int, 64>{})
+         : c.d == 128 ? go(std::integral_constant<int, 128>{})
+                      : go(std::integral_constant<int, 256>{});
 }
 
 // Whether units stay whole, one CTA each, or ranges of tiles may end inside them.
@@ -942,6 +1087,7 @@ PagedShape shape_of(const fm_kv_cache& c, const fm_paged_batch& b, int T, int H_
   s.extra = chunk ? (c.k_exp ? 3 : 2) : (c.k_exp ? 10 : 4);
   s.ctas = sm_count() * (chunk ? 1 : few_ctas(c.d, c.k_exp != nullptr));
   s.max_units = ((long long)T * s.G + s.step - 1) / s.step + b.R;
+  s.V = b.R;
   // Each CTA plans for itself where that is a few steps a warp; a plan kernel (one
   // CTA, about 4 us of the stream) for larger batches.
   const long long most = ((long long)b.width * s.page + s.tile - 1) / s.tile;  // tiles of a unit
@@ -970,29 +1116,142 @@ cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, i
   const PagedShape s = shape_of(c, b, T, H_q, causal, window, sinks, chunk);
   const PagedWork w = paged_work(s, rows, ws);
   const PagedOut out{static_cast<char*>(o.ptr), o.st, o.sh, lse, H_q};
-  cudaError_t e = cudaSuccess;
-  if (!s.local) {
-    const PlanParams pp{s, b.q_off, b.kv_len, w, err};
-    count_launches(1);
-    e = launch_dependent(plan_kernel, dim3(1), kPlanThreads, 0, st, pp);
-    if (e != cudaSuccess) return e;
-  }
-  const bool f8 = c.k_exp != nullptr;
-  if (chunk)
-    e = launch_paged_chunk(s, w, c, b, q, out, scale, st, err);
-  else if (c.d == 64)
-    e = f8 ? launch_few<64, true>(s, w, c, b, q, out, scale, st, err)
-           : launch_few<64, false>(s, w, c, b, q, out, scale, st, err);
-  else if (c.d == 128)
-    e = f8 ? launch_few<128, true>(s, w, c, b, q, out, scale, st, err)
-           : launch_few<128, false>(s, w, c, b, q, out, scale, st, err);
-  else
-    e = f8 ? launch_few<256, true>(s, w, c, b, q, out, scale, st, err)
-           : launch_few<256, false>(s, w, c, b, q, out, scale, st, err);
+  const PagedLists in{b.q_off, b.kv_len, nullptr, nullptr};
+  const cudaError_t e =
+      launch_attention<false>(chunk, s, w, c, in, b.page_table, q, out, SharedOut{}, scale, st, err);
   if (e != cudaSuccess || s.whole) return e;
   return c.d == 64    ? launch_join<64>(s, w, out, rows, st)
          : c.d == 128 ? launch_join<128>(s, w, out, rows, st)
                       : launch_join<256>(s, w, out, rows, st);
+}
+
+// ------------------------------------------------------------ shared prefixes
+namespace {
+
+// How a call whose sequences share prefixes runs.
+struct SharedPlan {
+  bool apart;     // as if nothing were shared
+  bool chunk[2];  // the kernel over the prefixes, and over the rest; one launch where it is the same one
+};
+
+SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q, const fm_rows* q) {
+  SharedPlan p = {};
+  const double rows = (double)T * (H_q / c.H_kv);
+  p.apart = b.R <= S || rows >= 128.0 * b.R;
+  p.chunk[1] = use_chunk(c, b, T, H_q, q);
+  fm_paged_batch groups = b;
+  groups.R = S;
+  p.chunk[0] = p.chunk[1] || (use_chunk(c, groups, T, H_q, q) && rows > 32.0 * S);
+  return p;
+}
+
+PagedShape shared_shape(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q, int causal, bool chunk,
+                        int kinds) {
+  PagedShape s = shape_of(c, b, T, H_q, causal, 0, 0, chunk);
+  const long long units = ((long long)T * s.G + s.step - 1) / s.step;  // of each kind, and one a sequence
+  const long long most = ((long long)b.width * s.page + s.tile - 1) / s.tile;
+  s.S = S;
+  s.kinds = kinds;
+  s.V = (kinds & 1 ? S : 0) + (kinds & 2 ? b.R : 0);
+  s.max_units = (kinds == 3 ? 2 : 1) * units + s.V;
+  s.whole = 0;
+  s.local = std::max(s.V, S) <= (chunk ? kLocalChunks : kLocalSeqs) && s.max_units - s.V <= kLocalUnits &&
+            s.max_units * (most + s.extra) * s.H_kv * (s.ctas + 1) < (1ll << 31);
+  return s;
+}
+
+// The workspace: full results and where the others are, then each launch's own.
+struct SharedWork {
+  SharedOut sh;
+  PagedShape s[2];
+  PagedWork w[2];
+  int launches;
+  size_t bytes;
+};
+
+SharedWork shared_work(const SharedPlan& p, const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q,
+                       int causal, void* ws) {
+  SharedWork k = {};
+  char* at = reinterpret_cast<char*>(round256(reinterpret_cast<uintptr_t>(ws)));
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    char* x = at ? at + o : nullptr;
+    o += round256(bytes);
+    return x;
+  };
+  const size_t rows = (size_t)T * H_q;
+  k.sh.rows = (long long)rows;
+  k.sh.full = reinterpret_cast<float*>(take(2 * rows * c.d * sizeof(float)));
+  k.sh.full_ml = reinterpret_cast<float2*>(take(2 * rows * sizeof(float2)));
+  k.sh.where = reinterpret_cast<uint32_t*>(take(2 * rows * sizeof(uint32_t)));
+  k.launches = p.chunk[0] == p.chunk[1] ? 1 : 2;
+  for (int i = 0; i < k.launches; ++i) {
+    k.s[i] = shared_shape(c, b, S, T, H_q, causal, p.chunk[i], k.launches == 1 ? 3 : i + 1);
+    const int slot = p.chunk[i] ? kChunkRows : kFewRows;
+    const size_t bytes = paged_work(k.s[i], slot, nullptr).bytes;
+    char* x = take(bytes);
+    k.w[i] = paged_work(k.s[i], slot, x);
+  }
+  k.bytes = o + 255;
+  return k;
+}
+
+template <int D>
+cudaError_t launch_merge(const MergeParams& m, double parts, cudaStream_t st) {
+  auto go = [&](auto kernel, int rows) {  // rows of a block
+    count_launches(1);
+    return launch_dependent(kernel, dim3((unsigned)((m.sh.rows + rows - 1) / rows)), 256, 0, st, m);
+  };
+  constexpr int RPW = D == 64 ? 2 : 1;
+  return parts > 9 ? go(merge_kernel<D, 4>, 2 * RPW) : go(merge_kernel<D, 1>, 8 * RPW);
+}
+
+}  // namespace
+
+size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q) {
+  // of every way a call of these sizes may run: it goes by the queries' strides too
+  const fm_rows broadcast{nullptr, 0, 0};
+  size_t bytes = paged_ws_bytes(c, b, T, H_q);
+  if (shared_plan(c, b, S, T, H_q, nullptr).apart) return bytes;
+  for (const fm_rows* q : {(const fm_rows*)nullptr, &broadcast})
+    bytes = std::max(bytes, shared_work(shared_plan(c, b, S, T, H_q, q), c, b, S, T, H_q, 1, nullptr).bytes);
+  return bytes;
+}
+
+cudaError_t launch_shared(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q,
+                          const fm_rows& q, const fm_rows& o, float* lse, float scale, int causal, void* ws,
+                          cudaStream_t st, int* err) {
+  const SharedPlan p = shared_plan(c, b, x.S, T, H_q, &q);
+  if (p.apart) return launch_paged(c, b, T, H_q, q, o, lse, scale, causal, 0, 0, ws, st, err);
+  const SharedWork k = shared_work(p, c, b, x.S, T, H_q, causal, ws);
+  const PagedOut out{static_cast<char*>(o.ptr), o.st, o.sh, lse, H_q};
+  const PagedLists in{b.q_off, b.kv_len, x.seq_off, x.prefix_len};
+  MergeParams m = {};
+  m.out = out;
+  m.sh = k.sh;
+  m.q_off = b.q_off;
+  m.R = b.R;
+  m.T = T;
+  double parts = 0;
+  for (int i = 0; i < k.launches; ++i) {
+    const cudaError_t e =
+        launch_attention<true>(p.chunk[i], k.s[i], k.w[i], c, in, b.page_table, q, out, k.sh, scale, st, err);
+    if (e != cudaSuccess) return e;
+  }
+  for (int kind = 0; kind < 2; ++kind) {
+    const int i = k.launches == 1 ? 0 : kind;
+    const PagedShape& s = k.s[i];
+    m.part[kind] = k.w[i].part;
+    m.part_floats[kind] = k.w[i].part_floats;
+    m.slot_rows[kind] = p.chunk[i] ? kChunkRows : kFewRows;
+    m.ctas[kind] = s.ctas;
+    // CTAs that a unit and head is divided among, about
+    const double units = std::max((double)(kind ? b.R : x.S), (double)T * s.G / s.step) * s.H_kv;
+    parts += std::min(s.ctas / units, (double)b.width * s.page / s.tile / s.least) + 1;
+  }
+  return c.d == 64    ? launch_merge<64>(m, parts, st)
+         : c.d == 128 ? launch_merge<128>(m, parts, st)
+                      : launch_merge<256>(m, parts, st);
 }
 
 }  // namespace fm

@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include "fm_internal.h"
@@ -80,8 +81,8 @@ struct ChunkParams {
   PagedOut out;
   const uint8_t* k_exp;
   const uint8_t* v_exp;
-  const int32_t* q_off;
-  const int32_t* kv_len;
+  PagedLists in;
+  SharedOut sh;
   const int32_t* table;
   int tile_rows;  // rows of a query tile: whole tokens, at most 128
   int wide;       // output rows start on 32-byte boundaries
@@ -104,7 +105,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool SH>
 __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const ChunkParams p) {
@@ -152,16 +153,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   const uint32_t tbase = *tmem_slot;
   __shared__ PagedStart start;
   __shared__ int4 seq[kLocalChunks];
-  __shared__ uint16_t first[kLocalChunks + 1], order[kWholeUnits];
+  __shared__ int2 more[SH ? kLocalChunks : 1];
+  __shared__ uint16_t first[SH ? 1 : kLocalChunks + 1], order[SH ? 1 : kWholeUnits];
   grid_dependency_wait();
   grid_launch_dependents();
   if (threadIdx.x == 0) *abort_flag = timeout_pending(p.err) ? 1 : 0;  // (the kernel before may have set it)
   // (the plans' scratch lies where the first keys will)
-  if (p.s.whole) {
-    plan_whole(p.s, p.q_off, p.kv_len, seq, first, order, reinterpret_cast<uint16_t*>(smem + C::K_OFF), &start, p.err);
+  if (!SH && p.s.whole) {
+    plan_whole(p.s, p.in, seq, first, order, reinterpret_cast<uint16_t*>(smem + C::K_OFF), &start, p.err);
   } else if (p.s.local) {
-    plan_locally(p.s, p.q_off, p.kv_len, seq, reinterpret_cast<unsigned*>(smem + C::K_OFF), &start, p.err);
-    if (threadIdx.x == 0) p.w.starts[blockIdx.x] = start;  // for join_kernel
+    plan_locally<SH>(p.s, p.in, seq, more, reinterpret_cast<unsigned*>(smem + C::K_OFF), &start, p.err);
+    if (!SH && threadIdx.x == 0) p.w.starts[blockIdx.x] = start;  // for join_kernel
   } else {
     if (threadIdx.x == 0) start = p.w.starts[blockIdx.x];
   }
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   __syncthreads();
   const int G = p.s.G, TR = p.tile_rows;
   bool ok = *abort_flag == 0;
-  PagedWalk walk(p.s, p.w.units, seq, first, order, start);
+  PagedWalk<SH> walk(p.s, p.w.units, seq, more, first, order, start);
 
   if (!ok) {
     // an unread timeout of an earlier launch: nothing is computed
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
     const float sl2 = p.scale_log2;
     uint32_t jt = 0, jh = 0, ends = 0;  // key tiles of the CTA, of this query tile, ended segments of this tile
     uint32_t nf = 0, nsf0 = 0, nsf1 = 0;  // waits done on SFULL[t], SSFULL[0, 1]
-    for (; walk.more() && ok; walk.next()) {
+    for (; walk.going() && ok; walk.next()) {
       const PagedUnit& u = walk.u;
       const int n = walk.n, T = u.nrows > TR ? 2 : 1;
       const int rr = t * TR + row;  // row of the unit
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
         continue;
       }
       for (int j = 0; j < n; ++j, ++jt, ++jh) {
-        const int key0 = tile_of(u, walk.kt + j) * 128;
+        const int key0 = key_of<SH, 128>(u, walk.kt + j);
         uint32_t buf, ph;
         uint64_t* full;
         if (T == 2) {
@@ -322,6 +324,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
       const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
       char* dst = p.out.o + 2 * (tok * p.out.st + head * p.out.sh);
       float* part = p.w.part + p.w.part_floats * (2 * (size_t)blockIdx.x + walk.slot());
+      const long long at = SH ? u.ns * p.sh.rows + tok * p.out.H_q + head : 0;
+      float* to = SH && whole ? p.sh.full + at * D : part + (size_t)rr * D;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t r[32];
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
         }
         if (!live) continue;
         const float* f = reinterpret_cast<const float*>(r);
-        if (whole) {
+        if (!SH && whole) {
           uint32_t w[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(f[2 * c] * inv, f[2 * c + 1] * inv);
@@ -350,14 +354,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
                   make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
           }
         } else {
-          float* at = part + (size_t)rr * D + c0;
 #pragma unroll
           for (int c = 0; c < 32; c += 8)
-            stg_b32x8(at + c, r[c], r[c + 1], r[c + 2], r[c + 3], r[c + 4], r[c + 5], r[c + 6], r[c + 7]);
+            stg_b32x8(to + c0 + c, r[c], r[c + 1], r[c + 2], r[c + 3], r[c + 4], r[c + 5], r[c + 6], r[c + 7]);
         }
       }
       if (live) {
-        if (whole) {
+        if constexpr (SH) {
+          const uint32_t mark = shared_mark(whole, walk.kt, start);
+          float2* ml = whole ? p.sh.full_ml + at : reinterpret_cast<float2*>(part + (size_t)(2 * 128) * D) + rr;
+          *ml = make_float2(m_run, l_run);
+          if (mark) p.sh.where[at] = whole ? mark : mark | (uint32_t)rr;
+        } else if (whole) {
           p.out.lse[tok * p.out.H_q + head] = l_run == 0.f ? -INFINITY : m_run * kLn2C + logf(l_run);
         } else {
           float* ml = part + (size_t)(2 * 128) * D + 2 * rr;
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
       uint32_t jt = 0, seg = 0;  // key tiles, segments with keys so far
       uint32_t asked = 0, asked_q = 0;  // tiles of keys and of values, and of queries, whose copies were started
       PageWindow pages;
-      for (; walk.more() && ok; walk.next()) {
+      for (; walk.going() && ok; walk.next()) {
         if (walk.n == 0) continue;
         const PagedUnit& u = walk.u;
         const int T = u.nrows > TR ? 2 : 1;
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
         ok = __shfl_sync(kAll, ok, 0);
         ++seg;
         for (int j = 0; j < walk.n && ok; ++j, ++jt) {
-          const int key0 = tile_of(u, walk.kt + j) * 128;
+          const int key0 = key_of<SH, 128>(u, walk.kt + j);
           const int pg0 = key0 >> p.s.page_log;
           pages.hold(pg0, per, lane);
           const int boxes = min(per, (u.kv_len - key0 + rows - 1) >> p.s.page_log);
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           mma_commit(&bars[C::ODONE + t]);
           return true;
         };
-        for (; walk.more() && ok; walk.next()) {
+        for (; walk.going() && ok; walk.next()) {
           const int n = walk.n;
           if (n == 0) continue;
           const bool two = walk.u.nrows > TR;
@@ -556,10 +564,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
     constexpr int ROW = D;  // bytes of a staged row: 128 or 64, swizzled as wide
     const int row = threadIdx.x & 127;
     uint32_t jt = 0;
-    for (; walk.more() && ok; walk.next()) {
+    for (; walk.going() && ok; walk.next()) {
       const PagedUnit& u = walk.u;
       for (int j = 0; j < walk.n && ok; ++j, ++jt) {
-        const int key = tile_of(u, walk.kt + j) * 128 + row;
+        const int key = key_of<SH, 128>(u, walk.kt + j) + row;
         // rows that no query of the unit sees become zeros, whatever they hold
         const bool dead = !(key < u.hi && (key >= u.lo || key < p.s.sinks));
         // keys and values in turn, or, with two groups, keys the first and values the second
@@ -642,13 +650,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   }
 }
 
-template <int D, bool F8>
-cudaError_t launch(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const fm_paged_batch& b,
-                   const fm_rows& q, const PagedOut& out, float scale, cudaStream_t st, int* err) {
+template <int D, bool F8, bool SH>
+cudaError_t launch(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const PagedLists& in,
+                   const int32_t* table, const fm_rows& q, const PagedOut& out, const SharedOut& sh, float scale,
+                   cudaStream_t st, int* err) {
   using C = ChunkCfg<D, F8>;
   static_assert(C::SMEM <= 232448, "chunk_kernel: shared memory of an SM");
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(chunk_kernel<D, F8>), C::SMEM, ready);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(chunk_kernel<D, F8, SH>), C::SMEM, ready);
   if (e != cudaSuccess) return e;
   const int rows = std::min(s.page, 128), tokens = 128 / s.G;
   CUtensorMap tq, tk, tv;
@@ -656,23 +665,26 @@ cudaError_t launch(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c
       !make_tmap_pages(&tk, c.k, c, rows, F8 ? D : 128) || !make_tmap_pages(&tv, c.v, c, rows, F8 ? D : 128))
     return cudaErrorInvalidValue;
   const int wide = reinterpret_cast<uintptr_t>(out.o) % 32 == 0 && out.st % 16 == 0 && out.sh % 16 == 0;
-  ChunkParams p{s,        w,            out,           c.k_exp, c.v_exp,
-                b.q_off,  b.kv_len,     b.page_table,  tokens * s.G,
-                wide,     scale * 1.4426950408889634f, err};
+  ChunkParams p{s,     w,            out,  c.k_exp,                      c.v_exp, in, sh,
+                table, tokens * s.G, wide, scale * 1.4426950408889634f, err};
   count_launches(1);
-  return launch_dependent(chunk_kernel<D, F8>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, tq, tk, tv, p);
+  return launch_dependent(chunk_kernel<D, F8, SH>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, tq, tk, tv, p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_chunk(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const fm_paged_batch& b,
-                               const fm_rows& q, const PagedOut& out, float scale, cudaStream_t st, int* err) {
-  const bool f8 = c.k_exp != nullptr;
-  if (s.d == 64)
-    return f8 ? launch<64, true>(s, w, c, b, q, out, scale, st, err)
-              : launch<64, false>(s, w, c, b, q, out, scale, st, err);
-  return f8 ? launch<128, true>(s, w, c, b, q, out, scale, st, err)
-            : launch<128, false>(s, w, c, b, q, out, scale, st, err);
+cudaError_t launch_paged_chunk(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const PagedLists& in,
+                               const int32_t* table, const fm_rows& q, const PagedOut& out, const SharedOut* sh,
+                               float scale, cudaStream_t st, int* err) {
+  const SharedOut none = {};
+  auto go = [&](auto d, auto f8) {
+    return sh ? launch<d.value, f8.value, true>(s, w, c, in, table, q, out, *sh, scale, st, err)
+              : launch<d.value, f8.value, false>(s, w, c, in, table, q, out, none, scale, st, err);
+  };
+  const std::integral_constant<int, 64> d64;
+  const std::integral_constant<int, 128> d128;
+  if (c.k_exp) return s.d == 64 ? go(d64, std::true_type{}) : go(d128, std::true_type{});
+  return s.d == 64 ? go(d64, std::false_type{}) : go(d128, std::false_type{});
 }
 
 }  // namespace fm

@@ -9,6 +9,11 @@
 // ragged batches, one long sequence or many short ones all fill the GPU. A
 // range that covers a unit only in part leaves (m, l, O) in a partial slot, and
 // the combining kernel joins the slots of such units in CTA order.
+//
+// Sequences that share a prefix (SH = true): a group's new tokens lie side by side,
+// so over the shared keys they are the rows of one long sequence, and each sequence
+// has rows of its own over the rest of its keys. Both kinds are virtual sequences of
+// one list, prefixes first; a row's results of both are joined by merge_kernel.
 #pragma once
 #include <atomic>
 #include <climits>
@@ -23,8 +28,8 @@ namespace fm {
 // tok + (g0 + i) / G, at position pos + (g0 + i) / G.
 struct __align__(16) PagedUnit {
   int tok, g0, nrows, pos;
-  int r, hi, ns, w0;  // sequence; keys [0, hi) may be visible; tiles [0, ns) hold sinks, then from w0 on
-  int ntiles, kv_len, lo, pad;  // lo: keys below it are visible as sinks only
+  int r, hi, ns, w0;  // row of the page table; keys [0, hi) may be visible; tiles [0, ns) hold sinks, then from w0 on
+  int ntiles, kv_len, lo, base;  // lo: keys below it are visible as sinks only; base (SH): key of the first tile
 };
 
 // A CTA's range: `count` tiles from tile kt of head h of a unit on. The unit is
@@ -47,10 +52,26 @@ struct PagedShape {
   int local;  // every CTA plans for itself: no plan kernel
   int whole;  // no unit and head is divided (every CTA plans for itself): nothing to join
   long long max_units;
+  int V;       // sequences of the plan: R, or (SH) groups' prefixes, then sequences, as `kinds` has them
+  int S;       // groups
+  int kinds;   // 1: prefixes, 2: what follows them, 3: both
 };
 
-// Tile number kt of a unit's list.
-__device__ __forceinline__ int tile_of(const PagedUnit& u, int kt) { return kt < u.ns ? kt : kt - u.ns + u.w0; }
+// A call's offsets and lengths; the last two where sequences share prefixes.
+struct PagedLists {
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  const int32_t* seq_off;
+  const int32_t* prefix_len;
+};
+
+// First key of tile number kt of a unit's list, of tiles of TILE keys. (SH: shared prefixes
+// end with a page, so that a unit's tiles start at the beginning of one, or a multiple of
+// TILE keys after it.)
+template <bool SH, int TILE>
+__device__ __forceinline__ int key_of(const PagedUnit& u, int kt) {
+  return SH ? u.base + kt * TILE : (kt < u.ns ? kt : kt - u.ns + u.w0) * TILE;
+}
 
 // The new tokens of sequence r, [a, a + n), kept inside [0, T] whatever q_off
 // holds, and its keys, kept inside the page table; true where either was not, or the
@@ -82,8 +103,82 @@ __device__ __forceinline__ PagedUnit unit_at(const PagedShape& s, int r, int a, 
   q.ns = s.window > 0 ? min((s.sinks + s.tile - 1) >> s.tile_log, all) : 0;
   q.w0 = max(q.ns, min(q.lo >> s.tile_log, all));
   q.ntiles = q.ns + max(0, all - q.w0);
-  q.pad = 0;
+  q.base = 0;
   return q;
+}
+
+// Sequences that share prefixes. more[v]: first key that virtual sequence v goes over (a
+// multiple of the page size), its row of the page table.
+__device__ __forceinline__ int prefixes(const PagedShape& s) { return s.kinds & 1 ? s.S : 0; }
+
+// Unit i of virtual sequence v. A prefix's rows see all of it: they stand behind it.
+__device__ __forceinline__ PagedUnit shared_unit_at(const PagedShape& s, int v, const int4& seq, const int2& more,
+                                                    int i) {
+  const int row0 = i * s.step, tok = row0 / s.G;
+  PagedUnit q;
+  q.r = more.y;
+  q.tok = seq.x + tok;
+  q.g0 = row0 - tok * s.G;
+  q.nrows = min(s.step, seq.y * s.G - row0);
+  q.ns = v < prefixes(s) ? 0 : 1;  // the kind
+  q.pos = q.ns ? seq.z - seq.y + tok : seq.z;
+  q.kv_len = seq.z;
+  const int last = q.pos + (q.g0 + q.nrows - 1) / s.G;
+  q.hi = s.causal ? min(max(last + 1, 0), seq.z) : seq.z;
+  q.lo = 0;
+  q.w0 = 0;
+  q.base = more.x;
+  q.ntiles = max(0, (q.hi - more.x + s.tile - 1) >> s.tile_log);
+  return q;
+}
+
+// Group g's sequences [s0, s1), kept inside [0, R], and its shared keys, whole pages of
+// them; true where offsets or length are none.
+__device__ __forceinline__ bool group_at(const PagedShape& s, const PagedLists& in, int g, int& s0, int& s1, int& P) {
+  const int a = in.seq_off[g], b = in.seq_off[g + 1], p = in.prefix_len[g];
+  s0 = min(max(a, 0), s.R);
+  s1 = min(max(b, s0), s.R);
+  P = min(max(p, 0), s.width * s.page) & -s.page;
+  return s0 != a || s1 != b || (g == 0 && a != 0) || (g == s.S - 1 && b != s.R) ||
+         (s1 > s0 && (p < 0 || p > s.width * s.page));
+}
+
+// Virtual sequence of group g: its tokens, keys [0, P) and the table row of its first
+// sequence that has tokens (one without may be a slot out of use).
+__device__ __forceinline__ bool prefix_at(const PagedShape& s, const PagedLists& in, int g, int4& seq, int2& more,
+                                          int& s0) {
+  int s1, P;
+  const bool bad = group_at(s, in, g, s0, s1, P);
+  const int a = min(max(in.q_off[s0], 0), s.T), n = min(max(in.q_off[s1], a), s.T) - a;
+  int row = s0;
+  while (row < s1 - 1 && in.q_off[row + 1] <= a) ++row;
+  seq = make_int4(a, n, P, (n * s.G + s.step - 1) / s.step);
+  more = make_int2(0, min(row, s.R - 1));
+  return bad;
+}
+
+// Sequence r behind its group's P shared keys (prefix: the group's length as it was given).
+// Flagged too where new tokens lie in the prefix.
+__device__ __forceinline__ bool rest_at(const PagedShape& s, const PagedLists& in, int r, int P, int prefix, int4& seq,
+                                        int2& more) {
+  int a, n, L;
+  const bool bad = sequence_at(s, in.q_off, in.kv_len, r, a, n, L);
+  seq = make_int4(a, n, L, (n * s.G + s.step - 1) / s.step);
+  more = make_int2(min(P, L & -s.page), r);
+  return bad || (n > 0 && prefix > L - n);
+}
+
+// The last g of n ascending starts that is at or below x.
+__device__ __forceinline__ int last_at(const int32_t* starts, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (starts[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
 }
 
 // Some row of the unit sees some of the keys [a, b): only then does it matter which page holds them.
@@ -129,37 +224,77 @@ struct PagedDivision {
 // The plan as one CTA makes it for itself, for a few hundred units at most and a
 // total work that 32 bits hold (offsets that descend, whose spans may overlap and add
 // up to more, plan nothing): every sequence into seq (first token, tokens,
-// keys, units), its work into work (both shared memory, R entries), the CTA's
-// range into *out (shared memory).
-__device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len,
-                                             int4* seq, unsigned* work, PagedStart* out, int* err) {
+// keys, units; SH: the rest of it into more), its work into work (all shared memory,
+// V entries; SH: work has room for 3 S more), the CTA's range into *out (shared memory).
+template <bool SH>
+__device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLists& in, int4* seq, int2* more,
+                                             unsigned* work, PagedStart* out, int* err) {
   bool bad = false, descends = false;
   const int lane = threadIdx.x & 31;
   constexpr int kAlone = 4;  // units that a thread counts by itself
-  for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
-    int a, n, L;
-    bad |= sequence_at(s, q_off, kv_len, r, a, n, L);
-    descends |= q_off[r + 1] < q_off[r];
-    const int units = (n * s.G + s.step - 1) / s.step;
+  auto unit = [&](int r, const int4& q, int i) {
+    if constexpr (SH)
+      return shared_unit_at(s, r, q, more[r], i);
+    else
+      return unit_at(s, r, q.x, q.y, q.z, i);
+  };
+  auto keep = [&](int r, const int4& q) {
     unsigned w = 0;
-    for (int i = 0; i < units && units <= kAlone; ++i) w += max(unit_at(s, r, a, n, L, i).ntiles, 1);
-    seq[r] = make_int4(a, n, L, units);
+    for (int i = 0; i < q.w && q.w <= kAlone; ++i) w += max(unit(r, q, i).ntiles, 1);
+    seq[r] = q;
     work[r] = w * s.H_kv;
+  };
+  if constexpr (SH) {
+    // groups into shared memory, then sequences, which look for theirs there
+    int32_t* gs = reinterpret_cast<int32_t*>(work + s.V);  // first sequences, shared keys, lengths as given
+    int32_t *gp = gs + s.S, *gl = gp + s.S;
+    const int vs = prefixes(s);
+    for (int g = threadIdx.x; g < s.S; g += blockDim.x) {
+      descends |= in.seq_off[g + 1] < in.seq_off[g];
+      int s0, s1, P;
+      if (vs) {
+        int4 q;
+        bad |= prefix_at(s, in, g, q, more[g], s0);
+        P = q.z;
+        keep(g, q);
+      } else {
+        bad |= group_at(s, in, g, s0, s1, P);
+      }
+      gs[g] = s0;
+      gp[g] = P;
+      gl[g] = in.prefix_len[g];
+    }
+    for (int r = threadIdx.x; r < s.R; r += blockDim.x) descends |= in.q_off[r + 1] < in.q_off[r];
+    __syncthreads();
+    if (s.kinds & 2)
+      for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
+        const int g = last_at(gs, s.S, r);
+        int4 q;
+        bad |= rest_at(s, in, r, gp[g], gl[g], q, more[vs + r]);
+        keep(vs + r, q);
+      }
+  } else {
+    for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
+      int a, n, L;
+      bad |= sequence_at(s, in.q_off, in.kv_len, r, a, n, L);
+      descends |= in.q_off[r + 1] < in.q_off[r];
+      keep(r, make_int4(a, n, L, (n * s.G + s.step - 1) / s.step));
+    }
   }
   if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
   const bool none = __syncthreads_or(descends);
-  for (int r = threadIdx.x >> 5; r < s.R; r += blockDim.x >> 5) {  // longer ones: a lane a unit
+  for (int r = threadIdx.x >> 5; r < s.V; r += blockDim.x >> 5) {  // longer ones: a lane a unit
     const int4 q = seq[r];
     if (q.w <= kAlone) continue;
     unsigned w = 0;
-    for (int i = lane; i < q.w; i += 32) w += max(unit_at(s, r, q.x, q.y, q.z, i).ntiles, 1);
+    for (int i = lane; i < q.w; i += 32) w += max(unit(r, q, i).ntiles, 1);
     w = __reduce_add_sync(0xffffffffu, w);
     if (lane == 0) work[r] = w * s.H_kv;
   }
   if (threadIdx.x == 0) *out = PagedStart{};
   __syncthreads();
   if (threadIdx.x < 32) {
-    const int per = (s.R + 31) / 32, r0 = lane * per, r1 = min(s.R, r0 + per);
+    const int per = (s.V + 31) / 32, r0 = lane * per, r1 = min(s.V, r0 + per);
     unsigned tiles = 0, units = 0;
     for (int r = r0; r < r1; ++r) {
       tiles += work[r];
@@ -194,7 +329,7 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
         PagedStart st = {};
         unsigned nt = 0;
         if (i < q.w) {
-          st.unit = unit_at(s, r, q.x, q.y, q.z, i);
+          st.unit = unit(r, q, i);
           nt = max(st.unit.ntiles, 1);
         }
         const unsigned places = i < q.w ? nt + div.extra : 0;
@@ -225,13 +360,12 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const int32_t*
 // For several sequences (one's units are in order as they are): first: R + 1 running
 // sums of the sequences' units; order: the units from the largest on; sizes: their
 // tiles (scratch); all shared memory.
-__device__ __forceinline__ void plan_whole(const PagedShape& s, const int32_t* q_off, const int32_t* kv_len,
-                                           int4* seq, uint16_t* first, uint16_t* order, uint16_t* sizes,
-                                           PagedStart* out, int* err) {
+__device__ __forceinline__ void plan_whole(const PagedShape& s, const PagedLists& in, int4* seq, uint16_t* first,
+                                           uint16_t* order, uint16_t* sizes, PagedStart* out, int* err) {
   bool bad = false;
   for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
     int a, n, L;
-    bad |= sequence_at(s, q_off, kv_len, r, a, n, L);
+    bad |= sequence_at(s, in.q_off, in.kv_len, r, a, n, L);
     seq[r] = make_int4(a, n, L, (n * s.G + s.step - 1) / s.step);
   }
   if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
@@ -288,26 +422,29 @@ __device__ __forceinline__ void plan_whole(const PagedShape& s, const int32_t* q
 }
 
 // A CTA's walk over its range of tiles, or its units: one (unit, head) at a time.
+template <bool SH>
 struct PagedWalk {
   const PagedShape& s;
   const PagedUnit* units;  // the plan kernel's list
   const int4* seq;         // or this CTA's own sequences
+  const int2* more;        // (SH) and what else belongs to them
   const uint16_t* first;   // (whole) their first units
   const uint16_t* order;   // (whole) the units, largest first
   int left, at, i, h, kt, n;  // current segment: tiles [kt, kt + n) of head h (n 0: a unit without keys)
   int extra;
   PagedUnit u;
 
-  __device__ PagedWalk(const PagedShape& s_, const PagedUnit* units_, const int4* seq_, const uint16_t* first_,
-                       const uint16_t* order_, const PagedStart& st)
-      : s(s_), units(units_), seq(seq_), first(first_), order(order_), left(st.count), at(st.u), i(st.i), h(st.h),
-        kt(st.kt), extra(st.extra), u(st.unit) {
-    if (s.whole && left > 0) deal();
-    n = s.whole ? u.ntiles : min(u.ntiles - kt, left);
+  __device__ PagedWalk(const PagedShape& s_, const PagedUnit* units_, const int4* seq_, const int2* more_,
+                       const uint16_t* first_, const uint16_t* order_, const PagedStart& st)
+      : s(s_), units(units_), seq(seq_), more(more_), first(first_), order(order_), left(st.count), at(st.u), i(st.i),
+        h(st.h), kt(st.kt), extra(st.extra), u(st.unit) {
+    if (dealt() && left > 0) deal();
+    n = dealt() ? u.ntiles : min(u.ntiles - kt, left);
   }
-  __device__ bool more() const { return left > 0; }
+  __device__ bool going() const { return left > 0; }
+  __device__ bool dealt() const { return !SH && s.whole; }
   // the segment covers its unit wholly
-  __device__ bool whole() const { return s.whole || (kt == 0 && n == u.ntiles); }
+  __device__ bool whole() const { return dealt() || (kt == 0 && n == u.ntiles); }
   __device__ int slot() const { return kt == 0 ? 1 : 0; }
   // (whole) row number `at` of the items
   __device__ void deal() {
@@ -329,9 +466,9 @@ struct PagedWalk {
     u = unit_at(s, r, seq[r].x, seq[r].y, seq[r].z, s.R == 1 ? v : v - first[r]);
   }
   __device__ void next() {
-    left -= s.whole ? 1 : max(n, 1) + extra;
+    left -= dealt() ? 1 : max(n, 1) + extra;
     if (left <= 0) return;
-    if (s.whole) {
+    if (dealt()) {
       ++at;
       deal();
       n = u.ntiles;
@@ -345,9 +482,12 @@ struct PagedWalk {
         if (++i >= q.w) {
           i = 0;
           do q = seq[++at];
-          while (q.w == 0 && at + 1 < s.R);
+          while (q.w == 0 && at + 1 < s.V);
         }
-        u = unit_at(s, at, q.x, q.y, q.z, i);
+        if constexpr (SH)
+          u = shared_unit_at(s, at, q, more[at], i);
+        else
+          u = unit_at(s, at, q.x, q.y, q.z, i);
       } else {
         u = units[++at];
       }
@@ -355,6 +495,25 @@ struct PagedWalk {
     n = min(u.ntiles, left);
   }
 };
+
+// Where results of rows with a shared prefix go: row i = token * H_q + head of kind k (0: over the
+// prefix, 1: over the rest) to where[k * rows + i]. ~0: all of it is in full (rows of d sums) and
+// full_ml; else it is in the partial slots of CTAs first .. first + n - 1 at `row`, first << 20 |
+// n << 8 | row.
+struct SharedOut {
+  float* full;
+  float2* full_ml;
+  uint32_t* where;
+  long long rows;  // T * H_q
+};
+
+// Which of a segment's rows' entries of `where` this CTA writes: whole units', and divided ones'
+// that it is the second CTA of (0: none).
+__device__ __forceinline__ uint32_t shared_mark(bool whole, int kt, const PagedStart& st) {
+  if (whole) return 0xffffffffu;
+  return kt > 0 && st.first == (int)blockIdx.x - 1 ? (uint32_t)st.first << 20 | (uint32_t)(st.last - st.first + 1) << 8
+                                                   : 0u;
+}
 
 // Limits of a CTA's own plan: sequences (kLocalChunks: chunk_kernel, whose shared
 // memory is nearly full), units more than one a sequence, all units where those of
@@ -366,7 +525,7 @@ constexpr int kWholeUnits = 320;
 // Workspace of one call: units, the running sum of their work, CTA starts, the
 // partial slots (two a CTA: rows x d sums, then rows x (m, l)).
 struct PagedWork {
-  int32_t* first;      // (R + 1) first unit of each sequence
+  int32_t* first;      // (V + 1) first unit of each sequence
   PagedUnit* units;    // max_units
   long long* sum;      // max_units + 1
   PagedStart* starts;  // ctas
@@ -388,7 +547,7 @@ inline PagedWork paged_work(const PagedShape& s, int rows, void* ws) {
     o += round256(bytes);
     return at;
   };
-  w.first = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * ((size_t)s.R + 1)));
+  w.first = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * ((size_t)s.V + 1)));
   w.units = reinterpret_cast<PagedUnit*>(take(sizeof(PagedUnit) * (size_t)s.max_units));
   w.sum = reinterpret_cast<long long*>(take(sizeof(long long) * ((size_t)s.max_units + 1)));
   w.starts = reinterpret_cast<PagedStart*>(take(sizeof(PagedStart) * (size_t)s.ctas));
@@ -477,7 +636,9 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
 }
 
 constexpr int kChunkRows = 256;  // rows of a chunk_kernel partial slot: two tiles
-cudaError_t launch_paged_chunk(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const fm_paged_batch& b,
-                               const fm_rows& q, const PagedOut& out, float scale, cudaStream_t st, int* err);
+// (sh: sequences share prefixes, results go there)
+cudaError_t launch_paged_chunk(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const PagedLists& in,
+                               const int32_t* table, const fm_rows& q, const PagedOut& out, const SharedOut* sh,
+                               float scale, cudaStream_t st, int* err);
 
 }  // namespace fm

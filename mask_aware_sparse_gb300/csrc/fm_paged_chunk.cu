@@ -595,6 +595,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < kPart; ++c) rr[c] = lds128(src + in_box<ROW>(row, part * kPart + c));
             if (part == D / 64 - 1) {
+              // (an arrival does not wait for loads that are on their way, and the copy that it
+              // lets in is of another proxy: without the fence the next tile's bytes were read)
+              fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) mbar_arrive(&bars[C::REMPTY + rs]);
             }

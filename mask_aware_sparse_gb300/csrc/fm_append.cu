@@ -13,6 +13,12 @@
 // need none of that and are in flight first; offsets and lengths are read once a block,
 // into shared memory, where each token looks its sequence up; a step's table entries are
 // loaded while the step before it is computed.
+// Between both it is issue slots and warps that count: four blocks an SM with one row
+// ahead a thread and nothing spilled take 213 us for 32768 tokens of 64 / 8 heads, d = 128
+// (6.3 TB/s, 93% of the copy rate), and 40.7 us for 8192 tokens of 32 / 8 into an e4m3
+// cache; with three blocks 231 and 44.9, two rows ahead in as many registers (spilled)
+// 257 and 48.8, rows by asynchronous copies three ahead 294 and 43.2, teams of warps that
+// wait for one another alone 237 and 45.1. 64 tokens of 64 sequences: 4.8 us.
 #include <type_traits>
 #include <cuda_bf16.h>
 #include "dependent.cuh"
@@ -25,6 +31,7 @@ namespace {
 
 constexpr int kThreads = kRopeThreads, kWarps = kRopeWarps;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kPerSm = 4;   // blocks of each side
 constexpr int kHeld = 256;  // sequences whose offsets and lengths a block keeps
 
 struct Rows3 {
@@ -81,24 +88,27 @@ __device__ __forceinline__ uint32_t quantise(const F2 (&a)[4], const F2 (&b)[4],
   return E == 255 ? 255u : (uint32_t)e;
 }
 
-// blockIdx.y 0: queries, 1: keys, then values, as one list of heads. Warps, rows and
-// steps are divided as in the norm and rotation by itself.
-template <int D, bool INTER, bool F8>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams p, const int TB) {
+template <int D>
+struct AppendShared {
+  static constexpr int kMost = kWarps * 512 / D;  // tokens of a step
+  float4 cs[kMost * D / 4];
+  float4 ws[D / 4];
+  unsigned long long frac[D / 2];
+  int64_t slot[kMost];  // keys: head 0's row of the cache; below 0: a token that is left out
+  int32_t held[2 * kHeld + 1];
+  int32_t pos[kMost];
+};
+
+// A block's steps over its tokens' queries, or their keys and then values as one list of
+// heads. Warps, rows and steps are divided as in the norm and rotation by itself.
+template <int D, bool INTER, bool F8, bool keys>
+__device__ __forceinline__ void append_rows(const AppendParams& p, const int TB, AppendShared<D>& sm) {
   using C = Chunks<D, INTER>;
   constexpr int TG = C::TG, HPW = 32 / TG;  // threads per row, rows per warp
-  constexpr int kAhead = 2, kMost = kWarps * HPW;  // tokens of a step
-  __shared__ __align__(16) float4 cs[kMost * D / 4];
-  __shared__ unsigned long long frac[D / 2];
-  __shared__ float4 ws[D / 4];
-  __shared__ int32_t held[2 * kHeld + 1];
-  __shared__ int32_t spos[kMost];
-  __shared__ int64_t sslot[kMost];  // keys: head 0's row of the cache; below 0: a token that is left out
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % TG, hl = lane / TG;
   const C ch(c, p.rot);
   const int RT = p.rot / 16;
-  const bool keys = blockIdx.y != 0;
   const int H = keys ? 2 * p.H_kv : p.H_q;
   const void* wp = keys ? p.wk : p.wq;
   const int TPW = tokens_per_warp(H, D), HS = HPW / TPW;  // tokens a warp, heads of each at a time
@@ -106,34 +116,23 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
   const int tw = warp / wpt, w0 = warp - tw * wpt;  // this warp's tokens of the step, its place among their warps
   const int ti = tw * TPW + hl / HS, h0 = hl % HS;  // this thread's token of the step, its first head
   const int tokens = kWarps / wpt * TPW;
-  const int groups = (H + HS - 1) / HS;
   const int stride = gridDim.x * tokens;  // (no more than 2^30 tokens)
   int tok0 = blockIdx.x * tokens;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  // Rows' loads, two groups ahead of the one computed, and the next step's first ones while
-  // its angles are.
-  uint4 ra[kAhead], rb[kAhead];
-  const char *row_q = nullptr, *row_v = nullptr;
-  auto fetch = [&](int k, int g) {
-    const int h = g * HS + h0;
-    if (row_q && h < H) {
+  // A row's loads are in flight while the one before is computed, and the next step's first
+  // ones while its angles are.
+  uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+  auto fetch = [&](int h) {  // of the token at tok0 + ti
+    const int64_t t = (int64_t)tok0 + ti;
+    if (h < H && t < p.T) {
       const bool val = keys && h >= p.H_kv;
-      const char* r = val ? row_v + 2 * (h - p.H_kv) * p.v.sh : row_q + 2 * h * (keys ? p.k.sh : p.q.sh);
-      ra[k] = *reinterpret_cast<const uint4*>(r + 2 * (val ? 16 * c : ch.oa));
-      rb[k] = *reinterpret_cast<const uint4*>(r + 2 * (val ? 16 * c + 8 : ch.ob));
+      const Rows3& in = val ? p.v : keys ? p.k : p.q;
+      const char* r = in.p + 2 * (t * in.st + (val ? h - p.H_kv : h) * in.sh);
+      ra = *reinterpret_cast<const uint4*>(r + 2 * (val ? 16 * c : ch.oa));
+      rb = *reinterpret_cast<const uint4*>(r + 2 * (val ? 16 * c + 8 : ch.ob));
     }
   };
-  auto begin = [&] {
-    const int64_t t = (int64_t)tok0 + ti;
-    row_q = t < p.T ? (keys ? p.k.p + 2 * t * p.k.st : p.q.p + 2 * t * p.q.st) : nullptr;
-    row_v = p.v.p + 2 * t * p.v.st;
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) fetch(k, w0 + k * wpt);
-  };
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) ra[k] = rb[k] = make_uint4(0, 0, 0, 0);
-  begin();
+  const int first = w0 * HS + h0, step = wpt * HS;  // this thread's heads
+  fetch(first);
   // Offsets that do not ascend from 0 or pass T, lengths outside the table: nothing is
   // written (flagged once), as tokens would be taken for those of other places.
   bool bad = false;
@@ -141,23 +140,23 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
   for (int r = threadIdx.x; r <= p.R; r += kThreads) {
     const int o = p.off[r];
     bad |= r == 0 ? o != 0 : o < p.off[r - 1];
-    if (hold) held[r] = o;
+    if (hold) sm.held[r] = o;
     if (r == p.R) {
       bad |= o > p.T;
     } else {
       const int L = p.kv_len[r];
       bad |= L < 0 || L > p.width * p.page;
-      if (hold) held[kHeld + 1 + r] = L;
+      if (hold) sm.held[kHeld + 1 + r] = L;
     }
   }
-  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) frac[i] = turn_fraction(p.inv_freq[i]);
+  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) sm.frac[i] = turn_fraction(p.inv_freq[i]);
   if (wp && threadIdx.x < TG) {
     // slot j * TG + c: a quarter of thread c's sixteen weights
     const C mine(threadIdx.x, p.rot);
     for (int j = 0; j < 4; ++j) {
       const int o = (j < 2 ? mine.oa : mine.ob) + 4 * (j & 1);
-      ws[j * TG + threadIdx.x] = make_float4(weight_at(wp, p.w_f32, o), weight_at(wp, p.w_f32, o + 1),
-                                             weight_at(wp, p.w_f32, o + 2), weight_at(wp, p.w_f32, o + 3));
+      sm.ws[j * TG + threadIdx.x] = make_float4(weight_at(wp, p.w_f32, o), weight_at(wp, p.w_f32, o + 1),
+                                                weight_at(wp, p.w_f32, o + 2), weight_at(wp, p.w_f32, o + 3));
     }
   }
   bad = __syncthreads_or(bad);
@@ -165,10 +164,11 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
     if (blockIdx.x == 0 && keys && threadIdx.x == 0) record_error(p.err, FM_DEV_ERR_RANGE);
     return;
   }
-  const int32_t *off = hold ? held : p.off, *len = hold ? held + kHeld + 1 : p.kv_len;
-  // A step's tokens, one a thread: sequence, place, position, page.
+  // A step's tokens, one a thread: sequence, place, position, page. (Keys: looked up while the
+  // step before is computed, as the page is a load that waits for another.)
   int look_pos = 0, look_page = 0, look_at = -1;  // look_at below 0: a token of no sequence, or without a place
   auto look = [&] {
+    const int32_t *off = hold ? sm.held : p.off, *len = hold ? sm.held + kHeld + 1 : p.kv_len;
     const int t = tok0 + (int)threadIdx.x;
     look_at = -1;
     if ((int)threadIdx.x >= tokens || t >= p.T || t >= off[p.R]) return;
@@ -182,16 +182,15 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
     }
     const int place = len[lo] - (off[lo + 1] - t);
     look_pos = p.pos ? p.pos[t] : place;
-    if (!keys) {
-      look_at = 0;
-      return;
+    look_at = 0;
+    if (keys) {
+      look_page = place >= 0 ? p.table[(int64_t)lo * p.width + place / p.page] : -1;
+      look_at = place >= 0 ? place % p.page : 0;
     }
-    look_page = -1;
-    if (place >= 0) look_page = p.table[(int64_t)lo * p.width + place / p.page];
-    look_at = place >= 0 ? place % p.page : 0;
   };
-  look();
+  if (keys) look();
   while (tok0 < p.T) {
+    if (!keys) look();
     if ((int)threadIdx.x < tokens) {
       int64_t s = look_at;
       if (keys && look_at >= 0) {
@@ -199,92 +198,114 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
         if (!there) record_error(p.err, FM_DEV_ERR_RANGE);
         s = there ? (int64_t)look_page * p.H_kv * p.page + look_at : -1;
       }
-      spos[threadIdx.x] = look_pos;
-      sslot[threadIdx.x] = s;
+      sm.pos[threadIdx.x] = look_pos;
+      sm.slot[threadIdx.x] = s;
     }
     __syncthreads();
     {
       const int half = p.rot / 2;
       for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
         const int t = i / half, f = i - t * half;
-        if (sslot[t] < 0) continue;
+        if (sm.slot[t] < 0) continue;
         float s, co;
-        angle_of(spos[t], frac[f], s, co);
-        store_angle(reinterpret_cast<float*>(cs + t * (p.rot / 4)), RT, f, co * p.rot_scale, s * p.rot_scale);
+        angle_of(sm.pos[t], sm.frac[f], s, co);
+        store_angle(reinterpret_cast<float*>(sm.cs + t * (p.rot / 4)), RT, f, co * p.rot_scale, s * p.rot_scale);
       }
     }
     __syncthreads();
-    const int64_t slot = sslot[ti], tok = (int64_t)tok0 + ti;
-    tok0 += stride;
-    look();
+    const int64_t slot = sm.slot[ti];
+    char* out = keys ? nullptr : p.qo + 2 * (((int64_t)tok0 + ti) * p.qo_st);
     F2 co[4], si[4];
     if (ch.turned) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 t = slot >= 0 ? cs[ti * (p.rot / 4) + j * RT + c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 t = slot >= 0 ? sm.cs[ti * (p.rot / 4) + j * RT + c] : make_float4(0.f, 0.f, 0.f, 0.f);
         co[j] = f2_pack(t.x, t.y);
         si[j] = f2_pack(t.z, t.w);
       }
     }
-    for (int g0 = w0; g0 < groups; g0 += kAhead * wpt) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int g = g0 + k * wpt;
-        if (g >= groups) break;
-        const int h = g * HS + h0;
-        const bool val = keys && h >= p.H_kv, live = slot >= 0 && h < H;
-        const uint4 xa = ra[k], xb = rb[k];
-        F2 fa[4], fb[4];
-        unpack8(xa, fa);
-        unpack8(xb, fb);
-        fetch(k, g + kAhead * wpt);
-        if (wp) {
-          F2 sa = f2_mul(fa[0], fa[0]), sb = f2_mul(fb[0], fb[0]);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) {
-            sa = f2_fma(fa[i], fa[i], sa);
-            sb = f2_fma(fb[i], fb[i], sb);
-          }
-          const F2 r = f2_both(rsqrtf(row_sum<D>(f2_sum(f2_add(sa, sb))) * (1.f / D) + p.eps));
-          if (!val) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              F2* f = j < 2 ? fa + 2 * j : fb + 2 * j - 4;
-              const float4 w = ws[j * TG + c];
-              f[0] = f2_mul(f[0], f2_mul(r, f2_pack(w.x, w.y)));
-              f[1] = f2_mul(f[1], f2_mul(r, f2_pack(w.z, w.w)));
-            }
-          }
+    if (keys) {
+      tok0 += stride;
+      look();
+      tok0 -= stride;
+    }
+    // (every lane of a warp takes the same number of turns: sums and maxima are exchanged)
+    for (int g = w0 * HS; g < H; g += step) {
+      const int h = g + h0;
+      const bool val = keys && h >= p.H_kv, live = slot >= 0 && h < H;
+      F2 fa[4], fb[4];
+      unpack8(ra, fa);
+      unpack8(rb, fb);
+      int64_t row = 0;
+      char* page = nullptr;
+      if constexpr (keys) {
+        row = slot + (int64_t)(val ? h - p.H_kv : h) * p.page;
+        page = val ? p.c[1] : p.c[0];
+        if (!F8 && val && live) {  // as they are
+          *reinterpret_cast<uint4*>(page + 2 * (row * D + 16 * c)) = ra;
+          *reinterpret_cast<uint4*>(page + 2 * (row * D + 16 * c + 8)) = rb;
         }
-        if (ch.turned && !val) turn<INTER, 1>(fa, fb, co, si);
-        const int oa = val ? 16 * c : ch.oa, ob = val ? 16 * c + 8 : ch.ob;
-        if (!keys) {
-          if (live) {
-            char* to = p.qo + 2 * (tok * p.qo_st + h * p.qo_sh);
-            *reinterpret_cast<uint4*>(to + 2 * oa) = pack8(fa);
-            *reinterpret_cast<uint4*>(to + 2 * ob) = pack8(fb);
-          }
-        } else {
-          const int64_t row = slot + (int64_t)(val ? h - p.H_kv : h) * p.page;
-          char* page = val ? p.c[1] : p.c[0];
-          if constexpr (F8) {
-            uint2 qa, qb;
-            const uint32_t e = quantise<TG>(fa, fb, qa, qb);
-            if (live) {
-              *reinterpret_cast<uint2*>(page + row * D + oa) = qa;
-              *reinterpret_cast<uint2*>(page + row * D + ob) = qb;
-              if (c == 0) (val ? p.e[1] : p.e[0])[row] = (uint8_t)e;
-            }
-          } else if (live) {
-            *reinterpret_cast<uint4*>(page + 2 * (row * D + oa)) = val ? xa : pack8(fa);
-            *reinterpret_cast<uint4*>(page + 2 * (row * D + ob)) = val ? xb : pack8(fb);
+      }
+      if (g + step < H) {
+        fetch(h + step);
+      } else {
+        tok0 += stride;
+        fetch(first);
+        tok0 -= stride;
+      }
+      if (wp) {
+        F2 sa = f2_mul(fa[0], fa[0]), sb = f2_mul(fb[0], fb[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          sa = f2_fma(fa[i], fa[i], sa);
+          sb = f2_fma(fb[i], fb[i], sb);
+        }
+        const F2 r = f2_both(rsqrtf(row_sum<D>(f2_sum(f2_add(sa, sb))) * (1.f / D) + p.eps));
+        if (!val) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            F2* f = j < 2 ? fa + 2 * j : fb + 2 * j - 4;
+            const float4 w = sm.ws[j * TG + c];
+            f[0] = f2_mul(f[0], f2_mul(r, f2_pack(w.x, w.y)));
+            f[1] = f2_mul(f[1], f2_mul(r, f2_pack(w.z, w.w)));
           }
         }
       }
+      if (ch.turned && !val) turn<INTER, 1>(fa, fb, co, si);
+      if constexpr (!keys) {
+        if (live) {
+          char* to = out + 2 * (h * p.qo_sh);
+          *reinterpret_cast<uint4*>(to + 2 * ch.oa) = pack8(fa);
+          *reinterpret_cast<uint4*>(to + 2 * ch.ob) = pack8(fb);
+        }
+      } else if constexpr (F8) {
+        uint2 qa, qb;
+        const uint32_t e = quantise<TG>(fa, fb, qa, qb);
+        if (live) {
+          *reinterpret_cast<uint2*>(page + row * D + (val ? 16 * c : ch.oa)) = qa;
+          *reinterpret_cast<uint2*>(page + row * D + (val ? 16 * c + 8 : ch.ob)) = qb;
+          if (c == 0) (val ? p.e[1] : p.e[0])[row] = (uint8_t)e;
+        }
+      } else if (live && !val) {
+        *reinterpret_cast<uint4*>(page + 2 * (row * D + ch.oa)) = pack8(fa);
+        *reinterpret_cast<uint4*>(page + 2 * (row * D + ch.ob)) = pack8(fb);
+      }
     }
-    begin();
+    tok0 += stride;
     __syncthreads();
   }
+}
+
+// blockIdx.y 0: queries, 1: keys and values.
+template <int D, bool INTER, bool F8>
+__global__ void __launch_bounds__(kThreads, kPerSm) append_kernel(const AppendParams p, const int TB) {
+  __shared__ __align__(16) AppendShared<D> sm;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.y == 0)
+    append_rows<D, INTER, F8, false>(p, TB, sm);
+  else
+    append_rows<D, INTER, F8, true>(p, TB, sm);
 }
 
 Rows3 rows_of(const fm_rows& r) { return Rows3{static_cast<const char*>(r.ptr), r.st, r.sh}; }
@@ -337,7 +358,7 @@ cudaError_t launch_cache_append(const fm_kv_cache& c, const fm_paged_batch& b, c
   while (tb < kWarps && groups >= (long long)tb * sm_count()) tb *= 2;
   int64_t grid = steps_of(p.T, p.H_q, c.d, tb);
   if (steps_of(p.T, 2 * p.H_kv, c.d, tb) > grid) grid = steps_of(p.T, 2 * p.H_kv, c.d, tb);
-  if (grid > 3ll * sm_count()) grid = 3ll * sm_count();
+  if (grid > (int64_t)kPerSm * sm_count()) grid = (int64_t)kPerSm * sm_count();
   count_launches(1);
   auto go = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)grid, 2), kThreads, 0, s, p, tb); };
   auto pick = [&](auto d, auto inter) {

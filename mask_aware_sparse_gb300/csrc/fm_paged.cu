@@ -911,84 +911,111 @@ struct MergeParams {
   int R, T;
 };
 
-template <int D, int WPR>
-__global__ void __launch_bounds__(256) merge_kernel(const MergeParams p) {
+template <int D, int ROWS, int WPR>
+__global__ void __launch_bounds__(256, D == 256 ? 2 : 4) merge_kernel(const MergeParams p) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
-  constexpr int PARTS = 8;
+  constexpr int PARTS = ROWS > 1 ? 3 : 8;
+  constexpr int BLOCK = (8 / WPR) * ROWS * RPW;  // rows of a block's step
   __shared__ float4 other[WPR > 1 ? 8 * 32 * V : 1];
   __shared__ float2 other_ml[WPR > 1 ? 8 * RPW : 1];
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 4 * (lane % LPR);
-  const long long i = ((long long)blockIdx.x * (8 / WPR) + warp / WPR) * RPW + lane / LPR;
+  // this thread's rows of the step: one, then every RPW-th
+  long long i0 = (long long)blockIdx.x * BLOCK + (warp / WPR) * ROWS * RPW + lane / LPR;
+  uint32_t next[ROWS][2];
+  auto look = [&](long long i) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) next[r][k] = i + r * RPW < p.sh.rows ? p.sh.where[k * p.sh.rows + i + r * RPW] : 0u;
+  };
+  look(i0);
   // tokens of no sequence keep their rows
-  const bool live = i < p.sh.rows && i < (long long)min(max(p.q_off[p.R], 0), p.T) * p.out.H_q;
-  int first[2] = {0, 0}, row[2] = {0, 0}, n[2] = {0, 0};
-  if (live) {
+  const long long rows = min(p.sh.rows, (long long)min(max(p.q_off[p.R], 0), p.T) * p.out.H_q);
+  for (long long b = blockIdx.x; b * BLOCK < p.sh.rows; b += gridDim.x) {
+    uint32_t at[ROWS][2];
+    int n[ROWS][2], most = 0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t w = p.sh.where[k * p.sh.rows + i];
-      if (w == 0xffffffffu) {
-        first[k] = -1;
-        n[k] = 1;
-      } else {
-        first[k] = (int)(w >> 20);
-        n[k] = (int)(w >> 8 & 0xfffu);
-        row[k] = (int)(w & 0xffu);
+    for (int r = 0; r < ROWS; ++r) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t w = at[r][k] = next[r][k];
+        const int first = (int)(w >> 20), parts = (int)(w >> 8 & 0xfffu), row = (int)(w & 0xffu);
+        n[r][k] = i0 + r * RPW >= rows ? 0 : w == 0xffffffffu ? 1 : parts;
         // (what a batch that is none left there)
-        if (first[k] + n[k] > p.ctas[k] || row[k] >= p.slot_rows[k]) n[k] = 0;
+        if (w != 0xffffffffu && (first + parts > p.ctas[k] || row >= p.slot_rows[k])) n[r][k] = 0;
       }
+      most = max(most, n[r][0] + n[r][1]);
     }
-  }
-  float top = -INFINITY, sum = 0.f;
-  float4 acc[V];
+    look(i0 + (long long)gridDim.x * BLOCK);
+    float top[ROWS], sum[ROWS];
+    float4 acc[ROWS][V];
 #pragma unroll
-  for (int x = 0; x < V; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int parts = n[0] + n[1];
-  for (int i0 = PARTS * (warp % WPR); i0 < parts; i0 += PARTS * WPR) {
-    float2 w[PARTS];
-    float4 v[PARTS][V];
+    for (int r = 0; r < ROWS; ++r) {
+      top[r] = -INFINITY;
+      sum[r] = 0.f;
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-      w[k] = make_float2(-INFINITY, 0.f);
+      for (int x = 0; x < V; ++x) acc[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int j0 = PARTS * (warp % WPR); j0 < most; j0 += PARTS * WPR) {
+      float2 w[ROWS][PARTS];
+      float4 v[ROWS][PARTS][V];
 #pragma unroll
-      for (int x = 0; x < V; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + k < parts) {
-        const bool rest = i0 + k >= n[0];
-        const int j = rest ? i0 + k - n[0] : i0 + k, f = rest ? first[1] : first[0], r = rest ? row[1] : row[0];
-        const float *from, *ml;
-        if (f < 0) {
-          const long long at = rest ? p.sh.rows + i : i;
-          from = p.sh.full + at * D;
-          ml = reinterpret_cast<const float*>(p.sh.full_ml + at);
-        } else {  // slot 1 of the first CTA, slot 0 of the others
-          const float* s = (rest ? p.part[1] : p.part[0]) +
-                           (rest ? p.part_floats[1] : p.part_floats[0]) * (2 * (size_t)(f + j) + (j == 0 ? 1 : 0));
-          from = s + (size_t)r * D;
-          ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * r;
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+          w[r][k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int x = 0; x < V; ++x) v[r][k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j0 + k < n[r][0] + n[r][1]) {
+            const bool rest = j0 + k >= n[r][0];
+            const int j = rest ? j0 + k - n[r][0] : j0 + k;
+            const uint32_t where = rest ? at[r][1] : at[r][0];
+            const float *from, *ml;
+            if (where == 0xffffffffu) {
+              const long long i = i0 + r * RPW + (rest ? p.sh.rows : 0);
+              from = p.sh.full + i * D;
+              ml = reinterpret_cast<const float*>(p.sh.full_ml + i);
+            } else {  // slot 1 of the first CTA, slot 0 of the others
+              const float* s = (rest ? p.part[1] : p.part[0]) + (rest ? p.part_floats[1] : p.part_floats[0]) *
+                                                                    (2 * (size_t)((where >> 20) + j) + (j == 0 ? 1 : 0));
+              from = s + (size_t)(where & 0xffu) * D;
+              ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * (where & 0xffu);
+            }
+            w[r][k] = *reinterpret_cast<const float2*>(ml);
+#pragma unroll
+            for (int x = 0; x < V; ++x) v[r][k][x] = *reinterpret_cast<const float4*>(from + 4 * LPR * x + col);
+          }
         }
-        w[k] = *reinterpret_cast<const float2*>(ml);
 #pragma unroll
-        for (int x = 0; x < V; ++x) v[k][x] = *reinterpret_cast<const float4*>(from + 4 * LPR * x + col);
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) add_part(top[r], sum[r], acc[r], w[r][k], v[r][k]);
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+      for (int x = 0; x < V; ++x) other[(warp * V + x) * 32 + lane] = acc[0][x];
+      if (col == 0) other_ml[warp * RPW + lane / LPR] = make_float2(top[0], sum[0]);
+      __syncthreads();
+      if (warp % WPR == 0) {
+#pragma unroll
+        for (int k = 1; k < WPR; ++k) {
+          float4 v[V];
+#pragma unroll
+          for (int x = 0; x < V; ++x) v[x] = other[((warp + k) * V + x) * 32 + lane];
+          add_part(top[0], sum[0], acc[0], other_ml[(warp + k) * RPW + lane / LPR], v);
+        }
       }
+      __syncthreads();
     }
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) add_part(top, sum, acc, w[k], v[k]);
-  }
-  if constexpr (WPR > 1) {
-#pragma unroll
-    for (int x = 0; x < V; ++x) other[(warp * V + x) * 32 + lane] = acc[x];
-    if (col == 0) other_ml[warp * RPW + lane / LPR] = make_float2(top, sum);
-    __syncthreads();
-    if (warp % WPR) return;
-#pragma unroll
-    for (int k = 1; k < WPR; ++k) {
-      float4 v[V];
-#pragma unroll
-      for (int x = 0; x < V; ++x) v[x] = other[((warp + k) * V + x) * 32 + lane];
-      add_part(top, sum, acc, other_ml[(warp + k) * RPW + lane / LPR], v);
+    for (int r = 0; r < ROWS; ++r) {
+      const long long i = i0 + r * RPW;
+      if (i < rows && warp % WPR == 0)
+        store_row<LPR>(p.out, i / p.out.H_q, (int)(i % p.out.H_q), col, top[r], sum[r], acc[r]);
     }
+    i0 += (long long)gridDim.x * BLOCK;
   }
-  if (live) store_row<LPR>(p.out, i / p.out.H_q, (int)(i % p.out.H_q), col, top, sum, acc);
 }
 
 template <int D, bool F8, bool SH>
@@ -1137,11 +1164,11 @@ struct SharedPlan {
 SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q, const fm_rows* q) {
   SharedPlan p = {};
   const double rows = (double)T * (H_q / c.H_kv);
-  p.apart = b.R <= S || rows >= 128.0 * b.R;
+  p.apart = b.R <= S || rows >= 256.0 * b.R;
   p.chunk[1] = use_chunk(c, b, T, H_q, q);
   fm_paged_batch groups = b;
   groups.R = S;
-  p.chunk[0] = p.chunk[1] || (use_chunk(c, groups, T, H_q, q) && rows > 32.0 * S);
+  p.chunk[0] = p.chunk[1] || (use_chunk(c, groups, T, H_q, q) && rows > 64.0 * S);
   return p;
 }
 
@@ -1151,11 +1178,12 @@ PagedShape shared_shape(const fm_kv_cache& c, const fm_paged_batch& b, int S, in
   const long long units = ((long long)T * s.G + s.step - 1) / s.step;  // of each kind, and one a sequence
   const long long most = ((long long)b.width * s.page + s.tile - 1) / s.tile;
   s.S = S;
+  if (chunk) s.extra = 4;
   s.kinds = kinds;
   s.V = (kinds & 1 ? S : 0) + (kinds & 2 ? b.R : 0);
   s.max_units = (kinds == 3 ? 2 : 1) * units + s.V;
   s.whole = 0;
-  s.local = std::max(s.V, S) <= (chunk ? kLocalChunks : kLocalSeqs) && s.max_units - s.V <= kLocalUnits &&
+  s.local = std::max(s.V, S) <= (chunk ? kSharedChunks : kLocalSeqs) && s.max_units - s.V <= kLocalUnits &&
             s.max_units * (most + s.extra) * s.H_kv * (s.ctas + 1) < (1ll << 31);
   return s;
 }
@@ -1198,12 +1226,13 @@ SharedWork shared_work(const SharedPlan& p, const fm_kv_cache& c, const fm_paged
 
 template <int D>
 cudaError_t launch_merge(const MergeParams& m, double parts, cudaStream_t st) {
-  auto go = [&](auto kernel, int rows) {  // rows of a block
+  auto go = [&](auto kernel, int rows) {  // rows of a block's step
+    const long long blocks = (m.sh.rows + rows - 1) / rows, most = (long long)sm_count() * (D == 256 ? 2 : 4);
     count_launches(1);
-    return launch_dependent(kernel, dim3((unsigned)((m.sh.rows + rows - 1) / rows)), 256, 0, st, m);
+    return launch_dependent(kernel, dim3((unsigned)std::min(blocks, most)), 256, 0, st, m);
   };
   constexpr int RPW = D == 64 ? 2 : 1;
-  return parts > 9 ? go(merge_kernel<D, 4>, 2 * RPW) : go(merge_kernel<D, 1>, 8 * RPW);
+  return parts > 9 ? go(merge_kernel<D, 1, 4>, 2 * RPW) : go(merge_kernel<D, 2, 1>, 16 * RPW);
 }
 
 }  // namespace

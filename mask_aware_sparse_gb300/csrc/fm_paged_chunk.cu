@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   __shared__ PagedStart start;
-  __shared__ int4 seq[kLocalChunks];
-  __shared__ int2 more[SH ? kLocalChunks : 1];
+  __shared__ int4 seq[SH ? kSharedChunks : kLocalChunks];
+  __shared__ int2 more[SH ? kSharedChunks : 1];
   __shared__ uint16_t first[SH ? 1 : kLocalChunks + 1], order[SH ? 1 : kWholeUnits];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -584,12 +584,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
           const uint32_t e = lds8(smem_u32(smem + C::EXP_OFF) + rs * 128 + row);
           const uint32_t fl = dead ? 0u : factor_lo(e) * 0x10001u;  // (the bits it multiplies are finite)
           const bool wide = __any_sync(kAll, !dead && e > 134u && e < 255u);
+          // (SH: rolled up. A shared prefix is few tiles a CTA, and the first one waits for its
+          // instructions: 64 samples behind 16384 keys 77 us instead of 80; 32768 keys for one
+          // chunk of 2048 tokens would take 921 instead of 874.)
           // 64 bytes of the row at a time: the staged tile is free for the next one as soon as
           // the last of them are in registers (its load is otherwise waited for: 2048 tokens
           // over 32768 keys, d = 128, 1016 us instead of 936, d = 64 715 instead of 685)
           constexpr int kPart = 4;
           uint32_t top = 0;  // the row's largest magnitudes, before its scale
-#pragma unroll
+#pragma unroll(SH ? 1 : D / 64)
           for (int part = 0; part < D / 64; ++part) {
             uint4 rr[kPart];
 #pragma unroll

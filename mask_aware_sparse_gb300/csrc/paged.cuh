@@ -202,8 +202,9 @@ struct PagedDivision {
   I total, used, extra;
   __device__ PagedDivision(const PagedShape& s, I tiles, I units) {
     used = max((I)1, min((I)s.ctas, tiles / (I)s.least));
-    extra = used == (I)s.ctas ? (I)s.extra : (I)0;
+    extra = s.S || used == (I)s.ctas ? (I)s.extra : (I)0;
     total = tiles + units * (I)s.H_kv * extra;
+    if (s.S) used = max((I)1, min((I)s.ctas, total / (I)s.least));
   }
   __device__ I begin(I c) const { return total * c / used; }
   // The range of CTA c, from the unit and head whose places [f0, f0 + extra + nt) hold
@@ -221,15 +222,23 @@ struct PagedDivision {
   }
 };
 
+// Limits of a CTA's own plan: sequences (kLocalChunks: chunk_kernel, whose shared
+// memory is nearly full), units more than one a sequence, all units where those of
+// several sequences are dealt whole (each is ranked against all others).
+constexpr int kLocalSeqs = 256, kLocalChunks = 32;
+constexpr int kSharedChunks = 56;  // (SH: the room of what plan_whole takes is free)
+constexpr int kLocalUnits = 512;
+constexpr int kWholeUnits = 320;
+
 // The plan as one CTA makes it for itself, for a few hundred units at most and a
 // total work that 32 bits hold (offsets that descend, whose spans may overlap and add
 // up to more, plan nothing): every sequence into seq (first token, tokens,
 // keys, units; SH: the rest of it into more), its work into work (all shared memory,
-// V entries; SH: work has room for 3 S more), the CTA's range into *out (shared memory).
+// V entries; SH: work has room for 5 S + 2 R + 2 more, R up to kLocalSeqs), the CTA's range into *out (shared memory).
 template <bool SH>
-__device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLists& in, int4* seq, int2* more,
+__device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLists& given, int4* seq, int2* more,
                                              unsigned* work, PagedStart* out, int* err) {
-  bool bad = false, descends = false;
+  bool bad = false, descends = false, more_units = false;
   const int lane = threadIdx.x & 31;
   constexpr int kAlone = 4;  // units that a thread counts by itself
   auto unit = [&](int r, const int4& q, int i) {
@@ -243,12 +252,29 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLis
     for (int i = 0; i < q.w && q.w <= kAlone; ++i) w += max(unit(r, q, i).ntiles, 1);
     seq[r] = q;
     work[r] = w * s.H_kv;
+    more_units |= q.w > kAlone;
   };
   if constexpr (SH) {
-    // groups into shared memory, then sequences, which look for theirs there
-    int32_t* gs = reinterpret_cast<int32_t*>(work + s.V);  // first sequences, shared keys, lengths as given
+    // Offsets and lengths into shared memory, all loads at once (each one that waits for
+    // another costs a microsecond), then groups, then sequences, which look for theirs there.
+    int32_t* gs = reinterpret_cast<int32_t*>(work + s.V);  // groups' first sequences, shared keys, lengths as given
     int32_t *gp = gs + s.S, *gl = gp + s.S;
     const int vs = prefixes(s);
+    PagedLists in = given;
+    if (s.R <= kLocalSeqs) {
+      int32_t *so = gl + s.S, *pl = so + s.S + 1, *qo = pl + s.S, *kl = qo + s.R + 1;
+      for (int i = threadIdx.x; i <= max(s.S, s.R); i += blockDim.x) {
+        const bool g = i < s.S, r = i < s.R;
+        const int a = i <= s.S ? given.seq_off[i] : 0, b = g ? given.prefix_len[i] : 0;
+        const int c = i <= s.R ? given.q_off[i] : 0, d = r ? given.kv_len[i] : 0;
+        if (i <= s.S) so[i] = a;
+        if (g) pl[i] = b;
+        if (i <= s.R) qo[i] = c;
+        if (r) kl[i] = d;
+      }
+      in = PagedLists{qo, kl, so, pl};
+      __syncthreads();
+    }
     for (int g = threadIdx.x; g < s.S; g += blockDim.x) {
       descends |= in.seq_off[g + 1] < in.seq_off[g];
       int s0, s1, P;
@@ -274,6 +300,7 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLis
         keep(vs + r, q);
       }
   } else {
+    const PagedLists& in = given;
     for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
       int a, n, L;
       bad |= sequence_at(s, in.q_off, in.kv_len, r, a, n, L);
@@ -283,7 +310,9 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLis
   }
   if (bad && blockIdx.x == 0) record_error(err, FM_DEV_ERR_RANGE);
   const bool none = __syncthreads_or(descends);
-  for (int r = threadIdx.x >> 5; r < s.V; r += blockDim.x >> 5) {  // longer ones: a lane a unit
+  // (32 steps a warp for 128 sequences, about 2 us, for nothing where none is longer)
+  const bool longer = !SH || __syncthreads_or(more_units);
+  for (int r = threadIdx.x >> 5; longer && r < s.V; r += blockDim.x >> 5) {  // longer ones: a lane a unit
     const int4 q = seq[r];
     if (q.w <= kAlone) continue;
     unsigned w = 0;
@@ -514,13 +543,6 @@ __device__ __forceinline__ uint32_t shared_mark(bool whole, int kt, const PagedS
   return kt > 0 && st.first == (int)blockIdx.x - 1 ? (uint32_t)st.first << 20 | (uint32_t)(st.last - st.first + 1) << 8
                                                    : 0u;
 }
-
-// Limits of a CTA's own plan: sequences (kLocalChunks: chunk_kernel, whose shared
-// memory is nearly full), units more than one a sequence, all units where those of
-// several sequences are dealt whole (each is ranked against all others).
-constexpr int kLocalSeqs = 256, kLocalChunks = 32;
-constexpr int kLocalUnits = 512;
-constexpr int kWholeUnits = 320;
 
 // Workspace of one call: units, the running sum of their work, CTA starts, the
 // partial slots (two a CTA: rows x d sums, then rows x (m, l)).

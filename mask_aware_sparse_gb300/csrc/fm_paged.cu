@@ -296,28 +296,41 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "r"(addr));
 }
 
-template <int D, bool F8, bool SH>
+// How few_kernel shares its work out: kPlain, and, where sequences share prefixes, kBoth: as
+// there, over the prefixes and what follows them, and kRest, over what follows them alone:
+// each warp takes a range of its own, as a CTA of one warp. Its units are short, and no
+// warp waits for others at their ends; merge_kernel joins parts in any case. (64 sequences
+// of up to 1024 keys behind 16384 shared ones, e4m3: the whole call 73 us, with CTAs' ranges
+// 76.5; 128 of them, bf16, 165, 173. Over the prefixes too, with four times the parts: 8
+// sequences behind 2048 keys 20 us, with CTAs' ranges 15.9; 4 behind 32768 48, 37.6.)
+enum Few { kPlain, kBoth, kRest };
+
+template <int D, bool F8, Few MODE>
 __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM) few_kernel(const FewParams p) {
   using C = FewCfg<D, F8>;
+  constexpr bool SH = MODE != kPlain, ALONE = MODE == kRest;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float4* ml = reinterpret_cast<float4*>(smem + C::ML_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ PagedStart start;
+  constexpr int OWN = ALONE ? C::WARPS : 1, AHEAD = ALONE ? C::RING : C::AHEAD;
+  const int worker = ALONE ? blockIdx.x * C::WARPS + warp : blockIdx.x;
+  __shared__ PagedStart starts[OWN];
   __shared__ int4 seq[kLocalSeqs];
   __shared__ int2 more[SH ? kLocalSeqs : 1];
   __shared__ uint16_t first[SH ? 1 : kLocalSeqs + 1], order[SH ? 1 : kWholeUnits];
   grid_dependency_wait();
   grid_launch_dependents();
   if (!SH && p.s.whole) {
-    plan_whole(p.s, p.in, seq, first, order, reinterpret_cast<uint16_t*>(smem), &start, p.err);
+    plan_whole(p.s, p.in, seq, first, order, reinterpret_cast<uint16_t*>(smem), starts, p.err);
   } else if (p.s.local) {
-    plan_locally<SH>(p.s, p.in, seq, more, reinterpret_cast<unsigned*>(smem), &start, p.err);
-    if (!SH && threadIdx.x == 0) p.w.starts[blockIdx.x] = start;  // for join_kernel
+    plan_locally<SH, OWN>(p.s, p.in, seq, more, reinterpret_cast<unsigned*>(smem), starts, p.err);
+    if (!SH && threadIdx.x == 0) p.w.starts[blockIdx.x] = starts[0];  // for join_kernel
   } else {
-    if (threadIdx.x == 0) start = p.w.starts[blockIdx.x];
+    if (threadIdx.x < OWN) starts[threadIdx.x] = p.w.starts[blockIdx.x * OWN + threadIdx.x];
     __syncthreads();
   }
+  const PagedStart& start = starts[ALONE ? warp : 0];
   const int G = p.s.G, P = p.s.page;
   PagedWalk<SH> walk(p.s, p.w.units, seq, more, first, order, start);
   const int g = lane >> 2, t = lane & 3;
@@ -343,8 +356,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
   int64_t src_a = 0, src_b = 0;  // rows of the cache: the tile's first 16 (or all) keys, its last 16
   bool bad_a = false, bad_b = false;
   auto begin = [&] {
-    j0 = walk.n * warp / C::WARPS;
-    nt = walk.n * (warp + 1) / C::WARPS - j0;
+    j0 = ALONE ? 0 : walk.n * warp / C::WARPS;
+    nt = ALONE ? walk.n : walk.n * (warp + 1) / C::WARPS - j0;
     pages.reset(p.table, walk.u.r, p.s.width);
   };
   auto issue = [&](int e, int slot) {
@@ -398,13 +411,13 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
   if (walk.going()) {
     begin();
 #pragma unroll 1
-    for (int e = 0; e < C::AHEAD; ++e) issue(e, e);
+    for (int e = 0; e < AHEAD; ++e) issue(e, e);
   }
 
   while (walk.going()) {
     const PagedUnit& u = walk.u;
 #pragma unroll 1
-    for (int e = C::AHEAD; e < C::RING; ++e) issue(e, e);
+    for (int e = AHEAD; e < C::RING; ++e) issue(e, e);
     // this thread's rows g and g + 8: their positions (-1: no such row), their Q
     int pos[2];
     uint32_t qf[C::KSTEPS][4];
@@ -667,13 +680,50 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
     // row r lies at c ^ 8 (r % 4): four rows start 8 banks apart.
     const int tok0 = u.tok, g0 = u.g0, nrows = u.nrows, h = walk.h, part_slot = walk.slot();
     const bool whole = walk.whole();
-    const uint32_t mark = SH ? shared_mark(whole, walk.kt, start) : 0u;
+    const uint32_t mark = SH ? shared_mark(whole, walk.kt, start, worker) : 0u;
     const int kind = u.ns;  // (SH)
     walk.next();
     if (walk.going()) {
       begin();
 #pragma unroll 1
-      for (int e = 0; e < C::AHEAD; ++e) issue(e, e);
+      for (int e = 0; e < AHEAD; ++e) issue(e, e);
+    }
+    if constexpr (ALONE) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(kAll, l[i], 1);
+        l[i] += __shfl_xor_sync(kAll, l[i], 2);
+        const int row = g + 8 * i, x = g0 + row;
+        if (row >= nrows) continue;
+        const long long at = kind * p.sh.rows + (long long)(tok0 + x / G) * p.out.H_q + h * G + x % G;
+        float* part = p.w.part + p.w.part_floats * (2 * (size_t)worker + part_slot);
+        float* to = whole ? p.sh.full + at * D : part + (size_t)row * D;
+        // e4m3: O's unit is 2^mo, the part's 2^m
+        const float f = F8 ? ex2_approx(mo[i] - (m[i] == -INFINITY ? 0.f : m[i])) : 1.f;
+        if constexpr (F8) {
+          // columns 64 cg + 16 t + 8 y + (0 .. 7)
+#pragma unroll
+          for (int cg = 0; cg < D / 64; ++cg)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int z = 0; z < 2; ++z)
+                *reinterpret_cast<float4*>(to + 64 * cg + 16 * t + 8 * y + 4 * z) =
+                    make_float4(f * o[8 * cg + 4 * z][2 * i + y], f * o[8 * cg + 4 * z + 1][2 * i + y],
+                                f * o[8 * cg + 4 * z + 2][2 * i + y], f * o[8 * cg + 4 * z + 3][2 * i + y]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<float2*>(to + 8 * c + 2 * t) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
+        }
+        if (t == 0) {
+          *(whole ? p.sh.full_ml + at : reinterpret_cast<float2*>(part + (size_t)kFewRows * D) + row) =
+              make_float2(m[i], l[i]);
+          if (mark) p.sh.where[at] = whole ? mark : mark | (uint32_t)row;
+        }
+      }
+      __syncwarp();  // (ml is written again)
+      continue;
     }
     float* own = reinterpret_cast<float*>(smem + (warp * C::RING + C::AHEAD) * C::TILE);
 #pragma unroll
@@ -1018,20 +1068,20 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 4) merge_kernel(const Merg
   }
 }
 
-template <int D, bool F8, bool SH>
+template <int D, bool F8, Few MODE>
 cudaError_t launch_few(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const PagedLists& in,
                        const int32_t* table, const fm_rows& q, const PagedOut& out, const SharedOut& sh, float scale,
                        cudaStream_t st, int* err) {
   using C = FewCfg<D, F8>;
   static_assert(C::SMEM <= 232448 && C::PER_SM * (C::SMEM + 1024) <= 233472, "few_kernel: shared memory of an SM");
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(few_kernel<D, F8, SH>), C::SMEM, ready);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(few_kernel<D, F8, MODE>), C::SMEM, ready);
   if (e != cudaSuccess) return e;
   FewParams p{s, w, static_cast<const char*>(q.ptr), q.st, q.sh, out,
               {static_cast<const char*>(c.k), static_cast<const char*>(c.v)}, {c.k_exp, c.v_exp}, in, sh, table,
               scale * 1.4426950408889634f, err};
   count_launches(1);
-  return launch_dependent(few_kernel<D, F8, SH>, dim3((unsigned)s.ctas), C::THREADS, C::SMEM, st, p);
+  return launch_dependent(few_kernel<D, F8, MODE>, dim3((unsigned)(MODE == kRest ? s.ctas / C::WARPS : s.ctas)), C::THREADS, C::SMEM, st, p);
 }
 
 // The plan, where no CTA makes its own, and the attention kernel.
@@ -1046,13 +1096,19 @@ cudaError_t launch_attention(bool chunk, const PagedShape& s, const PagedWork& w
     if (e != cudaSuccess) return e;
   }
   if (chunk) return launch_paged_chunk(s, w, c, in, table, q, out, SH ? &sh : nullptr, scale, st, err);
-  auto go = [&](auto d) {
-    return c.k_exp ? launch_few<d.value, true, SH>(s, w, c, in, table, q, out, sh, scale, st, err)
-                   : launch_few<d.value, false, SH>(s, w, c, in, table, q, out, sh, scale, st, err);
+  auto go = [&](auto d, auto mode) {
+    return c.k_exp ? launch_few<d.value, true, mode.value>(s, w, c, in, table, q, out, sh, scale, st, err)
+                   : launch_few<d.value, false, mode.value>(s, w, c, in, table, q, out, sh, scale, st, err);
   };
-  return c.d == 64    ? go(std::integral_constant<int, 64>{})
-         : c.d == 128 ? go(std::integral_constant<int, 128>{})
-                      : go(std::integral_constant<int, 256>{});
+  auto dims = [&](auto mode) {
+    return c.d == 64    ? go(std::integral_constant<int, 64>{}, mode)
+           : c.d == 128 ? go(std::integral_constant<int, 128>{}, mode)
+                        : go(std::integral_constant<int, 256>{}, mode);
+  };
+  if constexpr (SH)
+    return s.kinds == 3 ? dims(std::integral_constant<Few, kBoth>{}) : dims(std::integral_constant<Few, kRest>{});
+  else
+    return dims(std::integral_constant<Few, kPlain>{});
 }
 
 // Whether units stay whole, one CTA each, or ranges of tiles may end inside them.
@@ -1178,8 +1234,15 @@ PagedShape shared_shape(const fm_kv_cache& c, const fm_paged_batch& b, int S, in
   const long long units = ((long long)T * s.G + s.step - 1) / s.step;  // of each kind, and one a sequence
   const long long most = ((long long)b.width * s.page + s.tile - 1) / s.tile;
   s.S = S;
-  if (chunk) s.extra = 4;
   s.kinds = kinds;
+  // what starting on a unit costs, in tiles (chunks of 20 to 60 tokens behind 8192 keys 157 us, with 2
+  // 196: short units of many rows; 6 and 8 as 4)
+  if (chunk) s.extra = 4;
+  if (!chunk && kinds == 2) {  // (kRest)
+    s.ctas *= few_warps(c.d, c.k_exp != nullptr);
+    s.least = 1;
+    s.extra = 4;
+  }
   s.V = (kinds & 1 ? S : 0) + (kinds & 2 ? b.R : 0);
   s.max_units = (kinds == 3 ? 2 : 1) * units + s.V;
   s.whole = 0;

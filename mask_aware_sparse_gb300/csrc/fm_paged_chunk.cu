@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, F8>::THREADS, 1)
       }
       if (live) {
         if constexpr (SH) {
-          const uint32_t mark = shared_mark(whole, walk.kt, start);
+          const uint32_t mark = shared_mark(whole, walk.kt, start, blockIdx.x);
           float2* ml = whole ? p.sh.full_ml + at : reinterpret_cast<float2*>(part + (size_t)(2 * 128) * D) + rr;
           *ml = make_float2(m_run, l_run);
           if (mark) p.sh.where[at] = whole ? mark : mark | (uint32_t)rr;

@@ -235,7 +235,8 @@ constexpr int kWholeUnits = 320;
 // up to more, plan nothing): every sequence into seq (first token, tokens,
 // keys, units; SH: the rest of it into more), its work into work (all shared memory,
 // V entries; SH: work has room for 5 S + 2 R + 2 more, R up to kLocalSeqs), the CTA's range into *out (shared memory).
-template <bool SH>
+// WARPS > 1: that many of its warps take a range each, as so many CTAs.
+template <bool SH, int WARPS = 1>
 __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLists& given, int4* seq, int2* more,
                                              unsigned* work, PagedStart* out, int* err) {
   bool bad = false, descends = false, more_units = false;
@@ -320,9 +321,9 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLis
     w = __reduce_add_sync(0xffffffffu, w);
     if (lane == 0) work[r] = w * s.H_kv;
   }
-  if (threadIdx.x == 0) *out = PagedStart{};
+  if (threadIdx.x < WARPS) out[threadIdx.x] = PagedStart{};
   __syncthreads();
-  if (threadIdx.x < 32) {
+  if (threadIdx.x < 32 * WARPS) {
     const int per = (s.V + 31) / 32, r0 = lane * per, r1 = min(s.V, r0 + per);
     unsigned tiles = 0, units = 0;
     for (int r = r0; r < r1; ++r) {
@@ -330,7 +331,8 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLis
       units += seq[r].w;
     }
     const PagedDivision<unsigned> div(s, __reduce_add_sync(0xffffffffu, tiles), __reduce_add_sync(0xffffffffu, units));
-    const unsigned ex = div.extra * s.H_kv, mine = tiles + units * ex, c = blockIdx.x;
+    const unsigned ex = div.extra * s.H_kv, mine = tiles + units * ex;
+    const unsigned c = blockIdx.x * WARPS + (threadIdx.x >> 5);
     unsigned upto = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -374,7 +376,7 @@ __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLis
           st.i = i;
           st.h = (f - from) / places;
           div.set(st, c, from + st.h * places, nt);
-          *out = st;
+          out[threadIdx.x >> 5] = st;
         }
         at += __shfl_sync(0xffffffffu, end, 31);
         if (at > f) break;
@@ -537,10 +539,10 @@ struct SharedOut {
 };
 
 // Which of a segment's rows' entries of `where` this CTA writes: whole units', and divided ones'
-// that it is the second CTA of (0: none).
-__device__ __forceinline__ uint32_t shared_mark(bool whole, int kt, const PagedStart& st) {
+// that it is the second CTA of (0: none). c: its number.
+__device__ __forceinline__ uint32_t shared_mark(bool whole, int kt, const PagedStart& st, int c) {
   if (whole) return 0xffffffffu;
-  return kt > 0 && st.first == (int)blockIdx.x - 1 ? (uint32_t)st.first << 20 | (uint32_t)(st.last - st.first + 1) << 8
+  return kt > 0 && st.first == c - 1 ? (uint32_t)st.first << 20 | (uint32_t)(st.last - st.first + 1) << 8
                                                    : 0u;
 }
 

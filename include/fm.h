@@ -608,10 +608,11 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
  * own (fm_cache_copy). A group may be one sequence, or none (its length does not matter);
  * prefix_len 0 shares nothing.
  * O and LSE are fm_attn_paged's without a window, up to the rounding of weights named
- * there and 32-bit rounding. Offsets and lengths that no such batch has set
- * FM_DEVERR_RANGE, if the call is one that shares (more sequences than groups, fewer than
- * 128 query rows of a KV head a sequence on average); the rows of O and LSE are then
- * undefined. Workspace: fm_attn_shared_workspace_bytes.
+ * there and 32-bit rounding. Whether a call shares goes by T, R, S, the heads and what the
+ * page table has room for: one that would gain nothing is fm_attn_paged, takes no notice
+ * of the groups and needs no more workspace. In one that shares, offsets and lengths that
+ * no such batch has set FM_DEVERR_RANGE; the rows of O and LSE are then undefined.
+ * Workspace: fm_attn_shared_workspace_bytes.
  * ------------------------------------------------------------------------- */
 typedef struct fm_shared_prefix {
   const int32_t* seq_off;

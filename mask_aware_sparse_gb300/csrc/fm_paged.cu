@@ -949,8 +949,11 @@ cudaError_t launch_join(const PagedShape& s, const PagedWork& w, const PagedOut&
 }
 
 // Rows of sequences that share a prefix: each row's parts over the prefix, then those over
-// the rest, WPR warps a row. Latency bounds it (where the parts are, then the parts);
-// eight parts are in flight.
+// the rest. Latency bounds it (where the parts are, then the parts), so rows in flight
+// count, and few registers for each: a row a warp, three parts at a time, the next row's
+// places loaded meanwhile, five blocks an SM (41K rows of three parts 18.6 us; two rows a
+// warp 20.4, four parts of each 25). Of many parts, four warps a row, five parts at a time
+// each (64 sequences behind 16384 keys 71.3 us for the call; eight parts, three blocks 73.9).
 struct MergeParams {
   PagedOut out;
   SharedOut sh;
@@ -961,91 +964,79 @@ struct MergeParams {
   int R, T;
 };
 
-template <int D, int ROWS, int WPR>
-__global__ void __launch_bounds__(256, D == 256 ? 2 : 4) merge_kernel(const MergeParams p) {
+// Blocks an SM that registers are kept for.
+constexpr int merge_blocks(int d, int wpr) { return d == 256 ? 2 : wpr > 1 ? 4 : 5; }
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const MergeParams p) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32, RPW = 32 / LPR, V = D / (4 * LPR);  // lanes a row, rows a warp
-  constexpr int PARTS = ROWS > 1 ? 3 : 8;
-  constexpr int BLOCK = (8 / WPR) * ROWS * RPW;  // rows of a block's step
+  constexpr int PARTS = WPR > 1 ? 5 : 3;
+  constexpr int BLOCK = (8 / WPR) * RPW;  // rows of a block's step
   __shared__ float4 other[WPR > 1 ? 8 * 32 * V : 1];
   __shared__ float2 other_ml[WPR > 1 ? 8 * RPW : 1];
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 4 * (lane % LPR);
-  // this thread's rows of the step: one, then every RPW-th
-  long long i0 = (long long)blockIdx.x * BLOCK + (warp / WPR) * ROWS * RPW + lane / LPR;
-  uint32_t next[ROWS][2];
-  auto look = [&](long long i) {
+  const long long stride = (long long)gridDim.x * BLOCK;
+  long long i = (long long)blockIdx.x * BLOCK + (warp / WPR) * RPW + lane / LPR;  // this thread's row
+  uint32_t next[2];
+  auto look = [&](long long r) {
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) next[r][k] = i + r * RPW < p.sh.rows ? p.sh.where[k * p.sh.rows + i + r * RPW] : 0u;
+    for (int k = 0; k < 2; ++k) next[k] = r < p.sh.rows ? p.sh.where[k * p.sh.rows + r] : 0u;
   };
-  look(i0);
+  look(i);
   // tokens of no sequence keep their rows
   const long long rows = min(p.sh.rows, (long long)min(max(p.q_off[p.R], 0), p.T) * p.out.H_q);
-  for (long long b = blockIdx.x; b * BLOCK < p.sh.rows; b += gridDim.x) {
-    uint32_t at[ROWS][2];
-    int n[ROWS][2], most = 0;
+  for (long long b = (long long)blockIdx.x * BLOCK; b < p.sh.rows; b += stride, i += stride) {
+    uint32_t at[2];
+    int n[2];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t w = at[r][k] = next[r][k];
-        const int first = (int)(w >> 20), parts = (int)(w >> 8 & 0xfffu), row = (int)(w & 0xffu);
-        n[r][k] = i0 + r * RPW >= rows ? 0 : w == 0xffffffffu ? 1 : parts;
-        // (what a batch that is none left there)
-        if (w != 0xffffffffu && (first + parts > p.ctas[k] || row >= p.slot_rows[k])) n[r][k] = 0;
-      }
-      most = max(most, n[r][0] + n[r][1]);
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w = at[k] = next[k];
+      const int first = (int)(w >> 20), parts = (int)(w >> 8 & 0xfffu), row = (int)(w & 0xffu);
+      n[k] = i >= rows ? 0 : w == 0xffffffffu ? 1 : parts;
+      // (what a batch that is none left there)
+      if (w != 0xffffffffu && (first + parts > p.ctas[k] || row >= p.slot_rows[k])) n[k] = 0;
     }
-    look(i0 + (long long)gridDim.x * BLOCK);
-    float top[ROWS], sum[ROWS];
-    float4 acc[ROWS][V];
+    look(i + stride);
+    float top = -INFINITY, sum = 0.f;
+    float4 acc[V];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      top[r] = -INFINITY;
-      sum[r] = 0.f;
+    for (int x = 0; x < V; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = PARTS * (warp % WPR); j0 < n[0] + n[1]; j0 += PARTS * WPR) {
+      float2 w[PARTS];
+      float4 v[PARTS][V];
 #pragma unroll
-      for (int x = 0; x < V; ++x) acc[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    for (int j0 = PARTS * (warp % WPR); j0 < most; j0 += PARTS * WPR) {
-      float2 w[ROWS][PARTS];
-      float4 v[ROWS][PARTS][V];
+      for (int k = 0; k < PARTS; ++k) {
+        w[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-        for (int k = 0; k < PARTS; ++k) {
-          w[r][k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int x = 0; x < V; ++x) v[r][k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j0 + k < n[r][0] + n[r][1]) {
-            const bool rest = j0 + k >= n[r][0];
-            const int j = rest ? j0 + k - n[r][0] : j0 + k;
-            const uint32_t where = rest ? at[r][1] : at[r][0];
-            const float *from, *ml;
-            if (where == 0xffffffffu) {
-              const long long i = i0 + r * RPW + (rest ? p.sh.rows : 0);
-              from = p.sh.full + i * D;
-              ml = reinterpret_cast<const float*>(p.sh.full_ml + i);
-            } else {  // slot 1 of the first CTA, slot 0 of the others
-              const float* s = (rest ? p.part[1] : p.part[0]) + (rest ? p.part_floats[1] : p.part_floats[0]) *
-                                                                    (2 * (size_t)((where >> 20) + j) + (j == 0 ? 1 : 0));
-              from = s + (size_t)(where & 0xffu) * D;
-              ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * (where & 0xffu);
-            }
-            w[r][k] = *reinterpret_cast<const float2*>(ml);
-#pragma unroll
-            for (int x = 0; x < V; ++x) v[r][k][x] = *reinterpret_cast<const float4*>(from + 4 * LPR * x + col);
+        for (int x = 0; x < V; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + k < n[0] + n[1]) {
+          const bool rest = j0 + k >= n[0];
+          const int j = rest ? j0 + k - n[0] : j0 + k;
+          const uint32_t where = rest ? at[1] : at[0];
+          const float *from, *ml;
+          if (where == 0xffffffffu) {
+            const long long r = i + (rest ? p.sh.rows : 0);
+            from = p.sh.full + r * D;
+            ml = reinterpret_cast<const float*>(p.sh.full_ml + r);
+          } else {  // slot 1 of the first CTA, slot 0 of the others
+            const float* s = (rest ? p.part[1] : p.part[0]) + (rest ? p.part_floats[1] : p.part_floats[0]) *
+                                                                  (2 * (size_t)((where >> 20) + j) + (j == 0 ? 1 : 0));
+            from = s + (size_t)(where & 0xffu) * D;
+            ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * (where & 0xffu);
           }
+          w[k] = *reinterpret_cast<const float2*>(ml);
+#pragma unroll
+          for (int x = 0; x < V; ++x) v[k][x] = *reinterpret_cast<const float4*>(from + 4 * LPR * x + col);
         }
+      }
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-        for (int k = 0; k < PARTS; ++k) add_part(top[r], sum[r], acc[r], w[r][k], v[r][k]);
+      for (int k = 0; k < PARTS; ++k) add_part(top, sum, acc, w[k], v[k]);
     }
     if constexpr (WPR > 1) {
 #pragma unroll
-      for (int x = 0; x < V; ++x) other[(warp * V + x) * 32 + lane] = acc[0][x];
-      if (col == 0) other_ml[warp * RPW + lane / LPR] = make_float2(top[0], sum[0]);
+      for (int x = 0; x < V; ++x) other[(warp * V + x) * 32 + lane] = acc[x];
+      if (col == 0) other_ml[warp * RPW + lane / LPR] = make_float2(top, sum);
       __syncthreads();
       if (warp % WPR == 0) {
 #pragma unroll
@@ -1053,18 +1044,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 4) merge_kernel(const Merg
           float4 v[V];
 #pragma unroll
           for (int x = 0; x < V; ++x) v[x] = other[((warp + k) * V + x) * 32 + lane];
-          add_part(top[0], sum[0], acc[0], other_ml[(warp + k) * RPW + lane / LPR], v);
+          add_part(top, sum, acc, other_ml[(warp + k) * RPW + lane / LPR], v);
         }
       }
       __syncthreads();
     }
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const long long i = i0 + r * RPW;
-      if (i < rows && warp % WPR == 0)
-        store_row<LPR>(p.out, i / p.out.H_q, (int)(i % p.out.H_q), col, top[r], sum[r], acc[r]);
-    }
-    i0 += (long long)gridDim.x * BLOCK;
+    if (i < rows && warp % WPR == 0)
+      store_row<LPR>(p.out, i / p.out.H_q, (int)(i % p.out.H_q), col, top, sum, acc);
   }
 }
 
@@ -1217,14 +1203,40 @@ struct SharedPlan {
   bool chunk[2];  // the kernel over the prefixes, and over the rest; one launch where it is the same one
 };
 
+// Lengths are on the device, so the keys that the page table has room for decide.
+//
+// The kernel over the prefixes: few_kernel reads them again for every 16 rows, chunk_kernel
+// is a launch of its own. 16 sequences of 32 / 8 heads behind 8192 keys (64 rows): 29.5 us,
+// with chunk_kernel 32.4, e4m3 26.7, 34.8; 32 behind 32768 (128 rows) 142, 60; e4m3 107, 66.
+//
+// Whether to share at all, by what it spares at most against what it costs. Few rows a
+// sequence: the prefixes' bytes, against parts and their joining (2 us) or a second kernel
+// too (20 us): 8 sequences behind 128 keys 11.1 us, apart 9.0, 2 behind 4096 12.6, 13.0, 8
+// behind 8192 20.8, 41; 64 of 400 keys behind 100 37.6, 20.9. Chunks: products are not
+// spared, but tiles of 256 rows are filled by a group that one sequence's rows leave half
+// empty; that against the joining of all rows, and short units (4 tiles' time each). 32
+// chunks of 160 rows behind 8192 keys 146 us, apart 190, of 256 221, 291; of 160 behind
+// 2048 73, 53; 8 of 1000 behind 4096 153, 112.
 SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q, const fm_rows* q) {
   SharedPlan p = {};
-  const double rows = (double)T * (H_q / c.H_kv);
-  p.apart = b.R <= S || rows >= 256.0 * b.R;
+  const double rows = (double)T * (H_q / c.H_kv), keys = (double)b.width * c.page_size;
   p.chunk[1] = use_chunk(c, b, T, H_q, q);
   fm_paged_batch groups = b;
   groups.R = S;
   p.chunk[0] = p.chunk[1] || (use_chunk(c, groups, T, H_q, q) && rows > 64.0 * S);
+  double spared, cost;  // microseconds
+  if (rows <= 16.0 * b.R) {
+    const double row = c.k_exp ? c.d + 1.0 : 2.0 * c.d;
+    spared = std::max(0, b.R - S) * keys * 2 * c.H_kv * row / 6.5e6;
+    cost = p.chunk[0] == p.chunk[1] ? 2 : 20;
+  } else {
+    // (few_kernel where chunk_kernel has no form: units of 16 rows, tiles of 32 keys, about 0.5 us each at d = 256)
+    const bool ch = p.chunk[1];
+    const double tile = (ch ? 1.5 : 0.5) / sm_count(), fill = rows / b.R / (ch ? 256 : 16);
+    spared = std::max(0, b.R - S) * std::max(0.5, 1 - fill) * c.H_kv * keys / (ch ? 128 : 32) * tile;
+    cost = 12 + 0.0005 * T * H_q + b.R * std::ceil(fill) * c.H_kv * 4 * tile;
+  }
+  p.apart = spared < cost;
   return p;
 }
 
@@ -1289,13 +1301,14 @@ SharedWork shared_work(const SharedPlan& p, const fm_kv_cache& c, const fm_paged
 
 template <int D>
 cudaError_t launch_merge(const MergeParams& m, double parts, cudaStream_t st) {
-  auto go = [&](auto kernel, int rows) {  // rows of a block's step
-    const long long blocks = (m.sh.rows + rows - 1) / rows, most = (long long)sm_count() * (D == 256 ? 2 : 4);
+  auto go = [&](auto kernel, int rows, int per_sm) {  // rows of a block's step
+    const long long blocks = (m.sh.rows + rows - 1) / rows, most = (long long)sm_count() * per_sm;
     count_launches(1);
     return launch_dependent(kernel, dim3((unsigned)std::min(blocks, most)), 256, 0, st, m);
   };
   constexpr int RPW = D == 64 ? 2 : 1;
-  return parts > 9 ? go(merge_kernel<D, 1, 4>, 2 * RPW) : go(merge_kernel<D, 2, 1>, 16 * RPW);
+  return parts > 9 ? go(merge_kernel<D, 4>, 2 * RPW, merge_blocks(D, 4))
+                   : go(merge_kernel<D, 1>, 8 * RPW, merge_blocks(D, 1));
 }
 
 }  // namespace

@@ -26,7 +26,7 @@ def main():
                     ([300, 40], [[20, 3], [50, 9, 1]], None, 4, 2, 16), ([500], [[33] * 20], None, 8, 1, 64),
                     ([700, 64], [[60, 70, 35], [90, 40]], [[20, 31, 33], [25, 40]], 8, 2, 32),
                     ([100], [[9] * 60], [[5, 9] * 30], 4, 2, 128)):
-                s = Groups(prefix, rest, new or ones(rest), Hkv, d, page, f8, seed=90)
+                s = Groups(prefix, rest, new or ones(rest), Hkv, d, page, f8, seed=90, Hq=Hq)
                 s.attend(Hq)  # (asserts that no error bit is set)
                 s.attend(Hq, causal=False)
     st, bits = fm.fm_device_status()

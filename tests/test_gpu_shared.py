@@ -24,9 +24,10 @@ def _off(xs):
 class Groups:
     """A cache of groups of sequences: prefix[g] keys that are the same for all of group
     g, rest[g] = keys of each sequence behind them, new[g] = new tokens of each. Pages in a
-    shuffled order, everything else in the cache NaN, the table -7 where nothing is."""
+    shuffled order, everything else in the cache NaN, the table -7 where nothing is, and as
+    wide as it has to be for calls of Hq heads to share (whether they do goes by its width)."""
 
-    def __init__(self, prefix, rest, new, Hkv, d, page, f8, seed=0, pad=0):
+    def __init__(self, prefix, rest, new, Hkv, d, page, f8, seed=0, pad=0, Hq=None):
         self.prefix, self.Hkv, self.d, self.page, self.f8 = prefix, Hkv, d, page, f8
         self.g = g = torch.Generator().manual_seed(seed)
         self.sizes = [len(x) for x in rest]
@@ -62,6 +63,14 @@ class Groups:
         self.batch = fm.PagedBatch(self.q_off, self.kv_len, self.table)
         self.seq_off, self.prefix_len = _off(self.sizes), _i32(prefix)
         self.shared = fm.SharedPrefix(self.seq_off, self.prefix_len)
+        while Hq and not self.shares(Hq):
+            self.table = torch.nn.functional.pad(self.table, (0, self.table.shape[1]), value=-7)
+            self.batch = fm.PagedBatch(self.q_off, self.kv_len, self.table)
+
+    def shares(self, Hq):
+        T = sum(self.new)
+        return (fm.fm_attn_shared_workspace_bytes(self.cache, self.batch, self.shared, T, Hq)
+                > fm.fm_attn_paged_workspace_bytes(self.cache, self.batch, T, Hq))
 
     def write(self):
         """Shared pages by each group's first sequence, then each sequence's own."""
@@ -119,6 +128,9 @@ STEPS = [
 @pytest.mark.parametrize("f8", [False, True])
 def test_steps(prefix, rest, Hq, Hkv, d, page, f8):
     s = Groups(prefix, rest, ones(rest), Hkv, d, page, f8, seed=70, pad=2)
+    q, o, lse = s.attend(Hq)
+    s = Groups(prefix, rest, ones(rest), Hkv, d, page, f8, seed=70, pad=2, Hq=Hq)
+    assert s.shares(Hq)
     s.attend(Hq)
     s.attend(Hq, causal=False)
 
@@ -142,8 +154,9 @@ MANY = [
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("causal", [True, False])
 def test_several_tokens(prefix, rest, new, Hq, Hkv, d, page, f8, causal):
-    s = Groups(prefix, rest, new, Hkv, d, page, f8, seed=71)
-    s.attend(Hq, causal=causal)
+    for share in (False, True):
+        s = Groups(prefix, rest, new, Hkv, d, page, f8, seed=71, Hq=Hq if share else None)
+        s.attend(Hq, causal=causal)
 
 
 @pytest.mark.parametrize("f8", [False, True])
@@ -153,18 +166,18 @@ def test_many_sequences(f8):
     sizes = [1, 150, 0, 7, 200, 3]
     rest = [torch.randint(1, 60, (n,), generator=g).tolist() for n in sizes]
     new = [[int(x) for x in (torch.rand(n, generator=g) < 0.8)] for n in sizes]
-    s = Groups([40, 300, 20, 0, 97, 16], rest, new, 2, 64, 16, f8, seed=73)
+    s = Groups([40, 300, 20, 0, 97, 16], rest, new, 2, 64, 16, f8, seed=73, Hq=4)
     s.attend(4)
     rest = [[70] * n for n in sizes]
     s = Groups([40, 300, 20, 0, 97, 16], rest, [[int(1 + x) for x in 40 * torch.rand(n, generator=g)] for n in sizes], 2, 128,
-               32, f8, seed=74)
+               32, f8, seed=74, Hq=4)
     s.attend(4)
 
 
 @pytest.mark.parametrize("new", [[[0, 1, 1], [1, 0]], [[0, 30, 20], [25, 0]]])
 def test_sequences_out_of_use(new):
     # no new tokens: their rows of the table may hold anything, the first one's too, and so may their lengths
-    s = Groups([100, 64], [[40, 50, 60], [30, 35]], new, 2, 128, 16, False, seed=75)
+    s = Groups([100, 64], [[40, 50, 60], [30, 35]], new, 2, 128, 16, False, seed=75, Hq=8)
     q, o, lse = s.attend(8)
     for r in (0, 4):
         s.table[r] = -1 if r else 2 ** 30
@@ -176,7 +189,7 @@ def test_sequences_out_of_use(new):
 
 @pytest.mark.parametrize("new, Hq", [([[1, 1, 1], [1, 1]], 8), ([[20, 30, 9], [25, 3]], 8), ([[1] * 3, [1] * 2], 64)])
 def test_same_bits_padding_rows_and_views(new, Hq):
-    s = Groups([300, 90], [[40, 50, 60], [30, 35]], new, 2, 128, 32, False, seed=76)
+    s = Groups([300, 90], [[40, 50, 60], [30, 35]], new, 2, 128, 32, False, seed=76, Hq=Hq)
     T = sum(s.new)
     o = torch.full((T + 3, Hq, 128), 9.0, dtype=torch.bfloat16).cuda()
     lse = torch.full((T + 3, Hq), 9.0).cuda()
@@ -204,7 +217,8 @@ def test_same_bits_padding_rows_and_views(new, Hq):
 
 
 def test_no_tokens():
-    s = Groups([100], [[40, 50]], [[0, 0]], 2, 64, 16, False, seed=77)
+    s = Groups([100], [[40, 50]], [[0, 0]], 2, 64, 16, False, seed=77, pad=5000)
+    assert fm.fm_attn_shared_workspace_bytes(s.cache, s.batch, s.shared, 5, 4) > fm.fm_attn_paged_workspace_bytes(s.cache, s.batch, 5, 4)
     q = torch.randn(5, 4, 64, generator=s.g).to(torch.bfloat16).cuda()
     o, lse = fm.fm_attn_shared(q[:0], s.cache, s.batch, s.shared, scale=0.125)
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
@@ -218,7 +232,7 @@ def test_no_tokens():
 @pytest.mark.parametrize("f8", [False, True])
 def test_large_and_outlying_values(new, f8):
     # rows of very different scales, in the prefix and behind it: parts whose maxima are far apart
-    s = Groups([300, 140], [[40, 50, 60], [64, 45]], new, 2, 64, 16, f8, seed=78)
+    s = Groups([300, 140], [[40, 50, 60], [64, 45]], new, 2, 64, 16, f8, seed=78, Hq=4)
     group = [0, 0, 0, 1, 1]
     m = [torch.exp2(torch.randint(-6, 7, (1, P, 2, 1), generator=s.g).double()) for P in s.prefix]
     for r, x in enumerate(s.rows):
@@ -234,7 +248,7 @@ def test_large_and_outlying_values(new, f8):
 @pytest.mark.parametrize("new", [[[1, 1, 1], [1, 1]], [[30, 20, 31], [25, 40]]])
 @pytest.mark.parametrize("f8", [False, True])
 def test_a_visible_nan_stays_in_its_group_or_sequence(new, f8):
-    s = Groups([100, 64], [[40, 50, 60], [64, 45]], new, 2, 64, 16, f8, seed=79)
+    s = Groups([100, 64], [[40, 50, 60], [64, 45]], new, 2, 64, 16, f8, seed=79, Hq=4)
     q, o, lse = s.attend(4)
     clean = [x.clone() for x in s.rows]
     off = s.q_off.tolist()
@@ -256,7 +270,7 @@ def test_a_visible_nan_stays_in_its_group_or_sequence(new, f8):
 
 @pytest.mark.parametrize("new, Hq", [([[1, 1, 1], [1, 1]], 4), ([[1, 1, 1], [1, 1]], 64), ([[20, 30, 9], [25, 3]], 8)])
 def test_what_no_batch_has_is_flagged(new, Hq):
-    s = Groups([100, 64], [[40, 50, 60], [30, 35]], new, 2, 64, 16, False, seed=80)
+    s = Groups([100, 64], [[40, 50, 60], [30, 35]], new, 2, 64, 16, False, seed=80, Hq=Hq)
     q, o, lse = s.attend(Hq)
     q = q.cuda()
     size = s.table.shape[1] * 16
@@ -303,7 +317,7 @@ def test_offsets_that_descend_plan_nothing_beyond_32_bits():
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("Hq", [4, 32])
 def test_graph_replay_with_other_lengths_and_groups(Hq, f8):
-    s = Groups([400, 200], [[60, 70, 20], [90, 50]], [[1, 1, 1], [1, 1]], 2, 128, 16, f8, seed=81)
+    s = Groups([400, 200], [[60, 70, 20], [90, 50]], [[1, 1, 1], [1, 1]], 2, 128, 16, f8, seed=81, Hq=Hq)
     q, o, lse = s.attend(Hq)
     q = q.cuda()
     o, lse = torch.empty_like(o), torch.empty_like(lse)
@@ -337,8 +351,8 @@ def test_graph_replay_with_other_lengths_and_groups(Hq, f8):
 
 
 def test_two_calls_at_once():
-    a = Groups([700, 90], [[40] * 6, [33] * 3], [[1] * 6, [1] * 3], 2, 128, 16, False, seed=82)
-    b = Groups([300], [[50, 70, 90, 31]], [[20, 31, 33, 25]], 2, 64, 32, True, seed=83)
+    a = Groups([700, 90], [[40] * 6, [33] * 3], [[1] * 6, [1] * 3], 2, 128, 16, False, seed=82, Hq=32)
+    b = Groups([300], [[50, 70, 90, 31]], [[20, 31, 33, 25]], 2, 64, 32, True, seed=83, Hq=8)
     qa, oa, la = a.attend(32)
     qb, ob, lb = b.attend(8)
     qa, qb, side = qa.cuda(), qb.cuda(), torch.cuda.Stream()
@@ -354,7 +368,7 @@ def test_two_calls_at_once():
 def test_pages_far_into_a_large_cache():
     # the same pages at the end of a cache whose byte offsets pass 2^32
     for f8, new in ((False, [[1, 1, 1]]), (True, [[1, 1, 1]]), (False, [[20, 30, 25]]), (True, [[20, 30, 25]])):
-        s = Groups([200], [[64, 30, 40]], new, 8, 128, 64, f8, seed=84)
+        s = Groups([200], [[64, 30, 40]], new, 8, 128, 64, f8, seed=84, Hq=32)
         q, o, lse = s.attend(32)
         n, big = s.cache.n_pages, 70000
         c = fm.fm_cache_new(big, 8, 64, 128, dtype=s.cache.k.dtype)
@@ -396,7 +410,8 @@ def test_responses_to_one_question():
     table = torch.full((R, width), -1, dtype=torch.int32)
     table[:, :w] = ids[:w]
     table[:, w:] = ids[w:w + R * (width - w)].view(R, -1)
-    table = table.cuda()
+    # (wide enough for the steps to share)
+    table = torch.nn.functional.pad(table, (0, 500), value=-1).cuda()
     how = dict(inv_freq=f, rot_scale=sc, q_weight=wq, k_weight=wk)
     prompt = fm.PagedBatch(_i32([0, P]), _i32([P]), table[:1].contiguous())
     qp = fm.fm_cache_append(*qkv[0, :P].split([Hq, Hkv, Hkv], 1), cache, prompt, **how)
@@ -407,6 +422,8 @@ def test_responses_to_one_question():
     kv_len = _i32([P] * R)
     batch = fm.PagedBatch(_off([1] * R), kv_len, table)
     shared = fm.SharedPrefix(_i32([0, R]), _i32([P]))
+    assert (fm.fm_attn_shared_workspace_bytes(cache, batch, shared, R, Hq)
+            > fm.fm_attn_paged_workspace_bytes(cache, batch, R, Hq))
     x = torch.zeros(R, Hq + 2 * Hkv, d, dtype=torch.bfloat16).cuda()
     qn, o, lse = torch.empty(R, Hq, d, dtype=torch.bfloat16).cuda(), torch.empty(R, Hq, d, dtype=torch.bfloat16).cuda(), torch.empty(R, Hq).cuda()
     ws = torch.empty(fm.fm_attn_shared_workspace_bytes(cache, batch, shared, R, Hq), dtype=torch.uint8, device="cuda")

@@ -976,17 +976,18 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
   __shared__ float2 other_ml[WPR > 1 ? 8 * RPW : 1];
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 4 * (lane % LPR);
-  const long long stride = (long long)gridDim.x * BLOCK;
-  long long i = (long long)blockIdx.x * BLOCK + (warp / WPR) * RPW + lane / LPR;  // this thread's row
+  // (rows are below 2^30)
+  const int all = (int)p.sh.rows, stride = gridDim.x * BLOCK;
+  int i = blockIdx.x * BLOCK + (warp / WPR) * RPW + lane / LPR;  // this thread's row
   uint32_t next[2];
-  auto look = [&](long long r) {
+  auto look = [&](int r) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) next[k] = r < p.sh.rows ? p.sh.where[k * p.sh.rows + r] : 0u;
+    for (int k = 0; k < 2; ++k) next[k] = r < all ? p.sh.where[k * p.sh.rows + r] : 0u;
   };
   look(i);
   // tokens of no sequence keep their rows
-  const long long rows = min(p.sh.rows, (long long)min(max(p.q_off[p.R], 0), p.T) * p.out.H_q);
-  for (long long b = (long long)blockIdx.x * BLOCK; b < p.sh.rows; b += stride, i += stride) {
+  const int rows = min(all, min(max(p.q_off[p.R], 0), p.T) * p.out.H_q);
+  for (int b = blockIdx.x * BLOCK; b < all; b += stride, i += stride) {
     uint32_t at[2];
     int n[2];
 #pragma unroll
@@ -1002,7 +1003,8 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
     float4 acc[V];
 #pragma unroll
     for (int x = 0; x < V; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = PARTS * (warp % WPR); j0 < n[0] + n[1]; j0 += PARTS * WPR) {
+    const int parts = n[0] + n[1];
+    for (int j0 = PARTS * (warp % WPR); j0 < parts; j0 += PARTS * WPR) {
       float2 w[PARTS];
       float4 v[PARTS][V];
 #pragma unroll
@@ -1010,13 +1012,13 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
         w[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int x = 0; x < V; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + k < n[0] + n[1]) {
+        if (j0 + k < parts) {
           const bool rest = j0 + k >= n[0];
           const int j = rest ? j0 + k - n[0] : j0 + k;
           const uint32_t where = rest ? at[1] : at[0];
           const float *from, *ml;
           if (where == 0xffffffffu) {
-            const long long r = i + (rest ? p.sh.rows : 0);
+            const size_t r = i + (rest ? p.sh.rows : 0);
             from = p.sh.full + r * D;
             ml = reinterpret_cast<const float*>(p.sh.full_ml + r);
           } else {  // slot 1 of the first CTA, slot 0 of the others
@@ -1031,7 +1033,8 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
         }
       }
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) add_part(top, sum, acc, w[k], v[k]);
+      for (int k = 0; k < PARTS; ++k)
+        if (j0 + k < parts) add_part(top, sum, acc, w[k], v[k]);
     }
     if constexpr (WPR > 1) {
 #pragma unroll
@@ -1050,7 +1053,7 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
       __syncthreads();
     }
     if (i < rows && warp % WPR == 0)
-      store_row<LPR>(p.out, i / p.out.H_q, (int)(i % p.out.H_q), col, top, sum, acc);
+      store_row<LPR>(p.out, i / p.out.H_q, i % p.out.H_q, col, top, sum, acc);
   }
 }
 
@@ -1210,9 +1213,9 @@ struct SharedPlan {
 // with chunk_kernel 32.4, e4m3 26.7, 34.8; 32 behind 32768 (128 rows) 142, 60; e4m3 107, 66.
 //
 // Whether to share at all, by what it spares at most against what it costs. Few rows a
-// sequence: the prefixes' bytes, against parts and their joining (2 us) or a second kernel
-// too (20 us): 8 sequences behind 128 keys 11.1 us, apart 9.0, 2 behind 4096 12.6, 13.0, 8
-// behind 8192 20.8, 41; 64 of 400 keys behind 100 37.6, 20.9. Chunks: products are not
+// sequence: the prefixes' bytes, against parts and their joining (2 us, where units that share
+// nothing stay whole) or a second kernel too (30 us): 8 sequences behind 128 keys 11.1 us,
+// apart 9.0, 2 behind 1021 10.7, 12.3, 8 behind 8192 20.8, 41; 64 of 400 keys behind 100 37.6, 20.9. Chunks: products are not
 // spared, but tiles of 256 rows are filled by a group that one sequence's rows leave half
 // empty; that against the joining of all rows, and short units (4 tiles' time each). 32
 // chunks of 160 rows behind 8192 keys 146 us, apart 190, of 256 221, 291; of 160 behind
@@ -1228,7 +1231,7 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, int S, int
   if (rows <= 16.0 * b.R) {
     const double row = c.k_exp ? c.d + 1.0 : 2.0 * c.d;
     spared = std::max(0, b.R - S) * keys * 2 * c.H_kv * row / 6.5e6;
-    cost = p.chunk[0] == p.chunk[1] ? 2 : 20;
+    cost = p.chunk[0] != p.chunk[1] ? 30 : shape_of(c, b, T, H_q, 1, 0, 0, false).whole ? 2 : 0;
   } else {
     // (few_kernel where chunk_kernel has no form: units of 16 rows, tiles of 32 keys, about 0.5 us each at d = 256)
     const bool ch = p.chunk[1];
@@ -1236,7 +1239,7 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, int S, int
     spared = std::max(0, b.R - S) * std::max(0.5, 1 - fill) * c.H_kv * keys / (ch ? 128 : 32) * tile;
     cost = 12 + 0.0005 * T * H_q + b.R * std::ceil(fill) * c.H_kv * 4 * tile;
   }
-  p.apart = spared < cost;
+  p.apart = spared <= cost;
   return p;
 }
 

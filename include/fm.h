@@ -601,12 +601,12 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
  *
  * Sequences [seq_off[g], seq_off[g + 1]) hold the same first prefix_len[g] keys:
  * seq_off (S + 1) ascending from 0 to R, prefix_len (S), device int32; prefix_len[g] is
- * at most kv_len - n of each of them that has new tokens (n of them). The whole pages
- * below it, prefix_len[g] / page_size rounded down, are the same pages in their rows of
- * the page table; the call reads them by the row of one of them that has new tokens (or
- * by each one's own). What is left of the prefix each sequence holds in a page of its
- * own (fm_cache_copy). A group may be one sequence, or none (its length does not matter);
- * prefix_len 0 shares nothing.
+ * at most kv_len of each of them that has new tokens, or, causal, their keys before the
+ * new tokens (kv_len - n, at least 0). The whole pages below it, prefix_len[g] / page_size
+ * rounded down, are the same pages in their rows of the page table; the call reads them by
+ * the row of one of them that has new tokens (or by each one's own). What is left of the
+ * prefix each sequence holds in a page of its own (fm_cache_copy). A group may be one
+ * sequence, or none (its length does not matter); prefix_len 0 shares nothing.
  * O and LSE are fm_attn_paged's without a window, up to the rounding of weights named
  * there and 32-bit rounding. Whether a call shares goes by T, R, S, the heads and what the
  * page table has room for: one that would gain nothing is fm_attn_paged, takes no notice

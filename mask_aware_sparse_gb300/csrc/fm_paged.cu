@@ -1090,9 +1090,9 @@ cudaError_t launch_attention(bool chunk, const PagedShape& s, const PagedWork& w
                    : launch_few<d.value, false, mode.value>(s, w, c, in, table, q, out, sh, scale, st, err);
   };
   auto dims = [&](auto mode) {
-    return c.d == 64    ? go(std::integral_constant<int, 64>{}, mode)
-           : c.d == 128 ? go(std::integral_constant<int, 128>{}, mode)
-                        : go(std::integral_constant<int, 256>{}, mode);
+    if constexpr (mode.value != kRest)  // (goes with chunk_kernel over the prefixes)
+      if (c.d == 256) return go(std::integral_constant<int, 256>{}, mode);
+    return c.d == 64 ? go(std::integral_constant<int, 64>{}, mode) : go(std::integral_constant<int, 128>{}, mode);
   };
   if constexpr (SH)
     return s.kinds == 3 ? dims(std::integral_constant<Few, kBoth>{}) : dims(std::integral_constant<Few, kRest>{});
@@ -1320,9 +1320,10 @@ size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int S, int
   // of every way a call of these sizes may run: it goes by the queries' strides too
   const fm_rows broadcast{nullptr, 0, 0};
   size_t bytes = paged_ws_bytes(c, b, T, H_q);
-  if (shared_plan(c, b, S, T, H_q, nullptr).apart) return bytes;
-  for (const fm_rows* q : {(const fm_rows*)nullptr, &broadcast})
-    bytes = std::max(bytes, shared_work(shared_plan(c, b, S, T, H_q, q), c, b, S, T, H_q, 1, nullptr).bytes);
+  for (const fm_rows* q : {(const fm_rows*)nullptr, &broadcast}) {
+    const SharedPlan p = shared_plan(c, b, S, T, H_q, q);
+    if (!p.apart) bytes = std::max(bytes, shared_work(p, c, b, S, T, H_q, 1, nullptr).bytes);
+  }
   return bytes;
 }
 

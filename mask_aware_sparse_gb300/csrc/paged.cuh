@@ -158,14 +158,14 @@ __device__ __forceinline__ bool prefix_at(const PagedShape& s, const PagedLists&
 }
 
 // Sequence r behind its group's P shared keys (prefix: the group's length as it was given).
-// Flagged too where new tokens lie in the prefix.
+// Flagged too where new tokens would lie in the prefix, or it is longer than the sequence.
 __device__ __forceinline__ bool rest_at(const PagedShape& s, const PagedLists& in, int r, int P, int prefix, int4& seq,
                                         int2& more) {
   int a, n, L;
   const bool bad = sequence_at(s, in.q_off, in.kv_len, r, a, n, L);
   seq = make_int4(a, n, L, (n * s.G + s.step - 1) / s.step);
   more = make_int2(min(P, L & -s.page), r);
-  return bad || (n > 0 && prefix > L - n);
+  return bad || (n > 0 && prefix > (s.causal ? max(L - n, 0) : L));
 }
 
 // The last g of n ascending starts that is at or below x.

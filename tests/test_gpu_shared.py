@@ -216,6 +216,47 @@ def test_same_bits_padding_rows_and_views(new, Hq):
     assert fm.fm_device_status() == OK
 
 
+@pytest.mark.parametrize("new, Hq", [([[1, 1, 1], [1, 1]], 4), ([[1, 1, 1], [1, 1]], 64), ([[20, 30, 9], [25, 3]], 8)])
+def test_prefixes_as_long_as_their_sequences(new, Hq):
+    # all keys shared: seen by all (no causal mask), and, causal, with nothing between them and the new tokens
+    s = Groups([160, 64], [[0, 0, 0], [0, 0]], new, 2, 64, 16, False, seed=86, Hq=Hq)
+    s.attend(Hq, causal=False)
+    s = Groups([160, 64], new, new, 2, 64, 16, False, seed=87, Hq=Hq)
+    s.attend(Hq)
+
+
+@pytest.mark.parametrize("n, Hq", [(3, 4), (3, 64), (20, 8)])
+def test_more_new_tokens_than_keys_behind_no_prefix(n, Hq):
+    # the first new tokens see nothing, which is no error, as without groups
+    s = Groups([0], [[64, 30, 2]], [[n, n, n]], 2, 64, 16, False, seed=88, Hq=Hq)
+    s.kv_len[2] = 2
+    q = torch.randn(3 * n, Hq, 64, generator=s.g).to(torch.bfloat16).cuda()
+    o, lse = fm.fm_attn_shared(q, s.cache, s.batch, s.shared, scale=0.125)
+    assert fm.fm_device_status() == OK
+    assert (o[2 * n:3 * n - 2] == 0).all() and torch.isneginf(lse[2 * n:3 * n - 2]).all()
+    assert_paged(o, lse, s.reference(q.cpu(), 0.125, True), 64)
+
+
+@pytest.mark.parametrize("d, f8", [(64, False), (128, True), (256, False)])
+def test_the_workspace_is_enough_for_queries_of_any_strides(d, f8):
+    # which kernels run, and whether the call shares, goes by the queries' strides too: for every size the
+    # workspace covers both (a broadcast's kernels need other parts)
+    for T, R, width in ((6, 6, 4), (6, 6, 4000), (120, 6, 40), (120, 6, 400), (120, 6, 4000), (1300, 6, 2000)):
+        cache = fm.fm_cache_new(1, 2, 16, d, dtype=torch.float8_e4m3fn if f8 else torch.bfloat16)
+        for t in (cache.k, cache.v, cache.k_exp, cache.v_exp):
+            if t is not None:
+                t.view(torch.uint8).fill_(1)
+        batch = fm.PagedBatch(_off([T // R] * R), _i32([16] * R), torch.zeros(R, width, dtype=torch.int32).cuda())
+        shared = fm.SharedPrefix(_i32([0, R]), _i32([0]))
+        need = fm.fm_attn_shared_workspace_bytes(cache, batch, shared, T, 8)
+        buf = torch.full((need + 512,), 0x5a, dtype=torch.uint8).cuda()
+        one = torch.randn(1, 1, d).to(torch.bfloat16).cuda()
+        for q in (one.expand(T, 8, d), one.expand(T, 8, d).contiguous()):
+            fm.fm_attn_shared(q, cache, batch, shared, scale=0.1, ws=buf[256:256 + need], causal=False)
+            assert fm.fm_device_status() == OK
+            assert (buf[:256] == 0x5a).all() and (buf[256 + need:] == 0x5a).all()
+
+
 def test_no_tokens():
     s = Groups([100], [[40, 50]], [[0, 0]], 2, 64, 16, False, seed=77, pad=5000)
     assert fm.fm_attn_shared_workspace_bytes(s.cache, s.batch, s.shared, 5, 4) > fm.fm_attn_paged_workspace_bytes(s.cache, s.batch, 5, 4)

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     if (tid == kPlanThreads - 1) carry = in;
     __syncthreads();
   }
-  const PagedDivision<long long> div(s, carry, units);
+  const PagedDivision<SH, long long> div(s, carry, units);
   const long long ex = div.extra * s.H_kv;
   for (int c = tid; c < s.ctas; c += kPlanThreads) {
     PagedStart st = {};

@@ -150,8 +150,14 @@ __device__ __forceinline__ bool prefix_at(const PagedShape& s, const PagedLists&
   int s1, P;
   const bool bad = group_at(s, in, g, s0, s1, P);
   const int a = min(max(in.q_off[s0], 0), s.T), n = min(max(in.q_off[s1], a), s.T) - a;
-  int row = s0;
-  while (row < s1 - 1 && in.q_off[row + 1] <= a) ++row;
+  int row = s0;  // the first with q_off[row + 1] > a
+  for (int hi = s1 - 1; row < hi;) {
+    const int mid = (row + hi) >> 1;
+    if (in.q_off[mid + 1] > a)
+      hi = mid;
+    else
+      row = mid + 1;
+  }
   seq = make_int4(a, n, P, (n * s.G + s.step - 1) / s.step);
   more = make_int2(0, min(row, s.R - 1));
   return bad;
@@ -237,8 +243,9 @@ constexpr int kWholeUnits = 320;
 // total work that 32 bits hold (offsets that descend, whose spans may overlap and add
 // up to more, plan nothing): every sequence into seq (first token, tokens,
 // keys, units; SH: the rest of it into more), its work into work (all shared memory,
-// V entries; SH: work has room for 5 S + 2 R + 2 more, R up to kLocalSeqs), the CTA's range into *out (shared memory).
-// WARPS > 1: that many of its warps take a range each, as so many CTAs.
+// V entries; SH: work has room for 5 S + 2 R + 2 more, R up to kLocalSeqs), the CTA's
+// range into *out (shared memory). WARPS > 1: that many of its warps take a range each,
+// as so many CTAs.
 template <bool SH, int WARPS = 1>
 __device__ __forceinline__ void plan_locally(const PagedShape& s, const PagedLists& given, int4* seq, int2* more,
                                              unsigned* work, PagedStart* out, int* err) {

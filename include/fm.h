@@ -608,16 +608,21 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
  * prefix each sequence holds in a page of its own (fm_cache_copy). A group may be one
  * sequence, or none (its length does not matter); prefix_len 0 shares nothing.
  * O and LSE are fm_attn_paged's without a window, up to the rounding of weights named
- * there and 32-bit rounding. Whether a call shares goes by T, R, S, the heads and what the
- * page table has room for: one that would gain nothing is fm_attn_paged, takes no notice
- * of the groups and needs no more workspace. In one that shares, offsets and lengths that
- * no such batch has set FM_DEVERR_RANGE; the rows of O and LSE are then undefined.
- * Workspace: fm_attn_shared_workspace_bytes.
+ * there and 32-bit rounding. Whether a call shares goes by T, R, S, the heads and how long
+ * prefixes may be: max_prefix (a host integer), or, where that is 0, not known, all that the
+ * page table has room for. One that would gain nothing is fm_attn_paged and takes no
+ * notice of the groups; a table with room for far more than the prefixes and no max_prefix
+ * shares short ones at a loss (up to 1.5 times fm_attn_paged's time). max_prefix decides
+ * nothing else: a prefix that is longer is no error. In a call that shares, offsets and
+ * lengths that no such batch has set FM_DEVERR_RANGE; the rows of O and LSE are then
+ * undefined. Workspace: fm_attn_shared_workspace_bytes, by the same max_prefix (it covers
+ * queries of any strides, which decide too).
  * ------------------------------------------------------------------------- */
 typedef struct fm_shared_prefix {
   const int32_t* seq_off;
   const int32_t* prefix_len;
   int32_t S;
+  int32_t max_prefix;
 } fm_shared_prefix;
 
 size_t fm_attn_shared_workspace_bytes(const fm_kv_cache* cache, const fm_paged_batch* batch,

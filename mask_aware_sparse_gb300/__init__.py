@@ -92,7 +92,8 @@ class fm_paged_batch(ctypes.Structure):
 
 
 class fm_shared_prefix(ctypes.Structure):
-    _fields_ = [("seq_off", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("S", ctypes.c_int32)]
+    _fields_ = [("seq_off", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("S", ctypes.c_int32),
+                ("max_prefix", ctypes.c_int32)]
 
 
 class FMError(RuntimeError):
@@ -1277,28 +1278,34 @@ class SharedPrefix:
     """Groups of a batch's sequences that share their first keys, int32 CUDA tensors:
     sequences [seq_off[g], seq_off[g + 1]) hold the same first prefix_len[g] keys, the
     whole pages of them as the same pages. seq_off (S + 1,) ascends from 0 to R. Checked
-    once; the tensors' values may change between calls (their addresses may not)."""
+    once; the tensors' values may change between calls (their addresses may not).
+    max_prefix: how long prefixes are at most in such calls, by which a call decides
+    whether sharing them pays (0: not known, then what the page table has room for; a
+    longer one is no error)."""
 
-    __slots__ = ("seq_off", "prefix_len", "S", "index", "c", "at")
+    __slots__ = ("seq_off", "prefix_len", "S", "index", "c", "at", "__dict__")
+    max_prefix = 0
 
-    def __init__(self, seq_off, prefix_len):
+    def __init__(self, seq_off, prefix_len, max_prefix: int = 0):
         _need(isinstance(prefix_len, torch.Tensor) and prefix_len.dim() == 1, "prefix_len must be (S,)")
         S = prefix_len.shape[0]
         _need(0 < S <= _MOST, f"there must be 1 to 2^30 groups, got {S}")
+        _need(0 <= max_prefix <= _MOST, f"max_prefix must be in [0, 2^30], got {max_prefix}")
         _like(prefix_len, "prefix_len", (S,), torch.int32)
         _like(seq_off, "seq_off", (S + 1,), torch.int32)
         _same_cuda(seq_off=seq_off, prefix_len=prefix_len)
         self.seq_off, self.prefix_len, self.S, self.index = seq_off, prefix_len, S, seq_off.get_device()
-        self.c = fm_shared_prefix(seq_off.data_ptr(), prefix_len.data_ptr(), S)
+        self.max_prefix = int(max_prefix)
+        self.c = fm_shared_prefix(seq_off.data_ptr(), prefix_len.data_ptr(), S, self.max_prefix)
         self.at = ctypes.addressof(self.c)
 
 
 @functools.lru_cache(maxsize=1024)
-def _shared_bytes(dev, T, Hq, R, width, S, n_pages, H_kv, page, d, f8):
+def _shared_bytes(dev, T, Hq, R, width, S, max_prefix, n_pages, H_kv, page, d, f8):
     c = fm_kv_cache(16, 16, 16 if f8 else 0, 16 if f8 else 0, n_pages, H_kv, page, d)
     with torch.cuda.device(dev):
         return lib().fm_attn_shared_workspace_bytes(c, fm_paged_batch(16, 16, 16, R, width),
-                                                    fm_shared_prefix(16, 16, S), T, Hq)
+                                                    fm_shared_prefix(16, 16, S, max_prefix), T, Hq)
 
 
 def fm_attn_shared_workspace_bytes(cache: KVCache, batch: PagedBatch, shared: SharedPrefix, T: int, H_q: int) -> int:
@@ -1310,8 +1317,8 @@ def fm_attn_shared_workspace_bytes(cache: KVCache, batch: PagedBatch, shared: Sh
         raise ValueError("shared must be a SharedPrefix")
     if shared.index != dev:
         raise ValueError("the groups are on another device than the cache")
-    return _shared_bytes(dev, T, H_q, batch.R, batch.width, shared.S, cache.n_pages, cache.H_kv, cache.page_size,
-                         cache.d, cache.k_exp is not None)
+    return _shared_bytes(dev, T, H_q, batch.R, batch.width, shared.S, shared.max_prefix, cache.n_pages, cache.H_kv,
+                         cache.page_size, cache.d, cache.k_exp is not None)
 
 
 @_streamed

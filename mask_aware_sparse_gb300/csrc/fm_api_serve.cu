@@ -229,7 +229,7 @@ static fm_status check_shared(const fm_kv_cache* c, const fm_paged_batch* b, con
                               int32_t H_q) {
   const fm_status st = check_paged(c, b, T, H_q);
   if (st != FM_OK) return st;
-  if (!x || x->S <= 0 || !x->seq_off || !x->prefix_len) return FM_ERR_INVALID_ARG;
+  if (!x || x->S <= 0 || x->max_prefix < 0 || !x->seq_off || !x->prefix_len) return FM_ERR_INVALID_ARG;
   if ((int64_t)T * H_q + b->R + x->S > (1 << 30)) return FM_ERR_UNSUPPORTED;
   return FM_OK;
 }
@@ -237,7 +237,7 @@ static fm_status check_shared(const fm_kv_cache* c, const fm_paged_batch* b, con
 size_t fm_attn_shared_workspace_bytes(const fm_kv_cache* cache, const fm_paged_batch* batch,
                                       const fm_shared_prefix* shared, int32_t T, int32_t H_q) {
   if (check_shared(cache, batch, shared, T, H_q) != FM_OK || T == 0) return 0;
-  return shared_ws_bytes(*cache, *batch, shared->S, T, H_q);
+  return shared_ws_bytes(*cache, *batch, *shared, T, H_q);
 }
 
 fm_status fm_attn_shared(const fm_kv_cache* cache, const fm_paged_batch* batch, const fm_shared_prefix* shared,
@@ -248,7 +248,7 @@ fm_status fm_attn_shared(const fm_kv_cache* cache, const fm_paged_batch* batch, 
   if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return FM_ERR_INVALID_ARG;
   if (T == 0) return FM_OK;
   if (!rows_ok(q) || !rows_ok(o) || !lse) return FM_ERR_INVALID_ARG;
-  if (!ws || !aligned16(ws) || ws_bytes < shared_ws_bytes(*cache, *batch, shared->S, T, H_q)) return FM_ERR_WORKSPACE;
+  if (!ws || !aligned16(ws) || ws_bytes < shared_ws_bytes(*cache, *batch, *shared, T, H_q)) return FM_ERR_WORKSPACE;
   int* err = device_error_word();
   if (!err) return FM_ERR_CUDA;
   return from_cuda(launch_shared(*cache, *batch, *shared, T, H_q, *q, *o, lse, scale, causal ? 1 : 0, ws,

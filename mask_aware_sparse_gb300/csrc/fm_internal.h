@@ -140,7 +140,7 @@ cudaError_t launch_paged(const fm_kv_cache& c, const fm_paged_batch& b, int T, i
                          cudaStream_t st, int* err);
 
 // The same where groups of sequences share their first keys (fm_paged.cu).
-size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q);
+size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q);
 cudaError_t launch_shared(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q,
                           const fm_rows& q, const fm_rows& o, float* lse, float scale, int causal, void* ws,
                           cudaStream_t st, int* err);

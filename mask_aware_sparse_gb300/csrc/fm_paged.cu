@@ -1206,7 +1206,11 @@ struct SharedPlan {
   bool chunk[2];  // the kernel over the prefixes, and over the rest; one launch where it is the same one
 };
 
-// Lengths are on the device, so the keys that the page table has room for decide.
+// Lengths are on the device, so what the caller says that prefixes are at most decides, or
+// the keys that the page table has room for. (Where a table has room for much more and no
+// bound is given, to share is the smaller mistake: behind a table for 32768 keys, 64 sequences
+// of up to 400 keys behind 100 36 us, apart 24, chunks of 250 tokens behind 1024 86, 59, but
+// 64 single tokens behind 16384, d = 256, 246, apart 628.)
 //
 // The kernel over the prefixes: few_kernel reads them again for every 16 rows, chunk_kernel
 // is a launch of its own. 16 sequences of 32 / 8 heads behind 8192 keys (64 rows): 29.5 us,
@@ -1215,14 +1219,20 @@ struct SharedPlan {
 // Whether to share at all, by what it spares at most against what it costs. Few rows a
 // sequence: the prefixes' bytes, against parts and their joining (2 us, where units that share
 // nothing stay whole) or a second kernel too (30 us): 8 sequences behind 128 keys 11.1 us,
-// apart 9.0, 2 behind 1021 10.7, 12.3, 8 behind 8192 20.8, 41; 64 of 400 keys behind 100 37.6, 20.9. Chunks: products are not
-// spared, but tiles of 256 rows are filled by a group that one sequence's rows leave half
-// empty; that against the joining of all rows, and short units (4 tiles' time each). 32
-// chunks of 160 rows behind 8192 keys 146 us, apart 190, of 256 221, 291; of 160 behind
-// 2048 73, 53; 8 of 1000 behind 4096 153, 112.
-SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q, const fm_rows* q) {
+// apart 9.0, 2 behind 1021 10.7, 12.3, 8 behind 8192 20.8, 41; 64 of 400 keys behind 100 37.6, 20.9.
+// (Units that are divided anyway cost nothing more: 2 sequences of up to 12000 keys behind 512
+// 20.9 us, apart 19.7, 8 of 4000 behind 512 22.2, 22.8, 16 of 1000 behind 2048 19.9, 26.7.)
+// Chunks: products are not spared, but a group's rows fill the tiles of 256 rows, where each
+// sequence's last one is half empty on average, or emptier; that against the joining of all
+// rows, and short units (4 tiles' time each). 32 chunks of 160 rows behind 8192 keys 146 us,
+// apart 190, of 256 221, 291; of 160 behind 2048 73, 53; 8 of 1000 behind 4096 153, 112,
+// behind 16384 409, 415, behind 30000 713, 775.
+SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q,
+                       const fm_rows* q) {
   SharedPlan p = {};
-  const double rows = (double)T * (H_q / c.H_kv), keys = (double)b.width * c.page_size;
+  const int S = x.S, room = b.width * c.page_size;
+  const double rows = (double)T * (H_q / c.H_kv);
+  const double keys = (x.max_prefix > 0 ? std::min(x.max_prefix, room) : room) & -c.page_size;  // whole pages
   p.chunk[1] = use_chunk(c, b, T, H_q, q);
   fm_paged_batch groups = b;
   groups.R = S;
@@ -1316,13 +1326,13 @@ cudaError_t launch_merge(const MergeParams& m, double parts, cudaStream_t st) {
 
 }  // namespace
 
-size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int S, int T, int H_q) {
+size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q) {
   // of every way a call of these sizes may run: it goes by the queries' strides too
   const fm_rows broadcast{nullptr, 0, 0};
   size_t bytes = paged_ws_bytes(c, b, T, H_q);
   for (const fm_rows* q : {(const fm_rows*)nullptr, &broadcast}) {
-    const SharedPlan p = shared_plan(c, b, S, T, H_q, q);
-    if (!p.apart) bytes = std::max(bytes, shared_work(p, c, b, S, T, H_q, 1, nullptr).bytes);
+    const SharedPlan p = shared_plan(c, b, x, T, H_q, q);
+    if (!p.apart) bytes = std::max(bytes, shared_work(p, c, b, x.S, T, H_q, 1, nullptr).bytes);
   }
   return bytes;
 }
@@ -1330,7 +1340,7 @@ size_t shared_ws_bytes(const fm_kv_cache& c, const fm_paged_batch& b, int S, int
 cudaError_t launch_shared(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q,
                           const fm_rows& q, const fm_rows& o, float* lse, float scale, int causal, void* ws,
                           cudaStream_t st, int* err) {
-  const SharedPlan p = shared_plan(c, b, x.S, T, H_q, &q);
+  const SharedPlan p = shared_plan(c, b, x, T, H_q, &q);
   if (p.apart) return launch_paged(c, b, T, H_q, q, o, lse, scale, causal, 0, 0, ws, st, err);
   const SharedWork k = shared_work(p, c, b, x.S, T, H_q, causal, ws);
   const PagedOut out{static_cast<char*>(o.ptr), o.st, o.sh, lse, H_q};

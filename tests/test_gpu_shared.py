@@ -488,3 +488,45 @@ def test_responses_to_one_question():
         err = (o.double() - want[rows + i].double()).abs().max()
         assert float(err) <= 2 * 2.0 ** -7 * float(v.abs().max())
     assert fm.fm_device_status() == OK
+
+
+@pytest.mark.parametrize("d, f8", [(128, False), (128, True), (64, False)])
+def test_a_bound_of_the_prefixes_decides_whether_a_call_shares(d, f8):
+    # a table with room for 32768 keys says nothing about prefixes of 100: sharing them loses (64 sequences of up
+    # to 400 keys 36 us, for 24 apart)
+    R, Hq, Hkv = 64, 32, 8
+    s = Groups([100], [[1 + 7 * i % 300 for i in range(R)]], [[1] * R], Hkv, d, 64, f8, seed=91, pad=512)
+    q, *shared = s.attend(Hq)
+    q = q.cuda()
+    apart = fm.fm_attn_paged(q, s.cache, s.batch, scale=d ** -0.5)
+    assert not torch.equal(shared[0], apart[0])
+    for most, want in ((100, apart), (63, apart), (30000, shared), (2 ** 30, shared), (0, shared)):
+        s.shared = fm.SharedPrefix(s.seq_off, s.prefix_len, max_prefix=most)
+        o, lse = fm.fm_attn_shared(q, s.cache, s.batch, s.shared, scale=d ** -0.5)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), most
+    # groups that are none are no error of a call that does not share
+    s.shared = fm.SharedPrefix(s.seq_off + 1, s.prefix_len, max_prefix=100)
+    fm.fm_attn_shared(q, s.cache, s.batch, s.shared, scale=d ** -0.5)
+    assert fm.fm_device_status() == OK
+
+
+@pytest.mark.parametrize("d, f8", [(128, False), (64, True), (256, False)])
+def test_a_bound_of_the_prefixes_of_chunks(d, f8):
+    new = [90, 70, 62, 64, 80, 50, 77, 67]
+    s = Groups([1024], [new], [new], 4, d, 64, f8, seed=92, pad=512)
+    for most, same in ((0, False), (1024, True)):
+        s.shared = fm.SharedPrefix(s.seq_off, s.prefix_len, max_prefix=most)
+        q, o, lse = s.attend(16)
+        o2, l2 = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=d ** -0.5)
+        assert (torch.equal(o, o2) and torch.equal(lse, l2)) == same
+
+
+@pytest.mark.parametrize("P, R, n", [(3000, 8, 1), (3000, 40, 1), (6000, 16, 20)])
+def test_prefixes_longer_than_their_bound(P, R, n):
+    s = Groups([P], [[n + 5] * R], [[n] * R], 8, 128, 64, False, seed=93)
+    for most, same in ((P - 100, False), (1, True)):
+        s.shared = fm.SharedPrefix(s.seq_off, s.prefix_len, max_prefix=most)
+        assert s.shared.max_prefix == most
+        q, o, lse = s.attend(32)
+        o2, l2 = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=128 ** -0.5)
+        assert (torch.equal(o, o2) and torch.equal(lse, l2)) == same

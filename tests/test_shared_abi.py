@@ -159,3 +159,16 @@ def test_bindings_arguments_refused(lib, monkeypatch):  # noqa: F811
                                          torch.empty(big, dtype=i32, device="meta"))):
         with pytest.raises(ValueError, match="2\\^30"):
             call()
+
+
+def test_bounds_of_prefixes_refused(lib):  # noqa: F811
+    c, b = _cache(), _batch()
+    bad = fm.fm_shared_prefix(A, A, 1, -1)
+    assert lib.fm_attn_shared(c, b, bad, 3, 4, ROWS, 0.1, 1, ROWS, A, A, 1 << 30, 0) == I
+    assert lib.fm_attn_shared_workspace_bytes(c, b, bad, 3, 4) == 0
+    for most in (1, 2 ** 31 - 1):
+        assert lib.fm_attn_shared_workspace_bytes(c, b, fm.fm_shared_prefix(A, A, 1, most), 3, 4) > 0
+    off = torch.zeros(2, dtype=torch.int32)
+    for most in (-1, 2 ** 30 + 1, 2 ** 32):
+        with pytest.raises(ValueError, match="max_prefix"):
+            fm.SharedPrefix(off, off[1:], max_prefix=most)

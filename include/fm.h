@@ -609,8 +609,8 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
  * sequence, or none (its length does not matter); prefix_len 0 shares nothing.
  * O and LSE are fm_attn_paged's without a window, up to the rounding of weights named
  * there and 32-bit rounding. Whether a call shares goes by T, R, S, the heads and how long
- * prefixes may be: max_prefix (a host integer), or, where that is 0, not known, all that the
- * page table has room for. One that would gain nothing is fm_attn_paged and takes no
+ * prefixes may be: max_prefix (a host integer), or, where that is 0 or less, not known, all
+ * that the page table has room for. One that would gain nothing is fm_attn_paged and takes no
  * notice of the groups; a table with room for far more than the prefixes and no max_prefix
  * shares short ones at a loss (up to 1.5 times fm_attn_paged's time). max_prefix decides
  * nothing else: a prefix that is longer is no error. In a call that shares, offsets and

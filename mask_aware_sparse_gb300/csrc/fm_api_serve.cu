@@ -229,7 +229,7 @@ static fm_status check_shared(const fm_kv_cache* c, const fm_paged_batch* b, con
                               int32_t H_q) {
   const fm_status st = check_paged(c, b, T, H_q);
   if (st != FM_OK) return st;
-  if (!x || x->S <= 0 || x->max_prefix < 0 || !x->seq_off || !x->prefix_len) return FM_ERR_INVALID_ARG;
+  if (!x || x->S <= 0 || !x->seq_off || !x->prefix_len) return FM_ERR_INVALID_ARG;
   if ((int64_t)T * H_q + b->R + x->S > (1 << 30)) return FM_ERR_UNSUPPORTED;
   return FM_OK;
 }

@@ -161,13 +161,15 @@ def test_bindings_arguments_refused(lib, monkeypatch):  # noqa: F811
             call()
 
 
-def test_bounds_of_prefixes_refused(lib):  # noqa: F811
+def test_bounds_of_prefixes(lib):  # noqa: F811
+    # a program that leaves the bound as it finds it is not refused: below 0 it is not known, like 0
     c, b = _cache(), _batch()
-    bad = fm.fm_shared_prefix(A, A, 1, -1)
-    assert lib.fm_attn_shared(c, b, bad, 3, 4, ROWS, 0.1, 1, ROWS, A, A, 1 << 30, 0) == I
-    assert lib.fm_attn_shared_workspace_bytes(c, b, bad, 3, 4) == 0
-    for most in (1, 2 ** 31 - 1):
-        assert lib.fm_attn_shared_workspace_bytes(c, b, fm.fm_shared_prefix(A, A, 1, most), 3, 4) > 0
+    room = lib.fm_attn_shared_workspace_bytes(c, b, _groups(), 3, 4)
+    for most in (-2 ** 31, -1, 0, 1, 2 ** 31 - 1):
+        x = fm.fm_shared_prefix(A, A, 1, most)
+        need = lib.fm_attn_shared_workspace_bytes(c, b, x, 3, 4)
+        assert need > 0 and (most > 0 or need == room)
+        assert lib.fm_attn_shared(c, b, x, 3, 4, ROWS, 0.1, 1, ROWS, A, A, need - 1, 0) == W
     off = torch.zeros(2, dtype=torch.int32)
     for most in (-1, 2 ** 30 + 1, 2 ** 32):
         with pytest.raises(ValueError, match="max_prefix"):

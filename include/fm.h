@@ -606,7 +606,8 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
  * rounded down, are the same pages in their rows of the page table; the call reads them by
  * the row of one of them that has new tokens (or by each one's own). What is left of the
  * prefix each sequence holds in a page of its own (fm_cache_copy). A group may be one
- * sequence, or none (its length does not matter); prefix_len 0 shares nothing.
+ * sequence, or none (its length does not matter); prefix_len 0 shares nothing, nor does a
+ * group of which one sequence alone has new tokens.
  * O and LSE are fm_attn_paged's without a window, up to the rounding of weights named
  * there and 32-bit rounding. Whether a call shares goes by T, R, S, the heads and how long
  * prefixes may be: max_prefix (a host integer), or, where that is 0 or less, not known, all

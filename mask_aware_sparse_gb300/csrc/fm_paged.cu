@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       if (r < vs) return prefix_at(s, p.in, r, q, more, s0);
       const int g = last_at(p.in.seq_off, s.S, r - vs);
       const bool off = group_at(s, p.in, g, s0, s1, P);
+      if (alone(p.in, r - vs, s0, s1)) P = 0;
       return rest_at(s, p.in, r - vs, P, p.in.prefix_len[g], q, more) || off;
     } else {
       const bool off = sequence_at(s, p.in.q_off, p.in.kv_len, r, q.x, q.y, q.z);

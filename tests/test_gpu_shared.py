@@ -530,3 +530,23 @@ def test_prefixes_longer_than_their_bound(P, R, n):
         q, o, lse = s.attend(32)
         o2, l2 = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=128 ** -0.5)
         assert (torch.equal(o, o2) and torch.equal(lse, l2)) == same
+
+
+@pytest.mark.parametrize("new, Hq", [([[1], [0, 1, 0], [1, 1]], 4), ([[1], [0, 1, 0], [1, 1]], 160),
+                                     ([[20], [0, 33, 0], [25, 31]], 8), ([[1], [0, 3, 0], [2, 1]] + [[1]] * 260, 4)])
+@pytest.mark.parametrize("f8", [False, True])
+def test_a_prefix_that_one_sequence_alone_uses_is_no_prefix(new, Hq, f8):
+    # a group of one, and one whose other sequences have no new tokens: as if the group's length were 0
+    prefix = [300, 200, 90] + [37] * (len(new) - 3)
+    s = Groups(prefix, [[40], [50, 60, 30], [30, 35]] + [[9]] * (len(new) - 3), new, 2, 64, 16, f8, seed=94, Hq=Hq)
+    q, o, lse = s.attend(Hq)
+    plain = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=0.125)
+    s.prefix_len[0] = s.prefix_len[1] = 0
+    s.prefix_len[3:] = 0
+    o2, l2 = fm.fm_attn_shared(q.cuda(), s.cache, s.batch, s.shared, scale=0.125)
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+    assert not torch.equal(lse, plain[1])  # (the call shares)
+    # lengths that no sequence has are flagged all the same
+    s.prefix_len[0] = 340
+    fm.fm_attn_shared(q.cuda(), s.cache, s.batch, s.shared, scale=0.125)
+    assert fm.fm_device_status() == RANGE

@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 
 // -------------------------------------------------------------- few query rows
 constexpr int kFewRows = 16;
+static_assert(kFewRows <= kMarkRows, "a mark's row");
 constexpr int kTileKeys = 32;
 constexpr float kTopBits = 7.f;  // e4m3: weights go up to 2^(7 + 8)
 
@@ -994,10 +995,10 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t w = at[k] = next[k];
-      const int first = (int)(w >> 20), parts = (int)(w >> 8 & 0xfffu), row = (int)(w & 0xffu);
-      n[k] = i >= rows ? 0 : w == 0xffffffffu ? 1 : parts;
+      const int first = mark_first(w), parts = mark_parts(w), row = mark_row(w);
+      n[k] = i >= rows ? 0 : w == kMarkWhole ? 1 : parts;
       // (what a batch that is none left there)
-      if (w != 0xffffffffu && (first + parts > p.ctas[k] || row >= p.slot_rows[k])) n[k] = 0;
+      if (w != kMarkWhole && (first + parts > p.ctas[k] || row >= p.slot_rows[k])) n[k] = 0;
     }
     look(i + stride);
     float top = -INFINITY, sum = 0.f;
@@ -1018,15 +1019,15 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
           const int j = rest ? j0 + k - n[0] : j0 + k;
           const uint32_t where = rest ? at[1] : at[0];
           const float *from, *ml;
-          if (where == 0xffffffffu) {
+          if (where == kMarkWhole) {
             const size_t r = i + (rest ? p.sh.rows : 0);
             from = p.sh.full + r * D;
             ml = reinterpret_cast<const float*>(p.sh.full_ml + r);
           } else {  // slot 1 of the first CTA, slot 0 of the others
             const float* s = (rest ? p.part[1] : p.part[0]) + (rest ? p.part_floats[1] : p.part_floats[0]) *
-                                                                  (2 * (size_t)((where >> 20) + j) + (j == 0 ? 1 : 0));
-            from = s + (size_t)(where & 0xffu) * D;
-            ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * (where & 0xffu);
+                                                                  (2 * (size_t)(mark_first(where) + j) + (j == 0 ? 1 : 0));
+            from = s + (size_t)mark_row(where) * D;
+            ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * mark_row(where);
           }
           w[k] = *reinterpret_cast<const float2*>(ml);
 #pragma unroll
@@ -1264,8 +1265,9 @@ PagedShape shared_shape(const fm_kv_cache& c, const fm_paged_batch& b, int S, in
   // what starting on a unit costs, in tiles (chunks of 20 to 60 tokens behind 8192 keys 157 us, with 2
   // 196: short units of many rows; 6 and 8 as 4)
   if (chunk) s.extra = 4;
-  if (!chunk && kinds == 2) {  // (kRest)
-    s.ctas *= few_warps(c.d, c.k_exp != nullptr);
+  const bool rest = !chunk && kinds == 2;  // (kRest)
+  s.ctas = marked_workers(s.ctas, rest ? few_warps(c.d, c.k_exp != nullptr) : 1);
+  if (rest) {
     s.least = 1;
     s.extra = 4;
   }

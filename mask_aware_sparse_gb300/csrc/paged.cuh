@@ -550,9 +550,8 @@ struct PagedWalk {
 };
 
 // Where results of rows with a shared prefix go: row i = token * H_q + head of kind k (0: over the
-// prefix, 1: over the rest) to where[k * rows + i]. ~0: all of it is in full (rows of d sums) and
-// full_ml; else it is in the partial slots of CTAs first .. first + n - 1 at `row`, first << 20 |
-// n << 8 | row.
+// prefix, 1: over the rest) to where[k * rows + i], a mark. kMarkWhole: all of it is in full (rows
+// of d sums) and full_ml; else it is in the partial slots of CTAs first .. first + n - 1 at `row`.
 struct SharedOut {
   float* full;
   float2* full_ml;
@@ -560,12 +559,27 @@ struct SharedOut {
   long long rows;  // T * H_q
 };
 
+// A mark: 12 bits each of the first CTA and the parts, 8 of the row.
+constexpr uint32_t kMarkWhole = 0xffffffffu;
+constexpr int kMarkCtas = 0xfff, kMarkRows = 256;
+__host__ __device__ constexpr uint32_t mark_of(int first, int parts) {
+  return (uint32_t)first << 20 | (uint32_t)parts << 8;
+}
+__host__ __device__ constexpr int mark_first(uint32_t w) { return (int)(w >> 20); }
+__host__ __device__ constexpr int mark_parts(uint32_t w) { return (int)(w >> 8 & 0xfffu); }
+__host__ __device__ constexpr int mark_row(uint32_t w) { return (int)(w & 0xffu); }
+
+// Workers with a range each of a launch that leaves marks, `warps` a CTA: those of all the CTAs
+// that the SMs hold, but no more than a mark can name (on 152 SMs 1824 at most).
+constexpr int marked_workers(int ctas, int warps) {
+  return (ctas * warps < kMarkCtas ? ctas : kMarkCtas / warps) * warps;
+}
+
 // Which of a segment's rows' entries of `where` this CTA writes: whole units', and divided ones'
 // that it is the second CTA of (0: none). c: its number.
 __device__ __forceinline__ uint32_t shared_mark(bool whole, int kt, const PagedStart& st, int c) {
-  if (whole) return 0xffffffffu;
-  return kt > 0 && st.first == c - 1 ? (uint32_t)st.first << 20 | (uint32_t)(st.last - st.first + 1) << 8
-                                                   : 0u;
+  if (whole) return kMarkWhole;
+  return kt > 0 && st.first == c - 1 ? mark_of(st.first, st.last - st.first + 1) : 0u;
 }
 
 // Workspace of one call: units, the running sum of their work, CTA starts, the
@@ -682,6 +696,7 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
 }
 
 constexpr int kChunkRows = 256;  // rows of a chunk_kernel partial slot: two tiles
+static_assert(kChunkRows <= kMarkRows, "a mark's row");
 // (sh: sequences share prefixes, results go there)
 cudaError_t launch_paged_chunk(const PagedShape& s, const PagedWork& w, const fm_kv_cache& c, const PagedLists& in,
                                const int32_t* table, const fm_rows& q, const PagedOut& out, const SharedOut* sh,

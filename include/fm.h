@@ -497,9 +497,11 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  * reads back or (fm_attn_paged) shows some new token a key of that page: entries
  * past a sequence's end or behind its window may hold anything. All device int32.
  * Tokens from q_off[R] on belong to no sequence: what their rows hold has no effect,
- * and nothing is written for them. Values that no such batch has (a page outside
- * [0, n_pages), a length outside [0, width * page_size], offsets that do not ascend
- * from 0 or pass T, those of fm_cache_read n_rows) set FM_DEVERR_RANGE. The cache
+ * and nothing is written for them. A sequence may have no new tokens (a slot out of
+ * use): its row of the table may hold anything, its length anything that a length may be.
+ * Values that no such batch has (a page outside [0, n_pages), a length outside
+ * [0, width * page_size], of a slot out of use too, offsets that do not ascend from 0 or
+ * pass T, those of fm_cache_read n_rows) set FM_DEVERR_RANGE. The cache
  * calls then write nothing if an offset or a length is one of them, and leave out
  * the tokens whose page is; what rows of O and LSE such a batch receives is
  * undefined. Nothing outside the tensors is touched.

@@ -550,3 +550,37 @@ def test_a_prefix_that_one_sequence_alone_uses_is_no_prefix(new, Hq, f8):
     s.prefix_len[0] = 340
     fm.fm_attn_shared(q.cuda(), s.cache, s.batch, s.shared, scale=0.125)
     assert fm.fm_device_status() == RANGE
+
+
+@pytest.mark.parametrize("new, Hq", [([[0, 1, 1], [1, 0]], 8), ([[0, 1, 1], [1, 0]], 128), ([[0, 30, 20], [25, 0]], 8)])
+def test_lengths_of_slots_out_of_use(new, Hq):
+    # any that a length may be, without an effect; others are flagged, as those of slots in use, and nothing is written
+    s = Groups([100, 64], [[40, 50, 60], [30, 35]], new, 2, 64, 16, False, seed=95, Hq=Hq)
+    q, o, lse = s.attend(Hq)
+    T, room = sum(s.new), 16 * s.table.shape[1]
+    q, kv = q.cuda(), torch.randn(T, 4, 64, generator=s.g).to(torch.bfloat16).cuda()
+    k, v = kv.split([2, 2], 1)
+    fm.fm_cache_write(k, v, s.cache, s.batch)
+    want = (fm.fm_attn_shared(q, s.cache, s.batch, s.shared, scale=0.125), fm.fm_attn_paged(q, s.cache, s.batch, scale=0.125))
+    held = [s.cache.k.clone(), s.cache.v.clone()]
+    for length in (0, 1, room, -1, room + 1, 2 ** 31 - 1, -2 ** 31):
+        bits = OK if 0 <= length <= room else RANGE
+        for r in (0, 4):
+            s.table[r] = -1 if r else 2 ** 30
+            s.kv_len[r] = length
+        got = fm.fm_attn_shared(q, s.cache, s.batch, s.shared, scale=0.125)
+        assert fm.fm_device_status() == bits
+        also = fm.fm_attn_paged(q, s.cache, s.batch, scale=0.125)
+        assert fm.fm_device_status() == bits
+        if bits == OK:
+            assert all(torch.equal(a, b) for x, y in zip((got, also), want) for a, b in zip(x, y))
+        for write in (lambda a, b: fm.fm_cache_write(a, b, s.cache, s.batch),
+                      lambda a, b: fm.fm_cache_append(q, a, b, s.cache, s.batch)):
+            for x, y in zip((s.cache.k, s.cache.v), held):
+                x.copy_(y)
+            write(-k, -v)
+            assert fm.fm_device_status() == bits
+            same = [torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip((s.cache.k, s.cache.v), held)]
+            assert same == [bits == RANGE] * 2
+        for x, y in zip((s.cache.k, s.cache.v), held):
+            x.copy_(y)

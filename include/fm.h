@@ -533,7 +533,9 @@ fm_status fm_qk_norm_rope_bwd(const fm_qk_problem* p, const fm_view* dqo, const 
  * i < n (device int32): a sequence that forks gets its own copy of a page it will write
  * to. A pair of two -1 copies nothing; any other page outside [0, n_pages) sets
  * FM_DEVERR_RANGE and its pair is left out. A page that is copied to may be in no other
- * pair (its contents are undefined if it is).
+ * pair: pairs are copied in no order, so that it, and what is copied from it, would be
+ * undefined, without an error. Beams that change places copy to free pages, which then take
+ * the old ones' places in the table.
  * ------------------------------------------------------------------------- */
 typedef struct fm_rows {
   void* ptr;

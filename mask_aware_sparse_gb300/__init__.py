@@ -1205,7 +1205,8 @@ def fm_cache_append(q, k, v, cache: KVCache, batch: PagedBatch, *, positions=Non
 @_streamed
 def fm_cache_copy(cache: KVCache, src, dst):
     """Make page dst[i] a copy of page src[i] (int32 CUDA (n,); a pair of two -1 copies
-    nothing). A page that is copied to may be in no other pair."""
+    nothing). A page that is copied to may be in no other pair (pairs are copied in no order):
+    pages that change places go by way of free ones."""
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
     dev = cache.index

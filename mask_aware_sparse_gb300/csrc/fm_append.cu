@@ -13,8 +13,10 @@
 // need none of that and are in flight first; offsets and lengths are read once a block,
 // into shared memory, where each token looks its sequence up; a step's table entries are
 // loaded while the step before it is computed.
-// Between both it is issue slots and warps that count: four blocks an SM with one row
-// ahead a thread and nothing spilled take 213 us for 32768 tokens of 64 / 8 heads, d = 128
+// Between both no one resource is full (8192 tokens of 32 / 8 heads into an e4m3 cache:
+// issue slots 67%, memory 45%, the last of 1.7 rounds of steps part empty; the largest stall
+// is a step's barriers, of which there are three), and what counts is warps that have work
+// meanwhile: four blocks an SM with one row ahead a thread and nothing spilled take 213 us for 32768 tokens of 64 / 8 heads, d = 128
 // (6.3 TB/s, 93% of the copy rate), and 40.7 us for 8192 tokens of 32 / 8 into an e4m3
 // cache; with three blocks 231 and 44.9, two rows ahead in as many registers (spilled)
 // 257 and 48.8, rows by asynchronous copies three ahead 294 and 43.2, teams of warps that
@@ -31,7 +33,7 @@ namespace {
 
 constexpr int kThreads = kRopeThreads, kWarps = kRopeWarps;
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kPerSm = 4;   // blocks of each side
+constexpr int kPerSm = 4;   // blocks that an SM holds; of each side as many at most, queries' before keys'
 constexpr int kHeld = 256;  // sequences whose offsets and lengths a block keeps
 
 struct Rows3 {

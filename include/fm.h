@@ -613,7 +613,10 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
  * sequence, or none (its length does not matter); prefix_len 0 shares nothing, nor does a
  * group of which one sequence alone has new tokens.
  * O and LSE are fm_attn_paged's without a window, up to the rounding of weights named
- * there and 32-bit rounding. Whether a call shares goes by T, R, S, the heads and how long
+ * there and 32-bit rounding; which kernel a prefix takes goes by the rows of its groups, on
+ * average, not by each sequence's: behind a prefix that more than 64 rows a KV head share,
+ * single tokens' weights over it are rounded to bf16 once too (2^-8 of each, where
+ * fm_attn_paged keeps 2^-16 or fp16's 2^-11). Whether a call shares goes by T, R, S, the heads and how long
  * prefixes may be: max_prefix (a host integer), or, where that is 0 or less, not known, all
  * that the page table has room for. One that would gain nothing is fm_attn_paged and takes no
  * notice of the groups; a table with room for far more than the prefixes and no max_prefix
@@ -621,7 +624,8 @@ fm_status fm_attn_paged(const fm_kv_cache* cache, const fm_paged_batch* batch, i
  * nothing else: a prefix that is longer is no error. In a call that shares, offsets and
  * lengths that no such batch has set FM_DEVERR_RANGE; the rows of O and LSE are then
  * undefined. Workspace: fm_attn_shared_workspace_bytes, by the same max_prefix (it covers
- * queries of any strides, which decide too).
+ * queries of any strides, which decide too; 8 (d + 3) bytes a token and query head and the
+ * parts of divided units, where a call shares).
  * ------------------------------------------------------------------------- */
 typedef struct fm_shared_prefix {
   const int32_t* seq_off;

@@ -16,9 +16,9 @@
 // Between both no one resource is full (8192 tokens of 32 / 8 heads into an e4m3 cache:
 // issue slots 67%, memory 45%, the last of 1.7 rounds of steps part empty; the largest stall
 // is a step's barriers, of which there are three), and what counts is warps that have work
-// meanwhile: four blocks an SM with one row ahead a thread and nothing spilled take 213 us for 32768 tokens of 64 / 8 heads, d = 128
-// (6.3 TB/s, 93% of the copy rate), and 40.7 us for 8192 tokens of 32 / 8 into an e4m3
-// cache; with three blocks 231 and 44.9, two rows ahead in as many registers (spilled)
+// meanwhile: four blocks an SM with one row ahead a thread and nothing spilled take 213 us
+// for 32768 tokens of 64 / 8 heads, d = 128 (6.3 TB/s, 93% of the copy rate), and 40.7 us
+// for 8192 tokens of 32 / 8 into an e4m3 cache; with three blocks 231 and 44.9, two rows ahead in as many registers (spilled)
 // 257 and 48.8, rows by asynchronous copies three ahead 294 and 43.2, teams of warps that
 // wait for one another alone 237 and 45.1. 64 tokens of 64 sequences: 4.8 us.
 #include <type_traits>

@@ -1229,6 +1229,15 @@ struct SharedPlan {
 // rows, and short units (4 tiles' time each). 32 chunks of 160 rows behind 8192 keys 146 us,
 // apart 190, of 256 221, 291; of 160 behind 2048 73, 53; 8 of 1000 behind 4096 153, 112,
 // behind 16384 409, 415, behind 30000 713, 775.
+//
+// Chunks where chunk_kernel has no form (d = 256): few_kernel's units of 16 rows are full either
+// way, and ranges that start anywhere in a prefix read it from L2 at two thirds of the rate of
+// units that start together (32 sequences of 30 tokens of 16 / 4 heads behind 8192 keys 2006 us,
+// apart 1299, e4m3 1303, 779; of 5 tokens 319, 272, e4m3 225, 171). What sharing brings there is
+// that units are divided where whole ones, about 0.5 us a tile, would leave most CTAs idle: 4
+// sequences of 9 tokens of 8 / 4 heads behind 655 keys, e4m3, 18.0, apart 23.2. Long ones are
+// divided either way; sharing still gains with very few units (3 of 8 tokens of 4 / 1 heads
+// behind 4187 19.0, 24.6), not with more (4 of 18 of 16 / 4 behind 8192 164, 113).
 SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, const fm_shared_prefix& x, int T, int H_q,
                        const fm_rows* q) {
   SharedPlan p = {};
@@ -1244,12 +1253,15 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, const fm_s
     const double row = c.k_exp ? c.d + 1.0 : 2.0 * c.d;
     spared = std::max(0, b.R - S) * keys * 2 * c.H_kv * row / 6.5e6;
     cost = p.chunk[0] != p.chunk[1] ? 30 : shape_of(c, b, T, H_q, 1, 0, 0, false).whole ? 2 : 0;
-  } else {
-    // (few_kernel where chunk_kernel has no form: units of 16 rows, tiles of 32 keys, about 0.5 us each at d = 256)
-    const bool ch = p.chunk[1];
-    const double tile = (ch ? 1.5 : 0.5) / sm_count(), fill = rows / b.R / (ch ? 256 : 16);
-    spared = std::max(0, b.R - S) * std::max(0.5, 1 - fill) * c.H_kv * keys / (ch ? 128 : 32) * tile;
+  } else if (p.chunk[1]) {
+    const double tile = 1.5 / sm_count(), fill = rows / b.R / 256;
+    spared = std::max(0, b.R - S) * std::max(0.5, 1 - fill) * c.H_kv * keys / 128 * tile;
     cost = 12 + 0.0005 * T * H_q + b.R * std::ceil(fill) * c.H_kv * 4 * tile;
+  } else {
+    const double busy = b.R * std::ceil(rows / b.R / kFewRows) * c.H_kv / (sm_count() * few_ctas(c.d, c.k_exp != nullptr));
+    const double whole = keys / kTileKeys * 0.5 * c.d / 256;  // a unit's time
+    spared = whole > 32 && busy > 0.125 ? 0 : std::max(0, b.R - S) / (double)b.R * (1 - 1.5 * busy) * whole;
+    cost = 3;
   }
   p.apart = spared <= cost;
   return p;

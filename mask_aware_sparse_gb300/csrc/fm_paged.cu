@@ -700,8 +700,10 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
         const long long at = kind * p.sh.rows + (long long)(tok0 + x / G) * p.out.H_q + h * G + x % G;
         float* part = p.w.part + p.w.part_floats * (2 * (size_t)worker + part_slot);
         float* to = whole ? p.sh.full + at * D : part + (size_t)row * D;
-        // e4m3: O's unit is 2^mo, the part's 2^m
-        const float f = F8 ? ex2_approx(mo[i] - (m[i] == -INFINITY ? 0.f : m[i])) : 1.f;
+        // e4m3: O's unit is 2^mo, the part's 2^m (by two factors, as where warps are joined)
+        const float apart = F8 ? mo[i] - (m[i] == -INFINITY ? 0.f : m[i]) : 0.f;
+        const float f = F8 ? ex2_approx(apart < -64.f ? apart + 64.f : apart) : 1.f;
+        const float down = F8 && apart < -64.f ? 0x1p-64f : 1.f;
         if constexpr (F8) {
           // columns 64 cg + 16 t + 8 y + (0 .. 7)
 #pragma unroll
@@ -711,8 +713,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
 #pragma unroll
               for (int z = 0; z < 2; ++z)
                 *reinterpret_cast<float4*>(to + 64 * cg + 16 * t + 8 * y + 4 * z) =
-                    make_float4(f * o[8 * cg + 4 * z][2 * i + y], f * o[8 * cg + 4 * z + 1][2 * i + y],
-                                f * o[8 * cg + 4 * z + 2][2 * i + y], f * o[8 * cg + 4 * z + 3][2 * i + y]);
+                    make_float4(f * o[8 * cg + 4 * z][2 * i + y] * down, f * o[8 * cg + 4 * z + 1][2 * i + y] * down,
+                                f * o[8 * cg + 4 * z + 2][2 * i + y] * down, f * o[8 * cg + 4 * z + 3][2 * i + y] * down);
         } else {
 #pragma unroll
           for (int c = 0; c < D / 8; ++c)
@@ -762,11 +764,21 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
 #pragma unroll
         for (int k = 0; k < C::WARPS; ++k) top = fmaxf(top, ml[k * kFewRows + row].x);
         const float base = top == -INFINITY ? 0.f : top;
+        // e4m3: O's unit may be far below 2^m, by the values' scales (2^-126 and less): a factor
+        // that exp2's smallest numbers do not hold, so it is taken as two
+        float up = 0.f;
+        if constexpr (F8) {
+          float unit = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < C::WARPS; ++k) unit = fmaxf(unit, ml[k * kFewRows + row].z);
+          up = unit - base < -64.f ? 64.f : 0.f;
+        }
+        const float down = up > 0.f ? 0x1p-64f : 1.f;
 #pragma unroll
         for (int k = 0; k < C::WARPS; ++k) {
           const float4 v = ml[k * kFewRows + row];
           sum += ex2_approx(v.x - base) * v.y;
-          w[k] = ex2_approx(v.z - base);
+          w[k] = ex2_approx(v.z - base + up);
         }
         const float inv = SH || !whole ? 1.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
         const int64_t tok = tok0 + x / G;
@@ -789,6 +801,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
             a.z += w[k] * v.z;
             a.w += w[k] * v.w;
           }
+          a = make_float4(a.x * down, a.y * down, a.z * down, a.w * down);
           if (!SH && whole)
             *reinterpret_cast<uint2*>(dst + 2 * col) =
                 make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));

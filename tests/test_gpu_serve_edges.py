@@ -173,3 +173,18 @@ def test_angles_at_far_positions_of_any_frequency(inter):
         # theta's rounding to fp32 (2^-24 of half a turn), cos and sin (2^-22), one bf16 rounding
         assert bool(((x - want).abs() <= BF16_HALF * want.abs() * 1.01 + 2.0 ** -20).all())
     assert (got[:, 32:] == 1).all()
+
+
+@pytest.mark.parametrize("d, Hq, new", [(64, 4, [1, 1]), (128, 32, [1, 1]), (256, 4, [1, 1]), (128, 4, [40, 20]), (256, 4, [40, 20])])
+@pytest.mark.parametrize("power", [-120, -112, -108, -60, 100])
+def test_quantised_values_far_from_one(d, Hq, new, power):
+    # scales down to 2^-126 are further below a row's largest weight than exp2's smallest numbers
+    s = Setup([500, 33], new, 2, d, 16, True, seed=37)
+    s.v = (s.v.double() * 2.0 ** power).to(torch.bfloat16)
+    fm.fm_cache_write(s.k.cuda(), s.v.cuda(), s.cache, fm.PagedBatch(s.kv_off, s.kv_len, s.table))
+    q = torch.randn(sum(new), Hq, d, generator=s.g).to(torch.bfloat16)
+    o, lse = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=d ** -0.5)
+    k, v = s.values()
+    O, L, A, mag = paged(q.double(), k, v, s.q_off.tolist(), s.keys, d ** -0.5, True, 0, 0)
+    one = 2.0 ** -power  # (the bounds are relative)
+    assert_paged(o.double() * one, lse, (O * one, L, A * one, mag), d)

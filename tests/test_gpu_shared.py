@@ -596,3 +596,22 @@ def test_chunks_of_wide_heads_share_where_few_units_would_leave_the_rest_idle(R,
     q, o, lse = s.attend(4 * Hkv)
     o2, l2 = fm.fm_attn_paged(q.cuda(), s.cache, s.batch, scale=1 / 16)
     assert (torch.equal(o, o2) and torch.equal(lse, l2)) != shares
+
+
+@pytest.mark.parametrize("new, Hq", [([[1, 1, 1], [1, 1]], 4), ([[1, 1, 1], [1, 1]], 128), ([[30, 20, 31], [25, 40]], 8)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power", [-120, -108, 100])
+def test_quantised_values_far_from_one(new, Hq, d, power):
+    # scales down to 2^-126 are further below a row's largest weight than exp2's smallest numbers
+    # (such chunks at d = 256 are not shared)
+    s = Groups([300, 140], [[40, 50, 60], [64, 45]], new, 2, d, 16, True, seed=97,
+               Hq=None if d == 256 and new[0][0] > 1 else Hq)
+    for x in s.rows:
+        x[1] = (x[1].double() * 2.0 ** power).to(torch.bfloat16)
+    s.write()
+    q = torch.randn(sum(s.new), Hq, d, generator=s.g).to(torch.bfloat16)
+    o, lse = fm.fm_attn_shared(q.cuda(), s.cache, s.batch, s.shared, scale=d ** -0.5)
+    O, L, A, mag = s.reference(q, d ** -0.5, True)
+    one = 2.0 ** -power  # (the bounds are relative)
+    assert_paged(o.double() * one, lse, (O * one, L, A * one, mag), d)
+    assert fm.fm_device_status() == OK

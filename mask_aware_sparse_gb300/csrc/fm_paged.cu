@@ -711,10 +711,12 @@ __global__ void __launch_bounds__(FewCfg<D, F8>::THREADS, FewCfg<D, F8>::PER_SM)
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
-              for (int z = 0; z < 2; ++z)
+              for (int z = 0; z < 2; ++z) {
+                const float(*a)[4] = o + 8 * cg + 4 * z;
+                const int x = 2 * i + y;
                 *reinterpret_cast<float4*>(to + 64 * cg + 16 * t + 8 * y + 4 * z) =
-                    make_float4(f * o[8 * cg + 4 * z][2 * i + y] * down, f * o[8 * cg + 4 * z + 1][2 * i + y] * down,
-                                f * o[8 * cg + 4 * z + 2][2 * i + y] * down, f * o[8 * cg + 4 * z + 3][2 * i + y] * down);
+                    make_float4(f * a[0][x] * down, f * a[1][x] * down, f * a[2][x] * down, f * a[3][x] * down);
+              }
         } else {
 #pragma unroll
           for (int c = 0; c < D / 8; ++c)
@@ -1037,8 +1039,8 @@ __global__ void __launch_bounds__(256, merge_blocks(D, WPR)) merge_kernel(const 
             from = p.sh.full + r * D;
             ml = reinterpret_cast<const float*>(p.sh.full_ml + r);
           } else {  // slot 1 of the first CTA, slot 0 of the others
-            const float* s = (rest ? p.part[1] : p.part[0]) + (rest ? p.part_floats[1] : p.part_floats[0]) *
-                                                                  (2 * (size_t)(mark_first(where) + j) + (j == 0 ? 1 : 0));
+            const size_t slot = 2 * (size_t)(mark_first(where) + j) + (j == 0 ? 1 : 0);
+            const float* s = (rest ? p.part[1] : p.part[0]) + (rest ? p.part_floats[1] : p.part_floats[0]) * slot;
             from = s + (size_t)mark_row(where) * D;
             ml = s + (size_t)(rest ? p.slot_rows[1] : p.slot_rows[0]) * D + 2 * mark_row(where);
           }
@@ -1271,7 +1273,8 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_paged_batch& b, const fm_s
     spared = std::max(0, b.R - S) * std::max(0.5, 1 - fill) * c.H_kv * keys / 128 * tile;
     cost = 12 + 0.0005 * T * H_q + b.R * std::ceil(fill) * c.H_kv * 4 * tile;
   } else {
-    const double busy = b.R * std::ceil(rows / b.R / kFewRows) * c.H_kv / (sm_count() * few_ctas(c.d, c.k_exp != nullptr));
+    const double units = b.R * std::ceil(rows / b.R / kFewRows) * c.H_kv;
+    const double busy = units / (sm_count() * few_ctas(c.d, c.k_exp != nullptr));
     const double whole = keys / kTileKeys * 0.5 * c.d / 256;  // a unit's time
     spared = whole > 32 && busy > 0.125 ? 0 : std::max(0, b.R - S) / (double)b.R * (1 - 1.5 * busy) * whole;
     cost = 3;
